@@ -204,6 +204,81 @@ svdq_status svdq_gemm_qkv(const svdq_layer_desc* d, const void* w_packed, const 
 svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
                             int64_t ldx, void* Y, int64_t ldy, uint32_t epi, void* stream);
 
+/* A layer with 16-bit activations, for few tokens (one decoded token per stream, a
+ * conditioning vector): the packed layer of any format with its smoothing and its
+ * low-rank branch, the activations not quantized,
+ *     Y = act( X_hat deQ(Q4(R))^T + (X_hat L1) L2 + b ),  X_hat = fp32(X / lambda),
+ * on the same blob that svdq_linear takes.  Sums are fp32; X_hat enters as a sum of bf16
+ * parts that holds it to 2^-18 (bf16 output) or to fp32's own rounding (SVDQ_EPI_OUT_F32).
+ * Two launches: one prepares X_hat and X_hat L1, one streams the codes, once for up to 8
+ * tokens (5 with float32 output) and once per 16 tokens beyond; any M >= 0 is computed
+ * correctly.  A row with a non-finite element gives a non-finite row; no other row changes.
+ *   X, Y, epi  as for svdq_linear (all SVDQ_EPI_* flags)
+ *   workspace  device, at least svdq_w4a16_bytes(d, M) bytes, 256-byte aligned; every call
+ *              writes what it reads of it.  Calls that may overlap (other streams, captured
+ *              graphs that run at once) need workspaces of their own.
+ * Checks and errors as svdq_linear. */
+size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M);
+svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
+                              int64_t ldx, void* Y, int64_t ldy, uint32_t epi, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* Flags of svdq_moe_route. */
+enum {
+  SVDQ_ROUTE_SIGMOID = 1u, /* scores are sigmoid(logit); without it softmax over the E logits */
+  SVDQ_ROUTE_RENORM = 2u   /* a token's weights are divided by their sum (0 when that is 0)   */
+};
+
+/* The router of a mixture of experts:
+ *     logits = X router^T,  score[m, e] = softmax or sigmoid of the logits,
+ *     ids[m, :]     = the top_k experts by score[m, e] + bias[e], largest first, the lower
+ *                     index first among equals, a NaN behind every other value,
+ *     weights[m, j] = scale * score[m, ids[m, j]]  (bias is in the choice only).
+ * Logits, scores and the choice are computed in float64, so the choice does not hang on an
+ * order of summation; weights are rounded to float32 once.  ids are always top_k different
+ * experts in [0, E), also for a token with NaN or infinite features (whose weights are then
+ * not finite).
+ *   X        device, bf16 bits, M x K, row stride ldx (K <= ldx <= 2^24, multiple of 8)
+ *   router   device, bf16 bits, E x K row-major; X and router 16-byte aligned
+ *   bias     device, float32[E], or NULL
+ *   ids, weights  device, int32 and float32, M x top_k row-major
+ *   workspace     device, at least svdq_moe_route_bytes(M, E) bytes, 256-byte aligned
+ * 8 <= K <= 65536, 1 <= E <= 512, 1 <= top_k <= min(E, 32), scale not NaN, else
+ * SVDQ_ERR_SHAPE; K or ldx not a multiple of 8 gives SVDQ_ERR_ALIGN, unknown flags
+ * SVDQ_ERR_FORMAT. */
+size_t svdq_moe_route_bytes(int64_t M, int32_t E);
+svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K, const uint16_t* router, int32_t E,
+                           const float* bias, int32_t top_k, uint32_t flags, float scale, int32_t* ids, float* weights,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* The experts' products of a mixture of experts, for few tokens:
+ *     h[m, j] = act(X[m] Wg_e^T + bg_e) * (X[m] Wu_e^T + bu_e),   e = ids[m, j],
+ *     Y[m]    = sum_j weights[m, j] (h[m, j] Wd_e^T + bd_e),
+ * act = SiLU, or GELU (erf form) with SVDQ_EPI_GELU; the biases with SVDQ_EPI_BIAS.  Two
+ * launches, each reading the weights of an expert only if a token asks for it.  Sums are
+ * fp32 in a fixed order (the same call gives the same bits); h is not rounded to bf16 (it is
+ * kept to 2^-18, or to fp32's own rounding with SVDQ_EPI_OUT_F32).
+ *   dg, wg_packed  one expert's gate and up projection as one layer, K = H inputs, N = 2 F
+ *                  outputs, rows [gate | up]; E blobs of svdq_pack_weight, one after the
+ *                  other, svdq_weight_bytes(dg) apart
+ *   dd, wd_packed  one expert's down projection, K = F, N outputs; E blobs likewise
+ *                  Any of the formats each, rank 0; lambda is not applied (pack with 1).
+ *   X          device, bf16 bits, M x H, row stride ldx (H <= ldx <= 2^24)
+ *   ids, weights  device, int32 and float32, M x top_k (svdq_moe_route's, or any: the same
+ *              expert twice counts twice; an id outside [0, E) adds nothing, for example an
+ *              expert on another device or a padded token)
+ *   Y          device, M x N, row stride ldy, bf16, or float32 with SVDQ_EPI_OUT_F32
+ *   workspace  device, at least svdq_moe_bytes(dg, dd, M, top_k) bytes, 256-byte aligned
+ * Any M >= 0 is computed correctly (calls of more than 2048 pairs run in parts, two launches
+ * each).  dg->N != 2 dd->K, E outside [1, 512] or top_k outside [1, 32] give SVDQ_ERR_SHAPE,
+ * a rank other than 0 or other flags SVDQ_ERR_FORMAT; other checks and errors as svdq_linear.
+ * A token with non-finite features gives a non-finite row; no other row changes. */
+size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k);
+svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svdq_layer_desc* dd,
+                     const void* wd_packed, int32_t E, const uint16_t* X, int64_t M, int64_t ldx, const int32_t* ids,
+                     const float* weights, int32_t top_k, void* Y, int64_t ldy, uint32_t epi, void* workspace,
+                     size_t ws_bytes, void* stream);
+
 /* Both launches; workspace >= svdq_act_bytes(d, M) bytes (device, 256-aligned). */
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X,
                         int64_t M, int64_t ldx, void* Y, int64_t ldy, uint32_t epi,

@@ -9,10 +9,11 @@ call raises if the library is not built or the device is not gfx950.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 from ._lib import (EPI_BIAS, EPI_GELU, EPI_LOWRANK, EPI_OUT_F32, INT4_G64, MXFP4, NVFP4, LIB_PATH,  # noqa: F401
-                   LayerDesc, SvdqError, check, lib)
+                   ROUTE_RENORM, ROUTE_SIGMOID, LayerDesc, SvdqError, check, lib)
 
 FORMATS = {"mxfp4": MXFP4, "int4": INT4_G64, "nvfp4": NVFP4}
 GROUPS = {"mxfp4": 32, "int4": 64, "nvfp4": 16}
@@ -179,6 +180,196 @@ def linear_noalloc(layer: Layer, w_packed, X, epi: int, out=None, stream=None):
                                    _stream(stream))
     check("svdq_linear_noalloc", st)
     return out
+
+
+# ---- few tokens: 16-bit activations, experts ----
+#
+# These calls check what the C entry points cannot see of a tensor (type, device, shape,
+# inner stride, bytes of a packed weight) and raise ValueError.  They run on the device of
+# their tensors, on `stream` or its current stream; what they allocate belongs to that stream.
+
+@functools.lru_cache(maxsize=4096)
+def _kept_desc(layer: Layer):
+    d = layer.desc()
+    p = ctypes.byref(d)
+    return d, p, int(lib().svdq_weight_bytes(p))
+
+
+def _rows(t, name: str, cols: int, device, dtypes) -> int:
+    """Row stride of an M x cols matrix; a single row's is cols (its stride says nothing)."""
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype not in dtypes or t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name}: expected rows x {cols} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} "
+                         f"on {t.device}")
+    if t.shape[0] <= 1:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        return (cols + 7) // 8 * 8
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0)
+
+
+def _flat(t, name: str, shape, device, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} of {dtype} on {device}, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
+
+
+def _blob(t, name: str, nbytes: int, device):
+    if t.dtype != _torch().uint8 or t.numel() != nbytes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {nbytes} contiguous bytes on {device}, got {tuple(t.shape)} of {t.dtype} on "
+                         f"{t.device}")
+
+
+def _space(t, nbytes: int, device):
+    """A caller's workspace, checked, or a new one."""
+    if t is None:
+        return _empty_u8(nbytes or 256, device)        # 0 bytes: an invalid shape, which the call itself reports
+    if t.dtype != _torch().uint8 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous bytes on {device}, got {t.dtype} on {t.device}")
+    return t
+
+
+def _on(device, stream, call):
+    """call(stream pointer) with `device` current and allocations made on the call's stream."""
+    torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            return call(ctypes.c_void_p(stream.cuda_stream))
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return call(_stream())
+    return call(_stream())
+
+
+def w4a16_bytes(layer: Layer, M: int) -> int:
+    """Workspace bytes of linear_w4a16 for M tokens (0: invalid)."""
+    return int(lib().svdq_w4a16_bytes(_kept_desc(layer)[1], int(M)))
+
+
+def linear_w4a16(layer: Layer, w_packed, X, epi: int = 0, out=None, workspace=None, stream=None):
+    """Y = act(X_hat deQ(Q(R))^T + (X_hat L1) L2 + b), X_hat = X / lam not quantized: a packed
+    layer of any format for few tokens (X: M x K bf16); returns Y (M x N, bf16, or float32
+    with EPI_OUT_F32)."""
+    torch = _torch()
+    _, p, wb = _kept_desc(layer)
+    dev = X.device
+    ldx = _rows(X, "X", layer.K, dev, (torch.bfloat16, torch.int16))
+    _blob(w_packed, "w_packed", wb, dev)
+    M, dt = X.shape[0], torch.float32 if epi & EPI_OUT_F32 else torch.bfloat16
+
+    def call(s):
+        y = torch.empty((M, layer.N), dtype=dt, device=dev) if out is None else out
+        ldy = layer.N if out is None else _rows(y, "out", layer.N, dev, (dt,))
+        if y.shape[0] != M:
+            raise ValueError(f"out: {y.shape[0]} rows for {M} tokens")
+        ws = _space(workspace, lib().svdq_w4a16_bytes(p, M), dev)
+        check("svdq_linear_w4a16", lib().svdq_linear_w4a16(p, _ptr(w_packed), _ptr(X), M, ldx, _ptr(y), ldy, epi,
+                                                           _ptr(ws), ws.numel(), s))
+        return y
+
+    return _on(dev, stream, call)
+
+
+def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: bool = True, scale: float = 1.0,
+              ids=None, weights=None, workspace=None, stream=None):
+    """The router of a mixture of experts: X (M x K bf16), router (E x K bf16, contiguous), bias
+    (float32[E] or None, for the choice only).  Returns ids (int32 M x top_k, by falling score)
+    and weights (float32 M x top_k): softmax (or sigmoid) scores, divided by a token's sum with
+    `renorm`, times `scale`."""
+    torch = _torch()
+    dev, bf = X.device, (torch.bfloat16, torch.int16)
+    if router.dim() != 2 or router.dtype not in bf:
+        raise ValueError(f"router: expected experts x features of {bf}, got {tuple(router.shape)} of {router.dtype}")
+    E, K = router.shape
+    ldx = _rows(X, "X", K, dev, bf)
+    _flat(router, "router", (E, K), dev, router.dtype)
+    if bias is not None:
+        _flat(bias, "bias", (E,), dev, torch.float32)
+    M, top_k = X.shape[0], int(top_k)
+    flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_RENORM if renorm else 0)
+
+    def call(s):
+        shape = (M, max(top_k, 1))                           # an invalid top_k is the call's to report
+        i = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else ids
+        w = torch.empty(shape, dtype=torch.float32, device=dev) if weights is None else weights
+        _flat(i, "ids", shape, dev, torch.int32)
+        _flat(w, "weights", shape, dev, torch.float32)
+        ws = _space(workspace, lib().svdq_moe_route_bytes(M, E), dev)
+        check("svdq_moe_route", lib().svdq_moe_route(_ptr(X), M, ldx, K, _ptr(router), E, _ptr(bias), top_k, flags,
+                                                     scale, _ptr(i), _ptr(w), _ptr(ws), ws.numel(), s))
+        return i, w
+
+    return _on(dev, stream, call)
+
+
+def moe_route_bytes(M: int, E: int) -> int:
+    """Workspace bytes of moe_route (0: invalid)."""
+    return int(lib().svdq_moe_route_bytes(int(M), int(E)))
+
+
+def moe_bytes(gate_up: Layer, down: Layer, M: int, top_k: int) -> int:
+    """Workspace bytes of moe (0: invalid)."""
+    return int(lib().svdq_moe_bytes(_kept_desc(gate_up)[1], _kept_desc(down)[1], int(M), int(top_k)))
+
+
+def pack_experts(layer: Layer, R, bias=None, stream=None):
+    """E experts' weights of one layer shape (rank 0, lambda 1): R (E x N x K fp32), bias (E x N
+    bf16 or None) -> E x weight_bytes(layer) uint8, as moe takes them."""
+    torch = _torch()
+    if layer.rank != 0 or R.dim() != 3 or tuple(R.shape[1:]) != (layer.N, layer.K):
+        raise ValueError(f"expected rank 0 and weights E x {layer.N} x {layer.K}, got rank {layer.rank} and {tuple(R.shape)}")
+    dev, E = R.device, R.shape[0]
+    _flat(R, "R", R.shape, dev, torch.float32)
+    if bias is not None:
+        _flat(bias, "bias", (E, layer.N), dev, bias.dtype if bias.dtype in (torch.bfloat16, torch.int16) else torch.bfloat16)
+
+    def call(s):
+        out = torch.empty((E, weight_bytes(layer)), dtype=torch.uint8, device=dev)
+        one = torch.ones(layer.K, dtype=torch.float32, device=dev)
+        for e in range(E):
+            pack_weight(layer, R[e], None, None, one, None if bias is None else bias[e], out=out[e], stream=stream)
+        return out
+
+    return _on(dev, stream, call)
+
+
+def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi: int = 0, out=None, workspace=None,
+        stream=None):
+    """The experts' products of a mixture of experts for few tokens: X (M x K bf16), ids and
+    weights (M x top_k, int32 and float32), wg_packed and wd_packed (E packed experts each,
+    pack_experts: gate_up's outputs are [gate | up], twice down.K).  Y = sum_j weights[:, j]
+    down(act(gate) * up), act SiLU or, with EPI_GELU, GELU; returns Y (M x down.N, bf16, or
+    float32 with EPI_OUT_F32)."""
+    torch = _torch()
+    (_, pg, gb), (_, pd, db) = _kept_desc(gate_up), _kept_desc(down)
+    dev = X.device
+    ldx = _rows(X, "X", gate_up.K, dev, (torch.bfloat16, torch.int16))
+    if wg_packed.dim() != 2:
+        raise ValueError(f"wg_packed: expected experts x {gb} bytes, got {tuple(wg_packed.shape)}")
+    E, M = wg_packed.shape[0], X.shape[0]
+    _blob(wg_packed, "wg_packed", E * gb, dev)
+    _blob(wd_packed, "wd_packed", E * db, dev)
+    if ids.dim() != 2:
+        raise ValueError(f"ids: expected tokens x choices, got {tuple(ids.shape)}")
+    top_k = ids.shape[1]
+    _flat(ids, "ids", (M, top_k), dev, torch.int32)
+    _flat(weights, "weights", (M, top_k), dev, torch.float32)
+    dt = torch.float32 if epi & EPI_OUT_F32 else torch.bfloat16
+
+    def call(s):
+        y = torch.empty((M, down.N), dtype=dt, device=dev) if out is None else out
+        ldy = down.N if out is None else _rows(y, "out", down.N, dev, (dt,))
+        if y.shape[0] != M:
+            raise ValueError(f"out: {y.shape[0]} rows for {M} tokens")
+        ws = _space(workspace, lib().svdq_moe_bytes(pg, pd, M, top_k), dev)
+        check("svdq_moe", lib().svdq_moe(pg, _ptr(wg_packed), pd, _ptr(wd_packed), E, _ptr(X), M, ldx, _ptr(ids),
+                                         _ptr(weights), top_k, _ptr(y), ldy, epi, _ptr(ws), ws.numel(), s))
+        return y
+
+    return _on(dev, stream, call)
 
 
 def _scales_out(torch, layer: Layer, rows: int, dev):

@@ -13,6 +13,8 @@ EPI_LOWRANK = 1
 EPI_BIAS = 2
 EPI_GELU = 4
 EPI_OUT_F32 = 8
+ROUTE_SIGMOID = 1
+ROUTE_RENORM = 2
 
 STATUS = {0: "SVDQ_OK", 1: "SVDQ_ERR_NULL", 2: "SVDQ_ERR_SHAPE", 3: "SVDQ_ERR_FORMAT", 4: "SVDQ_ERR_ALIGN",
           5: "SVDQ_ERR_WORKSPACE", 6: "SVDQ_ERR_DEVICE", 7: "SVDQ_ERR_LAUNCH", 8: "SVDQ_ERR_TOO_LARGE"}
@@ -31,6 +33,14 @@ SIGNATURES = {
     "svdq_gemm_qkv": (ctypes.c_int, [_D, _P, _P, _I64, ctypes.c_uint32, ctypes.c_int32, _P, _P, ctypes.c_float,
                                      _P, _P, _P, _I64, _P]),
     "svdq_gemm_w4a16": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P]),
+    "svdq_w4a16_bytes": (ctypes.c_size_t, [_D, _I64]),
+    "svdq_linear_w4a16": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
+    "svdq_moe_route_bytes": (ctypes.c_size_t, [_I64, ctypes.c_int32]),
+    "svdq_moe_route": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_int32,
+                                      ctypes.c_uint32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
+    "svdq_moe_bytes": (ctypes.c_size_t, [_D, _D, _I64, ctypes.c_int32]),
+    "svdq_moe": (ctypes.c_int, [_D, _P, _D, _P, ctypes.c_int32, _P, _I64, _I64, _P, _P, ctypes.c_int32, _P, _I64,
+                                ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
     "svdq_linear": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
     "svdq_linear_noalloc": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P]),
     "svdq_unpack_weight": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P]),

@@ -30,6 +30,16 @@ hipError_t launch_gemm_qkv(int fmt, const uint8_t* wblob, const WeightLayout& wl
                            hipStream_t s);
 hipError_t launch_gemm_w4a16(const uint8_t* wblob, const WeightLayout& wl, int K, int N, const uint16_t* X,
                              int64_t ldx, int64_t M, void* Y, int64_t ldy, uint32_t epi, hipStream_t s);
+hipError_t launch_linear_w4a16(int fmt, const uint8_t* wblob, const WeightLayout& wl, int K, int N, const uint16_t* X,
+                               int64_t ldx, int64_t M, void* Y, int64_t ldy, uint32_t epi, void* planes, float* part,
+                               hipStream_t s);
+hipError_t launch_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int K, const uint16_t* Wr, const float* bias,
+                            int E, int top_k, uint32_t flags, float scale, int32_t* ids, float* weights, double* logits,
+                            hipStream_t s);
+hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int fmt_d, const uint8_t* wd,
+                      const WeightLayout& ld, int H, int F, int N, int E, const uint16_t* X, int64_t M, int64_t ldx,
+                      const int32_t* ids, const float* weights, int top_k, void* Y, int64_t ldy, uint32_t epi,
+                      void* h, hipStream_t s);
 hipError_t launch_unpack_weight(int fmt, int K, int N, int rank, const WeightLayout& wl, const uint8_t* blob,
                                 uint8_t* codes, void* scales, uint16_t* L1, uint16_t* L2, float* lam, uint16_t* bias,
                                 hipStream_t s);
@@ -107,6 +117,27 @@ svdq_status scratch_address(uint8_t** out) {
   }
   *out = p;
   return SVDQ_OK;
+}
+
+// Workspace of svdq_linear_w4a16: X_hat as up to three bf16 planes, then the down
+// projection's partial sums, one per 512 of K.
+struct W4A16Layout { size_t planes, part, total; };
+W4A16Layout w4a16_layout(const svdq_layer_desc* d, int64_t M) {
+  const size_t rows = size_t(M > 0 ? M : 1);
+  W4A16Layout l;
+  l.planes = 0;
+  l.part = align256(rows * d->K * 6);
+  l.total = align256(l.part + size_t(d->K / kKSuper) * rows * round_up(d->rank, kRankAlign) * 4);
+  return l;
+}
+
+bool valid_moe_shape(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
+  return check_shape(dg) == SVDQ_OK && check_shape(dd) == SVDQ_OK && dg->N == 2 * dd->K && M >= 0 && M <= kMaxRows &&
+         top_k >= 1 && top_k <= kMoeMaxTopK;
+}
+size_t moe_bytes(const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
+  const int64_t pairs = M * top_k < kMoeMaxPairs ? M * top_k : kMoeMaxPairs;
+  return align256(size_t(pairs > 0 ? pairs : 1) * dd->K * 6);
 }
 
 svdq_status check_act_args(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,
@@ -285,6 +316,82 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
   const WeightLayout wl = weight_layout(d->fmt, d->K, d->N, d->rank);
   return launched(launch_gemm_w4a16(static_cast<const uint8_t*>(w_packed), wl, d->K, d->N, X, ldx, M, Y, ldy, epi,
                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M) {
+  if (!d || check_shape(d) != SVDQ_OK || check_fmt(d) != SVDQ_OK || M < 0 || M > kMaxRows) return 0;
+  return w4a16_layout(d, M).total;
+}
+
+svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
+                              int64_t ldx, void* Y, int64_t ldy, uint32_t epi, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  svdq_status s = check_act_args(d, w_packed, X, M, ldx, workspace);
+  if (s != SVDQ_OK) return s;
+  if ((s = check_gemm_args(d, w_packed, workspace, M, Y, ldy, epi)) != SVDQ_OK) return s;
+  const W4A16Layout l = w4a16_layout(d, M);
+  if (ws_bytes < l.total) return SVDQ_ERR_WORKSPACE;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  const WeightLayout wl = weight_layout(d->fmt, d->K, d->N, d->rank);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return launched(launch_linear_w4a16(d->fmt, static_cast<const uint8_t*>(w_packed), wl, d->K, d->N, X, ldx, M, Y, ldy,
+                                      epi, ws + l.planes, reinterpret_cast<float*>(ws + l.part),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_moe_route_bytes(int64_t M, int32_t E) {
+  if (M < 0 || M > kMaxRows || E < 1 || E > kMoeMaxE) return 0;
+  return align256(size_t(M > 0 ? M : 1) * E * 8);
+}
+
+svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K, const uint16_t* router, int32_t E,
+                           const float* bias, int32_t top_k, uint32_t flags, float scale, int32_t* ids, float* weights,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  if (!router || !workspace || (M > 0 && (!X || !ids || !weights))) return SVDQ_ERR_NULL;
+  if (M < 0 || M > kMaxRows || K < 8 || K > 65536 || ldx < K || ldx > kMaxLdx || E < 1 || E > kMoeMaxE ||
+      top_k < 1 || top_k > kMoeMaxTopK || top_k > E || !(scale == scale))
+    return SVDQ_ERR_SHAPE;
+  if ((flags & ~uint32_t(SVDQ_ROUTE_SIGMOID | SVDQ_ROUTE_RENORM)) != 0) return SVDQ_ERR_FORMAT;
+  if (K % 8 != 0 || ldx % 8 != 0 || !aligned(X, 16) || !aligned(router, 16) || !aligned(bias, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4) || !aligned(workspace, 256))
+    return SVDQ_ERR_ALIGN;
+  if (ws_bytes < svdq_moe_route_bytes(M, E)) return SVDQ_ERR_WORKSPACE;
+  svdq_status s = device_check();
+  if (s != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  return launched(launch_moe_route(X, M, ldx, K, router, bias, E, top_k, flags, scale, ids, weights,
+                                   static_cast<double*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
+  if (!dg || !dd || !valid_moe_shape(dg, dd, M, top_k)) return 0;
+  return moe_bytes(dd, M, top_k);
+}
+
+svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svdq_layer_desc* dd,
+                     const void* wd_packed, int32_t E, const uint16_t* X, int64_t M, int64_t ldx, const int32_t* ids,
+                     const float* weights, int32_t top_k, void* Y, int64_t ldy, uint32_t epi, void* workspace,
+                     size_t ws_bytes, void* stream) {
+  if (!dg || !dd || !wg_packed || !wd_packed || !workspace || (M > 0 && (!X || !ids || !weights || !Y)))
+    return SVDQ_ERR_NULL;
+  if (!valid_moe_shape(dg, dd, M, top_k) || E < 1 || E > kMoeMaxE || ldx < dg->K || ldx > kMaxLdx ||
+      ldy < dd->N)
+    return SVDQ_ERR_SHAPE;
+  svdq_status s = check_fmt(dg);
+  if (s != SVDQ_OK || (s = check_fmt(dd)) != SVDQ_OK) return s;
+  if (dg->rank != 0 || dd->rank != 0 || (epi & ~uint32_t(SVDQ_EPI_BIAS | SVDQ_EPI_GELU | SVDQ_EPI_OUT_F32)) != 0)
+    return SVDQ_ERR_FORMAT;
+  if (!aligned(wg_packed, 256) || !aligned(wd_packed, 256) || !aligned(workspace, 256) || !aligned(X, 16) ||
+      !aligned(Y, 16) || !aligned(ids, 4) || !aligned(weights, 4) || ldx % 8 != 0 || ldy % 8 != 0)
+    return SVDQ_ERR_ALIGN;
+  if (ws_bytes < moe_bytes(dd, M, top_k)) return SVDQ_ERR_WORKSPACE;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  const WeightLayout lg = weight_layout(dg->fmt, dg->K, dg->N, 0), ld = weight_layout(dd->fmt, dd->K, dd->N, 0);
+  return launched(launch_moe(dg->fmt, static_cast<const uint8_t*>(wg_packed), lg, dd->fmt,
+                             static_cast<const uint8_t*>(wd_packed), ld, dg->K, dd->K, dd->N, E, X, M, ldx, ids, weights,
+                             top_k, Y, ldy, epi, workspace, static_cast<hipStream_t>(stream)));
 }
 
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,

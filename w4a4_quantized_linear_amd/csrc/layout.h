@@ -44,6 +44,12 @@ constexpr int kFmtINT4 = 2;
 constexpr int kFmtNVFP4 = 3;
 constexpr float kNvfp4GlobalDiv = 2688.0f;   // E2M1 max 6 times E4M3 max 448
 
+// svdq_moe: experts, choices per token, and (token, choice) pairs per pair of launches
+// (longer calls run in parts).
+constexpr int kMoeMaxE = 512;
+constexpr int kMoeMaxTopK = 32;
+constexpr int kMoeMaxPairs = 2048;
+
 // Scale bytes per row: K/32 (E8M0 per 32, or fp16 per 64), K/16 for NVFP4 (E4M3 per 16).
 __host__ __device__ inline size_t scale_row_bytes(int fmt, int K) { return fmt == kFmtNVFP4 ? K / 16 : K / 32; }
 constexpr uint32_t kLamRangeBit = 1;   // weight flags: a lambda outside [2^-32, 2^32]
