@@ -36,6 +36,7 @@ class Layer:
         return GROUPS[self.fmt]
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -187,90 +188,99 @@ def linear_noalloc(layer: Layer, w_packed, X, epi: int, out=None, stream=None):
 # These calls check what the C entry points cannot see of a tensor (type, device, shape,
 # inner stride, bytes of a packed weight) and raise ValueError.  They run on the device of
 # their tensors, on `stream` or its current stream; what they allocate belongs to that stream.
+# A decoding step makes many of them on kernels of a few microseconds, so a call keeps to
+# plain attribute reads, raw addresses and one lookup of the layer's descriptor.
 
 @functools.lru_cache(maxsize=4096)
 def _kept_desc(layer: Layer):
     d = layer.desc()
-    p = ctypes.byref(d)
-    return d, p, int(lib().svdq_weight_bytes(p))
+    p = ctypes.byref(d)                                   # keeps d alive
+    return p, int(lib().svdq_weight_bytes(p))
 
 
 def _rows(t, name: str, cols: int, device, dtypes) -> int:
-    """Row stride of an M x cols matrix; a single row's is cols (its stride says nothing)."""
-    if t.dim() != 2 or t.shape[1] != cols or t.dtype not in dtypes or t.device != device or t.device.type != "cuda":
-        raise ValueError(f"{name}: expected rows x {cols} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} "
+    """Row stride of a matrix of `cols` columns; a single row's is cols (its stride says nothing)."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or t.dtype not in dtypes or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: expected rows x {cols} of {dtypes} on {device}, got {tuple(shape)} of {t.dtype} "
                          f"on {t.device}")
-    if t.shape[0] <= 1:
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-        return (cols + 7) // 8 * 8
-    if t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0)
+    return ld if shape[0] > 1 else (cols + 7) // 8 * 8
 
 
 def _flat(t, name: str, shape, device, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {tuple(shape)} of {dtype} on {device}, got {tuple(t.shape)} of "
                          f"{t.dtype} on {t.device}")
 
 
-def _blob(t, name: str, nbytes: int, device):
+def _bytes(t, name: str, nbytes: int, device):
     if t.dtype != _torch().uint8 or t.numel() != nbytes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected {nbytes} contiguous bytes on {device}, got {tuple(t.shape)} of {t.dtype} on "
                          f"{t.device}")
 
 
 def _space(t, nbytes: int, device):
-    """A caller's workspace, checked, or a new one."""
+    """A caller's workspace, checked, or a new one; None where the call needs none (or is invalid,
+    which it then reports itself)."""
     if t is None:
-        return _empty_u8(nbytes or 256, device)        # 0 bytes: an invalid shape, which the call itself reports
+        return _empty_u8(nbytes, device) if nbytes else None
     if t.dtype != _torch().uint8 or t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace: expected contiguous bytes on {device}, got {t.dtype} on {t.device}")
     return t
 
 
-def _on(device, stream, call):
-    """call(stream pointer) with `device` current and allocations made on the call's stream."""
+def _elsewhere(device, stream, call):
+    """call() with `device` and, if given, `stream` current."""
     torch = _torch()
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            if stream.device != device:
-                raise ValueError(f"stream of {stream.device} for tensors on {device}")
-            return call(ctypes.c_void_p(stream.cuda_stream))
-    if device.index != torch.cuda.current_device():
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    if stream is None:
         with torch.cuda.device(device):
-            return call(_stream())
-    return call(_stream())
+            return call()
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def w4a16_bytes(layer: Layer, M: int) -> int:
-    """Workspace bytes of linear_w4a16 for M tokens (0: invalid)."""
-    return int(lib().svdq_w4a16_bytes(_kept_desc(layer)[1], int(M)))
+    """Workspace bytes of linear_w4a16 for M tokens (0: none needed, or invalid)."""
+    return int(lib().svdq_w4a16_bytes(_kept_desc(layer)[0], int(M)))
 
 
 def linear_w4a16(layer: Layer, w_packed, X, epi: int = 0, out=None, workspace=None, stream=None):
     """Y = act(X_hat deQ(Q(R))^T + (X_hat L1) L2 + b), X_hat = X / lam not quantized: a packed
     layer of any format for few tokens (X: M x K bf16); returns Y (M x N, bf16, or float32
     with EPI_OUT_F32)."""
-    torch = _torch()
-    _, p, wb = _kept_desc(layer)
-    dev = X.device
+    torch, dev = _torch(), X.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        return _elsewhere(dev, stream, lambda: linear_w4a16(layer, w_packed, X, epi, out, workspace))
+    p, wb = _kept_desc(layer)
     ldx = _rows(X, "X", layer.K, dev, (torch.bfloat16, torch.int16))
-    _blob(w_packed, "w_packed", wb, dev)
-    M, dt = X.shape[0], torch.float32 if epi & EPI_OUT_F32 else torch.bfloat16
+    _bytes(w_packed, "w_packed", wb, dev)
+    M, N, dt = X.shape[0], layer.N, torch.float32 if epi & EPI_OUT_F32 else torch.bfloat16
+    if out is None:
+        out, ldy = torch.empty((M, N), dtype=dt, device=dev), N
+    else:
+        ldy = _rows(out, "out", N, dev, (dt,))
+        if out.shape[0] != M:
+            raise ValueError(f"out: {out.shape[0]} rows for {M} tokens")
+    L = lib()
+    ws = _space(workspace, L.svdq_w4a16_bytes(p, M), dev)
+    st = L.svdq_linear_w4a16(p, w_packed.data_ptr(), X.data_ptr(), M, ldx, out.data_ptr(), ldy, epi,
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                             torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_linear_w4a16", st)
+    return out
 
-    def call(s):
-        y = torch.empty((M, layer.N), dtype=dt, device=dev) if out is None else out
-        ldy = layer.N if out is None else _rows(y, "out", layer.N, dev, (dt,))
-        if y.shape[0] != M:
-            raise ValueError(f"out: {y.shape[0]} rows for {M} tokens")
-        ws = _space(workspace, lib().svdq_w4a16_bytes(p, M), dev)
-        check("svdq_linear_w4a16", lib().svdq_linear_w4a16(p, _ptr(w_packed), _ptr(X), M, ldx, _ptr(y), ldy, epi,
-                                                           _ptr(ws), ws.numel(), s))
-        return y
 
-    return _on(dev, stream, call)
+def moe_route_bytes(M: int, E: int) -> int:
+    """Workspace bytes of moe_route (0: none needed, or invalid)."""
+    return int(lib().svdq_moe_route_bytes(int(M), int(E)))
 
 
 def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: bool = True, scale: float = 1.0,
@@ -279,61 +289,60 @@ def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: b
     (float32[E] or None, for the choice only).  Returns ids (int32 M x top_k, by falling score)
     and weights (float32 M x top_k): softmax (or sigmoid) scores, divided by a token's sum with
     `renorm`, times `scale`."""
-    torch = _torch()
-    dev, bf = X.device, (torch.bfloat16, torch.int16)
-    if router.dim() != 2 or router.dtype not in bf:
-        raise ValueError(f"router: expected experts x features of {bf}, got {tuple(router.shape)} of {router.dtype}")
-    E, K = router.shape
-    ldx = _rows(X, "X", K, dev, bf)
-    _flat(router, "router", (E, K), dev, router.dtype)
+    torch, dev = _torch(), X.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        return _elsewhere(dev, stream, lambda: moe_route(X, router, top_k, bias, sigmoid, renorm, scale, ids, weights,
+                                                         workspace))
+    shape = router.shape
+    if len(shape) != 2 or router.dtype not in (torch.bfloat16, torch.int16):
+        raise ValueError(f"router: expected experts x features of bf16, got {tuple(shape)} of {router.dtype}")
+    E, K = shape
+    ldx = _rows(X, "X", K, dev, (torch.bfloat16, torch.int16))
+    _flat(router, "router", shape, dev, router.dtype)
     if bias is not None:
         _flat(bias, "bias", (E,), dev, torch.float32)
     M, top_k = X.shape[0], int(top_k)
-    flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_RENORM if renorm else 0)
-
-    def call(s):
-        shape = (M, max(top_k, 1))                           # an invalid top_k is the call's to report
-        i = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else ids
-        w = torch.empty(shape, dtype=torch.float32, device=dev) if weights is None else weights
-        _flat(i, "ids", shape, dev, torch.int32)
-        _flat(w, "weights", shape, dev, torch.float32)
-        ws = _space(workspace, lib().svdq_moe_route_bytes(M, E), dev)
-        check("svdq_moe_route", lib().svdq_moe_route(_ptr(X), M, ldx, K, _ptr(router), E, _ptr(bias), top_k, flags,
-                                                     scale, _ptr(i), _ptr(w), _ptr(ws), ws.numel(), s))
-        return i, w
-
-    return _on(dev, stream, call)
-
-
-def moe_route_bytes(M: int, E: int) -> int:
-    """Workspace bytes of moe_route (0: invalid)."""
-    return int(lib().svdq_moe_route_bytes(int(M), int(E)))
-
-
-def moe_bytes(gate_up: Layer, down: Layer, M: int, top_k: int) -> int:
-    """Workspace bytes of moe (0: invalid)."""
-    return int(lib().svdq_moe_bytes(_kept_desc(gate_up)[1], _kept_desc(down)[1], int(M), int(top_k)))
+    out = (M, max(top_k, 1))                              # an invalid top_k is the call's to report
+    if ids is None:
+        ids = torch.empty(out, dtype=torch.int32, device=dev)
+    else:
+        _flat(ids, "ids", out, dev, torch.int32)
+    if weights is None:
+        weights = torch.empty(out, dtype=torch.float32, device=dev)
+    else:
+        _flat(weights, "weights", out, dev, torch.float32)
+    L = lib()
+    ws = _space(workspace, L.svdq_moe_route_bytes(M, E), dev)
+    st = L.svdq_moe_route(X.data_ptr(), M, ldx, K, router.data_ptr(), E, None if bias is None else bias.data_ptr(),
+                          top_k, (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_RENORM if renorm else 0), scale,
+                          ids.data_ptr(), weights.data_ptr(), None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_moe_route", st)
+    return ids, weights
 
 
 def pack_experts(layer: Layer, R, bias=None, stream=None):
     """E experts' weights of one layer shape (rank 0, lambda 1): R (E x N x K fp32), bias (E x N
     bf16 or None) -> E x weight_bytes(layer) uint8, as moe takes them."""
-    torch = _torch()
+    torch, dev = _torch(), R.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        return _elsewhere(dev, stream, lambda: pack_experts(layer, R, bias))
     if layer.rank != 0 or R.dim() != 3 or tuple(R.shape[1:]) != (layer.N, layer.K):
         raise ValueError(f"expected rank 0 and weights E x {layer.N} x {layer.K}, got rank {layer.rank} and {tuple(R.shape)}")
-    dev, E = R.device, R.shape[0]
     _flat(R, "R", R.shape, dev, torch.float32)
     if bias is not None:
-        _flat(bias, "bias", (E, layer.N), dev, bias.dtype if bias.dtype in (torch.bfloat16, torch.int16) else torch.bfloat16)
+        _flat(bias, "bias", (R.shape[0], layer.N), dev, bias.dtype if bias.dtype == torch.int16 else torch.bfloat16)
+    out = torch.empty((R.shape[0], weight_bytes(layer)), dtype=torch.uint8, device=dev)
+    one = torch.ones(layer.K, dtype=torch.float32, device=dev)
+    for e in range(R.shape[0]):
+        pack_weight(layer, R[e], None, None, one, None if bias is None else bias[e], out=out[e])
+    return out
 
-    def call(s):
-        out = torch.empty((E, weight_bytes(layer)), dtype=torch.uint8, device=dev)
-        one = torch.ones(layer.K, dtype=torch.float32, device=dev)
-        for e in range(E):
-            pack_weight(layer, R[e], None, None, one, None if bias is None else bias[e], out=out[e], stream=stream)
-        return out
 
-    return _on(dev, stream, call)
+def moe_bytes(gate_up: Layer, down: Layer, M: int, top_k: int) -> int:
+    """Workspace bytes of moe (0: invalid)."""
+    return int(lib().svdq_moe_bytes(_kept_desc(gate_up)[0], _kept_desc(down)[0], int(M), int(top_k)))
 
 
 def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi: int = 0, out=None, workspace=None,
@@ -343,33 +352,37 @@ def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi:
     pack_experts: gate_up's outputs are [gate | up], twice down.K).  Y = sum_j weights[:, j]
     down(act(gate) * up), act SiLU or, with EPI_GELU, GELU; returns Y (M x down.N, bf16, or
     float32 with EPI_OUT_F32)."""
-    torch = _torch()
-    (_, pg, gb), (_, pd, db) = _kept_desc(gate_up), _kept_desc(down)
-    dev = X.device
+    torch, dev = _torch(), X.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        return _elsewhere(dev, stream, lambda: moe(gate_up, wg_packed, down, wd_packed, X, ids, weights, epi, out,
+                                                   workspace))
+    (pg, gb), (pd, db) = _kept_desc(gate_up), _kept_desc(down)
     ldx = _rows(X, "X", gate_up.K, dev, (torch.bfloat16, torch.int16))
     if wg_packed.dim() != 2:
         raise ValueError(f"wg_packed: expected experts x {gb} bytes, got {tuple(wg_packed.shape)}")
-    E, M = wg_packed.shape[0], X.shape[0]
-    _blob(wg_packed, "wg_packed", E * gb, dev)
-    _blob(wd_packed, "wd_packed", E * db, dev)
+    E, M, N = wg_packed.shape[0], X.shape[0], down.N
+    _bytes(wg_packed, "wg_packed", E * gb, dev)
+    _bytes(wd_packed, "wd_packed", E * db, dev)
     if ids.dim() != 2:
         raise ValueError(f"ids: expected tokens x choices, got {tuple(ids.shape)}")
     top_k = ids.shape[1]
     _flat(ids, "ids", (M, top_k), dev, torch.int32)
     _flat(weights, "weights", (M, top_k), dev, torch.float32)
     dt = torch.float32 if epi & EPI_OUT_F32 else torch.bfloat16
-
-    def call(s):
-        y = torch.empty((M, down.N), dtype=dt, device=dev) if out is None else out
-        ldy = down.N if out is None else _rows(y, "out", down.N, dev, (dt,))
-        if y.shape[0] != M:
-            raise ValueError(f"out: {y.shape[0]} rows for {M} tokens")
-        ws = _space(workspace, lib().svdq_moe_bytes(pg, pd, M, top_k), dev)
-        check("svdq_moe", lib().svdq_moe(pg, _ptr(wg_packed), pd, _ptr(wd_packed), E, _ptr(X), M, ldx, _ptr(ids),
-                                         _ptr(weights), top_k, _ptr(y), ldy, epi, _ptr(ws), ws.numel(), s))
-        return y
-
-    return _on(dev, stream, call)
+    if out is None:
+        out, ldy = torch.empty((M, N), dtype=dt, device=dev), N
+    else:
+        ldy = _rows(out, "out", N, dev, (dt,))
+        if out.shape[0] != M:
+            raise ValueError(f"out: {out.shape[0]} rows for {M} tokens")
+    L = lib()
+    ws = _space(workspace, L.svdq_moe_bytes(pg, pd, M, top_k), dev)
+    st = L.svdq_moe(pg, wg_packed.data_ptr(), pd, wd_packed.data_ptr(), E, X.data_ptr(), M, ldx, ids.data_ptr(),
+                    weights.data_ptr(), top_k, out.data_ptr(), ldy, epi, None if ws is None else ws.data_ptr(),
+                    0 if ws is None else ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_moe", st)
+    return out
 
 
 def _scales_out(torch, layer: Layer, rows: int, dev):
