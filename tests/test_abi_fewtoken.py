@@ -28,9 +28,11 @@ def D(fmt=1, K=1024, N=512, rank=16):
 
 
 def test_sizes(L):
-    one, many = L.svdq_w4a16_bytes(D(), 1), L.svdq_w4a16_bytes(D(), 100)
-    assert one >= 1024 * 6 + 2 * 32 * 4 and many >= 100 * one // 2 and one % 256 == 0
-    assert L.svdq_w4a16_bytes(D(), 0) > 0 and L.svdq_w4a16_bytes(D(K=1000), 1) == 0
+    assert L.svdq_w4a16_bytes(D(), 1) == 0                                  # one kernel, in LDS
+    assert L.svdq_w4a16_bytes(D(rank=256), 1) >= 2 * 256 * 4                # its down projection's sums
+    many = L.svdq_w4a16_bytes(D(), 100)
+    assert many >= 100 * (1024 * 6 + 2 * 32 * 4) and many % 256 == 0
+    assert L.svdq_w4a16_bytes(D(K=1000), 1) == 0
     assert L.svdq_w4a16_bytes(D(), -1) == 0 and L.svdq_w4a16_bytes(None, 1) == 0 and L.svdq_w4a16_bytes(D(fmt=9), 1) == 0
     assert L.svdq_moe_route_bytes(7, 64) >= 7 * 64 * 8 and L.svdq_moe_route_bytes(0, 1) > 0
     assert L.svdq_moe_route_bytes(-1, 64) == 0 and L.svdq_moe_route_bytes(1, 0) == 0 and L.svdq_moe_route_bytes(1, 513) == 0
@@ -43,8 +45,8 @@ def test_sizes(L):
 
 def test_linear_w4a16_validation(L, forced_device_error):
     f, d = L.svdq_linear_w4a16, D()
-    n = L.svdq_w4a16_bytes(d, 4)
-    ok = [d, P, P, 4, 1024, P, 512, 15, P, n, None]
+    n = L.svdq_w4a16_bytes(d, 40)
+    ok = [d, P, P, 40, 1024, P, 512, 15, P, n, None]
 
     def call(**kw):
         a = list(ok)
@@ -64,6 +66,9 @@ def test_linear_w4a16_validation(L, forced_device_error):
     assert call(_9=n - 1) == 5
     for fmt in (1, 2, 3):
         assert call(_0=D(fmt=fmt)) == 6
+    # a call that needs no workspace takes NULL
+    assert call(_3=1, _8=None, _9=0) == 6 and call(_3=1, _8=None, _9=0, _0=D(rank=256)) == 1
+    assert call(_3=1, _8=P, _9=0) == 6 and call(_3=1, _8=P + 8, _9=0) == 4
 
 
 def test_route_validation(L, forced_device_error):

@@ -25,7 +25,7 @@ FMTS = ["mxfp4", "int4", "nvfp4"]
 # N of one tile, ends inside and at a padded 256 rows, every kind of rank
 CASES = [(1, 512, 16, 0), (1, 1024, 1040, 16), (1, 4096, 256, 32), (2, 1536, 48, 8), (5, 2048, 272, 64),
          (6, 2560, 528, 40), (8, 512, 512, 128), (9, 1024, 144, 16), (16, 512, 64, 256), (17, 1536, 32, 24),
-         (33, 2048, 784, 48), (100, 1024, 112, 32), (300, 512, 16, 16)]
+         (33, 2048, 784, 48), (3, 512, 16400, 32), (8, 4096, 64, 64), (2, 20480, 32, 16), (100, 1024, 112, 32), (300, 512, 16, 16)]
 
 
 @pytest.fixture(scope="module")
@@ -170,9 +170,12 @@ def test_streams_graphs_and_repeats(torch_dev):
     layer = sq.Layer("mxfp4", K, N, rank)
     w, X = pack(layer, L, torch, dev), dev_tensor(L["X"], torch, dev)
     want = sq.linear_w4a16(layer, w, X, EPI)
-    ws = torch.empty(sq.w4a16_bytes(layer, M), dtype=torch.uint8, device=dev)
-    ws.fill_(0xFF)
-    assert torch.equal(sq.linear_w4a16(layer, w, X, EPI, workspace=ws), want)
+    for r in (128, 32):                                  # with a workspace (its contents never matter) and without
+        Lr = _draw("mxfp4", M, K, N, r, 61)
+        lr = sq.Layer("mxfp4", K, N, r)
+        wr = pack(lr, Lr, torch, dev)
+        ws = torch.full((sq.w4a16_bytes(lr, M) or 256,), 0xFF, dtype=torch.uint8, device=dev)
+        assert torch.equal(sq.linear_w4a16(lr, wr, X, EPI, workspace=ws), sq.linear_w4a16(lr, wr, X, EPI))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     y = sq.linear_w4a16(layer, w, X, EPI, stream=side)
@@ -206,8 +209,9 @@ def test_refusals(torch_dev):
                 torch.zeros((4, 64), dtype=X.dtype)):
         with pytest.raises(ValueError):
             sq.linear_w4a16(layer, w, X, out=out)
-    for kw, status in ((dict(workspace=w[:256]), 5), (dict(epi=64), 3),
-                       (dict(out=torch.zeros((4, 68), dtype=X.dtype, device=dev)[:, :64]), 4)):
+    many = torch.zeros((40, 1024), dtype=torch.bfloat16, device=dev)
+    for x, kw, status in ((many, dict(workspace=w[:256]), 5), (X, dict(epi=64), 3),
+                          (X, dict(out=torch.zeros((4, 68), dtype=X.dtype, device=dev)[:, :64]), 4)):
         with pytest.raises(sq.SvdqError) as e:
-            sq.linear_w4a16(layer, w, X, **kw)
+            sq.linear_w4a16(layer, w, x, **kw)
         assert e.value.status == status

@@ -119,18 +119,6 @@ svdq_status scratch_address(uint8_t** out) {
   return SVDQ_OK;
 }
 
-// Workspace of svdq_linear_w4a16: X_hat as up to three bf16 planes, then the down
-// projection's partial sums, one per 512 of K.
-struct W4A16Layout { size_t planes, part, total; };
-W4A16Layout w4a16_layout(const svdq_layer_desc* d, int64_t M) {
-  const size_t rows = size_t(M > 0 ? M : 1);
-  W4A16Layout l;
-  l.planes = 0;
-  l.part = align256(rows * d->K * 6);
-  l.total = align256(l.part + size_t(d->K / kKSuper) * rows * round_up(d->rank, kRankAlign) * 4);
-  return l;
-}
-
 bool valid_moe_shape(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
   return check_shape(dg) == SVDQ_OK && check_shape(dd) == SVDQ_OK && dg->N == 2 * dd->K && M >= 0 && M <= kMaxRows &&
          top_k >= 1 && top_k <= kMoeMaxTopK;
@@ -320,16 +308,18 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
 
 size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M) {
   if (!d || check_shape(d) != SVDQ_OK || check_fmt(d) != SVDQ_OK || M < 0 || M > kMaxRows) return 0;
-  return w4a16_layout(d, M).total;
+  return w4a16_layout(d->K, d->rank, M).total;
 }
 
 svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
                               int64_t ldx, void* Y, int64_t ldy, uint32_t epi, void* workspace, size_t ws_bytes,
                               void* stream) {
-  svdq_status s = check_act_args(d, w_packed, X, M, ldx, workspace);
+  // a call that needs no workspace takes NULL: w_packed stands in for it in the checks
+  const void* ws_or = workspace ? workspace : d && svdq_w4a16_bytes(d, M) == 0 ? w_packed : nullptr;
+  svdq_status s = check_act_args(d, w_packed, X, M, ldx, ws_or);
   if (s != SVDQ_OK) return s;
-  if ((s = check_gemm_args(d, w_packed, workspace, M, Y, ldy, epi)) != SVDQ_OK) return s;
-  const W4A16Layout l = w4a16_layout(d, M);
+  if ((s = check_gemm_args(d, w_packed, ws_or, M, Y, ldy, epi)) != SVDQ_OK) return s;
+  const W4A16Layout l = w4a16_layout(d->K, d->rank, M);
   if (ws_bytes < l.total) return SVDQ_ERR_WORKSPACE;
   if ((s = device_check()) != SVDQ_OK) return s;
   if (M == 0) return SVDQ_OK;

@@ -58,6 +58,46 @@ constexpr uint32_t kDivSlowBit = 2;    // weight flags: the two-operation divisi
 __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 __host__ __device__ inline size_t align256(size_t a) { return (a + 255) & ~size_t(255); }
 
+// svdq_linear_w4a16: which form a call takes.  Few tokens (`few`): one kernel that holds
+// x_hat's S planes of all tokens in LDS beside the down projection's sums, when the columns of
+// one 16-column MFMA hold them and they fit; it forms the down projection itself (`own_d`) for
+// small K x rank, since every workgroup then reads all of L1.
+constexpr int kFewWaves = 8;
+constexpr int kFewMaxRank = 64;
+constexpr int kFewMaxL1Bytes = 262144;
+constexpr int64_t kFewLds = 155648;    // of 160 KiB
+__host__ __device__ inline int few_row_bytes(int K) { return K * 2 + 16; }   // 16 skews the banks
+
+struct W4A16Plan {
+  bool few, own_d;
+  int64_t lds;
+};
+__host__ __device__ inline W4A16Plan w4a16_plan(int K, int64_t r_pad, int64_t M, int S) {
+  W4A16Plan p;
+  p.own_d = r_pad <= kFewMaxRank && K * r_pad * 2 <= kFewMaxL1Bytes;
+  // x_hat, the down projection, and one space for its waves' sums and then for the tiles' (two buffers)
+  const int64_t sums = p.own_d && r_pad > 32 ? kFewWaves * r_pad / 16 * 1024 : 2 * kFewWaves * 1024;
+  p.lds = S * M * few_row_bytes(K) + M * r_pad * 4 + sums;
+  p.few = M <= 16 / S && p.lds <= kFewLds;
+  return p;
+}
+
+// Its workspace: x_hat as up to three bf16 planes, and the down projection's partial sums, one
+// per 512 of K; nothing where the one kernel does all, whatever the output type.
+struct W4A16Layout {
+  size_t planes, part, total;
+};
+__host__ __device__ inline W4A16Layout w4a16_layout(int K, int rank, int64_t M) {
+  const int64_t rows = M > 0 ? M : 1, r_pad = round_up(rank, kRankAlign);
+  const W4A16Plan p2 = w4a16_plan(K, r_pad, rows, 2), p3 = w4a16_plan(K, r_pad, rows, 3);
+  const bool few = p2.few && p3.few;
+  W4A16Layout l;
+  l.planes = 0;
+  l.part = few ? 0 : align256(size_t(rows) * K * 6);
+  l.total = few && p2.own_d ? 0 : align256(l.part + size_t(K / kKSuper) * rows * r_pad * 4);
+  return l;
+}
+
 struct WeightLayout {
   int64_t N_pad, r_pad;
   size_t codes, scales, L1, L2, lam, rlam, rlo, bias, flags, amax, total;

@@ -215,8 +215,7 @@ __global__ void __launch_bounds__(512) moe_gate_up_kernel(MoeArgs a) {
   const uint8_t* blob = a.wg + size_t(ex) * a.blob_g;
   const int KS = a.H / kKStep, FT = a.F / 16;
   const int ft = blockIdx.x;
-  const W4Tile<FMT> gate(blob + a.g_codes, blob + a.g_scales, ft, a.H, a.Ng_pad, lane);
-  const W4Tile<FMT> up(blob + a.g_codes, blob + a.g_scales, FT + ft, a.H, a.Ng_pad, lane);
+  const W4Rows<FMT> rows(blob + a.g_codes, blob + a.g_scales, a.H, a.Ng_pad);
   const float gs = w4_tensor_scale<FMT>(blob + a.g_amax);
   const int n = KS > w ? (KS - w + kGateWaves - 1) / kGateWaves : 0;
   struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
@@ -229,8 +228,8 @@ __global__ void __launch_bounds__(512) moe_gate_up_kernel(MoeArgs a) {
     }
     auto load = [&](int i, Stage& st) {
       const int ks = w + (i < n ? i : n - 1) * kGateWaves;
-      gate.load(ks, st.g);
-      up.load(ks, st.u);
+      rows.load(ft, ks, i < n, lane, st.g);
+      rows.load(FT + ft, ks, i < n, lane, st.u);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -363,14 +362,14 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     const int f0 = first[ex] + t0, cnt = first[ex + 1] - f0 < TPB ? first[ex + 1] - f0 : TPB;
     const int ks0 = kc * KS / KC, n = (kc + 1) * KS / KC - ks0;
     const uint8_t* blob = a.wd + size_t(ex) * a.blob_d;
-    const W4Tile<FMT> tile(blob + a.d_codes, blob + a.d_scales, rt, a.F, a.Nd_pad, lane);
+    const W4Rows<FMT> rows(blob + a.d_codes, blob + a.d_scales, a.F, a.Nd_pad);
     const int t = tl % TPB < cnt ? tl % TPB : cnt - 1, pl = tl / TPB < S ? tl / TPB : S - 1;
     const int pair = list[f0 + t];
     const uint16_t* xp = a.h + (int64_t(pl) * a.P + pair) * a.F;
     struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };
     auto load = [&](int i, Stage& st) {
       const int ks = ks0 + (i < n ? i : n - 1);
-      tile.load(ks, st.w);
+      rows.load(uint32_t(rt), ks, i < n, lane, st.w);
 #pragma unroll
       for (int q = 0; q < 4; ++q) st.x[0][q] = *reinterpret_cast<const uint4*>(xp + ks * kKStep + k_of<FMT>(c, q));
     };

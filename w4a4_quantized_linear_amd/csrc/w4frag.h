@@ -40,28 +40,43 @@ struct W4Stage {
   typename std::conditional<FMT == kFmtINT4, uint4, uint32_t>::type s;
 };
 
-// The lane's view of one 16-row tile (rows 16 rt ..) of a packed weight.
+__device__ __forceinline__ uint4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  const v4i v = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+  return make_uint4(uint32_t(v[0]), uint32_t(v[1]), uint32_t(v[2]), uint32_t(v[3]));
+}
+
+// A packed weight's codes and scales as buffers.  A step that is not there (valid false) loads
+// zeros through a buffer of no bytes: the load is issued all the same, so that the wait counts
+// of a software pipeline stay exact, and reads no memory.
 template <int FMT>
-struct W4Tile {
-  const uint8_t* q;
-  const uint8_t* s;
-  size_t s_step;                       // INT4: bytes from one step's scales to the next
-  __device__ __forceinline__ W4Tile(const uint8_t* codes, const uint8_t* scales, int64_t rt, int K, int64_t N_pad,
-                                    int lane) {
-    const int KS = K / kKStep;
-    q = codes + size_t(rt) * KS * 1024 + lane * 16;
-    if (FMT == kFmtMXFP4) s = scales + size_t(rt) * (K / kKSuper) * 256 + lane * 4;
-    if (FMT == kFmtNVFP4) s = scales + size_t(rt) * KS * 128 + lane * 2;
-    if (FMT == kFmtINT4) s = scales + size_t(rt) * 64 + (lane >> 4) * 16;   // rows 4 c .. 4 c + 3 of the tile
-    s_step = size_t(N_pad) * 4;
-  }
-  __device__ __forceinline__ void load(int ks, W4Stage<FMT>& st) const {
-    st.q = *reinterpret_cast<const uint4*>(q + size_t(ks) * 1024);
-    if constexpr (FMT == kFmtMXFP4) st.s = *reinterpret_cast<const uint32_t*>(s + size_t(ks >> 2) * 256);
-    if constexpr (FMT == kFmtNVFP4) st.s = *reinterpret_cast<const uint16_t*>(s + size_t(ks) * 128);
-    if constexpr (FMT == kFmtINT4) st.s = *reinterpret_cast<const uint4*>(s + ks * s_step);
+struct W4Rows {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  uint32_t code_bytes, scale_bytes, KS, s_step;
+  __device__ __forceinline__ W4Rows(const uint8_t* c, const uint8_t* s, int K, int64_t N_pad)
+      : codes(c), scales(s), code_bytes(uint32_t(N_pad * K / 2)),
+        scale_bytes(uint32_t(N_pad * K / (FMT == kFmtNVFP4 ? 16 : 32))), KS(uint32_t(K / kKStep)),
+        s_step(uint32_t(N_pad) * 4) {}
+  __device__ __forceinline__ void load(uint32_t rt, uint32_t ks, bool valid, int lane, W4Stage<FMT>& st) const {
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(codes, valid ? code_bytes : 0);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales, valid ? scale_bytes : 0);
+    st.q = buffer_load16(rc, uint32_t(lane) * 16, (rt * KS + ks) * 1024);
+    if constexpr (FMT == kFmtMXFP4)
+      st.s = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rs, uint32_t(lane) * 4, (rt * (KS / 4) + ks / 4) * 256, 0));
+    if constexpr (FMT == kFmtNVFP4)
+      st.s = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, uint32_t(lane) * 2, (rt * KS + ks) * 128, 0));
+    if constexpr (FMT == kFmtINT4) st.s = buffer_load16(rs, uint32_t(lane >> 4) * 16, ks * s_step + rt * 64);  // rows 4 c ..
   }
 };
+
+// Workgroup barrier for data in LDS: waits for this wave's LDS operations and not, as a fence
+// would, for its global loads in flight; the empty asm keeps memory accesses from moving across.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0); vmcnt and expcnt at their maxima
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ float f16_value(uint32_t bits) {
   return float(__builtin_bit_cast(_Float16, uint16_t(bits)));
