@@ -25,7 +25,8 @@ FMTS = ["mxfp4", "int4", "nvfp4"]
 # N of one tile, ends inside and at a padded 256 rows, every kind of rank
 CASES = [(1, 512, 16, 0), (1, 1024, 1040, 16), (1, 4096, 256, 32), (2, 1536, 48, 8), (5, 2048, 272, 64),
          (6, 2560, 528, 40), (8, 512, 512, 128), (9, 1024, 144, 16), (16, 512, 64, 256), (17, 1536, 32, 24),
-         (33, 2048, 784, 48), (3, 512, 16400, 32), (8, 4096, 64, 64), (2, 20480, 32, 16), (100, 1024, 112, 32), (300, 512, 16, 16)]
+         (33, 2048, 784, 48), (3, 512, 16400, 32), (8, 4096, 64, 64), (2, 20480, 32, 16), (100, 1024, 112, 32), (300, 512, 16, 16),
+         (40, 8192, 64, 32), (12, 6144, 16, 16), (25, 4096, 272, 64), (48, 3584, 80, 0)]
 
 
 @pytest.fixture(scope="module")

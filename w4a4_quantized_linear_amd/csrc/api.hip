@@ -32,7 +32,7 @@ hipError_t launch_gemm_w4a16(const uint8_t* wblob, const WeightLayout& wl, int K
                              int64_t ldx, int64_t M, void* Y, int64_t ldy, uint32_t epi, hipStream_t s);
 hipError_t launch_linear_w4a16(int fmt, const uint8_t* wblob, const WeightLayout& wl, int K, int N, const uint16_t* X,
                                int64_t ldx, int64_t M, void* Y, int64_t ldy, uint32_t epi, void* planes, float* part,
-                               hipStream_t s);
+                               float* zsum, hipStream_t s);
 hipError_t launch_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int K, const uint16_t* Wr, const float* bias,
                             int E, int top_k, uint32_t flags, float scale, int32_t* ids, float* weights, double* logits,
                             hipStream_t s);
@@ -308,7 +308,7 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
 
 size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M) {
   if (!d || check_shape(d) != SVDQ_OK || check_fmt(d) != SVDQ_OK || M < 0 || M > kMaxRows) return 0;
-  return w4a16_layout(d->K, d->rank, M).total;
+  return w4a16_layout(d->fmt, d->K, d->N, d->rank, M).total;
 }
 
 svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
@@ -319,7 +319,7 @@ svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, co
   svdq_status s = check_act_args(d, w_packed, X, M, ldx, ws_or);
   if (s != SVDQ_OK) return s;
   if ((s = check_gemm_args(d, w_packed, ws_or, M, Y, ldy, epi)) != SVDQ_OK) return s;
-  const W4A16Layout l = w4a16_layout(d->K, d->rank, M);
+  const W4A16Layout l = w4a16_layout(d->fmt, d->K, d->N, d->rank, M);
   if (ws_bytes < l.total) return SVDQ_ERR_WORKSPACE;
   if ((s = device_check()) != SVDQ_OK) return s;
   if (M == 0) return SVDQ_OK;
@@ -327,7 +327,7 @@ svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, co
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   return launched(launch_linear_w4a16(d->fmt, static_cast<const uint8_t*>(w_packed), wl, d->K, d->N, X, ldx, M, Y, ldy,
                                       epi, ws + l.planes, reinterpret_cast<float*>(ws + l.part),
-                                      static_cast<hipStream_t>(stream)));
+                                      reinterpret_cast<float*>(ws + l.zsum), static_cast<hipStream_t>(stream)));
 }
 
 size_t svdq_moe_route_bytes(int64_t M, int32_t E) {

@@ -82,19 +82,59 @@ __host__ __device__ inline W4A16Plan w4a16_plan(int K, int64_t r_pad, int64_t M,
   return p;
 }
 
-// Its workspace: x_hat as up to three bf16 planes, and the down projection's partial sums, one
-// per 512 of K; nothing where the one kernel does all, whatever the output type.
-struct W4A16Layout {
-  size_t planes, part, total;
+// More tokens: x_hat's planes go to memory in the order of the MFMA's B operands, groups of `Mg`
+// tokens in NB blocks of 16 columns (column p Mg + t: plane p of token t), and each workgroup takes
+// T row tiles, reading a group's columns once for them.  When that leaves CUs without a workgroup,
+// T is halved if the columns read altogether stay within kWideTraffic; otherwise K is split over Z
+// workgroups, whose sums a last kernel adds, while a wave keeps two 128-K steps.
+constexpr int kWideWaves = 8;
+constexpr int kWideBlocks = 6;         // at most
+constexpr int kWideGroups = 256;       // one workgroup a CU
+constexpr int64_t kWideTraffic = 100000000;
+
+struct W4A16Wide {
+  int64_t groups, Mg;
+  int NB, T, Z;
 };
-__host__ __device__ inline W4A16Layout w4a16_layout(int K, int rank, int64_t M) {
+__host__ __device__ inline W4A16Wide w4a16_wide(int fmt, int K, int N, int64_t M, int S) {
+  W4A16Wide p;
+  const int64_t most = kWideBlocks * 16 / S, tiles = N / 16;
+  p.groups = (M + most - 1) / most;
+  p.Mg = (M + p.groups - 1) / p.groups;
+  const int nb = int((S * p.Mg + 15) / 16);
+  p.NB = nb <= 2 ? 2 : nb;
+  p.T = fmt == kFmtINT4 && p.NB > 3 ? 2 : 4;       // registers: INT4 holds a group's sums beside the accumulators
+  const int64_t slab = int64_t(p.NB) * K * 32;     // a group's columns
+  while (p.T > 1 && (tiles + p.T - 1) / p.T * p.groups < kWideGroups &&
+         (tiles + p.T / 2 - 1) / (p.T / 2) * p.groups * slab <= kWideTraffic)
+    p.T /= 2;
+  const int64_t wgs = (tiles + p.T - 1) / p.T * p.groups;
+  const int zmax = K / kKStep / (2 * kWideWaves);
+  const int64_t z = wgs * 2 <= kWideGroups ? kWideGroups / wgs : 1;
+  p.Z = int(z < 1 || zmax < 1 ? 1 : z < zmax ? z : zmax);
+  return p;
+}
+
+// Its workspace: x_hat's planes, the down projection's partial sums (one per 512 of K) and the
+// sums of the Z parts; nothing where the one kernel does all, whatever the output type.
+struct W4A16Layout {
+  size_t planes, part, zsum, total;
+};
+__host__ __device__ inline W4A16Layout w4a16_layout(int fmt, int K, int N, int rank, int64_t M) {
   const int64_t rows = M > 0 ? M : 1, r_pad = round_up(rank, kRankAlign);
-  const W4A16Plan p2 = w4a16_plan(K, r_pad, rows, 2), p3 = w4a16_plan(K, r_pad, rows, 3);
-  const bool few = p2.few && p3.few;
-  W4A16Layout l;
-  l.planes = 0;
-  l.part = few ? 0 : align256(size_t(rows) * K * 6);
-  l.total = few && p2.own_d ? 0 : align256(l.part + size_t(K / kKSuper) * rows * r_pad * 4);
+  W4A16Layout l{0, 0, 0, 0};
+  size_t part = 0;
+  for (int S = 2; S <= 3; ++S) {
+    const W4A16Plan few = w4a16_plan(K, r_pad, rows, S);
+    const W4A16Wide w = w4a16_wide(fmt, K, N, rows, S);
+    const size_t planes = few.few ? 0 : align256(size_t(w.groups) * w.NB * K * 32);
+    const size_t zsum = few.few || w.Z == 1 ? 0 : align256(size_t(w.Z) * rows * N * 4);
+    if (!few.few || !few.own_d) part = align256(size_t(K / kKSuper) * rows * r_pad * 4);
+    if (planes > l.part) l.part = planes;
+    if (zsum > l.total) l.total = zsum;
+  }
+  l.zsum = l.part + part;
+  l.total += l.zsum;
   return l;
 }
 

@@ -17,12 +17,15 @@ struct W4A16LinearArgs {
   const uint8_t* wblob;
   size_t w_codes, w_scales, w_L1, w_L2, w_lam, w_bias, w_amax;
   const uint16_t* X;
-  uint16_t* planes;        // S x M x K bf16
+  uint4* planes;           // groups x K / 128 x 4 x NB x 64 B operands (null: not wanted)
   float* part;             // K / 512 x M x r_pad
+  float* zsum;             // Z x M x N
   void* Y;
   int64_t ldx, ldy, M, N_pad;
   int K, r_pad;            // r_pad 0: no low-rank branch
   uint32_t epi;
+  int N, NB, Z, int4;
+  int64_t Mg, groups;
 };
 
 constexpr int kPrepWaves = 8;          // 64 K each
@@ -40,7 +43,13 @@ __global__ void __launch_bounds__(512) w4a16_prepare_kernel(W4A16LinearArgs a) {
   const uint4* L1f = reinterpret_cast<const uint4*>(a.wblob + a.w_L1);
   for (int64_t m0 = int64_t(blockIdx.y) * 16; m0 < a.M; m0 += int64_t(gridDim.y) * 16) {
     const int64_t m = m0 + tl < a.M ? m0 + tl : a.M - 1;
-    uint4 p[2][S];
+    uint4 p[2][S], l1f[2][2];                              // the first two rank tiles' L1 fragments, ahead
+    if (RT) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l1f[s][i] = L1f[(size_t(k0 / 32 + s) * RT + i) * 64 + lane];
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int k = k0 + s * 32 + c * 8;
@@ -52,17 +61,26 @@ __global__ void __launch_bounds__(512) w4a16_prepare_kernel(W4A16LinearArgs a) {
       for (int e = 0; e < 8; ++e) v[e] = v[e] / l[e];       // IEEE: x_hat is this quotient by definition
       split_planes<S>(v, p[s]);
       if (a.planes && m0 + tl < a.M) {
+        // lane group and MFMA that these 8 K elements belong to (k_of)
+        const int kk = k & 127, kc = a.int4 ? (kk & 63) >> 4 : kk >> 5;
+        const int u = a.int4 ? ((kk >> 6) << 1) + ((kk >> 3) & 1) : (kk >> 3) & 3;
+        uint4* const at = a.planes + (((m / a.Mg) * (a.K / kKStep) + k / kKStep) * 4 + u) * a.NB * 64 + kc * 16;
 #pragma unroll
-        for (int i = 0; i < S; ++i) *reinterpret_cast<uint4*>(a.planes + (i * a.M + m) * a.K + k) = p[s][i];
+        for (int i = 0; i < S; ++i) {
+          const int col = int(i * a.Mg + m % a.Mg);
+          at[(col >> 4) * 64 + (col & 15)] = p[s][i];
+        }
       }
     }
     for (int i0 = 0; i0 < RT; i0 += kPrepTiles) {
       const int tiles = RT - i0 < kPrepTiles ? RT - i0 : kPrepTiles;
-      for (int i = 0; i < tiles; ++i) {
+#pragma unroll
+      for (int i = 0; i < kPrepTiles; ++i) {
+        if (i >= tiles) break;
         v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint4 l1 = L1f[(size_t(k0 / 32 + s) * RT + i0 + i) * 64 + lane];
+          const uint4 l1 = i < 2 && i0 == 0 ? l1f[s][i & 1] : L1f[(size_t(k0 / 32 + s) * RT + i0 + i) * 64 + lane];
 #pragma unroll
           for (int q = 0; q < S; ++q) acc = mfma_bf16(p[s][q], l1, acc);
         }
@@ -83,6 +101,23 @@ __global__ void __launch_bounds__(512) w4a16_prepare_kernel(W4A16LinearArgs a) {
       __syncthreads();
     }
   }
+}
+
+// Y[m, row .. row + 3] = act(y + b)
+__device__ __forceinline__ void w4a16_store(const W4A16LinearArgs& a, int64_t m, int64_t row, v4f y, bool f32) {
+  if (a.epi & SVDQ_EPI_BIAS) {
+    const uint2 b = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.wblob + a.w_bias) + row);
+    y += v4f{bf_lo(b.x), bf_hi(b.x), bf_lo(b.y), bf_hi(b.y)};
+  }
+  if (a.epi & SVDQ_EPI_GELU) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = gelu_erf(y[e]);
+  }
+  if (f32)
+    *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + m * a.ldy + row) = y;
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + m * a.ldy + row) =
+        make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
 }
 
 // Few tokens, one launch: all S planes of the M tokens are columns of one MFMA.
@@ -312,126 +347,175 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
   }
 }
 
-constexpr int kLinWaves = 8;
-
-// One workgroup: one 16-row tile, its waves taking every eighth 128-K step.
-// PACKED: all planes of the (at most 16 / S) tokens are columns of one MFMA.
-// Otherwise blocks of 16 tokens, one MFMA per plane.
-template <int FMT, int S, bool PACKED, bool OUT_F32>
-__global__ void __launch_bounds__(512) w4a16_kernel(W4A16LinearArgs a) {
-  constexpr int NB = PACKED ? 1 : S;               // B operands per step and MFMA
-  constexpr int TPB = PACKED ? tokens_per_block(S) : 16;
-  constexpr int DEPTH = PACKED ? 3 : 2;            // steps in flight
-  __shared__ v4f red[kLinWaves][64];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// More tokens.  A workgroup takes T row tiles, one group of tokens and one of Z parts of K; its
+// eight waves take every eighth 128-K step of the part with all NB column blocks, so a step's codes
+// are converted once and its columns are read once for T tiles, straight from L2 in whole 1 KiB
+// operands (two halves of a step in flight; no wave shares another's).  The waves' sums meet in LDS.
+template <int FMT, int NB, int T>
+__global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int S) {
+  constexpr int W = kWideWaves;
+  extern __shared__ uint4 lds[];
+  v4f* const slot = reinterpret_cast<v4f*>(lds);           // W / 2 x T x NB x 64
+  float* const dsum = reinterpret_cast<float*>(slot + W / 2 * T * NB * 64);      // Mg x r_pad
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
-  const int KS = a.K / kKStep;
-  const int64_t rt = blockIdx.x;
+  const int KS = a.K / kKStep, tiles = a.N / 16, rt0 = blockIdx.x * T, Mg = int(a.Mg);
+  const int ks0 = int(blockIdx.z) * KS / a.Z, ks1 = int(blockIdx.z + 1) * KS / a.Z;
+  const int n = ks1 - ks0 > w ? (ks1 - ks0 - w + W - 1) / W : 0;
   const W4Rows<FMT> rows(a.wblob + a.w_codes, a.wblob + a.w_scales, a.K, a.N_pad);
-  const int n = KS > w ? (KS - w + kLinWaves - 1) / kLinWaves : 0;
   const float gs = w4_tensor_scale<FMT>(a.wblob + a.w_amax);
-  for (int64_t m0 = int64_t(blockIdx.y) * TPB; m0 < a.M; m0 += int64_t(gridDim.y) * TPB) {
-    const int64_t left = a.M - m0;
-    // this lane's column(s): past the last they repeat it (columns are independent)
-    const int t_raw = PACKED ? tl % TPB : tl;
-    const int64_t t = m0 + (t_raw < left ? t_raw : left - 1);
-    const int pl = PACKED ? (tl / TPB < S ? tl / TPB : S - 1) : 0;
-    const uint16_t* xp = a.planes + (pl * a.M + t) * a.K;
-    struct Stage { W4Stage<FMT> w; uint4 x[NB][4]; };
-    auto load = [&](int i, Stage& st) {
-      const int ks = w + (i < n ? i : n - 1) * kLinWaves;
-      rows.load(uint32_t(rt), ks, i < n, lane, st.w);
+  const uint32_t slab = uint32_t(KS) * 4 * NB * 1024;      // a group's columns
+  const int rp = blockIdx.z == 0 ? a.r_pad : 0;
+  for (int64_t g = blockIdx.y; g < a.groups; g += gridDim.y) {
+    const uint8_t* const xg = reinterpret_cast<const uint8_t*>(a.planes) + g * slab;
+    auto load_w = [&](int i, W4Stage<FMT> (&st)[T]) {
+      // a tile past the last is one of the packed weight's padding rows
+      rows.template load<T>(uint32_t(rt0), uint32_t(ks0 + w + i * W), i < n, lane, st);
+    };
+    auto load_x = [&](int i, int u, uint4 (&x)[NB]) {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(xg, i < n ? slab : 0);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st.x[b][u] = *reinterpret_cast<const uint4*>(xp + b * a.M * a.K + ks * kKStep + k_of<FMT>(c, u));
+        x[b] = buffer_load16(r, uint32_t(lane) * 16 + b * 1024, ((ks0 + w + i * W) * 4 + u) * NB * 1024);
     };
-    v4f acc[NB];
+    v4f acc[T][NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[b] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (n > 0) {
-      Stage st[DEPTH];
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int j = 0; j < DEPTH; ++j) load(j, st[j]);
-      for (int i0 = 0; i0 < n; i0 += DEPTH) {
+      for (int b = 0; b < NB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
+    // XD operand sets in flight; past the last step codes and columns are zeros
+    constexpr int XD = FMT == kFmtINT4 || NB <= 3 ? 4 : 2;
+    W4Stage<FMT> st[2][T];
+    uint4 x[XD / 2][2][NB];
+    load_w(0, st[0]);
 #pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {
-          if (i0 + j < n) w4_step<FMT, NB>(st[j].w, w + (i0 + j) * kLinWaves, st[j].x, acc);
-          load(i0 + j + DEPTH, st[j]);
+    for (int q = 0; q < XD; ++q) load_x(0, q, x[q / 2][q % 2]);
+    load_w(1, st[1]);
+    // the down projection of the group's tokens (the first part of K adds the low-rank branch);
+    // the rows of a group lie one after the other in each partial sum
+    const int64_t left = a.M - g * Mg < Mg ? a.M - g * Mg : Mg;
+    for (int i = tid * 4; i < int(left) * rp; i += 512 * 4) {
+      const float* const pp = a.part + g * Mg * rp + i;
+      v4f v = {0.f, 0.f, 0.f, 0.f};
+      for (int q0 = 0; q0 < a.K / kKSuper; q0 += 8) {
+        v4f d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int q = q0 + j < a.K / kKSuper ? q0 + j : q0;
+          d[j] = *reinterpret_cast<const v4f*>(pp + q * a.M * rp);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (q0 + j < a.K / kKSuper) v += d[j];
+      }
+      *reinterpret_cast<v4f*>(dsum + i) = v;
+    }
+    for (int i0 = 0; i0 < n; i0 += 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (FMT == kFmtINT4) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            w4_half<T, NB>(st[j], half, x[half], acc);
+            load_x(i0 + j + 1, half * 2, x[half][0]);
+            load_x(i0 + j + 1, half * 2 + 1, x[half][1]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint4 (&xs)[NB] = x[u % XD / 2][u % 2];
+            w4_mfma<FMT, T, NB>(st[j], ks0 + w + (i0 + j) * W, u, xs, acc);
+            load_x(i0 + j + (u + XD) / 4, (u + XD) % 4, xs);
+          }
+        }
+        load_w(i0 + j + 2, st[j]);
       }
     }
-    v4f sum = acc[0];
+    if (FMT == kFmtNVFP4) {
 #pragma unroll
-    for (int b = 1; b < NB; ++b) sum += acc[b];
-    if (FMT == kFmtNVFP4) sum *= gs;
-    // up projection: wave w takes ranks 32 w .. 32 w + 31
-    if (w * 32 < a.r_pad) {
-      const uint4 l2 = reinterpret_cast<const uint4*>(a.wblob + a.w_L2)[(size_t(rt) * (a.r_pad / 32) + w) * 64 + lane];
-      float d[8] = {};
-      const float* dp = a.part + t * a.r_pad + w * 32 + c * 8;
-      for (int s = 0; s < a.K / kKSuper; ++s) {
-        const float4 d0 = *reinterpret_cast<const float4*>(dp + int64_t(s) * a.M * a.r_pad);
-        const float4 d1 = *reinterpret_cast<const float4*>(dp + int64_t(s) * a.M * a.r_pad + 4);
-        d[0] += d0.x; d[1] += d0.y; d[2] += d0.z; d[3] += d0.w;
-        d[4] += d1.x; d[5] += d1.y; d[6] += d1.z; d[7] += d1.w;
-      }
-      uint4 p[S];
-      split_planes<S>(d, p);
-      if constexpr (PACKED) {
-        uint4 x = p[0];
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int i = 1; i < S; ++i) x = pl == i ? p[i] : x;
-        sum = mfma_bf16(l2, x, sum);
-      } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i) sum = mfma_bf16(l2, p[i], sum);
-      }
+        for (int b = 0; b < NB; ++b) acc[t][b] *= gs;
     }
-    red[w][lane] = sum;
-    __syncthreads();
-    if (w == 0 && tl < (left < TPB ? left : TPB)) {
+    // the waves' sums: 4 .. 7 onto 0 .. 3, then all eight waves add four
+    auto at = [&](int q, int t, int b) -> v4f& { return slot[((q * T + t) * NB + b) * 64 + lane]; };
+    if (w >= W / 2) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) at(w - W / 2, t, b) = acc[t][b];
+    }
+    lds_barrier();
+    if (w < W / 2) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) at(w, t, b) += acc[t][b];
+    }
+    lds_barrier();
+    const int TB = (Mg + 15) / 16;
+    for (int u = w; u < T * TB; u += W) {
+      const int t = u / TB, tok = (u % TB) * 16 + tl;
+      const int64_t m = g * Mg + tok;
+      if (rt0 + t >= tiles) continue;
       v4f y = {0.f, 0.f, 0.f, 0.f};
+      for (int r32 = 0; r32 < rp / 32; ++r32) {
+        const uint4 l2 = reinterpret_cast<const uint4*>(a.wblob + a.w_L2)[(size_t(rt0 + t) * (rp / 32) + r32) * 64 + lane];
+        const float4* dq = reinterpret_cast<const float4*>(dsum + (tok < Mg ? tok : Mg - 1) * rp + r32 * 32 + c * 8);
+        const float4 d0 = dq[0], d1 = dq[1];
+        float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        uint4 pl[3];
+        split_planes<3>(dv, pl);
 #pragma unroll
-      for (int v = 0; v < kLinWaves; ++v)
-#pragma unroll
-        for (int i = 0; i < (PACKED ? S : 1); ++i) y += red[v][lane + i * TPB];
-      const int64_t row = rt * 16 + c * 4;
-      if (a.epi & SVDQ_EPI_BIAS) {
-        const uint2 b = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.wblob + a.w_bias) + row);
-        y += v4f{bf_lo(b.x), bf_hi(b.x), bf_lo(b.y), bf_hi(b.y)};
+        for (int i = 0; i < 3; ++i) y = mfma_bf16(l2, pl[i], y);
       }
-      if (a.epi & SVDQ_EPI_GELU) {
+      if (tok >= Mg || m >= a.M) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = gelu_erf(y[e]);
+      for (int q = 0; q < W / 2; ++q)
+        for (int p = 0; p < S; ++p) {
+          const int col = p * Mg + tok;
+          y += slot[((q * T + t) * NB + (col >> 4)) * 64 + c * 16 + (col & 15)];
+        }
+      const int64_t row = int64_t(rt0 + t) * 16 + c * 4;
+      if (a.Z > 1) {
+        *reinterpret_cast<v4f*>(a.zsum + (int64_t(blockIdx.z) * a.M + m) * a.N + row) = y;
+        continue;
       }
-      const int64_t o = (m0 + tl) * a.ldy + row;
-      if (OUT_F32)
-        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + o) = y;
-      else
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + o) =
-            make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
+      w4a16_store(a, m, row, y, S == 3);
     }
-    __syncthreads();
+    lds_barrier();
+  }
+}
+
+// The Z parts' sums in order.
+__global__ void __launch_bounds__(256) w4a16_join_kernel(W4A16LinearArgs a, int S) {
+  const int64_t per = a.N / 4, total = a.M * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int64_t m = i / per, row = i % per * 4;
+    v4f y = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < a.Z; ++z) y += *reinterpret_cast<const v4f*>(a.zsum + (z * a.M + m) * a.N + row);
+    w4a16_store(a, m, row, y, S == 3);
   }
 }
 
 // Requires K % 512 == 0, N % 16 == 0, X and Y rows 16-byte aligned, M >= 1.
 hipError_t launch_linear_w4a16(int fmt, const uint8_t* wblob, const WeightLayout& wl, int K, int N, const uint16_t* X,
                                int64_t ldx, int64_t M, void* Y, int64_t ldy, uint32_t epi, void* planes, float* part,
-                               hipStream_t s) {
+                               float* zsum, hipStream_t s) {
   W4A16LinearArgs a{};
   a.wblob = wblob;
   a.w_codes = wl.codes; a.w_scales = wl.scales; a.w_L1 = wl.L1; a.w_L2 = wl.L2; a.w_lam = wl.lam;
   a.w_bias = wl.bias; a.w_amax = wl.amax;
-  a.X = X; a.planes = static_cast<uint16_t*>(planes); a.part = part; a.Y = Y;
+  a.X = X; a.planes = static_cast<uint4*>(planes); a.part = part; a.zsum = zsum; a.Y = Y;
   a.ldx = ldx; a.ldy = ldy; a.M = M; a.N_pad = wl.N_pad;
   a.K = K; a.r_pad = (epi & SVDQ_EPI_LOWRANK) ? int(wl.r_pad) : 0; a.epi = epi;
   const bool f32 = (epi & SVDQ_EPI_OUT_F32) != 0;
   const int S = f32 ? 3 : 2;                       // planes: see w4frag.h
   const auto blocks = [](int64_t v) { return unsigned(v < 65535 ? v : 65535); };
   const W4A16Plan plan = w4a16_plan(K, a.r_pad, M, S);
+  const W4A16Wide wide = w4a16_wide(fmt, K, N, M, S);
+  a.N = N; a.NB = wide.NB; a.Z = wide.Z; a.Mg = wide.Mg; a.groups = wide.groups; a.int4 = fmt == kFmtINT4;
   if (!plan.few || !plan.own_d) {
     if (plan.few) a.planes = nullptr;
     const dim3 pgrid(unsigned(K / kKSuper), blocks((M + 15) / 16));
@@ -467,25 +551,36 @@ hipError_t launch_linear_w4a16(int fmt, const uint8_t* wblob, const WeightLayout
 #undef SVDQ_FEW_S
     return hipGetLastError();
   }
-  const bool packed = M <= tokens_per_block(S);
-  const dim3 grid(unsigned(N / 16), packed ? 1 : blocks((M + 15) / 16));
-#define SVDQ_LIN(FMT_, P_)                                                                            \
-  do {                                                                                                \
-    if (f32)                                                                                          \
-      hipLaunchKernelGGL((w4a16_kernel<FMT_, 3, P_, true>), grid, dim3(512), 0, s, a);                \
-    else                                                                                              \
-      hipLaunchKernelGGL((w4a16_kernel<FMT_, 2, P_, false>), grid, dim3(512), 0, s, a);               \
+  const dim3 grid(unsigned((N / 16 + wide.T - 1) / wide.T), blocks(wide.groups), unsigned(wide.Z));
+  const size_t lds = size_t(kWideWaves / 2) * wide.T * wide.NB * 1024 + size_t(wide.Mg) * a.r_pad * 4;
+#define SVDQ_WIDE(FMT_, NB_, T_) \
+  hipLaunchKernelGGL((w4a16_wide_kernel<FMT_, NB_, T_>), grid, dim3(512), lds, s, a, S)
+#define SVDQ_WIDE_T(FMT_, NB_)                                                   \
+  do {                                                                           \
+    constexpr int kT = FMT_ == kFmtINT4 && NB_ > 3 ? 2 : 4;                      \
+    if (wide.T == 1) SVDQ_WIDE(FMT_, NB_, 1);                                    \
+    else if (wide.T == 2) SVDQ_WIDE(FMT_, NB_, 2);                               \
+    else SVDQ_WIDE(FMT_, NB_, kT);                                               \
   } while (0)
-#define SVDQ_LIN_FMT(FMT_)                                                                            \
-  do {                                                                                                \
-    if (packed) SVDQ_LIN(FMT_, true);                                                                 \
-    else SVDQ_LIN(FMT_, false);                                                                       \
+#define SVDQ_WIDE_FMT(FMT_)                                       \
+  do {                                                            \
+    if (wide.NB == 2) SVDQ_WIDE_T(FMT_, 2);                       \
+    else if (wide.NB == 3) SVDQ_WIDE_T(FMT_, 3);                  \
+    else if (wide.NB == 4) SVDQ_WIDE_T(FMT_, 4);                  \
+    else if (wide.NB == 5) SVDQ_WIDE_T(FMT_, 5);                  \
+    else SVDQ_WIDE_T(FMT_, 6);                                    \
   } while (0)
-  if (fmt == kFmtMXFP4) SVDQ_LIN_FMT(kFmtMXFP4);
-  else if (fmt == kFmtINT4) SVDQ_LIN_FMT(kFmtINT4);
-  else SVDQ_LIN_FMT(kFmtNVFP4);
-#undef SVDQ_LIN_FMT
-#undef SVDQ_LIN
+  if (fmt == kFmtMXFP4) SVDQ_WIDE_FMT(kFmtMXFP4);
+  else if (fmt == kFmtINT4) SVDQ_WIDE_FMT(kFmtINT4);
+  else SVDQ_WIDE_FMT(kFmtNVFP4);
+#undef SVDQ_WIDE_FMT
+#undef SVDQ_WIDE_T
+#undef SVDQ_WIDE
+  if (wide.Z > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(w4a16_join_kernel, dim3(blocks((M * N / 4 + 255) / 256)), dim3(256), 0, s, a, S);
+  }
   return hipGetLastError();
 }
 

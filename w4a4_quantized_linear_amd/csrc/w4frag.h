@@ -57,15 +57,28 @@ struct W4Rows {
       : codes(c), scales(s), code_bytes(uint32_t(N_pad * K / 2)),
         scale_bytes(uint32_t(N_pad * K / (FMT == kFmtNVFP4 ? 16 : 32))), KS(uint32_t(K / kKStep)),
         s_step(uint32_t(N_pad) * 4) {}
-  __device__ __forceinline__ void load(uint32_t rt, uint32_t ks, bool valid, int lane, W4Stage<FMT>& st) const {
+  // T tiles from rt on.  A tile's distance is in the lane's offset, so all share scalar operands.
+  template <int T>
+  __device__ __forceinline__ void load(uint32_t rt, uint32_t ks, bool valid, int lane, W4Stage<FMT> (&st)[T]) const {
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(codes, valid ? code_bytes : 0);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales, valid ? scale_bytes : 0);
-    st.q = buffer_load16(rc, uint32_t(lane) * 16, (rt * KS + ks) * 1024);
-    if constexpr (FMT == kFmtMXFP4)
-      st.s = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rs, uint32_t(lane) * 4, (rt * (KS / 4) + ks / 4) * 256, 0));
-    if constexpr (FMT == kFmtNVFP4)
-      st.s = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, uint32_t(lane) * 2, (rt * KS + ks) * 128, 0));
-    if constexpr (FMT == kFmtINT4) st.s = buffer_load16(rs, uint32_t(lane >> 4) * 16, ks * s_step + rt * 64);  // rows 4 c ..
+#pragma unroll
+    for (uint32_t t = 0; t < T; ++t) {
+      st[t].q = buffer_load16(rc, uint32_t(lane) * 16 + t * KS * 1024, (rt * KS + ks) * 1024);
+      if constexpr (FMT == kFmtMXFP4)
+        st[t].s = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(rs, uint32_t(lane) * 4 + t * KS * 64,
+                                                                (rt * KS + (ks & ~3u)) * 64, 0));
+      if constexpr (FMT == kFmtNVFP4)
+        st[t].s = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, uint32_t(lane) * 2 + t * KS * 128,
+                                                                (rt * KS + ks) * 128, 0));
+      if constexpr (FMT == kFmtINT4)               // rows 4 c .. 4 c + 3 of the tile
+        st[t].s = buffer_load16(rs, uint32_t(lane >> 4) * 16 + t * 64, ks * s_step + rt * 64);
+    }
+  }
+  __device__ __forceinline__ void load(uint32_t rt, uint32_t ks, bool valid, int lane, W4Stage<FMT>& st) const {
+    W4Stage<FMT> one[1];
+    load<1>(rt, ks, valid, lane, one);
+    st = one[0];
   }
 };
 
@@ -110,50 +123,87 @@ __device__ __forceinline__ uint4 i4_to_bf16(uint32_t d, uint32_t k41) {
                     __builtin_amdgcn_perm(k41, hi, 0x04010400u), __builtin_amdgcn_perm(k41, hi, 0x04030402u));
 }
 
-// acc[b] += (tile's 16 rows) x (16 columns of x[b]) over one 128-K step, for NB blocks
-// of columns; x[b][u] is the B operand of MFMA u.
-template <int FMT, int NB>
-__device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const uint4 (&x)[NB][4], v4f (&acc)[NB]) {
-  const uint32_t d[4] = {st.q.x, st.q.y, st.q.z, st.q.w};
-  if constexpr (FMT == kFmtMXFP4) {
-    const float sc = __uint_as_float(((st.s >> ((ks & 3) * 8)) & 0xFFu) << 23);
+// acc[t][b] += (rows of tile t) x (16 columns of block b) over MFMA u of a 128-K step (MXFP4,
+// NVFP4); x[b] is the B operand.
+template <int FMT, int T, int NB>
+__device__ __forceinline__ void w4_mfma(const W4Stage<FMT> (&st)[T], int ks, int u, const uint4 (&x)[NB],
+                                        v4f (&acc)[T][NB]) {
+  static_assert(FMT != kFmtINT4, "INT4 takes half a step");
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4 a = mx_to_bf16(d[u], sc);
+  for (int t = 0; t < T; ++t) {
+    const uint32_t d[4] = {st[t].q.x, st[t].q.y, st[t].q.z, st[t].q.w};
+    uint4 a;
+    if constexpr (FMT == kFmtMXFP4)
+      a = mx_to_bf16(d[u], __uint_as_float(((st[t].s >> ((ks & 3) * 8)) & 0xFFu) << 23));
+    else
+      a = nv_to_bf16(d[u], e4m3_value((st[t].s >> ((u >> 1) * 8)) & 0xFFu));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[b] = mfma_bf16(a, x[b][u], acc[b]);
-    }
-  } else if constexpr (FMT == kFmtNVFP4) {
-    const float sc[2] = {e4m3_value(st.s & 0xFFu), e4m3_value((st.s >> 8) & 0xFFu)};
+    for (int b = 0; b < NB; ++b) acc[t][b] = mfma_bf16(a, x[b], acc[t][b]);
+  }
+}
+
+// The same over half `half` of a step (MFMAs 2 half and 2 half + 1) for INT4, a scale group;
+// x[u][b] is the B operand of MFMA 2 half + u.
+template <int T, int NB>
+__device__ __forceinline__ void w4_half(const W4Stage<kFmtINT4> (&st)[T], int half, const uint4 (&x)[2][NB],
+                                        v4f (&acc)[T][NB]) {
+  const uint4 m24 = make_uint4(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);   // bf16 -24
+  uint32_t k41 = 0x41414141u;
+  asm volatile("" : "+v"(k41));                             // kept in a register for the byte permutes
+  uint4 a[T][2];
+  float s[T][4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4 a = nv_to_bf16(d[u], sc[u >> 1]);
+  for (int t = 0; t < T; ++t) {
+    const uint32_t d[4] = {st[t].q.x, st[t].q.y, st[t].q.z, st[t].q.w};
+    const uint32_t sd[4] = {st[t].s.x, st[t].s.y, st[t].s.z, st[t].s.w};
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[b] = mfma_bf16(a, x[b][u], acc[b]);
-    }
-  } else {
-    const uint4 m24 = make_uint4(0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u);   // bf16 -24
-    uint32_t k41 = 0x41414141u;
-    asm volatile("" : "+v"(k41));                           // kept in a register for the byte permutes
-    const uint32_t sd[4] = {st.s.x, st.s.y, st.s.z, st.s.w};
+    for (int u = 0; u < 2; ++u) a[t][u] = i4_to_bf16(d[2 * half + u], k41);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const uint4 a0 = i4_to_bf16(d[2 * g], k41), a1 = i4_to_bf16(d[2 * g + 1], k41);
-      float s[4];
+    for (int e = 0; e < 4; ++e) s[t][e] = f16_value(half == 0 ? sd[e] : sd[e] >> 16);
+  }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = f16_value(g == 0 ? sd[e] : sd[e] >> 16);
+  for (int b = 0; b < NB; ++b) {
+    v4f off = {0.f, 0.f, 0.f, 0.f};                         // -24 times the group's sum, for all tiles
+    off = mfma_bf16(m24, x[0][b], off);
+    off = mfma_bf16(m24, x[1][b], off);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        v4f p = {0.f, 0.f, 0.f, 0.f};
-        p = mfma_bf16(a0, x[b][2 * g], p);
-        p = mfma_bf16(a1, x[b][2 * g + 1], p);
-        p = mfma_bf16(m24, x[b][2 * g], p);
-        p = mfma_bf16(m24, x[b][2 * g + 1], p);
+    for (int t = 0; t < T; ++t) {
+      v4f p = mfma_bf16(a[t][0], x[0][b], off);
+      p = mfma_bf16(a[t][1], x[1][b], p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[b][e] = fmaf(s[e], p[e], acc[b][e]);
-      }
+      for (int e = 0; e < 4; ++e) acc[t][b][e] = fmaf(s[t][e], p[e], acc[t][b][e]);
     }
   }
+}
+
+// A whole 128-K step of one tile; x[b][u] is the B operand of MFMA u.
+template <int FMT, int NB>
+__device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const uint4 (&x)[NB][4], v4f (&acc)[NB]) {
+  const W4Stage<FMT> one[1] = {st};
+  v4f a[1][NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) a[0][b] = acc[b];
+  if constexpr (FMT == kFmtINT4) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint4 h[2][NB];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) h[u][b] = x[b][2 * half + u];
+      w4_half<1, NB>(one, half, h, a);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4 h[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) h[b] = x[b][u];
+      w4_mfma<FMT, 1, NB>(one, ks, u, h, a);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = a[0][b];
 }
 
 // The factor that the sums of a packed weight still lack: NVFP4's tensor scale
