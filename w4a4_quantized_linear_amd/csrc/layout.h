@@ -90,7 +90,8 @@ __host__ __device__ inline W4A16Plan w4a16_plan(int K, int64_t r_pad, int64_t M,
 constexpr int kWideWaves = 8;
 constexpr int kWideBlocks = 6;         // at most
 constexpr int kWideGroups = 256;       // one workgroup a CU
-constexpr int64_t kWideTraffic = 100000000;
+constexpr int64_t kWideTraffic = 450000000;   // sweep at M 16..48: 1e8 25.3, 2e8 20.1, 4.5e8 18.6 us at 48 x 4096 -> 4096;
+                                               // 1e9 slower where the columns are many (33 x 12288 -> 4096: 26.9 -> 31.2)
 
 struct W4A16Wide {
   int64_t groups, Mg;
