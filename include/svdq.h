@@ -210,13 +210,15 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
  *     Y = act( X_hat deQ(Q4(R))^T + (X_hat L1) L2 + b ),  X_hat = fp32(X / lambda),
  * on the same blob that svdq_linear takes.  Sums are fp32; X_hat enters as a sum of bf16
  * parts that holds it to 2^-18 (bf16 output) or to fp32's own rounding (SVDQ_EPI_OUT_F32).
- * Two launches: one prepares X_hat and X_hat L1, one streams the codes, once for up to 8
- * tokens (5 with float32 output) and once per 16 tokens beyond; any M >= 0 is computed
- * correctly.  A row with a non-finite element gives a non-finite row; no other row changes.
+ * Up to 8 tokens (5 with float32 output) whose K x rank is small take one launch; others a
+ * launch that prepares X_hat and X_hat L1, the product, and, where few output rows would leave
+ * CUs idle, a launch that adds parts of K.  Any M >= 0 is computed correctly.  A row with a
+ * non-finite element gives a non-finite row; no other row changes.
  *   X, Y, epi  as for svdq_linear (all SVDQ_EPI_* flags)
  *   workspace  device, at least svdq_w4a16_bytes(d, M) bytes, 256-byte aligned; every call
- *              writes what it reads of it.  Calls that may overlap (other streams, captured
- *              graphs that run at once) need workspaces of their own.
+ *              writes what it reads of it.  A call that needs none (0 bytes: few tokens at a
+ *              small K x rank) takes NULL.  Calls that may overlap (other streams, captured
+ *              graphs that run at once) need workspaces of their own, here and below.
  * Checks and errors as svdq_linear. */
 size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M);
 svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M,
@@ -242,11 +244,12 @@ enum {
  *   router   device, bf16 bits, E x K row-major; X and router 16-byte aligned
  *   bias     device, float32[E], or NULL
  *   ids, weights  device, int32 and float32, M x top_k row-major
- *   workspace     device, at least svdq_moe_route_bytes(M, E) bytes, 256-byte aligned
+ *   workspace     device, at least svdq_moe_route_bytes(M, K, E) bytes, 256-byte aligned (a call
+ *                 that needs none, 0 bytes, takes NULL)
  * 8 <= K <= 65536, 1 <= E <= 512, 1 <= top_k <= min(E, 32), scale not NaN, else
  * SVDQ_ERR_SHAPE; K or ldx not a multiple of 8 gives SVDQ_ERR_ALIGN, unknown flags
  * SVDQ_ERR_FORMAT. */
-size_t svdq_moe_route_bytes(int64_t M, int32_t E);
+size_t svdq_moe_route_bytes(int64_t M, int32_t K, int32_t E);
 svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K, const uint16_t* router, int32_t E,
                            const float* bias, int32_t top_k, uint32_t flags, float scale, int32_t* ids, float* weights,
                            void* workspace, size_t ws_bytes, void* stream);

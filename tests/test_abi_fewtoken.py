@@ -34,8 +34,10 @@ def test_sizes(L):
     assert many >= 100 * (1024 * 6 + 2 * 32 * 4) and many % 256 == 0
     assert L.svdq_w4a16_bytes(D(K=1000), 1) == 0
     assert L.svdq_w4a16_bytes(D(), -1) == 0 and L.svdq_w4a16_bytes(None, 1) == 0 and L.svdq_w4a16_bytes(D(fmt=9), 1) == 0
-    assert L.svdq_moe_route_bytes(7, 64) >= 7 * 64 * 8 and L.svdq_moe_route_bytes(0, 1) > 0
-    assert L.svdq_moe_route_bytes(-1, 64) == 0 and L.svdq_moe_route_bytes(1, 0) == 0 and L.svdq_moe_route_bytes(1, 513) == 0
+    assert L.svdq_moe_route_bytes(1, 1024, 64) == 0                         # one kernel
+    assert L.svdq_moe_route_bytes(700, 1024, 64) >= 700 * 64 * 8
+    for bad in ((-1, 1024, 64), (700, 1024, 0), (700, 1024, 513), (700, 0, 64)):
+        assert L.svdq_moe_route_bytes(*bad) == 0
     g, d = D(K=1024, N=1024, rank=0), D(K=512, N=256, rank=0)
     assert L.svdq_moe_bytes(g, d, 5, 3) >= 15 * 512 * 6
     assert L.svdq_moe_bytes(g, d, 10 ** 6, 3) <= 2048 * 512 * 6 + 256       # parts share it
@@ -74,7 +76,8 @@ def test_linear_w4a16_validation(L, forced_device_error):
 def test_route_validation(L, forced_device_error):
     f = L.svdq_moe_route
     # X, M, ldx, K, router, E, bias, top_k, flags, scale, ids, weights, workspace, bytes, stream
-    ok = [P, 4, 1024, 1024, P, 64, None, 8, 3, 1.0, P, P, P, BIG, None]
+    ok = [P, 400, 1024, 1024, P, 64, None, 8, 3, 1.0, P, P, P, BIG, None]
+    n = L.svdq_moe_route_bytes(400, 1024, 64)
 
     def call(**kw):
         a = list(ok)
@@ -92,7 +95,8 @@ def test_route_validation(L, forced_device_error):
     for kw in (dict(_3=1020), dict(_2=1028), dict(_0=P + 8), dict(_4=P + 8), dict(_6=P + 2), dict(_10=P + 2),
                dict(_11=P + 2), dict(_12=P + 64)):
         assert call(**kw) == 4, kw
-    assert call(_13=4 * 64 * 8 - 1) == 5 and call(_13=4 * 64 * 8) == 6
+    assert call(_13=n - 1) == 5 and call(_13=n) == 6
+    assert call(_1=4, _12=None, _13=0) == 6                                 # needs none
 
 
 def test_moe_validation(L, forced_device_error):

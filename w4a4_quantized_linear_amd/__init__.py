@@ -278,9 +278,9 @@ def linear_w4a16(layer: Layer, w_packed, X, epi: int = 0, out=None, workspace=No
     return out
 
 
-def moe_route_bytes(M: int, E: int) -> int:
+def moe_route_bytes(M: int, K: int, E: int) -> int:
     """Workspace bytes of moe_route (0: none needed, or invalid)."""
-    return int(lib().svdq_moe_route_bytes(int(M), int(E)))
+    return int(lib().svdq_moe_route_bytes(int(M), int(K), int(E)))
 
 
 def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: bool = True, scale: float = 1.0,
@@ -312,7 +312,7 @@ def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: b
     else:
         _flat(weights, "weights", out, dev, torch.float32)
     L = lib()
-    ws = _space(workspace, L.svdq_moe_route_bytes(M, E), dev)
+    ws = _space(workspace, L.svdq_moe_route_bytes(M, K, E), dev)
     st = L.svdq_moe_route(X.data_ptr(), M, ldx, K, router.data_ptr(), E, None if bias is None else bias.data_ptr(),
                           top_k, (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_RENORM if renorm else 0), scale,
                           ids.data_ptr(), weights.data_ptr(), None if ws is None else ws.data_ptr(),

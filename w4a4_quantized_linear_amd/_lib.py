@@ -35,7 +35,7 @@ SIGNATURES = {
     "svdq_gemm_w4a16": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P]),
     "svdq_w4a16_bytes": (ctypes.c_size_t, [_D, _I64]),
     "svdq_linear_w4a16": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
-    "svdq_moe_route_bytes": (ctypes.c_size_t, [_I64, ctypes.c_int32]),
+    "svdq_moe_route_bytes": (ctypes.c_size_t, [_I64, ctypes.c_int32, ctypes.c_int32]),
     "svdq_moe_route": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_int32,
                                       ctypes.c_uint32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
     "svdq_moe_bytes": (ctypes.c_size_t, [_D, _D, _I64, ctypes.c_int32]),

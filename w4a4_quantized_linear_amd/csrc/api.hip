@@ -330,15 +330,16 @@ svdq_status svdq_linear_w4a16(const svdq_layer_desc* d, const void* w_packed, co
                                       reinterpret_cast<float*>(ws + l.zsum), static_cast<hipStream_t>(stream)));
 }
 
-size_t svdq_moe_route_bytes(int64_t M, int32_t E) {
-  if (M < 0 || M > kMaxRows || E < 1 || E > kMoeMaxE) return 0;
-  return align256(size_t(M > 0 ? M : 1) * E * 8);
+size_t svdq_moe_route_bytes(int64_t M, int32_t K, int32_t E) {
+  if (M < 0 || M > kMaxRows || K < 8 || K > 65536 || E < 1 || E > kMoeMaxE || route_one(M, K, E)) return 0;
+  return align256(size_t(M) * E * 8 * route_splits(M, K, E));
 }
 
 svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K, const uint16_t* router, int32_t E,
                            const float* bias, int32_t top_k, uint32_t flags, float scale, int32_t* ids, float* weights,
                            void* workspace, size_t ws_bytes, void* stream) {
-  if (!router || !workspace || (M > 0 && (!X || !ids || !weights))) return SVDQ_ERR_NULL;
+  const size_t need = svdq_moe_route_bytes(M, K, E);
+  if (!router || (!workspace && need) || (M > 0 && (!X || !ids || !weights))) return SVDQ_ERR_NULL;
   if (M < 0 || M > kMaxRows || K < 8 || K > 65536 || ldx < K || ldx > kMaxLdx || E < 1 || E > kMoeMaxE ||
       top_k < 1 || top_k > kMoeMaxTopK || top_k > E || !(scale == scale))
     return SVDQ_ERR_SHAPE;
@@ -346,7 +347,7 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
   if (K % 8 != 0 || ldx % 8 != 0 || !aligned(X, 16) || !aligned(router, 16) || !aligned(bias, 4) || !aligned(ids, 4) ||
       !aligned(weights, 4) || !aligned(workspace, 256))
     return SVDQ_ERR_ALIGN;
-  if (ws_bytes < svdq_moe_route_bytes(M, E)) return SVDQ_ERR_WORKSPACE;
+  if (ws_bytes < need) return SVDQ_ERR_WORKSPACE;
   svdq_status s = device_check();
   if (s != SVDQ_OK) return s;
   if (M == 0) return SVDQ_OK;

@@ -50,6 +50,21 @@ constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxPairs = 2048;
 
+// svdq_moe_route: one kernel, a workgroup per token, while one CU's fp64 rate computes all of a
+// token's logits about as fast as a second launch costs and each token has a CU; otherwise the
+// logits are formed in tiles of 16 experts x 16 tokens, K split over
+// route_splits workgroups while there are CUs for them, and a second kernel chooses.
+constexpr int64_t kRouteOneMacs = 163840;
+constexpr int64_t kRouteOneTokens = 256;
+__host__ __device__ inline bool route_one(int64_t M, int K, int E) {
+  return M <= kRouteOneTokens && int64_t(E) * K <= kRouteOneMacs;
+}
+__host__ __device__ inline int route_splits(int64_t M, int K, int E) {
+  const int64_t tiles = ((M + 15) / 16) * ((E + 15) / 16), z = 256 / (tiles > 0 ? tiles : 1);
+  const int64_t most = (K + 511) / 512 < 8 ? (K + 511) / 512 : 8;      // a wave keeps four 32-K steps
+  return int(z < 1 ? 1 : z < most ? z : most);
+}
+
 // Scale bytes per row: K/32 (E8M0 per 32, or fp16 per 64), K/16 for NVFP4 (E4M3 per 16).
 __host__ __device__ inline size_t scale_row_bytes(int fmt, int K) { return fmt == kFmtNVFP4 ? K / 16 : K / 32; }
 constexpr uint32_t kLamRangeBit = 1;   // weight flags: a lambda outside [2^-32, 2^32]

@@ -18,123 +18,267 @@ struct RouteArgs {
   const uint16_t* X;
   const uint16_t* Wr;
   const float* bias;       // added to the scores for the choice only; may be null
-  double* logits;          // M x E
+  double* logits;          // Z x M x E
   int32_t* ids;
   float* weights;
   int64_t ldx, M;
-  int K, E, top_k;
+  int K, E, top_k, Z;
   uint32_t flags;
   float scale;
 };
 
+// Lane 63's combination of a wave's values over the row shifts and broadcasts of DPP: sums of
+// doubles, maxima of unsigned words.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));   // 0 where no lane is read
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, uint64_t(dpp<CTRL, ROWS>(uint32_t(u))) | uint64_t(dpp<CTRL, ROWS>(uint32_t(u >> 32))) << 32);
+}
+constexpr int kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114, kShr8 = 0x118, kBcast15 = 0x142, kBcast31 = 0x143;
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, dpp<kShr1, 0xF>(v));
+  v = up(v, dpp<kShr2, 0xF>(v));
+  v = up(v, dpp<kShr4, 0xF>(v));
+  v = up(v, dpp<kShr8, 0xF>(v));
+  v = up(v, dpp<kBcast15, 0xA>(v));
+  v = up(v, dpp<kBcast31, 0xC>(v));
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, uint64_t(uint32_t(__builtin_amdgcn_readlane(int(u), lane))) |
+                                        uint64_t(uint32_t(__builtin_amdgcn_readlane(int(u >> 32), lane))) << 32);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += dpp<kShr1, 0xF>(v);
+  v += dpp<kShr2, 0xF>(v);
+  v += dpp<kShr4, 0xF>(v);
+  v += dpp<kShr8, 0xF>(v);
+  v += dpp<kBcast15, 0xA>(v);
+  v += dpp<kBcast31, 0xC>(v);
+  return lane_value(v, 63);
 }
 
-// Logits in fp64: products of two bf16 are exact in fp32, and the sums keep 53 bits, so
-// which expert is chosen does not depend on the order of summation.  A wave takes TE experts
-// and TM tokens, its lanes 8 consecutive K each.
-template <int TE, int TM>
-__global__ void __launch_bounds__(256) route_logits_kernel(RouteArgs a) {
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e0 = (blockIdx.x * 4 + w) * TE;
-  if (e0 >= a.E) return;
-  for (int64_t m0 = int64_t(blockIdx.y) * TM; m0 < a.M; m0 += int64_t(gridDim.y) * TM) {
-    const uint16_t* wp[TE];
-    const uint16_t* xp[TM];
-#pragma unroll
-    for (int i = 0; i < TE; ++i) wp[i] = a.Wr + int64_t(e0 + i < a.E ? e0 + i : a.E - 1) * a.K;
-#pragma unroll
-    for (int j = 0; j < TM; ++j) xp[j] = a.X + (m0 + j < a.M ? m0 + j : a.M - 1) * a.ldx;
-    double acc[TE][TM] = {};
-    for (int k = lane * 8; k < a.K; k += 512) {
-      uint4 wq[TE], xq[TM];
-#pragma unroll
-      for (int i = 0; i < TE; ++i) wq[i] = *reinterpret_cast<const uint4*>(wp[i] + k);
-#pragma unroll
-      for (int j = 0; j < TM; ++j) xq[j] = *reinterpret_cast<const uint4*>(xp[j] + k);
-      float xf[TM][8];
-#pragma unroll
-      for (int j = 0; j < TM; ++j) unpack_bf8(xq[j], xf[j]);
-#pragma unroll
-      for (int i = 0; i < TE; ++i) {
-        float wf[8];
-        unpack_bf8(wq[i], wf);
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-          for (int q = 0; q < 8; ++q) acc[i][j] = fma(double(wf[q]), double(xf[j][q]), acc[i][j]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < TE; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const double v = wave_sum(acc[i][j]);
-        if (lane == 0 && e0 + i < a.E && m0 + j < a.M) a.logits[(m0 + j) * a.E + e0 + i] = v;
-      }
-  }
+// A double's place among doubles as an unsigned number above 0 (NaN as -infinity, -0 as 0).
+__device__ __forceinline__ uint64_t order_of(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v == v ? v + 0.0 : -__builtin_huge_val());
+  return u >> 63 ? ~u : u | (uint64_t(1) << 63);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = wave_max(uint32_t(v >> 32));
+  return uint64_t(hi) << 32 | wave_max(uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
 }
 
-// Scores, the choice and the weights of one token whose logits lie in `l` (LDS); every thread
-// of the workgroup takes part.  An expert's place is the number of experts that come before it:
-// a larger key, or the same and a lower index; a NaN key counts as -infinity.
-__device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, const double* l, double* key, double* red,
-                                               double* chosen) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, w = tid >> 6, nw = nt >> 6;
+template <int PER>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&bias)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) bias[i] = a.bias && i * 64 + lane < a.E ? a.bias[i * 64 + lane] : 0.f;
+}
+
+// One wave chooses one token's experts and writes their weights; l[i] and bias[i] are those of expert
+// 64 i + lane.  Each round takes the largest key left, the lowest index among equals; lane t keeps
+// the t-th choice.
+template <int PER>
+__device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, const double (&l)[PER], const float (&bias)[PER],
+                                               int lane) {
   const bool sig = (a.flags & SVDQ_ROUTE_SIGMOID) != 0;
-  double top = -__builtin_huge_val(), sum = 0.0;
+  double top = 0.0, sum = 1.0;
   if (!sig) {
-    for (int e = tid; e < a.E; e += nt) top = fmax(top, l[e]);
+    uint64_t t = 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-    if (lane == 0) red[w] = top;
-    __syncthreads();
-    for (int v = 0; v < nw; ++v) top = fmax(top, red[v]);
-    __syncthreads();
-    for (int e = tid; e < a.E; e += nt) sum += exp(l[e] - top);
-    sum = wave_sum(sum);
-    if (lane == 0) red[w] = sum;
-    __syncthreads();
+    for (int i = 0; i < PER; ++i) {
+      const uint64_t o = i * 64 + lane < a.E ? order_of(l[i]) : 0;
+      t = o > t ? o : t;
+    }
+    t = wave_max(t);
+    top = __builtin_bit_cast(double, t >> 63 ? t & ~(uint64_t(1) << 63) : ~t);
     sum = 0.0;
-    for (int v = 0; v < nw; ++v) sum += red[v];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 64 + lane < a.E) sum += exp(l[i] - top);
+    sum = wave_sum(sum);
   }
-  auto score = [&](int e) { return sig ? 1.0 / (1.0 + exp(-l[e])) : exp(l[e] - top) / sum; };
-  for (int e = tid; e < a.E; e += nt) {
-    const double k = a.bias ? score(e) + double(a.bias[e]) : l[e];   // without a bias the logits order the scores
-    key[e] = k == k ? k : -__builtin_huge_val();
+  auto score = [&](double v) { return sig ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum; };
+  uint64_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 64 + lane;
+    // without a bias the logits order the scores
+    key[i] = e < a.E ? order_of(a.bias ? score(l[i]) + double(bias[i]) : l[i]) : 0;
   }
-  __syncthreads();
-  for (int e = tid; e < a.E; e += nt) {
-    const double k = key[e];
-    int place = 0;
-    for (int f = 0; f < a.E; ++f) place += (key[f] > k || (key[f] == k && f < e)) ? 1 : 0;
-    if (place < a.top_k) {
-      a.ids[m * a.top_k + place] = e;
-      chosen[place] = score(e);
+  int id = 0;
+  double mine = 0.0;
+  for (int t = 0; t < a.top_k; ++t) {
+    uint64_t best = 0;
+    int at = 0;
+    double v = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] > best) { best = key[i]; at = i; v = l[i]; }
+    const uint64_t most = wave_max(best);
+    const uint64_t tied = __ballot(best == most);
+    int from = __ffsll((unsigned long long)tied) - 1;
+    if (tied & (tied - 1)) {                               // equal keys: the lowest index
+      const uint32_t low = ~wave_max(best == most ? ~uint32_t(at * 64 + lane) : 0u);
+      from = int(low & 63u);
     }
+    const int e = __builtin_amdgcn_readlane(at, from) * 64 + from;
+    const double won = lane_value(v, from);
+    if (lane == t) { id = e; mine = won; }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane == from && at == i) key[i] = 0;
   }
-  __syncthreads();
-  if (tid < a.top_k) {
-    double v = chosen[tid];
-    if (a.flags & SVDQ_ROUTE_RENORM) {
-      double s = 0.0;
-      for (int j = 0; j < a.top_k; ++j) s += chosen[j];
-      v = s == 0.0 ? 0.0 : v / s;
-    }
-    a.weights[m * a.top_k + tid] = float(v * double(a.scale));
+  double p = lane < a.top_k ? score(mine) : 0.0;
+  if (a.flags & SVDQ_ROUTE_RENORM) {
+    const double s = wave_sum(p);
+    p = s == 0.0 ? 0.0 : p / s;
   }
-  __syncthreads();
+  if (lane < a.top_k) {
+    a.ids[m * a.top_k + lane] = id;
+    a.weights[m * a.top_k + lane] = float(p * double(a.scale));
+  }
 }
 
-__global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
-  __shared__ double l[kMoeMaxE], key[kMoeMaxE], red[4], chosen[kMoeMaxTopK];
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-    for (int e = threadIdx.x; e < a.E; e += 256) l[e] = a.logits[m * a.E + e];
+// Logits in fp64: products of two bf16 are exact there and the sums keep 53 bits, so which expert
+// is chosen does not hang on the order of summation.
+//
+// One workgroup: a token.  Wave w takes experts w, w + 16, ..., four at a time, its lanes 8
+// consecutive K each; wave 0 then chooses.  Bound by the CU's fp64 conversions and FMAs.
+constexpr int kRouteOneWaves = 16;
+template <int PER>
+__global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a) {
+  __shared__ double logit[kMoeMaxE];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = blockIdx.x;
+  const uint16_t* const x = a.X + m * a.ldx;
+  for (int e0 = w; e0 < a.E; e0 += 4 * kRouteOneWaves) {
+    double acc[4] = {};
+    for (int k = lane * 8; k < a.K; k += 512) {
+      uint4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + i * kRouteOneWaves;
+        q[i] = *reinterpret_cast<const uint4*>(a.Wr + int64_t(e < a.E ? e : e0) * a.K + k);
+      }
+      float xf[8];
+      unpack_bf8(*reinterpret_cast<const uint4*>(x + k), xf);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float wf[8];
+        unpack_bf8(q[i], wf);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i] = fma(double(wf[j]), double(xf[j]), acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double v = wave_sum(acc[i]);
+      if (lane == 0 && e0 + i * kRouteOneWaves < a.E) logit[e0 + i * kRouteOneWaves] = v;
+    }
+  }
+  float bias[PER];
+  load_bias<PER>(a, lane, bias);
+  __syncthreads();
+  if (w) return;
+  double l[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) l[i] = i * 64 + lane < a.E ? logit[i * 64 + lane] : 0.0;
+  choose_experts<PER>(a, m, l, bias, lane);
+}
+
+// A tile of 16 experts x 16 tokens and one of Z parts of K on the fp64 MFMA (16x16x4): lane (r, c)
+// holds 8 consecutive K of expert and token r, so element e of both operands is one MFMA's K.  The
+// waves take every fourth 32 of K; their sums meet in LDS, the parts' in the next kernel.  Bound by
+// the fp64 units (1000 x 2888 -> 128: 23 us; tiles of 32 x 32, half the conversions an MFMA: 26 us).
+typedef double v4d __attribute__((ext_vector_type(4)));
+__global__ void __launch_bounds__(256) route_logits_kernel(RouteArgs a) {
+  constexpr int AHEAD = 4;                                 // steps of one batch of loads
+  __shared__ v4d part[4][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  const int e0 = blockIdx.x * 16, steps = (a.K + 31) / 32;
+  const int s0 = int(int64_t(blockIdx.z) * steps / a.Z), s1 = int(int64_t(blockIdx.z + 1) * steps / a.Z);
+  const uint16_t* const wp = a.Wr + int64_t(e0 + r < a.E ? e0 + r : a.E - 1) * a.K;
+  for (int64_t m0 = int64_t(blockIdx.y) * 16; m0 < a.M; m0 += int64_t(gridDim.y) * 16) {
+    const uint16_t* const xp = a.X + (m0 + r < a.M ? m0 + r : a.M - 1) * a.ldx;
+    v4d acc = {0.0, 0.0, 0.0, 0.0};
+    // two batches in flight; past the part's end and K's (a multiple of 8) zeros
+    uint4 q[2][AHEAD], x[2][AHEAD];
+    auto load = [&](int s, uint4 (&qs)[AHEAD], uint4 (&xs)[AHEAD]) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const int k = (s + 4 * j) * 32 + c * 8;
+        const bool there = s + 4 * j < s1 && k < a.K;
+        qs[j] = *reinterpret_cast<const uint4*>(wp + (there ? k : 0));
+        xs[j] = *reinterpret_cast<const uint4*>(xp + (there ? k : 0));
+        if (!there) qs[j] = xs[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto add = [&](const uint4 (&qs)[AHEAD], const uint4 (&xs)[AHEAD]) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        float wf[8], xf[8];
+        unpack_bf8(qs[j], wf);
+        unpack_bf8(xs[j], xf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64(double(wf[e]), double(xf[e]), acc, 0, 0, 0);
+      }
+    };
+    load(s0 + w, q[0], x[0]);
+    for (int s = s0 + w; s < s1; s += 8 * AHEAD) {
+      load(s + 4 * AHEAD, q[1], x[1]);
+      add(q[0], x[0]);
+      if (s + 4 * AHEAD >= s1) break;
+      load(s + 8 * AHEAD, q[0], x[0]);
+      add(q[1], x[1]);
+    }
+    part[w][lane] = acc;
     __syncthreads();
-    choose_experts(a, m, l, key, red, chosen);
+    if (w == 0) {
+      acc = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
+      // column (token) r, rows (experts) c, c + 4, c + 8, c + 12
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (m0 + r < a.M && e0 + i * 4 + c < a.E)
+          a.logits[(blockIdx.z * a.M + m0 + r) * a.E + e0 + i * 4 + c] = acc[i];
+    }
+    __syncthreads();
+  }
+}
+
+// One wave a token.
+template <int PER>
+__global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float bias[PER];
+  load_bias<PER>(a, lane, bias);
+  for (int64_t m = int64_t(blockIdx.x) * 4 + w; m < a.M; m += int64_t(gridDim.x) * 4) {
+    double l[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = 0.0;
+    for (int z0 = 0; z0 < a.Z; z0 += 4) {                  // four parts' loads at once
+      double v[4][PER];
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int e = i * 64 + lane;
+          v[z][i] = a.logits[((z0 + z < a.Z ? z0 + z : z0) * a.M + m) * a.E + (e < a.E ? e : 0)];
+        }
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (z0 + z < a.Z) l[i] += v[z][i];
+    }
+    choose_experts<PER>(a, m, l, bias, lane);
   }
 }
 
@@ -145,13 +289,24 @@ hipError_t launch_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int K, co
   a.X = X; a.Wr = Wr; a.bias = bias; a.logits = logits; a.ids = ids; a.weights = weights;
   a.ldx = ldx; a.M = M; a.K = K; a.E = E; a.top_k = top_k; a.flags = flags; a.scale = scale;
   const auto cap = [](int64_t v) { return unsigned(v < 65535 ? v : 65535); };
-  if (M < 4)
-    hipLaunchKernelGGL((route_logits_kernel<1, 1>), dim3((E + 3) / 4, cap(M)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((route_logits_kernel<2, 4>), dim3((E + 7) / 8, cap((M + 3) / 4)), dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
+#define SVDQ_ROUTE(KERNEL_, GRID_, BLOCK_)                                                   \
+  do {                                                                                       \
+    if (E <= 64) hipLaunchKernelGGL((KERNEL_<1>), GRID_, BLOCK_, 0, s, a);                   \
+    else if (E <= 128) hipLaunchKernelGGL((KERNEL_<2>), GRID_, BLOCK_, 0, s, a);             \
+    else if (E <= 256) hipLaunchKernelGGL((KERNEL_<4>), GRID_, BLOCK_, 0, s, a);             \
+    else hipLaunchKernelGGL((KERNEL_<8>), GRID_, BLOCK_, 0, s, a);                           \
+  } while (0)
+  if (route_one(M, K, E)) {
+    SVDQ_ROUTE(route_one_kernel, dim3(unsigned(M)), dim3(64 * kRouteOneWaves));
+    return hipGetLastError();
+  }
+  a.Z = route_splits(M, K, E);
+  hipLaunchKernelGGL(route_logits_kernel, dim3(unsigned((E + 15) / 16), cap((M + 15) / 16), unsigned(a.Z)), dim3(256), 0,
+                     s, a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_choose_kernel, dim3(cap(M)), dim3(256), 0, s, a);
+  SVDQ_ROUTE(route_choose_kernel, dim3(cap((M + 3) / 4)), dim3(256));
+#undef SVDQ_ROUTE
   return hipGetLastError();
 }
 
