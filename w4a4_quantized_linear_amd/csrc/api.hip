@@ -39,7 +39,7 @@ hipError_t launch_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int K, co
 hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int fmt_d, const uint8_t* wd,
                       const WeightLayout& ld, int H, int F, int N, int E, const uint16_t* X, int64_t M, int64_t ldx,
                       const int32_t* ids, const float* weights, int top_k, void* Y, int64_t ldy, uint32_t epi,
-                      void* h, hipStream_t s);
+                      void* ws, hipStream_t s);
 hipError_t launch_unpack_weight(int fmt, int K, int N, int rank, const WeightLayout& wl, const uint8_t* blob,
                                 uint8_t* codes, void* scales, uint16_t* L1, uint16_t* L2, float* lam, uint16_t* bias,
                                 hipStream_t s);
@@ -125,7 +125,7 @@ bool valid_moe_shape(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64
 }
 size_t moe_bytes(const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
   const int64_t pairs = M * top_k < kMoeMaxPairs ? M * top_k : kMoeMaxPairs;
-  return align256(size_t(pairs > 0 ? pairs : 1) * dd->K * 6);
+  return kMoePlanBytes + align256(size_t(pairs > 0 ? pairs : 1) * dd->K * 6);
 }
 
 svdq_status check_act_args(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,

@@ -49,6 +49,9 @@ constexpr float kNvfp4GlobalDiv = 2688.0f;   // E2M1 max 6 times E4M3 max 448
 constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxPairs = 2048;
+// The down kernel's plan: 16 words, then 16 for each column block, of which there are at most
+// min(E, P) + P / 5 < 1024.
+constexpr size_t kMoePlanBytes = 65536;
 
 // svdq_moe_route: one kernel, a workgroup per token, while one CU's fp64 rate computes all of a
 // token's logits about as fast as a second launch costs and each token has a CU; otherwise the

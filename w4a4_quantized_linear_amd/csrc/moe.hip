@@ -321,109 +321,220 @@ struct MoeArgs {
   const int32_t* ids;
   const float* weights;
   uint16_t* h;                         // S x P x F bf16 planes
+  int32_t* plan;                       // the down kernel's column blocks (moe_plan)
   void* Y;
   int64_t ldx, ldy, Ng_pad, Nd_pad;
   int H, F, N, E, top_k, P;            // gate/up: H -> 2 F, down: F -> N
+  int slots, KW;                       // gate/up: blocks of pairs at most, waves that share a tile's K
   uint32_t epi;
 };
 
-constexpr int kGateWaves = 8;
+// A column of an MFMA that no pair has: beyond every buffer, so its loads read nothing (zeros).
+constexpr uint32_t kNoColumn = 0x80000000u;
 
-// One workgroup: 16 gate and 16 up rows of the blockIdx.y-th expert that some pair asks for.
-template <int FMT, int S, int NB>
-__global__ void __launch_bounds__(512) moe_gate_up_kernel(MoeArgs a) {
-  constexpr int DEPTH = 2;
-  __shared__ int list[kMoeMaxPairs];
-  __shared__ int asked[kMoeMaxE];
-  __shared__ int count;
+// The plan: plan[0] column blocks, then kPlanWords words each: expert, pairs, and the pairs (at
+// most 16 / S of one expert, all their planes being columns of one MFMA).  Their order, which the
+// atomics leave open, does not reach the results: every pair has a column and a place of its own.
+constexpr int kPlanWords = 16;
+template <int S, int THREADS>
+__device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* base) {
+  constexpr int TPB = tokens_per_block(S);
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < a.P; p += THREADS) {
+    const int id = a.ids[p];
+    if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
+  }
+  __syncthreads();
+  if (tid < 64) {
+    int blocks = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+      const int e = e0 + lane, cnt = e < a.E ? cursor[e] : 0, nb = (cnt + TPB - 1) / TPB;
+      int sb = nb;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sb, o);
+        if (lane >= o) sb += v;
+      }
+      if (e < a.E) {
+        base[e] = blocks + sb - nb;                        // the expert's first block
+        cursor[e] = 0;
+        for (int b = 0; b < nb; ++b) {
+          int32_t* const r = a.plan + kPlanWords * (1 + blocks + sb - nb + b);
+          r[0] = e;
+          r[1] = cnt - b * TPB < TPB ? cnt - b * TPB : TPB;
+        }
+      }
+      blocks += __shfl(sb, 63);
+    }
+    if (lane == 0) a.plan[0] = blocks;
+  }
+  __syncthreads();
+  for (int p = tid; p < a.P; p += THREADS) {
+    const int id = a.ids[p];
+    if (id >= 0 && id < a.E) {
+      const int i = atomicAdd(&cursor[id], 1);
+      a.plan[kPlanWords * (1 + base[id] + i / TPB) + 2 + i % TPB] = p;
+    }
+  }
+}
+
+// Gate and up rows.  The workgroup takes 8 / KW tiles (16 gate and the same 16 up rows) and the
+// blockIdx.y-th block of pairs: up to 16 NB pairs of one expert, experts in order.  KW waves share
+// a tile's K (every KW-th 128-K step each); KW is the smallest that fills the GPU, since with few
+// there is little exchange and a wave streams long runs of codes.
+// SMALL (at most 64 pairs): every wave finds its block by ballots, no barrier.
+// The grid's last row (blockIdx.y == slots) holds one workgroup that writes the down kernel's plan.
+constexpr int kGateWaves = 8;
+constexpr int kGateFill = 4096;
+template <int FMT, int S, int NB, bool SMALL>
+__global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeArgs a) {
+  constexpr int DEPTH = NB == 1 && FMT != kFmtINT4 ? 3 : 2;   // registers for two workgroups a CU
+  constexpr int COLS = 16 * NB;
   __shared__ v4f red[kGateWaves][2][NB][64];
+  __shared__ int list[COLS];
+  __shared__ int cursor[kMoeMaxE], base[kMoeMaxE];
+  __shared__ int found[kGateWaves];
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
-  for (int e = tid; e < a.E; e += 512) asked[e] = 0;
-  if (tid == 0) count = 0;
-  __syncthreads();
-  for (int p = tid; p < a.P; p += 512) {
-    const int id = a.ids[p];
-    if (id >= 0 && id < a.E) asked[id] = 1;
+  const int slot = blockIdx.y;
+  if (slot == a.slots) {
+    if (blockIdx.x == 0) moe_plan<S, 512>(a, cursor, base);
+    return;
   }
-  __syncthreads();
-  int ex = -1, before = 0;
-  for (int e0 = 0; e0 < a.E && ex < 0; e0 += 64) {
-    const uint64_t b = __ballot(e0 + lane < a.E && asked[e0 + lane] != 0);
-    const int here = __popcll(b), want = int(blockIdx.y) - before;
-    if (want < here) {
-      uint64_t m = b;
-      for (int i = 0; i < want; ++i) m &= m - 1;
-      ex = e0 + __ffsll((unsigned long long)m) - 1;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  int ex = -1, T = 0, mine = 0;        // the expert, the block's pairs; SMALL: lane i holds the i-th
+  if constexpr (SMALL) {
+    const int id = lane < a.P ? a.ids[lane] : -1;
+    uint64_t left = __ballot(id >= 0 && id < a.E), eq = 0;
+    int t0 = slot * COLS;                                  // the block's first pair among the expert's
+    while (left) {
+      ex = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
+      eq = __ballot(id == ex);
+      const int blocks = (__popcll(eq) + COLS - 1) / COLS;
+      if (t0 < blocks * COLS) break;
+      t0 -= blocks * COLS;
+      left &= ~eq;
     }
-    before += here;
+    if (!left) return;
+    T = __popcll(eq);
+    const int to = eq >> lane & 1 ? __popcll(eq & below) : T + __popcll(~eq & below);
+    mine = __shfl(__builtin_amdgcn_ds_permute(to * 4, lane), (lane + t0) & 63);
+    T = T - t0 < COLS ? T - t0 : COLS;
+  } else {
+    for (int e = tid; e < a.E; e += 512) cursor[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < a.P; p += 512) {
+      const int id = a.ids[p];
+      if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
+    }
+    __syncthreads();
+    int before = 0, t0 = 0;
+    for (int e0 = 0; e0 < a.E && ex < 0; e0 += 64) {
+      const int cnt = e0 + lane < a.E ? cursor[e0 + lane] : 0, nb = (cnt + COLS - 1) / COLS;
+      int sum = nb;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sum, o);
+        if (lane >= o) sum += v;
+      }
+      const uint64_t hit = __ballot(slot >= before + sum - nb && slot < before + sum);
+      if (hit) {
+        const int at = __ffsll((unsigned long long)hit) - 1;
+        ex = e0 + at;
+        t0 = (slot - before - __builtin_amdgcn_readlane(sum - nb, at)) * COLS;
+        T = __builtin_amdgcn_readlane(cnt, at) - t0;
+      }
+      before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    if (ex < 0) return;
+    T = T < COLS ? T : COLS;
+    // the expert's pairs in order: every workgroup finds the same blocks
+    const int span = (a.P + 511) / 512 * 64;               // pairs of one wave
+    int n = 0;
+    for (int p0 = w * span; p0 < (w + 1) * span; p0 += 64)
+      n += __popcll(__ballot(p0 + lane < a.P && a.ids[p0 + lane] == ex));
+    if (lane == 0) found[w] = n;
+    __syncthreads();
+    int rank = -t0;
+    for (int v = 0; v < w; ++v) rank += found[v];
+    for (int p0 = w * span; p0 < (w + 1) * span; p0 += 64) {
+      const bool hit = p0 + lane < a.P && a.ids[p0 + lane] == ex;
+      const uint64_t m = __ballot(hit);
+      const int r = rank + __popcll(m & below);
+      if (hit && r >= 0 && r < COLS) list[r] = p0 + lane;
+      rank += __popcll(m);
+    }
+    __syncthreads();
   }
-  if (ex < 0) return;                                       // fewer experts are asked for
   ex = __builtin_amdgcn_readfirstlane(ex);
-  // the expert's pairs, in any order: a pair is a column of its own
-  for (int p = tid; p < a.P; p += 512)
-    if (a.ids[p] == ex) list[atomicAdd(&count, 1)] = p;
-  __syncthreads();
-  const int T = count;
+  auto pair_of = [&](int i) { return SMALL ? __shfl(mine, i) : list[i]; };
 
   const uint8_t* blob = a.wg + size_t(ex) * a.blob_g;
-  const int KS = a.H / kKStep, FT = a.F / 16;
-  const int ft = blockIdx.x;
+  const int KS = a.H / kKStep, FT = a.F / 16, KW = a.KW, kq = w % KW;
+  const int ft = blockIdx.x * (kGateWaves / KW) + w / KW;
+  const int n = KS > kq ? (KS - kq + KW - 1) / KW : 0;
   const W4Rows<FMT> rows(blob + a.g_codes, blob + a.g_scales, a.H, a.Ng_pad);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, uint32_t((int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2));
   const float gs = w4_tensor_scale<FMT>(blob + a.g_amax);
-  const int n = KS > w ? (KS - w + kGateWaves - 1) / kGateWaves : 0;
   struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
-  for (int t0 = 0; t0 < T; t0 += 16 * NB) {
-    const uint16_t* xp[NB];
+  {
+    uint32_t xoff[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int i = t0 + b * 16 + tl;
-      xp[b] = a.X + int64_t(list[i < T ? i : T - 1] / a.top_k) * a.ldx;
+      const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
+      xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + k_of<FMT>(c, 0)) * 2 : kNoColumn;
     }
     auto load = [&](int i, Stage& st) {
-      const int ks = w + (i < n ? i : n - 1) * kGateWaves;
+      const uint32_t ks = uint32_t(kq + i * KW);
       rows.load(ft, ks, i < n, lane, st.g);
       rows.load(FT + ft, ks, i < n, lane, st.u);
+      const __amdgpu_buffer_rsrc_t r = i < n ? rx : make_rsrc(a.X, 0);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) st.x[b][u] = *reinterpret_cast<const uint4*>(xp[b] + ks * kKStep + k_of<FMT>(c, u));
+        for (int u = 0; u < 4; ++u)
+          st.x[b][u] = buffer_load16(r, xoff[b] + (k_of<FMT>(0, u) - k_of<FMT>(0, 0)) * 2, ks * kKStep * 2);
     };
     v4f ag[NB], au[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) ag[b] = au[b] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (n > 0) {
-      Stage st[DEPTH];
+    Stage st[DEPTH];
 #pragma unroll
-      for (int j = 0; j < DEPTH; ++j) load(j, st[j]);
-      for (int i0 = 0; i0 < n; i0 += DEPTH) {
+    for (int j = 0; j < DEPTH; ++j) {
+      load(j, st[j]);
+      keep_order();
+    }
+    for (int i0 = 0; i0 < n; i0 += DEPTH) {
 #pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {
-          if (i0 + j < n) {
-            const int ks = w + (i0 + j) * kGateWaves;
-            w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
-            w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
-          }
-          load(i0 + j + DEPTH, st[j]);
-        }
+      for (int j = 0; j < DEPTH; ++j) {
+        // past the last step codes and columns are zeros
+        const int ks = kq + (i0 + j) * KW;
+        w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
+        w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
+        load(i0 + j + DEPTH, st[j]);
+        keep_order();
       }
     }
+    if (KW > 1) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      red[w][0][b][lane] = ag[b];
-      red[w][1][b][lane] = au[b];
+      for (int b = 0; b < NB; ++b) {
+        red[w][0][b][lane] = ag[b];
+        red[w][1][b][lane] = au[b];
+      }
+      lds_barrier();
     }
-    __syncthreads();
-    // wave b finishes block b: rows 4 c .. 4 c + 3 of pair tl
-    for (int b = w; b < NB; b += kGateWaves) {
-      const int i = t0 + b * 16 + tl;
-      if (i < T) {
-        v4f g = red[0][0][b][lane], u = red[0][1][b][lane];
+    if (kq == 0) {
 #pragma unroll
-        for (int v = 1; v < kGateWaves; ++v) {
-          g += red[v][0][b][lane];
-          u += red[v][1][b][lane];
+      for (int b = 0; b < NB; ++b) {
+        const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
+        if (i >= T) continue;
+        v4f g = ag[b], u = au[b];                          // rows 4 c .. 4 c + 3 of pair p
+        for (int v = 1; v < KW; ++v) {
+          g += red[w + v][0][b][lane];
+          u += red[w + v][1][b][lane];
         }
         if (FMT == kFmtNVFP4) { g *= gs; u *= gs; }
         const int row = ft * 16 + c * 4;
@@ -437,160 +548,171 @@ __global__ void __launch_bounds__(512) moe_gate_up_kernel(MoeArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           hv[e] = ((a.epi & SVDQ_EPI_GELU) ? gelu_erf(g[e]) : g[e] / (1.0f + expf(-g[e]))) * u[e];
-        uint4 p[S];
-        split_planes<S>(hv, p);
+        uint4 pl[S];
+        split_planes<S>(hv, pl);
 #pragma unroll
         for (int s = 0; s < S; ++s)
-          *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + list[i]) * a.F + row) = make_uint2(p[s].x, p[s].y);
+          *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + row) = make_uint2(pl[s].x, pl[s].y);
       }
     }
-    __syncthreads();
   }
 }
 
+// Down rows.  One workgroup: 16 output rows of all tokens, 16 waves.  A unit is one column block of
+// the plan and one of KC chunks of K; waves take every sixteenth unit, one pipeline running on from
+// unit to unit, and leave each pair's sums in a place of its own, so the sum over a token's experts
+// has one order.
 constexpr int kDownWaves = 16;
 constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
-constexpr int kDownMaxBlocks = 1024;   // column blocks: at most min(E, P) + P / 5
 
-// One workgroup: 16 output rows of all tokens.  A unit is one block of an expert's pairs (all S
-// planes of up to 16 / S pairs are columns) and one chunk of K; waves take units in turn and
-// leave each pair's sums in a place of its own, so the final sums have one order.
 template <int FMT, int S, bool OUT_F32>
 __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   constexpr int TPB = tokens_per_block(S);
   constexpr int DEPTH = 3;
-  extern __shared__ v4f slot[];                    // [chunk][pair][4]: 16 rows of a pair
-  __shared__ int list[kMoeMaxPairs];
-  __shared__ int first[kMoeMaxE + 1], cursor[kMoeMaxE];
-  __shared__ int blk_e[kDownMaxBlocks], blk_t[kDownMaxBlocks];
-  __shared__ int nblocks;
+  extern __shared__ v4f slot[];                    // [chunk][pair][4]: 16 rows of a pair; then the pairs' weights
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
-  // pairs sorted by expert, and the column blocks
-  for (int e = tid; e < a.E; e += 1024) cursor[e] = 0;
-  __syncthreads();
-  for (int p = tid; p < a.P; p += 1024) {
-    const int id = a.ids[p];
-    if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
-  }
-  __syncthreads();
-  if (w == 0) {
-    int pairs = 0, blocks = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + lane, cnt = e < a.E ? cursor[e] : 0, nb = (cnt + TPB - 1) / TPB;
-      int sp = cnt, sb = nb;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int vp = __shfl_up(sp, o), vb = __shfl_up(sb, o);
-        if (lane >= o) { sp += vp; sb += vb; }
-      }
-      if (e < a.E) {
-        first[e] = pairs + sp - cnt;
-        cursor[e] = first[e];
-        for (int b = 0; b < nb; ++b) {
-          blk_e[blocks + sb - nb + b] = e;
-          blk_t[blocks + sb - nb + b] = b * TPB;
-        }
-      }
-      pairs += __shfl(sp, 63);
-      blocks += __shfl(sb, 63);
-    }
-    if (lane == 0) { first[a.E] = pairs; nblocks = blocks; }
-  }
-  __syncthreads();
-  for (int p = tid; p < a.P; p += 1024) {
-    const int id = a.ids[p];
-    if (id >= 0 && id < a.E) list[atomicAdd(&cursor[id], 1)] = p;
-  }
-  __syncthreads();
-
-  const int KS = a.F / kKStep;
   const int slots = a.P > kDownMinSlots ? a.P : kDownMinSlots;
+  float* const wt = reinterpret_cast<float*>(slot + slots * 4);
+  const int KS = a.F / kKStep;
+  const int nblocks = __builtin_amdgcn_readfirstlane(a.plan[0]);
   // as many chunks of K as it takes to give every wave a unit, where the LDS has room
   int KC = 1;
   while (nblocks * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
-  const int64_t rt = blockIdx.x;
-  for (int u = w; u < nblocks * KC; u += kDownWaves) {
-    const int b = u / KC, kc = u % KC;
-    const int ex = __builtin_amdgcn_readfirstlane(blk_e[b]), t0 = blk_t[b];
-    const int f0 = first[ex] + t0, cnt = first[ex + 1] - f0 < TPB ? first[ex + 1] - f0 : TPB;
-    const int ks0 = kc * KS / KC, n = (kc + 1) * KS / KC - ks0;
-    const uint8_t* blob = a.wd + size_t(ex) * a.blob_d;
-    const W4Rows<FMT> rows(blob + a.d_codes, blob + a.d_scales, a.F, a.Nd_pad);
-    const int t = tl % TPB < cnt ? tl % TPB : cnt - 1, pl = tl / TPB < S ? tl / TPB : S - 1;
-    const int pair = list[f0 + t];
-    const uint16_t* xp = a.h + (int64_t(pl) * a.P + pair) * a.F;
-    struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };
-    auto load = [&](int i, Stage& st) {
-      const int ks = ks0 + (i < n ? i : n - 1);
-      rows.load(uint32_t(rt), ks, i < n, lane, st.w);
+  const int units = nblocks * KC;
+  const int rt = blockIdx.x;
+  const int t = tl % TPB, pl = tl / TPB;
+
+  // a unit as its wave sees it; the plan's words are loaded one unit ahead
+  struct Unit { const uint8_t* blob; int cnt, pair, kc, ks0, n; uint32_t xoff; };
+  auto fetch = [&](int u) -> int {
+    return u < units ? a.plan[kPlanWords * (1 + u / KC) + tl] : 0;
+  };
+  auto open = [&](int u, int words, Unit& d) {
+    d.kc = u % KC;
+    d.cnt = __builtin_amdgcn_readlane(words, 1);
+    d.blob = a.wd + size_t(__builtin_amdgcn_readlane(words, 0)) * a.blob_d;
+    const bool column = pl < S && t < d.cnt;
+    d.pair = __shfl(words, 2 + (t < d.cnt ? t : 0));
+    d.ks0 = d.kc * KS / KC;
+    d.n = u < units ? (d.kc + 1) * KS / KC - d.ks0 : 0;
+    d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + k_of<FMT>(c, 0)) * 2) : kNoColumn;
+  };
+  const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
+  struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };
+  Stage st[DEPTH];
+  int lu = w, li = 0, words = fetch(w);
+  Unit ld, cu;                                             // the unit being loaded, the one being computed
+  auto enter = [&]() {                                     // the load side's next unit
+    open(lu, words, ld);
+    words = fetch(lu + kDownWaves);
+  };
+  auto load = [&](Stage& s) {
+    const bool valid = li < ld.n;
+    const uint32_t ks = uint32_t(ld.ks0 + li);
+    const W4Rows<FMT> rows(ld.blob + a.d_codes, ld.blob + a.d_scales, a.F, a.Nd_pad);
+    rows.load(rt, ks, valid, lane, s.w);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.h, valid ? h_bytes : 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) st.x[0][q] = *reinterpret_cast<const uint4*>(xp + ks * kKStep + k_of<FMT>(c, q));
-    };
-    v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
-    Stage st[DEPTH];
+    for (int q = 0; q < 4; ++q)
+      s.x[0][q] = buffer_load16(r, ld.xoff + (k_of<FMT>(0, q) - k_of<FMT>(0, 0)) * 2, ks * kKStep * 2);
+    if (++li >= ld.n && lu < units) {
+      li = 0;
+      lu += kDownWaves;
+      enter();
+    }
+  };
+  int u = w;
+  const int first_words = words;
+  enter();
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) load(j, st[j]);
-    for (int i0 = 0; i0 < n; i0 += DEPTH) {
+  for (int j = 0; j < DEPTH; ++j) {
+    load(st[j]);
+    keep_order();
+  }
+  // the compute side: the words one unit ahead too, the unit's tensor scale and bias when it opens
+  int cwords = first_words;
+  float gs = 1.0f;
+  uint2 bias = make_uint2(0u, 0u);
+  auto begin = [&]() {
+    open(u, cwords, cu);
+    cwords = fetch(u + kDownWaves);
+    gs = w4_tensor_scale<FMT>(cu.blob + a.d_amax);
+    if (cu.kc == 0 && (a.epi & SVDQ_EPI_BIAS))
+      bias = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(cu.blob + a.d_bias) + rt * 16 + c * 4);
+    else
+      bias = make_uint2(0u, 0u);
+  };
+  begin();
+  // the pairs' weights; a pair without an expert adds zero
+  for (int p = tid; p < a.P; p += 1024) {
+    const int id = a.ids[p];
+    const bool there = id >= 0 && id < a.E;
+    wt[p] = there ? a.weights[p] : 0.0f;
+    if (!there)
+      for (int k = 0; k < KC; ++k)
+        for (int q = 0; q < 4; ++q) slot[(k * a.P + p) * 4 + q] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  int i = 0;
+  v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
+  while (u < units) {
 #pragma unroll
-      for (int j = 0; j < DEPTH; ++j) {
-        if (i0 + j < n) w4_step<FMT, 1>(st[j].w, ks0 + i0 + j, st[j].x, acc);
-        load(i0 + j + DEPTH, st[j]);
+    for (int j = 0; j < DEPTH; ++j) {
+      w4_step<FMT, 1>(st[j].w, cu.ks0 + i, st[j].x, acc);
+      load(st[j]);
+      keep_order();
+      if (u < units && ++i == cu.n) {
+        v4f y = acc[0];
+        if (FMT == kFmtNVFP4) y *= gs;
+        v4f sum = y;                                       // the planes' columns of a pair
+#pragma unroll
+        for (int p = 1; p < S; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] += __shfl(y[e], lane + p * TPB);
+        sum += v4f{bf_lo(bias.x), bf_hi(bias.x), bf_lo(bias.y), bf_hi(bias.y)};
+        if (tl < cu.cnt) slot[(cu.kc * a.P + cu.pair) * 4 + c] = sum;
+        acc[0] = v4f{0.f, 0.f, 0.f, 0.f};
+        i = 0;
+        u += kDownWaves;
+        begin();
       }
     }
-    v4f y = acc[0];
-    if (FMT == kFmtNVFP4) y *= w4_tensor_scale<FMT>(blob + a.d_amax);
-    // the planes' columns of a pair
-    v4f sum = y;
-#pragma unroll
-    for (int i = 1; i < S; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += __shfl(y[e], lane + i * TPB);
-    if (kc == 0 && (a.epi & SVDQ_EPI_BIAS)) {
-      const uint2 bb = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(blob + a.d_bias) + rt * 16 + c * 4);
-      sum += v4f{bf_lo(bb.x), bf_hi(bb.x), bf_lo(bb.y), bf_hi(bb.y)};
-    }
-    if (tl < cnt) slot[(kc * a.P + pair) * 4 + c] = sum;
   }
-  __syncthreads();
-  // Y[m] = sum_j w_j (sum over chunks), j and chunks in order; pairs without an expert add nothing
+  lds_barrier();
+  // Y[m] = sum_j w_j (sum over chunks), j and chunks in order
   const int M = a.P / a.top_k;
-  for (int i = tid; i < M * 4; i += 1024) {
-    const int m = i >> 2, q = i & 3;
+  for (int o = tid; o < M * 4; o += 1024) {
+    const int m = o >> 2, q = o & 3;
     v4f y = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.top_k; ++j) {
-      const int p = m * a.top_k + j, id = a.ids[p];
-      if (id < 0 || id >= a.E) continue;
+      const int p = m * a.top_k + j;
       v4f v = slot[p * 4 + q];
       for (int k = 1; k < KC; ++k) v += slot[(k * a.P + p) * 4 + q];
-      const float wt = a.weights[p];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = fmaf(wt, v[e], y[e]);
+      for (int e = 0; e < 4; ++e) y[e] = fmaf(wt[p], v[e], y[e]);
     }
-    const int64_t o = int64_t(m) * a.ldy + rt * 16 + q * 4;
+    const int64_t at = int64_t(m) * a.ldy + rt * 16 + q * 4;
     if (OUT_F32)
-      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + o) = y;
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + at) = y;
     else
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + o) =
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + at) =
           make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
   }
 }
 
-template <int FMT, int S>
+template <int FMT, int S, int NB>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
-  const int slots = a.E < a.P ? a.E : a.P;
-  const dim3 grid(unsigned(a.F / 16), unsigned(slots));
-  const int avg = (a.P + slots - 1) / slots;
-  if (avg <= 8)
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, 1>), grid, dim3(512), 0, s, a);
+  const dim3 grid(unsigned(a.F / 16 * a.KW / kGateWaves), unsigned(a.slots + 1));
+  if (a.P <= 64)
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, true>), grid, dim3(512), 0, s, a);
   else
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, 2>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, false>), grid, dim3(512), 0, s, a);
 }
 
 template <int FMT>
 static void down(const MoeArgs& a, bool f32, hipStream_t s) {
-  const size_t lds = size_t(a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64;
+  const size_t lds = size_t(a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64 + size_t(a.P) * 4;
   const dim3 grid(unsigned(a.N / 16));
   if (f32)
     hipLaunchKernelGGL((moe_down_kernel<FMT, 3, true>), grid, dim3(1024), lds, s, a);
@@ -598,20 +720,22 @@ static void down(const MoeArgs& a, bool f32, hipStream_t s) {
     hipLaunchKernelGGL((moe_down_kernel<FMT, 2, false>), grid, dim3(1024), lds, s, a);
 }
 
-// Requires 1 <= top_k <= kMoeMaxTopK, 1 <= E <= kMoeMaxE, H % 512 == 0, F % 512 == 0, N % 16 == 0, M >= 1.  h has room for
-// 3 planes of F values for each pair of one part (at most kMoeMaxPairs).
+// Requires 1 <= top_k <= kMoeMaxTopK, 1 <= E <= kMoeMaxE, H % 512 == 0, F % 512 == 0, N % 16 == 0, M >= 1.  ws has room for
+// the plan and 3 planes of F values for each pair of one part (at most kMoeMaxPairs).
 hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int fmt_d, const uint8_t* wd,
                       const WeightLayout& ld, int H, int F, int N, int E, const uint16_t* X, int64_t M, int64_t ldx,
                       const int32_t* ids, const float* weights, int top_k, void* Y, int64_t ldy, uint32_t epi,
-                      void* h, hipStream_t s) {
+                      void* ws, hipStream_t s) {
   MoeArgs a{};
   a.wg = wg; a.blob_g = lg.total; a.g_codes = lg.codes; a.g_scales = lg.scales; a.g_bias = lg.bias; a.g_amax = lg.amax;
   a.wd = wd; a.blob_d = ld.total; a.d_codes = ld.codes; a.d_scales = ld.scales; a.d_bias = ld.bias; a.d_amax = ld.amax;
-  a.h = static_cast<uint16_t*>(h);
+  a.plan = static_cast<int32_t*>(ws);
+  a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kMoePlanBytes);
   a.ldx = ldx; a.ldy = ldy; a.Ng_pad = lg.N_pad; a.Nd_pad = ld.N_pad;
   a.H = H; a.F = F; a.N = N; a.E = E; a.top_k = top_k; a.epi = epi;
   const bool f32 = (epi & SVDQ_EPI_OUT_F32) != 0;
-  const int64_t part = kMoeMaxPairs / top_k;
+  // a part's pairs fit the kernels' LDS and its rows of X one buffer
+  const int64_t span = (int64_t(1) << 31) / (2 * ldx), most = kMoeMaxPairs / top_k, part = span < most ? span : most;
   for (int64_t m0 = 0; m0 < M; m0 += part) {
     const int64_t mc = M - m0 < part ? M - m0 : part;
     a.P = int(mc * top_k);
@@ -619,10 +743,18 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     a.ids = ids + m0 * top_k;
     a.weights = weights + m0 * top_k;
     a.Y = static_cast<uint8_t*>(Y) + m0 * ldy * (f32 ? 4 : 2);
-#define SVDQ_GATE(FMT_)                       \
-  do {                                        \
-    if (f32) gate_up<FMT_, 3>(a, s);          \
-    else gate_up<FMT_, 2>(a, s);              \
+    const int experts = E < a.P ? E : a.P; // that may be asked for
+    const bool two = a.P > 8 * experts;    // more than a block of pairs is usual: two at a time
+    a.slots = experts + a.P / (two ? 32 : 16);
+    const int tiles = experts * (F / 16);
+    a.KW = 1;
+    while (a.KW < kGateWaves && tiles * a.KW < kGateFill) a.KW *= 2;
+#define SVDQ_GATE(FMT_)                                       \
+  do {                                                        \
+    if (f32 && two) gate_up<FMT_, 3, 2>(a, s);                \
+    else if (f32) gate_up<FMT_, 3, 1>(a, s);                  \
+    else if (two) gate_up<FMT_, 2, 2>(a, s);                  \
+    else gate_up<FMT_, 2, 1>(a, s);                           \
   } while (0)
     if (fmt_g == kFmtMXFP4) SVDQ_GATE(kFmtMXFP4);
     else if (fmt_g == kFmtINT4) SVDQ_GATE(kFmtINT4);

@@ -158,7 +158,10 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
   };
   if (n > 0) {
 #pragma unroll
-    for (int j = 0; j < kFewDepth; ++j) load(st[j]);
+    for (int j = 0; j < kFewDepth; ++j) {
+      load(st[j]);
+      keep_order();
+    }
   }
   const float gs = w4_tensor_scale<FMT>(a.wblob + a.w_amax);
   // L1 fragments in batches of U 32-K steps (the wave's: w, w + 8, ...), two batches in flight
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
       for (int u = 0; u < 4; ++u) x[0][u] = *reinterpret_cast<const uint4*>(xp + (ks * kKStep + k_of<FMT>(c, u)) * 2);
       w4_step<FMT, 1>(st[j], ks, x, acc);
       load(st[j]);
+      keep_order();
       if (++i == n) {
         finish(rt, acc[0]);
         acc[0] = zero;
@@ -390,8 +394,13 @@ __global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int 
     uint4 x[XD / 2][2][NB];
     load_w(0, st[0]);
 #pragma unroll
-    for (int q = 0; q < XD; ++q) load_x(0, q, x[q / 2][q % 2]);
+    for (int q = 0; q < XD; ++q) {
+      keep_order();
+      load_x(0, q, x[q / 2][q % 2]);
+    }
+    keep_order();
     load_w(1, st[1]);
+    keep_order();
     // the down projection of the group's tokens (the first part of K adds the low-rank branch);
     // the rows of a group lie one after the other in each partial sum
     const int64_t left = a.M - g * Mg < Mg ? a.M - g * Mg : Mg;
@@ -420,6 +429,7 @@ __global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int 
             w4_half<T, NB>(st[j], half, x[half], acc);
             load_x(i0 + j + 1, half * 2, x[half][0]);
             load_x(i0 + j + 1, half * 2 + 1, x[half][1]);
+            keep_order();
           }
         } else {
 #pragma unroll
@@ -427,9 +437,11 @@ __global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int 
             uint4 (&xs)[NB] = x[u % XD / 2][u % 2];
             w4_mfma<FMT, T, NB>(st[j], ks0 + w + (i0 + j) * W, u, xs, acc);
             load_x(i0 + j + (u + XD) / 4, (u + XD) % 4, xs);
+            keep_order();
           }
         }
         load_w(i0 + j + 2, st[j]);
+        keep_order();
       }
     }
     if (FMT == kFmtNVFP4) {

@@ -82,6 +82,13 @@ struct W4Rows {
   }
 };
 
+// Keeps the loads before it ahead of those after it: a wait for the oldest of a pipeline's loads
+// must not become a wait for all of them.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Workgroup barrier for data in LDS: waits for this wave's LDS operations and not, as a fence
 // would, for its global loads in flight; the empty asm keeps memory accesses from moving across.
 __device__ __forceinline__ void lds_barrier() {
