@@ -320,11 +320,12 @@ struct MoeArgs {
   const uint16_t* X;
   const int32_t* ids;
   const float* weights;
-  uint16_t* h;                         // S x P x F bf16 planes
+  uint16_t* h;                         // S x P x F bf16 planes, each 128 of F in operand order (stored_at)
   int32_t* plan;                       // the down kernel's column blocks (moe_plan)
   void* Y;
   int64_t ldx, ldy, Ng_pad, Nd_pad;
   int H, F, N, E, top_k, P;            // gate/up: H -> 2 F, down: F -> N
+  int d_int4;
   int slots, KW;                       // gate/up: blocks of pairs at most, waves that share a tile's K
   uint32_t epi;
 };
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
-      xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + k_of<FMT>(c, 0)) * 2 : kNoColumn;
+      xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + c * 8) * 2 : kNoColumn;
     }
     auto load = [&](int i, Stage& st) {
       const uint32_t ks = uint32_t(kq + i * KW);
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          st.x[b][u] = buffer_load16(r, xoff[b] + (k_of<FMT>(0, u) - k_of<FMT>(0, 0)) * 2, ks * kKStep * 2);
+          st.x[b][u] = buffer_load16(r, xoff[b] + u * 64, ks * kKStep * 2);
     };
     v4f ag[NB], au[NB];
 #pragma unroll
@@ -512,6 +513,8 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
       for (int j = 0; j < DEPTH; ++j) {
         // past the last step codes and columns are zeros
         const int ks = kq + (i0 + j) * KW;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) to_operands<FMT>(st[j].x[b]);
         w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
         w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
         load(i0 + j + DEPTH, st[j]);
@@ -550,9 +553,11 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
           hv[e] = ((a.epi & SVDQ_EPI_GELU) ? gelu_erf(g[e]) : g[e] / (1.0f + expf(-g[e]))) * u[e];
         uint4 pl[S];
         split_planes<S>(hv, pl);
+        // in the order of the down product's operands
+        const int kk = row & (kKStep - 1), at = row - kk + (a.d_int4 ? stored_at<kFmtINT4>(kk) : stored_at<kFmtMXFP4>(kk));
 #pragma unroll
         for (int s = 0; s < S; ++s)
-          *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + row) = make_uint2(pl[s].x, pl[s].y);
+          *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + at) = make_uint2(pl[s].x, pl[s].y);
       }
     }
   }
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     d.pair = __shfl(words, 2 + (t < d.cnt ? t : 0));
     d.ks0 = d.kc * KS / KC;
     d.n = u < units ? (d.kc + 1) * KS / KC - d.ks0 : 0;
-    d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + k_of<FMT>(c, 0)) * 2) : kNoColumn;
+    d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + c * 8) * 2) : kNoColumn;
   };
   const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
   struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     const __amdgpu_buffer_rsrc_t r = make_rsrc(a.h, valid ? h_bytes : 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      s.x[0][q] = buffer_load16(r, ld.xoff + (k_of<FMT>(0, q) - k_of<FMT>(0, 0)) * 2, ks * kKStep * 2);
+      s.x[0][q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
     if (++li >= ld.n && lu < units) {
       li = 0;
       lu += kDownWaves;
@@ -732,7 +737,7 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
   a.plan = static_cast<int32_t*>(ws);
   a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kMoePlanBytes);
   a.ldx = ldx; a.ldy = ldy; a.Ng_pad = lg.N_pad; a.Nd_pad = ld.N_pad;
-  a.H = H; a.F = F; a.N = N; a.E = E; a.top_k = top_k; a.epi = epi;
+  a.H = H; a.F = F; a.N = N; a.E = E; a.top_k = top_k; a.epi = epi; a.d_int4 = fmt_d == kFmtINT4;
   const bool f32 = (epi & SVDQ_EPI_OUT_F32) != 0;
   // a part's pairs fit the kernels' LDS and its rows of X one buffer
   const int64_t span = (int64_t(1) << 31) / (2 * ldx), most = kMoeMaxPairs / top_k, part = span < most ? span : most;

@@ -33,6 +33,46 @@ __device__ __forceinline__ int k_of(int c, int u) {
   return FMT == kFmtINT4 ? (u >> 1) * 64 + c * 16 + (u & 1) * 8 : c * 32 + u * 8;
 }
 
+// Where those elements lie in a step stored in the order of the operands: MFMA u's four lane
+// groups one after the other, so that a row's piece of one operand is 64 bytes at a stretch.  (At
+// k_of it is four pieces of 16 bytes, and the address unit takes a cycle for each.)
+template <int FMT>
+__device__ __forceinline__ int stored_at(int kk) {           // kk: an element of the step; 8 go together
+  const int c = FMT == kFmtINT4 ? (kk & 63) >> 4 : kk >> 5;
+  const int u = FMT == kFmtINT4 ? ((kk >> 6) << 1) + ((kk >> 3) & 1) : (kk >> 3) & 3;
+  return u * 32 + c * 8 + (kk & 7);
+}
+
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {   // a's upper half of lanes with b's lower
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {   // a's odd rows of 16 lanes with b's even rows
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap32(uint4& a, uint4& b) {
+  swap32(a.x, b.x); swap32(a.y, b.y); swap32(a.z, b.z); swap32(a.w, b.w);
+}
+__device__ __forceinline__ void swap16(uint4& a, uint4& b) {
+  swap16(a.x, b.x); swap16(a.y, b.y); swap16(a.z, b.z); swap16(a.w, b.w);
+}
+
+// A step of a row loaded in its natural order, x[v] of lane group c the elements 32 v + 8 c .. + 7
+// (64 bytes of a row at a time), to the MFMAs' operands: x[u] the elements k_of(c, u) .. + 7.
+template <int FMT>
+__device__ __forceinline__ void to_operands(uint4 (&x)[4]) {
+  if (FMT == kFmtINT4) {
+    swap32(x[0], x[1]); swap16(x[0], x[1]);
+    swap32(x[2], x[3]); swap16(x[2], x[3]);
+  } else {                                                   // a 4 x 4 transpose of registers and lane groups
+    swap32(x[0], x[2]); swap32(x[1], x[3]);
+    swap16(x[0], x[1]); swap16(x[2], x[3]);
+  }
+}
+
 // Codes and scales of one 16-row tile and 128-K step, as one lane holds them.
 template <int FMT>
 struct W4Stage {
