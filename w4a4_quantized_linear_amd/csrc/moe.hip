@@ -389,10 +389,12 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* bas
 // The grid's last row (blockIdx.y == slots) holds one workgroup that writes the down kernel's plan.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
+constexpr int kGateXLds = 49152;       // beside 20 KiB, two workgroups a CU
 template <int FMT, int S, int NB, bool SMALL>
 __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeArgs a) {
   constexpr int DEPTH = NB == 1 && FMT != kFmtINT4 ? 3 : 2;   // registers for two workgroups a CU
   constexpr int COLS = 16 * NB;
+  extern __shared__ uint4 xlds[];                          // kGateXLds bytes
   __shared__ v4f red[kGateWaves][2][NB][64];
   __shared__ int list[COLS];
   __shared__ int cursor[kMoeMaxE], base[kMoeMaxE];
@@ -480,45 +482,88 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
   const W4Rows<FMT> rows(blob + a.g_codes, blob + a.g_scales, a.H, a.Ng_pad);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, uint32_t((int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2));
   const float gs = w4_tensor_scale<FMT>(blob + a.g_amax);
-  struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
   {
-    uint32_t xoff[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
-      xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + c * 8) * 2 : kNoColumn;
-    }
-    auto load = [&](int i, Stage& st) {
-      const uint32_t ks = uint32_t(kq + i * KW);
-      rows.load(ft, ks, i < n, lane, st.g);
-      rows.load(FT + ft, ks, i < n, lane, st.u);
-      const __amdgpu_buffer_rsrc_t r = i < n ? rx : make_rsrc(a.X, 0);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st.x[b][u] = buffer_load16(r, xoff[b] + u * 64, ks * kKStep * 2);
-    };
     v4f ag[NB], au[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) ag[b] = au[b] = v4f{0.f, 0.f, 0.f, 0.f};
-    Stage st[DEPTH];
+    auto load_w = [&](int i, W4Stage<FMT>& g, W4Stage<FMT>& u) {
+      const uint32_t ks = uint32_t(kq + i * KW);
+      rows.load(ft, ks, i < n, lane, g);
+      rows.load(FT + ft, ks, i < n, lane, u);
+    };
+    const int row_b = few_row_bytes(a.H);
+    if (T * row_b <= kGateXLds) {
+      // few pairs: their rows of X once into LDS.  A load of a step's columns costs the L1 as many
+      // cycles whatever the number of columns that are there.
+      constexpr int AHEAD = FMT == kFmtINT4 ? 3 : 4;
+      W4Stage<FMT> sg[AHEAD], su[AHEAD];
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) {
-      load(j, st[j]);
-      keep_order();
-    }
-    for (int i0 = 0; i0 < n; i0 += DEPTH) {
+      for (int j = 0; j < AHEAD; ++j) {
+        load_w(j, sg[j], su[j]);
+        keep_order();
+      }
+      uint8_t* const xl = reinterpret_cast<uint8_t*>(xlds);
+      for (int r = 0; r < T; ++r) {
+        const int p = pair_of(r);
+        const uint16_t* const src = a.X + int64_t(p / a.top_k) * a.ldx;
+        for (int k = tid * 8; k < a.H; k += 512 * 8)
+          *reinterpret_cast<uint4*>(xl + r * row_b + k * 2) = *reinterpret_cast<const uint4*>(src + k);
+      }
+      lds_barrier();
+      const uint8_t* xp[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xp[b] = xl + (b * 16 + tl < T ? b * 16 + tl : T - 1) * row_b;
+      for (int i0 = 0; i0 < n; i0 += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int ks = kq + (i0 + j < n ? i0 + j : n - 1) * KW;   // past the last step: codes are zeros
+          uint4 x[NB][4];
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              x[b][u] = *reinterpret_cast<const uint4*>(xp[b] + (ks * kKStep + k_of<FMT>(c, u)) * 2);
+          w4_step<FMT, NB>(sg[j], ks, x, ag);
+          w4_step<FMT, NB>(su[j], ks, x, au);
+          load_w(i0 + j + AHEAD, sg[j], su[j]);
+          keep_order();
+        }
+      }
+    } else {
+      uint32_t xoff[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
+        xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + c * 8) * 2 : kNoColumn;
+      }
+      struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
+      auto load = [&](int i, Stage& st) {
+        load_w(i, st.g, st.u);
+        const __amdgpu_buffer_rsrc_t r = i < n ? rx : make_rsrc(a.X, 0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            st.x[b][u] = buffer_load16(r, xoff[b] + u * 64, uint32_t(kq + i * KW) * kKStep * 2);
+      };
+      Stage st[DEPTH];
 #pragma unroll
       for (int j = 0; j < DEPTH; ++j) {
-        // past the last step codes and columns are zeros
-        const int ks = kq + (i0 + j) * KW;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) to_operands<FMT>(st[j].x[b]);
-        w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
-        w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
-        load(i0 + j + DEPTH, st[j]);
+        load(j, st[j]);
         keep_order();
+      }
+      for (int i0 = 0; i0 < n; i0 += DEPTH) {
+#pragma unroll
+        for (int j = 0; j < DEPTH; ++j) {
+          // past the last step codes and columns are zeros
+          const int ks = kq + (i0 + j) * KW;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) to_operands<FMT>(st[j].x[b]);
+          w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
+          w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
+          load(i0 + j + DEPTH, st[j]);
+          keep_order();
+        }
       }
     }
     if (KW > 1) {
@@ -568,13 +613,14 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
 // unit to unit, and leave each pair's sums in a place of its own, so the sum over a token's experts
 // has one order.
 constexpr int kDownWaves = 16;
+constexpr int64_t kDownLds = 163840;   // HL: all of h in LDS where it fits (one workgroup a CU)
 constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
 
-template <int FMT, int S, bool OUT_F32>
+template <int FMT, int S, bool HL>
 __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   constexpr int TPB = tokens_per_block(S);
-  constexpr int DEPTH = 3;
-  extern __shared__ v4f slot[];                    // [chunk][pair][4]: 16 rows of a pair; then the pairs' weights
+  constexpr int DEPTH = HL ? 5 : 3;
+  extern __shared__ v4f slot[];                    // [chunk][pair][4]: 16 rows of a pair; the pairs' weights; HL: h
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
@@ -590,7 +636,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   const int t = tl % TPB, pl = tl / TPB;
 
   // a unit as its wave sees it; the plan's words are loaded one unit ahead
-  struct Unit { const uint8_t* blob; int cnt, pair, kc, ks0, n; uint32_t xoff; };
+  struct Unit { const uint8_t* blob; int cnt, pair, kc, ks0, n, row; uint32_t xoff; };
   auto fetch = [&](int u) -> int {
     return u < units ? a.plan[kPlanWords * (1 + u / KC) + tl] : 0;
   };
@@ -600,13 +646,16 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     d.blob = a.wd + size_t(__builtin_amdgcn_readlane(words, 0)) * a.blob_d;
     const bool column = pl < S && t < d.cnt;
     d.pair = __shfl(words, 2 + (t < d.cnt ? t : 0));
+    d.row = column ? pl * a.P + d.pair : 0;                // HL: any row where there is no column
     d.ks0 = d.kc * KS / KC;
     d.n = u < units ? (d.kc + 1) * KS / KC - d.ks0 : 0;
     d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + c * 8) * 2) : kNoColumn;
   };
   const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
-  struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };
+  struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };                 // x unused with HL
   Stage st[DEPTH];
+  uint8_t* const hl = reinterpret_cast<uint8_t*>(wt + (a.P + 3) / 4 * 4);
+  const int row_b = few_row_bytes(a.F);
   int lu = w, li = 0, words = fetch(w);
   Unit ld, cu;                                             // the unit being loaded, the one being computed
   auto enter = [&]() {                                     // the load side's next unit
@@ -618,10 +667,11 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     const uint32_t ks = uint32_t(ld.ks0 + li);
     const W4Rows<FMT> rows(ld.blob + a.d_codes, ld.blob + a.d_scales, a.F, a.Nd_pad);
     rows.load(rt, ks, valid, lane, s.w);
-    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.h, valid ? h_bytes : 0);
+    if constexpr (!HL) {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(a.h, valid ? h_bytes : 0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      s.x[0][q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
+      for (int q = 0; q < 4; ++q) s.x[0][q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
+    }
     if (++li >= ld.n && lu < units) {
       li = 0;
       lu += kDownWaves;
@@ -650,6 +700,11 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       bias = make_uint2(0u, 0u);
   };
   begin();
+  if constexpr (HL) {
+    const int per = a.F / 8;                               // 16-byte pieces of a row
+    for (int i = tid; i < S * a.P * per; i += 1024)
+      *reinterpret_cast<uint4*>(hl + i / per * row_b + i % per * 16) = reinterpret_cast<const uint4*>(a.h)[i];
+  }
   // the pairs' weights; a pair without an expert adds zero
   for (int p = tid; p < a.P; p += 1024) {
     const int id = a.ids[p];
@@ -659,12 +714,22 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       for (int k = 0; k < KC; ++k)
         for (int q = 0; q < 4; ++q) slot[(k * a.P + p) * 4 + q] = v4f{0.f, 0.f, 0.f, 0.f};
   }
+  if (HL) lds_barrier();
   int i = 0;
   v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
   while (u < units) {
 #pragma unroll
     for (int j = 0; j < DEPTH; ++j) {
-      w4_step<FMT, 1>(st[j].w, cu.ks0 + i, st[j].x, acc);
+      if constexpr (HL) {
+        uint4 x[1][4];
+        const int at = cu.ks0 + i < KS ? cu.ks0 + i : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          x[0][q] = *reinterpret_cast<const uint4*>(hl + cu.row * row_b + (at * kKStep + q * 32 + c * 8) * 2);
+        w4_step<FMT, 1>(st[j].w, cu.ks0 + i, x, acc);
+      } else {
+        w4_step<FMT, 1>(st[j].w, cu.ks0 + i, st[j].x, acc);
+      }
       load(st[j]);
       keep_order();
       if (u < units && ++i == cu.n) {
@@ -698,7 +763,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       for (int e = 0; e < 4; ++e) y[e] = fmaf(wt[p], v[e], y[e]);
     }
     const int64_t at = int64_t(m) * a.ldy + rt * 16 + q * 4;
-    if (OUT_F32)
+    if (S == 3)                                            // three planes: float32 output
       *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + at) = y;
     else
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + at) =
@@ -710,19 +775,20 @@ template <int FMT, int S, int NB>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
   const dim3 grid(unsigned(a.F / 16 * a.KW / kGateWaves), unsigned(a.slots + 1));
   if (a.P <= 64)
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, true>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, true>), grid, dim3(512), kGateXLds, s, a);
   else
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, false>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, false>), grid, dim3(512), kGateXLds, s, a);
 }
 
-template <int FMT>
-static void down(const MoeArgs& a, bool f32, hipStream_t s) {
-  const size_t lds = size_t(a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64 + size_t(a.P) * 4;
+template <int FMT, int S>
+static void down(const MoeArgs& a, hipStream_t s) {
+  const int64_t sums = (a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64 + int64_t(a.P + 3) / 4 * 16;
+  const int64_t all = sums + int64_t(S) * a.P * few_row_bytes(a.F);
   const dim3 grid(unsigned(a.N / 16));
-  if (f32)
-    hipLaunchKernelGGL((moe_down_kernel<FMT, 3, true>), grid, dim3(1024), lds, s, a);
+  if (all <= kDownLds)
+    hipLaunchKernelGGL((moe_down_kernel<FMT, S, true>), grid, dim3(1024), size_t(all), s, a);
   else
-    hipLaunchKernelGGL((moe_down_kernel<FMT, 2, false>), grid, dim3(1024), lds, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<FMT, S, false>), grid, dim3(1024), size_t(sums), s, a);
 }
 
 // Requires 1 <= top_k <= kMoeMaxTopK, 1 <= E <= kMoeMaxE, H % 512 == 0, F % 512 == 0, N % 16 == 0, M >= 1.  ws has room for
@@ -767,9 +833,15 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
 #undef SVDQ_GATE
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (fmt_d == kFmtMXFP4) down<kFmtMXFP4>(a, f32, s);
-    else if (fmt_d == kFmtINT4) down<kFmtINT4>(a, f32, s);
-    else down<kFmtNVFP4>(a, f32, s);
+#define SVDQ_DOWN(FMT_)             \
+  do {                              \
+    if (f32) down<FMT_, 3>(a, s);   \
+    else down<FMT_, 2>(a, s);       \
+  } while (0)
+    if (fmt_d == kFmtMXFP4) SVDQ_DOWN(kFmtMXFP4);
+    else if (fmt_d == kFmtINT4) SVDQ_DOWN(kFmtINT4);
+    else SVDQ_DOWN(kFmtNVFP4);
+#undef SVDQ_DOWN
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
