@@ -161,7 +161,10 @@ MOE = [(1, 1, 1, 512, 512, 16, "mxfp4", "mxfp4", 0), (1, 4, 9, 1024, 512, 528, "
        (1, 8, 16, 512, 1024, 272, "nvfp4", "nvfp4", 0), (5, 3, 4, 1536, 512, 144, "int4", "mxfp4", 0),
        (9, 2, 2, 512, 512, 256, "mxfp4", "nvfp4", 0), (33, 4, 6, 512, 512, 96, "nvfp4", "int4", 9),
        (64, 6, 40, 512, 512, 64, "mxfp4", "mxfp4", 0), (70, 1, 1, 512, 1024, 48, "int4", "nvfp4", 0),
-       (3, 32, 64, 512, 512, 32, "mxfp4", "int4", 0)]
+       (3, 32, 64, 512, 512, 32, "mxfp4", "int4", 0),
+       # pairs' products through memory (many pairs): N that ends inside a 32-row tile, every format
+       (200, 10, 10, 512, 512, 16, "mxfp4", "mxfp4", 0), (220, 10, 11, 512, 512, 80, "int4", "int4", 0),
+       (210, 10, 12, 512, 512, 48, "nvfp4", "nvfp4", 4)]
 
 
 @pytest.mark.parametrize("case", MOE, ids=["-".join(map(str, c)) for c in MOE])
@@ -172,6 +175,54 @@ def test_experts(torch_dev, case):
     ids, wt = mix.route(M, k, skew)
     X = _bits(mix.rng.standard_normal((M, H)))
     mix.check(torch, dev, X, ids, wt, f"moe {case}", gelu=M % 2 == 0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
+@pytest.mark.parametrize("M,k,E,H,Fh,N", [(12, 4, 36, 512, 2048, 4144), (24, 8, 40, 1536, 2048, 4096),
+                                           (6, 5, 24, 4096, 512, 512)])
+def test_experts_large(torch_dev, fmt, M, k, E, H, Fh, N):
+    """Sizes that take the other forms (pairs' products through memory for at most 64 pairs and for
+    more, few rows in LDS and many), against float64 on the GPU from the packed weights' own codes
+    and scales."""
+    torch, dev = torch_dev
+    g = torch.Generator(device=dev)
+    g.manual_seed(M)
+    gu, dn = sq.Layer(fmt, H, 2 * Fh, 0), sq.Layer(fmt, Fh, N, 0)
+    packed, deq = [], []
+    for layer in (gu, dn):
+        R = torch.randn((E, layer.N, layer.K), generator=g, device=dev) * layer.K ** -0.5
+        packed.append(sq.pack_experts(layer, R))
+        deq.append([])
+        for e in range(E):
+            u = sq.unpack_weight(layer, packed[-1][e])
+            c = torch.stack([u["codes"] & 15, u["codes"] >> 4], 2).reshape(layer.N, layer.K).long()
+            if fmt == "int4":
+                v, s = ((c ^ 8) - 8).double(), u["scales"].view(torch.float16).double()
+            else:
+                t = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64,
+                                 device=dev)
+                v = t[c]
+                s = torch.exp2(u["scales"].double() - 127) if fmt == "mxfp4" else \
+                    u["scales"].view(torch.float8_e4m3fn).double() * (R[e].abs().amax() / 2688).double()
+            deq[-1].append(v * s.repeat_interleave(layer.group, 1))
+        del R
+    ids = torch.rand((M, E), generator=g, device=dev).topk(k, 1)[1].int()
+    wt = torch.rand((M, k), generator=g, device=dev)
+    X = torch.randn((M, H), generator=g, device=dev).bfloat16()
+    y = sq.moe(gu, packed[0], dn, packed[1], X, ids, wt, sq.EPI_OUT_F32).double()
+    yb = sq.moe(gu, packed[0], dn, packed[1], X, ids, wt).double()
+    want, size = torch.zeros((M, N), dtype=torch.float64, device=dev), torch.zeros((M, 1), dtype=torch.float64, device=dev)
+    for m in range(M):
+        for j in range(k):
+            e = int(ids[m, j])
+            z = deq[0][e] @ X[m].double()
+            h = z[:Fh] * torch.sigmoid(z[:Fh]) * z[Fh:]
+            want[m] += wt[m, j].double() * (deq[1][e] @ h)
+            size[m] += wt[m, j].double() * h.abs().norm() * deq[1][e].norm(dim=1).max()
+    # an error of 2^-17 of the products' size (Cauchy-Schwarz) would be 2^-24 for each of 128
+    # roundings in a row; bf16 output rounds once more
+    assert bool(((y - want).abs() <= 2.0 ** -17 * size).all())
+    assert bool(((yb - want).abs() <= 2.0 ** -16 * size + 2.0 ** -8 * want.abs()).all())
 
 
 def test_experts_without_bias_in_parts_and_odd_choices(torch_dev):

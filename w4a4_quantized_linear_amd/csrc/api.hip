@@ -123,11 +123,6 @@ bool valid_moe_shape(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64
   return check_shape(dg) == SVDQ_OK && check_shape(dd) == SVDQ_OK && dg->N == 2 * dd->K && M >= 0 && M <= kMaxRows &&
          top_k >= 1 && top_k <= kMoeMaxTopK;
 }
-size_t moe_bytes(const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
-  const int64_t pairs = M * top_k < kMoeMaxPairs ? M * top_k : kMoeMaxPairs;
-  return kMoePlanBytes + align256(size_t(pairs > 0 ? pairs : 1) * dd->K * 6);
-}
-
 svdq_status check_act_args(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,
                            const void* a_packed) {
   if (!d || !w_packed || !a_packed || (M > 0 && !X)) return SVDQ_ERR_NULL;
@@ -357,7 +352,7 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
 
 size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
   if (!dg || !dd || !valid_moe_shape(dg, dd, M, top_k)) return 0;
-  return moe_bytes(dd, M, top_k);
+  return moe_workspace(M, top_k, dd->K, dd->N);
 }
 
 svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svdq_layer_desc* dd,
@@ -376,7 +371,7 @@ svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svd
   if (!aligned(wg_packed, 256) || !aligned(wd_packed, 256) || !aligned(workspace, 256) || !aligned(X, 16) ||
       !aligned(Y, 16) || !aligned(ids, 4) || !aligned(weights, 4) || ldx % 8 != 0 || ldy % 8 != 0)
     return SVDQ_ERR_ALIGN;
-  if (ws_bytes < moe_bytes(dd, M, top_k)) return SVDQ_ERR_WORKSPACE;
+  if (ws_bytes < moe_workspace(M, top_k, dd->K, dd->N)) return SVDQ_ERR_WORKSPACE;
   if ((s = device_check()) != SVDQ_OK) return s;
   if (M == 0) return SVDQ_OK;
   const WeightLayout lg = weight_layout(dg->fmt, dg->K, dg->N, 0), ld = weight_layout(dd->fmt, dd->K, dd->N, 0);

@@ -76,6 +76,29 @@ constexpr uint32_t kDivSlowBit = 2;    // weight flags: the two-operation divisi
 __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 __host__ __device__ inline size_t align256(size_t a) { return (a + 255) & ~size_t(255); }
 
+// svdq_moe's down product.  One kernel whose workgroups each take 16 rows of all tokens and add a
+// token's pairs in LDS, or (moe_by_pairs) pairs' products to memory and a kernel that adds them:
+// the first is bound by its L1, about 170 cycles for each column block and 128 of F, in N / 16
+// workgroups over 256 CUs; the second shares a block's columns between two row tiles and fills the
+// GPU whatever N is, for a launch more and the products' way through memory.
+constexpr int64_t kMoeDownSteps = 600;     // steps a CU (48 us) from which the second is taken
+__host__ __device__ inline bool moe_by_pairs(int64_t experts, int64_t pairs, int F, int N) {
+  return (experts + pairs / 8) * (F / kKStep) * ((N / 16 + 255) / 256) > kMoeDownSteps;
+}
+__host__ __device__ inline int64_t moe_part_pairs(int64_t M, int top_k) {
+  const int64_t pairs = M * top_k;
+  return pairs < 1 ? 1 : pairs < kMoeMaxPairs ? pairs : kMoeMaxPairs;
+}
+__host__ __device__ inline size_t moe_h_bytes(int64_t M, int top_k, int F) {
+  return align256(size_t(moe_part_pairs(M, top_k)) * F * 6);
+}
+// The plan, h's planes and, where any number of experts up to the pairs' may need them, the products.
+__host__ __device__ inline size_t moe_workspace(int64_t M, int top_k, int F, int N) {
+  const int64_t pairs = moe_part_pairs(M, top_k);
+  const bool by_pairs = moe_by_pairs(pairs < kMoeMaxE ? pairs : kMoeMaxE, pairs, F, N);
+  return kMoePlanBytes + moe_h_bytes(M, top_k, F) + (by_pairs ? align256(size_t(pairs) * N * 4) : 0);
+}
+
 // svdq_linear_w4a16: which form a call takes.  Few tokens (`few`): one kernel that holds
 // x_hat's S planes of all tokens in LDS beside the down projection's sums, when the columns of
 // one 16-column MFMA hold them and they fit; it forms the down projection itself (`own_d`) for

@@ -322,6 +322,7 @@ struct MoeArgs {
   const float* weights;
   uint16_t* h;                         // S x P x F bf16 planes, each 128 of F in operand order (stored_at)
   int32_t* plan;                       // the down kernel's column blocks (moe_plan)
+  float* o;                            // P x N: the pairs' down products (long calls)
   void* Y;
   int64_t ldx, ldy, Ng_pad, Nd_pad;
   int H, F, N, E, top_k, P;            // gate/up: H -> 2 F, down: F -> N
@@ -381,29 +382,84 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* bas
   }
 }
 
-// Gate and up rows.  The workgroup takes 8 / KW tiles (16 gate and the same 16 up rows) and the
-// blockIdx.y-th block of pairs: up to 16 NB pairs of one expert, experts in order.  KW waves share
-// a tile's K (every KW-th 128-K step each); KW is the smallest that fills the GPU, since with few
-// there is little exchange and a wave streams long runs of codes.
+// Rows in LDS (S planes x n rows of K bf16, row_b bytes apart) to fp16, in place, scaled by
+// f16_row_scale of each row's largest magnitude, whose bits go to top[0 .. n): the planes' sum becomes
+// fp16 hi (+ lo).  One wave takes a row.  The rows are written before; the caller's barrier follows.
+template <int S, int WAVES>
+__device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n, uint32_t* top) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  lds_barrier();
+  for (int r = w; r < n; r += WAVES) {
+    uint32_t m = 0;
+    for (int k = lane * 8; k < K; k += 512) {
+      const uint4 q = *reinterpret_cast<const uint4*>(xl + r * row_b + k * 2);
+      const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t hi = d[i] & 0x7FFF0000u, lo = (d[i] << 16) & 0x7FFF0000u;
+        m = hi > m ? hi : m;
+        m = lo > m ? lo : m;
+      }
+    }
+    m = wave_max(m);
+    if (lane == 0) top[r] = m;
+    const float s = f16_row_scale(__uint_as_float(m));
+    for (int k = lane * 8; k < K; k += 512) {
+      float v[8];
+      unpack_bf8(*reinterpret_cast<const uint4*>(xl + r * row_b + k * 2), v);
+#pragma unroll
+      for (int p = 1; p < S; ++p) {
+        float l[8];
+        unpack_bf8(*reinterpret_cast<const uint4*>(xl + (p * n + r) * row_b + k * 2), l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += l[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= s;
+#pragma unroll
+      for (int p = 0; p < S; ++p) {
+        const uint4 h = to_f16(v);
+        *reinterpret_cast<uint4*>(xl + (p * n + r) * row_b + k * 2) = h;
+        float b[8];
+        unpack_h8(h, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] -= b[e];
+      }
+    }
+  }
+}
+
+// Rows of one expert for a block of its pairs: the gate and up rows (a tile is 16 gate and the same
+// 16 up rows), or, DOWN, down rows of long calls (a tile is 32 rows, and a pair's sums go to memory,
+// where moe_join_kernel adds a token's pairs).
+// The workgroup takes 8 / KW tiles and the blockIdx.y-th block: up to 16 NB pairs (DOWN: 16 / S, all
+// their planes being columns), experts in order.  KW waves share a tile's K (every KW-th 128-K step
+// each); KW is the smallest that fills the GPU, since with few there is little exchange and a wave
+// streams long runs of codes.
 // SMALL (at most 64 pairs): every wave finds its block by ballots, no barrier.
-// The grid's last row (blockIdx.y == slots) holds one workgroup that writes the down kernel's plan.
+// The gate/up grid's last row (blockIdx.y == slots) holds one workgroup that writes the plan of
+// moe_down_kernel.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
 constexpr int kGateXLds = 49152;       // beside 20 KiB, two workgroups a CU
-template <int FMT, int S, int NB, bool SMALL>
-__global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeArgs a) {
+template <int FMT, int S, int NB, bool SMALL, bool DOWN>
+__global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs a) {
+  static_assert(!DOWN || NB == 1, "a block of down columns holds all planes");
   constexpr int DEPTH = NB == 1 && FMT != kFmtINT4 ? 3 : 2;   // registers for two workgroups a CU
-  constexpr int COLS = 16 * NB;
+  constexpr int TPB = tokens_per_block(S);
+  constexpr int COLS = DOWN ? TPB : 16 * NB;
   extern __shared__ uint4 xlds[];                          // kGateXLds bytes
   __shared__ v4f red[kGateWaves][2][NB][64];
   __shared__ int list[COLS];
   __shared__ int cursor[kMoeMaxE], base[kMoeMaxE];
   __shared__ int found[kGateWaves];
+  constexpr bool F16 = FMT == kFmtNVFP4;                   // rows in LDS become fp16
+  __shared__ uint32_t top[COLS];
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
   const int slot = blockIdx.y;
-  if (slot == a.slots) {
+  if (!DOWN && slot == a.slots) {
     if (blockIdx.x == 0) moe_plan<S, 512>(a, cursor, base);
     return;
   }
@@ -475,24 +531,30 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
   ex = __builtin_amdgcn_readfirstlane(ex);
   auto pair_of = [&](int i) { return SMALL ? __shfl(mine, i) : list[i]; };
 
-  const uint8_t* blob = a.wg + size_t(ex) * a.blob_g;
-  const int KS = a.H / kKStep, FT = a.F / 16, KW = a.KW, kq = w % KW;
+  const uint8_t* const blob = DOWN ? a.wd + size_t(ex) * a.blob_d : a.wg + size_t(ex) * a.blob_g;
+  const int K = DOWN ? a.F : a.H, KS = K / kKStep, KW = a.KW, kq = w % KW;
   const int ft = blockIdx.x * (kGateWaves / KW) + w / KW;
-  const int n = KS > kq ? (KS - kq + KW - 1) / KW : 0;
-  const W4Rows<FMT> rows(blob + a.g_codes, blob + a.g_scales, a.H, a.Ng_pad);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, uint32_t((int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2));
-  const float gs = w4_tensor_scale<FMT>(blob + a.g_amax);
+  const bool there = !DOWN || ft * 32 < a.N;               // the last workgroup may have tiles too many
+  const int rt0 = DOWN ? ft * 2 : ft, rt1 = DOWN ? ft * 2 + 1 : a.F / 16 + ft;
+  const int n = there && KS > kq ? (KS - kq + KW - 1) / KW : 0;
+  const W4Rows<FMT> rows(blob + (DOWN ? a.d_codes : a.g_codes), blob + (DOWN ? a.d_scales : a.g_scales), K,
+                         DOWN ? a.Nd_pad : a.Ng_pad);
+  const uint16_t* const xbase = DOWN ? a.h : a.X;
+  const uint32_t xbytes = uint32_t((DOWN ? int64_t(S) * a.P * a.F : int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2);
+  const float gs = w4_tensor_scale<FMT>(blob + (DOWN ? a.d_amax : a.g_amax));
+  // column b * 16 + tl: element offset of its row of X (of h), or no pair
+  auto row_of = [&](int p, int plane) -> int64_t { return DOWN ? (int64_t(plane) * a.P + p) * a.F : int64_t(p / a.top_k) * a.ldx; };
   {
     v4f ag[NB], au[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) ag[b] = au[b] = v4f{0.f, 0.f, 0.f, 0.f};
     auto load_w = [&](int i, W4Stage<FMT>& g, W4Stage<FMT>& u) {
       const uint32_t ks = uint32_t(kq + i * KW);
-      rows.load(ft, ks, i < n, lane, g);
-      rows.load(FT + ft, ks, i < n, lane, u);
+      rows.load(rt0, ks, i < n, lane, g);
+      rows.load(rt1, ks, i < n, lane, u);
     };
-    const int row_b = few_row_bytes(a.H);
-    if (T * row_b <= kGateXLds) {
+    const int row_b = few_row_bytes(K), xrows = DOWN ? S * T : T;
+    if (xrows * row_b <= kGateXLds) {
       // few pairs: their rows of X once into LDS.  A load of a step's columns costs the L1 as many
       // cycles whatever the number of columns that are there.
       constexpr int AHEAD = FMT == kFmtINT4 ? 3 : 4;
@@ -503,16 +565,19 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
         keep_order();
       }
       uint8_t* const xl = reinterpret_cast<uint8_t*>(xlds);
-      for (int r = 0; r < T; ++r) {
-        const int p = pair_of(r);
-        const uint16_t* const src = a.X + int64_t(p / a.top_k) * a.ldx;
-        for (int k = tid * 8; k < a.H; k += 512 * 8)
+      for (int r = 0; r < xrows; ++r) {
+        const uint16_t* const src = xbase + row_of(pair_of(DOWN ? r % T : r), DOWN ? r / T : 0);
+        for (int k = tid * 8; k < K; k += 512 * 8)
           *reinterpret_cast<uint4*>(xl + r * row_b + k * 2) = *reinterpret_cast<const uint4*>(src + k);
       }
+      if constexpr (F16) rows_to_f16<DOWN ? S : 1, kGateWaves>(xl, row_b, K, T, top);
       lds_barrier();
       const uint8_t* xp[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xp[b] = xl + (b * 16 + tl < T ? b * 16 + tl : T - 1) * row_b;
+      for (int b = 0; b < NB; ++b) {
+        const int i = b * 16 + tl, t = tl % TPB, pl = tl / TPB;
+        xp[b] = xl + (DOWN ? (pl < S && t < T ? pl * T + t : 0) : i < T ? i : T - 1) * row_b;
+      }
       for (int i0 = 0; i0 < n; i0 += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
@@ -522,24 +587,34 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              x[b][u] = *reinterpret_cast<const uint4*>(xp[b] + (ks * kKStep + k_of<FMT>(c, u)) * 2);
-          w4_step<FMT, NB>(sg[j], ks, x, ag);
-          w4_step<FMT, NB>(su[j], ks, x, au);
+              x[b][u] = *reinterpret_cast<const uint4*>(xp[b] + (ks * kKStep + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
+          w4_step<FMT, NB, F16>(sg[j], ks, x, ag);
+          w4_step<FMT, NB, F16>(su[j], ks, x, au);
           load_w(i0 + j + AHEAD, sg[j], su[j]);
           keep_order();
+        }
+      }
+      if constexpr (F16) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int i = DOWN ? tl % TPB : b * 16 + tl;
+          const float back = 1.0f / f16_row_scale(__uint_as_float(top[i < T ? i : 0]));   // a power of two
+          ag[b] *= back;
+          au[b] *= back;
         }
       }
     } else {
       uint32_t xoff[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
-        xoff[b] = i < T ? uint32_t(p / a.top_k * a.ldx + c * 8) * 2 : kNoColumn;
+        const int i = DOWN ? tl % TPB : b * 16 + tl, plane = DOWN ? tl / TPB : 0;
+        const int p = pair_of(i < T ? i : 0);
+        xoff[b] = i < T && plane < S ? uint32_t(row_of(p, plane) + c * 8) * 2 : kNoColumn;
       }
       struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
       auto load = [&](int i, Stage& st) {
         load_w(i, st.g, st.u);
-        const __amdgpu_buffer_rsrc_t r = i < n ? rx : make_rsrc(a.X, 0);
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(xbase, i < n ? xbytes : 0);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -558,7 +633,8 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
           // past the last step codes and columns are zeros
           const int ks = kq + (i0 + j) * KW;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) to_operands<FMT>(st[j].x[b]);
+          for (int b = 0; b < NB; ++b)
+            if (!DOWN) to_operands<FMT>(st[j].x[b]);       // h is stored as operands
           w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
           w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
           load(i0 + j + DEPTH, st[j]);
@@ -574,7 +650,34 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
       }
       lds_barrier();
     }
-    if (kq == 0) {
+    if constexpr (DOWN) {
+      if (kq == 0) {
+        v4f y[2] = {ag[0], au[0]};
+#pragma unroll
+        for (int v = 1; v < kGateWaves; ++v)
+          if (v < KW) {
+            y[0] += red[w + v][0][0][lane];
+            y[1] += red[w + v][1][0][lane];
+          }
+        const int p = pair_of(tl < T ? tl : 0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          v4f sum = y[q];                                  // the planes' columns of a pair
+#pragma unroll
+          for (int i = 1; i < S; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += __shfl(y[q][e], lane + i * TPB);
+          const int row = ft * 32 + q * 16 + c * 4;
+          if (tl >= T || row >= a.N) continue;
+          if (FMT == kFmtNVFP4) sum *= gs;
+          if (a.epi & SVDQ_EPI_BIAS) {
+            const uint2 bd = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(blob + a.d_bias) + row);
+            sum += v4f{bf_lo(bd.x), bf_hi(bd.x), bf_lo(bd.y), bf_hi(bd.y)};
+          }
+          *reinterpret_cast<v4f*>(a.o + int64_t(p) * a.N + row) = sum;
+        }
+      }
+    } else if (kq == 0) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
@@ -605,6 +708,30 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_gate_up_kernel(MoeAr
           *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + at) = make_uint2(pl[s].x, pl[s].y);
       }
     }
+  }
+}
+
+// Y[m] = sum_j w_j o[m, j], j in order; a pair without an expert adds nothing.
+template <bool OUT_F32>
+__global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
+  const int per = a.N / 4, total = a.P / a.top_k * per;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const int m = i / per, row = i % per * 4;
+    v4f y = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < a.top_k; ++j) {
+      const int p = m * a.top_k + j, id = a.ids[p];
+      if (id < 0 || id >= a.E) continue;
+      const v4f v = *reinterpret_cast<const v4f*>(a.o + int64_t(p) * a.N + row);
+      const float wt = a.weights[p];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = fmaf(wt, v[e], y[e]);
+    }
+    const int64_t at = int64_t(m) * a.ldy + row;
+    if (OUT_F32)
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.Y) + at) = y;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.Y) + at) =
+          make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
   }
 }
 
@@ -654,7 +781,9 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
   struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };                 // x unused with HL
   Stage st[DEPTH];
-  uint8_t* const hl = reinterpret_cast<uint8_t*>(wt + (a.P + 3) / 4 * 4);
+  constexpr bool F16 = HL && FMT == kFmtNVFP4;             // h becomes fp16
+  uint32_t* const top = reinterpret_cast<uint32_t*>(wt + (a.P + 3) / 4 * 4);
+  uint8_t* const hl = reinterpret_cast<uint8_t*>(top + (a.P + 3) / 4 * 4);
   const int row_b = few_row_bytes(a.F);
   int lu = w, li = 0, words = fetch(w);
   Unit ld, cu;                                             // the unit being loaded, the one being computed
@@ -714,6 +843,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       for (int k = 0; k < KC; ++k)
         for (int q = 0; q < 4; ++q) slot[(k * a.P + p) * 4 + q] = v4f{0.f, 0.f, 0.f, 0.f};
   }
+  if constexpr (F16) rows_to_f16<S, kDownWaves>(hl, row_b, a.F, a.P, top);
   if (HL) lds_barrier();
   int i = 0;
   v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
@@ -726,7 +856,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           x[0][q] = *reinterpret_cast<const uint4*>(hl + cu.row * row_b + (at * kKStep + q * 32 + c * 8) * 2);
-        w4_step<FMT, 1>(st[j].w, cu.ks0 + i, x, acc);
+        w4_step<FMT, 1, F16>(st[j].w, cu.ks0 + i, x, acc);
       } else {
         w4_step<FMT, 1>(st[j].w, cu.ks0 + i, st[j].x, acc);
       }
@@ -735,6 +865,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       if (u < units && ++i == cu.n) {
         v4f y = acc[0];
         if (FMT == kFmtNVFP4) y *= gs;
+        if constexpr (F16) y *= 1.0f / f16_row_scale(__uint_as_float(top[cu.pair]));   // a power of two
         v4f sum = y;                                       // the planes' columns of a pair
 #pragma unroll
         for (int p = 1; p < S; ++p)
@@ -773,16 +904,37 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
 
 template <int FMT, int S, int NB>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned(a.F / 16 * a.KW / kGateWaves), unsigned(a.slots + 1));
+  const dim3 grid(unsigned(a.F / 16 * a.KW / kGateWaves), unsigned(a.slots + (a.o ? 0 : 1)));
   if (a.P <= 64)
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, true>), grid, dim3(512), kGateXLds, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, NB, true, false>), grid, dim3(512), kGateXLds, s, a);
   else
-    hipLaunchKernelGGL((moe_gate_up_kernel<FMT, S, NB, false>), grid, dim3(512), kGateXLds, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, NB, false, false>), grid, dim3(512), kGateXLds, s, a);
+}
+
+// Waves that share a tile's K, for this many tiles at least.
+static int waves_per_tile(int64_t tiles) {
+  int kw = 1;
+  while (kw < kGateWaves && tiles * kw < kGateFill) kw *= 2;
+  return kw;
 }
 
 template <int FMT, int S>
-static void down(const MoeArgs& a, hipStream_t s) {
-  const int64_t sums = (a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64 + int64_t(a.P + 3) / 4 * 16;
+static void down(MoeArgs a, hipStream_t s) {
+  if (a.o) {
+    const int experts = a.E < a.P ? a.E : a.P, tiles = (a.N + 31) / 32;
+    a.slots = experts + a.P / tokens_per_block(S);
+    a.KW = waves_per_tile(int64_t(experts) * tiles);
+    const int per = kGateWaves / a.KW;
+    const dim3 grid(unsigned((tiles + per - 1) / per), unsigned(a.slots));
+    if (a.P <= 64)
+      hipLaunchKernelGGL((moe_rows_kernel<FMT, S, 1, true, true>), grid, dim3(512), kGateXLds, s, a);
+    else
+      hipLaunchKernelGGL((moe_rows_kernel<FMT, S, 1, false, true>), grid, dim3(512), kGateXLds, s, a);
+    const int64_t quads = int64_t(a.P) / a.top_k * (a.N / 4);
+    hipLaunchKernelGGL((moe_join_kernel<S == 3>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, s, a);
+    return;
+  }
+  const int64_t sums = (a.P > kDownMinSlots ? a.P : kDownMinSlots) * 64 + int64_t(a.P + 3) / 4 * 32;
   const int64_t all = sums + int64_t(S) * a.P * few_row_bytes(a.F);
   const dim3 grid(unsigned(a.N / 16));
   if (all <= kDownLds)
@@ -802,6 +954,7 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
   a.wd = wd; a.blob_d = ld.total; a.d_codes = ld.codes; a.d_scales = ld.scales; a.d_bias = ld.bias; a.d_amax = ld.amax;
   a.plan = static_cast<int32_t*>(ws);
   a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kMoePlanBytes);
+  float* const o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMoePlanBytes + moe_h_bytes(M, top_k, F));
   a.ldx = ldx; a.ldy = ldy; a.Ng_pad = lg.N_pad; a.Nd_pad = ld.N_pad;
   a.H = H; a.F = F; a.N = N; a.E = E; a.top_k = top_k; a.epi = epi; a.d_int4 = fmt_d == kFmtINT4;
   const bool f32 = (epi & SVDQ_EPI_OUT_F32) != 0;
@@ -817,9 +970,8 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     const int experts = E < a.P ? E : a.P; // that may be asked for
     const bool two = a.P > 8 * experts;    // more than a block of pairs is usual: two at a time
     a.slots = experts + a.P / (two ? 32 : 16);
-    const int tiles = experts * (F / 16);
-    a.KW = 1;
-    while (a.KW < kGateWaves && tiles * a.KW < kGateFill) a.KW *= 2;
+    a.KW = waves_per_tile(int64_t(experts) * (F / 16));
+    a.o = moe_by_pairs(experts, a.P, F, N) ? o : nullptr;
 #define SVDQ_GATE(FMT_)                                       \
   do {                                                        \
     if (f32 && two) gate_up<FMT_, 3, 2>(a, s);                \

@@ -160,6 +160,40 @@ __device__ __forceinline__ uint4 nv_to_bf16(uint32_t d, float s) {
                     cvt_bf2(e.x * s, e.y * s));
 }
 
+// The same in fp16, where it is exact too (2^-10 .. 2688) and a product is one packed multiply: half
+// the operations, for activations that are fp16.  s holds the value twice.
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint4 nv_to_f16(uint32_t d, v2h s) {
+  return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 0) * s),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 1) * s),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 2) * s),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 3) * s));
+}
+
+// fp16 activations of a row: the row times a power of two that brings its largest magnitude `top`
+// into [2^14, 2^15) (1 for zero, infinity and NaN).  A bf16 is then exact in fp16 down to 2^-28 of
+// the row's largest, and off by at most 2^-39 of it below; hi + lo hold an fp32 to 2^-22.
+__device__ __forceinline__ float f16_row_scale(float top) {
+  const int e = int(__float_as_uint(top) >> 23 & 0xFFu);
+  return e == 0 || e == 255 ? 1.0f : __uint_as_float(uint32_t(268 - e < 247 ? 268 - e : 247) << 23);
+}
+__device__ __forceinline__ uint4 to_f16(const float (&v)[8]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __builtin_bit_cast(uint32_t, v2h{static_cast<_Float16>(v[2 * i]), static_cast<_Float16>(v[2 * i + 1])});
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void unpack_h8(const uint4& r, float (&a)[8]) {
+  const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2h h = __builtin_bit_cast(v2h, d[i]);
+    a[2 * i] = float(h.x);
+    a[2 * i + 1] = float(h.y);
+  }
+}
+
 // 8 INT4 codes in the packed dword order -> 8 bf16 24 + q.  k41 holds 0x41 in every byte
 // (the high byte of bf16 16 .. 31).
 __device__ __forceinline__ uint4 i4_to_bf16(uint32_t d, uint32_t k41) {
@@ -172,20 +206,24 @@ __device__ __forceinline__ uint4 i4_to_bf16(uint32_t d, uint32_t k41) {
 
 // acc[t][b] += (rows of tile t) x (16 columns of block b) over MFMA u of a 128-K step (MXFP4,
 // NVFP4); x[b] is the B operand.
-template <int FMT, int T, int NB>
+template <int FMT, int T, int NB, bool F16 = false>
 __device__ __forceinline__ void w4_mfma(const W4Stage<FMT> (&st)[T], int ks, int u, const uint4 (&x)[NB],
                                         v4f (&acc)[T][NB]) {
   static_assert(FMT != kFmtINT4, "INT4 takes half a step");
+  static_assert(!F16 || FMT == kFmtNVFP4, "fp16 activations: NVFP4 weights");
 #pragma unroll
   for (int t = 0; t < T; ++t) {
     const uint32_t d[4] = {st[t].q.x, st[t].q.y, st[t].q.z, st[t].q.w};
     uint4 a;
     if constexpr (FMT == kFmtMXFP4)
       a = mx_to_bf16(d[u], __uint_as_float(((st[t].s >> ((ks & 3) * 8)) & 0xFFu) << 23));
-    else
+    else if constexpr (F16) {
+      const _Float16 s = static_cast<_Float16>(e4m3_value((st[t].s >> ((u >> 1) * 8)) & 0xFFu));
+      a = nv_to_f16(d[u], v2h{s, s});
+    } else
       a = nv_to_bf16(d[u], e4m3_value((st[t].s >> ((u >> 1) * 8)) & 0xFFu));
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[t][b] = mfma_bf16(a, x[b], acc[t][b]);
+    for (int b = 0; b < NB; ++b) acc[t][b] = F16 ? mfma_f16(a, x[b], acc[t][b]) : mfma_bf16(a, x[b], acc[t][b]);
   }
 }
 
@@ -224,7 +262,7 @@ __device__ __forceinline__ void w4_half(const W4Stage<kFmtINT4> (&st)[T], int ha
 }
 
 // A whole 128-K step of one tile; x[b][u] is the B operand of MFMA u.
-template <int FMT, int NB>
+template <int FMT, int NB, bool F16 = false>
 __device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const uint4 (&x)[NB][4], v4f (&acc)[NB]) {
   const W4Stage<FMT> one[1] = {st};
   v4f a[1][NB];
@@ -246,7 +284,7 @@ __device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const ui
       uint4 h[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) h[b] = x[b][u];
-      w4_mfma<FMT, 1, NB>(one, ks, u, h, a);
+      w4_mfma<FMT, 1, NB, F16>(one, ks, u, h, a);
     }
   }
 #pragma unroll
