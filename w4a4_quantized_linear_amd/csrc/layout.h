@@ -49,8 +49,8 @@ constexpr float kNvfp4GlobalDiv = 2688.0f;   // E2M1 max 6 times E4M3 max 448
 constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxPairs = 2048;
-// The down kernel's plan: 16 words, then 16 for each column block, of which there are at most
-// min(E, P) + P / 5 < 1024.
+// The down kernel's plan: 16 words for each unit, of which there are at most min(E, P) + P / 5 < 922,
+// and 32 that end it.
 constexpr size_t kMoePlanBytes = 65536;
 
 // svdq_moe_route: one kernel, a workgroup per token, while one CU's fp64 rate computes all of a

@@ -334,13 +334,19 @@ struct MoeArgs {
 // A column of an MFMA that no pair has: beyond every buffer, so its loads read nothing (zeros).
 constexpr uint32_t kNoColumn = 0x80000000u;
 
-// The plan: plan[0] column blocks, then kPlanWords words each: expert, pairs, and the pairs (at
-// most 16 / S of one expert, all their planes being columns of one MFMA).  Their order, which the
-// atomics leave open, does not reach the results: every pair has a column and a place of its own.
+// The plan of moe_down_kernel: its units, kPlanWords words each: expert, pairs, K chunk, K chunks,
+// and the pairs (at most 16 / S of one expert, all their planes being columns of one MFMA); units
+// without pairs end every wave's sequence.  The pairs' order in a unit, which the atomics leave open,
+// does not reach the results: every pair has a column and a place of its own.
 constexpr int kPlanWords = 16;
+constexpr int kDownWaves = 16;
+constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
+__device__ __forceinline__ int down_slots(int P) { return P > kDownMinSlots ? P : kDownMinSlots; }
+
 template <int S, int THREADS>
 __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* base) {
   constexpr int TPB = tokens_per_block(S);
+  __shared__ int total;
   const int tid = threadIdx.x, lane = tid & 63;
   for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
   __syncthreads();
@@ -352,33 +358,40 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* bas
   if (tid < 64) {
     int blocks = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + lane, cnt = e < a.E ? cursor[e] : 0, nb = (cnt + TPB - 1) / TPB;
+      const int e = e0 + lane, nb = e < a.E ? (cursor[e] + TPB - 1) / TPB : 0;
       int sb = nb;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(sb, o);
         if (lane >= o) sb += v;
       }
-      if (e < a.E) {
-        base[e] = blocks + sb - nb;                        // the expert's first block
-        cursor[e] = 0;
-        for (int b = 0; b < nb; ++b) {
-          int32_t* const r = a.plan + kPlanWords * (1 + blocks + sb - nb + b);
-          r[0] = e;
-          r[1] = cnt - b * TPB < TPB ? cnt - b * TPB : TPB;
-        }
-      }
+      if (e < a.E) base[e] = blocks + sb - nb;             // the expert's first block
       blocks += __shfl(sb, 63);
     }
-    if (lane == 0) a.plan[0] = blocks;
+    if (lane == 0) total = blocks;
   }
+  __syncthreads();
+  // as many chunks of K as it takes to give every wave a unit, where the LDS has room
+  const int KS = a.F / kKStep, slots = down_slots(a.P);
+  int KC = 1;
+  while (total * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
+  for (int e = tid; e < a.E; e += THREADS) {
+    const int cnt = cursor[e];
+    for (int b = 0; b * TPB < cnt; ++b)
+      for (int k = 0; k < KC; ++k)
+        *reinterpret_cast<int4*>(a.plan + kPlanWords * ((base[e] + b) * KC + k)) =
+            make_int4(e, cnt - b * TPB < TPB ? cnt - b * TPB : TPB, k, KC);
+  }
+  for (int i = tid; i < 2 * kDownWaves; i += THREADS)
+    *reinterpret_cast<int4*>(a.plan + kPlanWords * (total * KC + i)) = make_int4(0, 0, 0, KC);
+  __syncthreads();
+  for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
   __syncthreads();
   for (int p = tid; p < a.P; p += THREADS) {
     const int id = a.ids[p];
-    if (id >= 0 && id < a.E) {
-      const int i = atomicAdd(&cursor[id], 1);
-      a.plan[kPlanWords * (1 + base[id] + i / TPB) + 2 + i % TPB] = p;
-    }
+    if (id < 0 || id >= a.E) continue;
+    const int i = atomicAdd(&cursor[id], 1);
+    for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[id] + i / TPB) * KC + k) + 4 + i % TPB] = p;
   }
 }
 
@@ -565,10 +578,22 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
         keep_order();
       }
       uint8_t* const xl = reinterpret_cast<uint8_t*>(xlds);
-      for (int r = 0; r < xrows; ++r) {
-        const uint16_t* const src = xbase + row_of(pair_of(DOWN ? r % T : r), DOWN ? r / T : 0);
-        for (int k = tid * 8; k < K; k += 512 * 8)
-          *reinterpret_cast<uint4*>(xl + r * row_b + k * 2) = *reinterpret_cast<const uint4*>(src + k);
+      // a wave's copies of 64 lanes x 16 bytes, eight in flight
+      const int segs = K / 512, all = xrows * segs;
+      for (int g0 = w; g0 < all; g0 += 8 * kGateWaves) {
+        uint4 v[8];
+        int r[8], sg[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int g = g0 + j * kGateWaves < all ? g0 + j * kGateWaves : g0;
+          r[j] = g / segs;
+          sg[j] = g - r[j] * segs;
+          const uint16_t* const src = xbase + row_of(pair_of(DOWN ? r[j] % T : r[j]), DOWN ? r[j] / T : 0);
+          v[j] = *reinterpret_cast<const uint4*>(src + sg[j] * 512 + lane * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (g0 + j * kGateWaves < all) *reinterpret_cast<uint4*>(xl + r[j] * row_b + sg[j] * 1024 + lane * 16) = v[j];
       }
       if constexpr (F16) rows_to_f16<DOWN ? S : 1, kGateWaves>(xl, row_b, K, T, top);
       lds_barrier();
@@ -739,9 +764,7 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
 // the plan and one of KC chunks of K; waves take every sixteenth unit, one pipeline running on from
 // unit to unit, and leave each pair's sums in a place of its own, so the sum over a token's experts
 // has one order.
-constexpr int kDownWaves = 16;
 constexpr int64_t kDownLds = 163840;   // HL: all of h in LDS where it fits (one workgroup a CU)
-constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
 
 template <int FMT, int S, bool HL>
 __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
@@ -751,31 +774,24 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
-  const int slots = a.P > kDownMinSlots ? a.P : kDownMinSlots;
-  float* const wt = reinterpret_cast<float*>(slot + slots * 4);
+  float* const wt = reinterpret_cast<float*>(slot + down_slots(a.P) * 4);
   const int KS = a.F / kKStep;
-  const int nblocks = __builtin_amdgcn_readfirstlane(a.plan[0]);
-  // as many chunks of K as it takes to give every wave a unit, where the LDS has room
-  int KC = 1;
-  while (nblocks * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
-  const int units = nblocks * KC;
   const int rt = blockIdx.x;
   const int t = tl % TPB, pl = tl / TPB;
 
   // a unit as its wave sees it; the plan's words are loaded one unit ahead
   struct Unit { const uint8_t* blob; int cnt, pair, kc, ks0, n, row; uint32_t xoff; };
-  auto fetch = [&](int u) -> int {
-    return u < units ? a.plan[kPlanWords * (1 + u / KC) + tl] : 0;
-  };
-  auto open = [&](int u, int words, Unit& d) {
-    d.kc = u % KC;
+  auto fetch = [&](int u) -> int { return a.plan[kPlanWords * u + tl]; };
+  auto open = [&](int words, Unit& d) {
     d.cnt = __builtin_amdgcn_readlane(words, 1);
+    d.kc = __builtin_amdgcn_readlane(words, 2);
+    const int KC = __builtin_amdgcn_readlane(words, 3);
     d.blob = a.wd + size_t(__builtin_amdgcn_readlane(words, 0)) * a.blob_d;
     const bool column = pl < S && t < d.cnt;
-    d.pair = __shfl(words, 2 + (t < d.cnt ? t : 0));
+    d.pair = __shfl(words, 4 + (t < d.cnt ? t : 0));
     d.row = column ? pl * a.P + d.pair : 0;                // HL: any row where there is no column
     d.ks0 = d.kc * KS / KC;
-    d.n = u < units ? (d.kc + 1) * KS / KC - d.ks0 : 0;
+    d.n = d.cnt ? (d.kc + 1) * KS / KC - d.ks0 : 0;
     d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + c * 8) * 2) : kNoColumn;
   };
   const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
@@ -788,8 +804,8 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   int lu = w, li = 0, words = fetch(w);
   Unit ld, cu;                                             // the unit being loaded, the one being computed
   auto enter = [&]() {                                     // the load side's next unit
-    open(lu, words, ld);
-    words = fetch(lu + kDownWaves);
+    open(words, ld);
+    if (ld.n) words = fetch(lu + kDownWaves);
   };
   auto load = [&](Stage& s) {
     const bool valid = li < ld.n;
@@ -801,14 +817,14 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) s.x[0][q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
     }
-    if (++li >= ld.n && lu < units) {
+    if (++li >= ld.n && ld.n) {
       li = 0;
       lu += kDownWaves;
       enter();
     }
   };
   int u = w;
-  const int first_words = words;
+  const int first_words = words, KC = __builtin_amdgcn_readlane(words, 3);
   enter();
 #pragma unroll
   for (int j = 0; j < DEPTH; ++j) {
@@ -820,8 +836,8 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   float gs = 1.0f;
   uint2 bias = make_uint2(0u, 0u);
   auto begin = [&]() {
-    open(u, cwords, cu);
-    cwords = fetch(u + kDownWaves);
+    open(cwords, cu);
+    if (cu.n) cwords = fetch(u + kDownWaves);
     gs = w4_tensor_scale<FMT>(cu.blob + a.d_amax);
     if (cu.kc == 0 && (a.epi & SVDQ_EPI_BIAS))
       bias = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(cu.blob + a.d_bias) + rt * 16 + c * 4);
@@ -830,9 +846,19 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   };
   begin();
   if constexpr (HL) {
-    const int per = a.F / 8;                               // 16-byte pieces of a row
-    for (int i = tid; i < S * a.P * per; i += 1024)
-      *reinterpret_cast<uint4*>(hl + i / per * row_b + i % per * 16) = reinterpret_cast<const uint4*>(a.h)[i];
+    // a wave's copies of 64 lanes x 16 bytes, eight in flight
+    const int segs = a.F / 512, all = S * a.P * segs;
+    for (int g0 = w; g0 < all; g0 += 8 * kDownWaves) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = reinterpret_cast<const uint4*>(a.h)[(g0 + j * kDownWaves < all ? g0 + j * kDownWaves : g0) * 64 + lane];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int g = g0 + j * kDownWaves;
+        if (g < all) *reinterpret_cast<uint4*>(hl + g / segs * row_b + g % segs * 1024 + lane * 16) = v[j];
+      }
+    }
   }
   // the pairs' weights; a pair without an expert adds zero
   for (int p = tid; p < a.P; p += 1024) {
@@ -847,7 +873,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   if (HL) lds_barrier();
   int i = 0;
   v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
-  while (u < units) {
+  while (cu.n) {
 #pragma unroll
     for (int j = 0; j < DEPTH; ++j) {
       if constexpr (HL) {
@@ -862,7 +888,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       }
       load(st[j]);
       keep_order();
-      if (u < units && ++i == cu.n) {
+      if (cu.n && ++i == cu.n) {
         v4f y = acc[0];
         if (FMT == kFmtNVFP4) y *= gs;
         if constexpr (F16) y *= 1.0f / f16_row_scale(__uint_as_float(top[cu.pair]));   // a power of two
