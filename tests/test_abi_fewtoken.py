@@ -40,7 +40,7 @@ def test_sizes(L):
         assert L.svdq_moe_route_bytes(*bad) == 0
     g, d = D(K=1024, N=1024, rank=0), D(K=512, N=256, rank=0)
     assert L.svdq_moe_bytes(g, d, 5, 3) >= 15 * 512 * 6
-    assert L.svdq_moe_bytes(g, d, 10 ** 6, 3) <= 2048 * (512 * 6 + 256 * 4) + 65536       # parts share it
+    assert L.svdq_moe_bytes(g, d, 10 ** 6, 3) <= 2048 * (512 * 6 + 256 * 4) + 150000       # parts share it
     assert L.svdq_moe_bytes(g, D(K=1024, N=256, rank=0), 5, 3) == 0 and L.svdq_moe_bytes(g, d, 5, 0) == 0
     assert L.svdq_moe_bytes(g, d, 5, 33) == 0 and L.svdq_moe_bytes(None, d, 5, 3) == 0
 

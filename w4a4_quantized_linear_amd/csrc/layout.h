@@ -49,9 +49,10 @@ constexpr float kNvfp4GlobalDiv = 2688.0f;   // E2M1 max 6 times E4M3 max 448
 constexpr int kMoeMaxE = 512;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxPairs = 2048;
-// The down kernel's plan: 16 words for each unit, of which there are at most min(E, P) + P / 5 < 922,
-// and 32 that end it.
-constexpr size_t kMoePlanBytes = 65536;
+// The plan: 16 words for each unit of the down product, of which there are at most min(E, P) + P / 5
+// < 922, and 32 that end it; from 64 KiB on 32 words for each of at most min(E, P) + P / 16 = 640
+// blocks of the gate/up product.
+constexpr size_t kMoePlanBytes = 65536 + 640 * 128;
 
 // svdq_moe_route: one kernel, a workgroup per token, while one CU's fp64 rate computes all of a
 // token's logits about as fast as a second launch costs and each token has a CU; otherwise the
@@ -81,7 +82,7 @@ __host__ __device__ inline size_t align256(size_t a) { return (a + 255) & ~size_
 // the first is bound by its L1, about 170 cycles for each column block and 128 of F, in N / 16
 // workgroups over 256 CUs; the second shares a block's columns between two row tiles and fills the
 // GPU whatever N is, for a launch more and the products' way through memory.
-constexpr int64_t kMoeDownSteps = 600;     // steps a CU (48 us) from which the second is taken
+constexpr int64_t kMoeDownSteps = 350;     // steps a CU from which the second is taken
 __host__ __device__ inline bool moe_by_pairs(int64_t experts, int64_t pairs, int F, int N) {
   return (experts + pairs / 8) * (F / kKStep) * ((N / 16 + 255) / 256) > kMoeDownSteps;
 }

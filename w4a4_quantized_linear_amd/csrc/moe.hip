@@ -327,7 +327,7 @@ struct MoeArgs {
   int64_t ldx, ldy, Ng_pad, Nd_pad;
   int H, F, N, E, top_k, P;            // gate/up: H -> 2 F, down: F -> N
   int d_int4;
-  int slots, KW;                       // gate/up: blocks of pairs at most, waves that share a tile's K
+  int slots, down_slots, KW;           // blocks of pairs at most; waves that share a tile's K
   uint32_t epi;
 };
 
@@ -343,10 +343,15 @@ constexpr int kDownWaves = 16;
 constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
 __device__ __forceinline__ int down_slots(int P) { return P > kDownMinSlots ? P : kDownMinSlots; }
 
-template <int S, int THREADS>
-__device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* base) {
-  constexpr int TPB = tokens_per_block(S);
-  __shared__ int total;
+// With GATE it also holds, from kGatePlan on, the gate/up product's blocks: expert, pairs and up to 16
+// pairs of kGatePlanWords words each, ended by blocks without pairs up to the grid's `slots`.
+constexpr int kGatePlan = 16384;       // in words
+constexpr int kGatePlanWords = 32;
+template <int S, bool GATE>
+__device__ __forceinline__ void moe_plan(const MoeArgs& a) {
+  constexpr int TPB = tokens_per_block(S), THREADS = 512;
+  __shared__ int cursor[kMoeMaxE], base[kMoeMaxE], gbase[kMoeMaxE];
+  __shared__ int total, gtotal;
   const int tid = threadIdx.x, lane = tid & 63;
   for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
   __syncthreads();
@@ -355,35 +360,45 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* bas
     if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
   }
   __syncthreads();
-  if (tid < 64) {
+  if (tid < (GATE ? 128 : 64)) {                           // one wave for each kind of block
+    const int size = tid < 64 ? TPB : 16;
     int blocks = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + lane, nb = e < a.E ? (cursor[e] + TPB - 1) / TPB : 0;
+      const int e = e0 + lane, nb = e < a.E ? (cursor[e] + size - 1) / size : 0;
       int sb = nb;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(sb, o);
         if (lane >= o) sb += v;
       }
-      if (e < a.E) base[e] = blocks + sb - nb;             // the expert's first block
+      if (e < a.E) (tid < 64 ? base : gbase)[e] = blocks + sb - nb;   // the expert's first block
       blocks += __shfl(sb, 63);
     }
-    if (lane == 0) total = blocks;
+    if (lane == 0) (tid < 64 ? total : gtotal) = blocks;
   }
   __syncthreads();
   // as many chunks of K as it takes to give every wave a unit, where the LDS has room
   const int KS = a.F / kKStep, slots = down_slots(a.P);
   int KC = 1;
-  while (total * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
+  while (!a.o && total * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
+  int32_t* const gate = a.plan + kGatePlan;
   for (int e = tid; e < a.E; e += THREADS) {
     const int cnt = cursor[e];
+    if (GATE)
+      for (int b = 0; b * 16 < cnt; ++b)
+        *reinterpret_cast<int2*>(gate + kGatePlanWords * (gbase[e] + b)) = make_int2(e, cnt - b * 16 < 16 ? cnt - b * 16 : 16);
     for (int b = 0; b * TPB < cnt; ++b)
       for (int k = 0; k < KC; ++k)
         *reinterpret_cast<int4*>(a.plan + kPlanWords * ((base[e] + b) * KC + k)) =
             make_int4(e, cnt - b * TPB < TPB ? cnt - b * TPB : TPB, k, KC);
   }
-  for (int i = tid; i < 2 * kDownWaves; i += THREADS)
+  // (the down product by pairs has a grid of its own, which may reach further)
+  const int ends = a.o ? a.down_slots - total : 2 * kDownWaves;
+  for (int i = tid; i < ends; i += THREADS)
     *reinterpret_cast<int4*>(a.plan + kPlanWords * (total * KC + i)) = make_int4(0, 0, 0, KC);
+  if (GATE)
+    for (int i = gtotal + tid; i < a.slots; i += THREADS)
+      *reinterpret_cast<int2*>(gate + kGatePlanWords * i) = make_int2(0, 0);
   __syncthreads();
   for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
   __syncthreads();
@@ -392,7 +407,13 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* cursor, int* bas
     if (id < 0 || id >= a.E) continue;
     const int i = atomicAdd(&cursor[id], 1);
     for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[id] + i / TPB) * KC + k) + 4 + i % TPB] = p;
+    if (GATE) gate[kGatePlanWords * (gbase[id] + i / 16) + 2 + i % 16] = p;
   }
+}
+
+template <int S>
+__global__ void __launch_bounds__(512) moe_plan_kernel(MoeArgs a) {
+  moe_plan<S, true>(a);
 }
 
 // Rows in LDS (S planes x n rows of K bf16, row_b bytes apart) to fp16, in place, scaled by
@@ -445,40 +466,44 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // Rows of one expert for a block of its pairs: the gate and up rows (a tile is 16 gate and the same
 // 16 up rows), or, DOWN, down rows of long calls (a tile is 32 rows, and a pair's sums go to memory,
 // where moe_join_kernel adds a token's pairs).
-// The workgroup takes 8 / KW tiles and the blockIdx.y-th block: up to 16 NB pairs (DOWN: 16 / S, all
-// their planes being columns), experts in order.  KW waves share a tile's K (every KW-th 128-K step
-// each); KW is the smallest that fills the GPU, since with few there is little exchange and a wave
-// streams long runs of codes.
-// SMALL (at most 64 pairs): every wave finds its block by ballots, no barrier.
-// The gate/up grid's last row (blockIdx.y == slots) holds one workgroup that writes the plan of
-// moe_down_kernel.
+// The workgroup takes 8 / KW tiles and the blockIdx.y-th block: up to 16 pairs (DOWN: 16 / S, all
+// their planes being columns).  KW waves share a tile's K (every KW-th 128-K step each); KW is the
+// smallest that fills the GPU, since with few there is little exchange and a wave streams long runs
+// of codes.  (Blocks of 32 pairs, which halve the reads of an expert with many, leave one workgroup
+// a CU: 67 against 62 us at 48 tokens, 8 of 24 experts, 3584 -> 2 x 1536.)
+// PLANNED: the blocks are in the plan.  Otherwise (gate/up of at most 64 pairs) every wave finds its
+// block by ballots, and the grid's last row (blockIdx.y == slots) holds one workgroup that writes
+// the plan for the down product.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
-constexpr int kGateXLds = 49152;       // beside 20 KiB, two workgroups a CU
-template <int FMT, int S, int NB, bool SMALL, bool DOWN>
-__global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs a) {
-  static_assert(!DOWN || NB == 1, "a block of down columns holds all planes");
-  constexpr int DEPTH = NB == 1 && FMT != kFmtINT4 ? 3 : 2;   // registers for two workgroups a CU
+constexpr int kGateXLds = 49152;       // beside 16 KiB, two workgroups a CU
+template <int FMT, int S, bool DOWN, bool PLANNED>
+__global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
+  constexpr int DEPTH = FMT != kFmtINT4 ? 3 : 2;           // registers for two workgroups a CU
   constexpr int TPB = tokens_per_block(S);
-  constexpr int COLS = DOWN ? TPB : 16 * NB;
+  constexpr int COLS = DOWN ? TPB : 16;
+  static_assert(PLANNED || !DOWN, "down blocks are planned");
   extern __shared__ uint4 xlds[];                          // kGateXLds bytes
-  __shared__ v4f red[kGateWaves][2][NB][64];
-  __shared__ int list[COLS];
-  __shared__ int cursor[kMoeMaxE], base[kMoeMaxE];
-  __shared__ int found[kGateWaves];
+  __shared__ v4f red[kGateWaves][2][64];
   constexpr bool F16 = FMT == kFmtNVFP4;                   // rows in LDS become fp16
   __shared__ uint32_t top[COLS];
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
   const int slot = blockIdx.y;
-  if (!DOWN && slot == a.slots) {
-    if (blockIdx.x == 0) moe_plan<S, 512>(a, cursor, base);
-    return;
-  }
-  const uint64_t below = (uint64_t(1) << lane) - 1;
-  int ex = -1, T = 0, mine = 0;        // the expert, the block's pairs; SMALL: lane i holds the i-th
-  if constexpr (SMALL) {
+  int ex = -1, T = 0, mine = 0;        // the expert, the block's pairs; lane i holds the i-th
+  if constexpr (PLANNED) {
+    const int words = DOWN ? a.plan[kPlanWords * slot + tl] : a.plan[kGatePlan + kGatePlanWords * slot + (lane & 31)];
+    ex = __builtin_amdgcn_readlane(words, 0);
+    T = __builtin_amdgcn_readlane(words, 1);
+    if (T == 0) return;
+    mine = __shfl(words, (lane & 15) + (DOWN ? 4 : 2));
+  } else {
+    if (slot == a.slots) {
+      if (blockIdx.x == 0) moe_plan<S, false>(a);
+      return;
+    }
+    const uint64_t below = (uint64_t(1) << lane) - 1;
     const int id = lane < a.P ? a.ids[lane] : -1;
     uint64_t left = __ballot(id >= 0 && id < a.E), eq = 0;
     int t0 = slot * COLS;                                  // the block's first pair among the expert's
@@ -495,54 +520,9 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
     const int to = eq >> lane & 1 ? __popcll(eq & below) : T + __popcll(~eq & below);
     mine = __shfl(__builtin_amdgcn_ds_permute(to * 4, lane), (lane + t0) & 63);
     T = T - t0 < COLS ? T - t0 : COLS;
-  } else {
-    for (int e = tid; e < a.E; e += 512) cursor[e] = 0;
-    __syncthreads();
-    for (int p = tid; p < a.P; p += 512) {
-      const int id = a.ids[p];
-      if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
-    }
-    __syncthreads();
-    int before = 0, t0 = 0;
-    for (int e0 = 0; e0 < a.E && ex < 0; e0 += 64) {
-      const int cnt = e0 + lane < a.E ? cursor[e0 + lane] : 0, nb = (cnt + COLS - 1) / COLS;
-      int sum = nb;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(sum, o);
-        if (lane >= o) sum += v;
-      }
-      const uint64_t hit = __ballot(slot >= before + sum - nb && slot < before + sum);
-      if (hit) {
-        const int at = __ffsll((unsigned long long)hit) - 1;
-        ex = e0 + at;
-        t0 = (slot - before - __builtin_amdgcn_readlane(sum - nb, at)) * COLS;
-        T = __builtin_amdgcn_readlane(cnt, at) - t0;
-      }
-      before += __builtin_amdgcn_readlane(sum, 63);
-    }
-    if (ex < 0) return;
-    T = T < COLS ? T : COLS;
-    // the expert's pairs in order: every workgroup finds the same blocks
-    const int span = (a.P + 511) / 512 * 64;               // pairs of one wave
-    int n = 0;
-    for (int p0 = w * span; p0 < (w + 1) * span; p0 += 64)
-      n += __popcll(__ballot(p0 + lane < a.P && a.ids[p0 + lane] == ex));
-    if (lane == 0) found[w] = n;
-    __syncthreads();
-    int rank = -t0;
-    for (int v = 0; v < w; ++v) rank += found[v];
-    for (int p0 = w * span; p0 < (w + 1) * span; p0 += 64) {
-      const bool hit = p0 + lane < a.P && a.ids[p0 + lane] == ex;
-      const uint64_t m = __ballot(hit);
-      const int r = rank + __popcll(m & below);
-      if (hit && r >= 0 && r < COLS) list[r] = p0 + lane;
-      rank += __popcll(m);
-    }
-    __syncthreads();
   }
   ex = __builtin_amdgcn_readfirstlane(ex);
-  auto pair_of = [&](int i) { return SMALL ? __shfl(mine, i) : list[i]; };
+  auto pair_of = [&](int i) { return __shfl(mine, i); };
 
   const uint8_t* const blob = DOWN ? a.wd + size_t(ex) * a.blob_d : a.wg + size_t(ex) * a.blob_g;
   const int K = DOWN ? a.F : a.H, KS = K / kKStep, KW = a.KW, kq = w % KW;
@@ -558,9 +538,7 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
   // column b * 16 + tl: element offset of its row of X (of h), or no pair
   auto row_of = [&](int p, int plane) -> int64_t { return DOWN ? (int64_t(plane) * a.P + p) * a.F : int64_t(p / a.top_k) * a.ldx; };
   {
-    v4f ag[NB], au[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) ag[b] = au[b] = v4f{0.f, 0.f, 0.f, 0.f};
+    v4f ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
     auto load_w = [&](int i, W4Stage<FMT>& g, W4Stage<FMT>& u) {
       const uint32_t ks = uint32_t(kq + i * KW);
       rows.load(rt0, ks, i < n, lane, g);
@@ -597,54 +575,38 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
       }
       if constexpr (F16) rows_to_f16<DOWN ? S : 1, kGateWaves>(xl, row_b, K, T, top);
       lds_barrier();
-      const uint8_t* xp[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int i = b * 16 + tl, t = tl % TPB, pl = tl / TPB;
-        xp[b] = xl + (DOWN ? (pl < S && t < T ? pl * T + t : 0) : i < T ? i : T - 1) * row_b;
-      }
+      const int t = tl % TPB, pl = tl / TPB;
+      const uint8_t* const xp = xl + (DOWN ? (pl < S && t < T ? pl * T + t : 0) : tl < T ? tl : T - 1) * row_b;
       for (int i0 = 0; i0 < n; i0 += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
           const int ks = kq + (i0 + j < n ? i0 + j : n - 1) * KW;   // past the last step: codes are zeros
-          uint4 x[NB][4];
+          uint4 x[4];
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              x[b][u] = *reinterpret_cast<const uint4*>(xp[b] + (ks * kKStep + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
-          w4_step<FMT, NB, F16>(sg[j], ks, x, ag);
-          w4_step<FMT, NB, F16>(su[j], ks, x, au);
+          for (int u = 0; u < 4; ++u)
+            x[u] = *reinterpret_cast<const uint4*>(xp + (ks * kKStep + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
+          w4_step<FMT, F16>(sg[j], ks, x, ag);
+          w4_step<FMT, F16>(su[j], ks, x, au);
           load_w(i0 + j + AHEAD, sg[j], su[j]);
           keep_order();
         }
       }
       if constexpr (F16) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int i = DOWN ? tl % TPB : b * 16 + tl;
-          const float back = 1.0f / f16_row_scale(__uint_as_float(top[i < T ? i : 0]));   // a power of two
-          ag[b] *= back;
-          au[b] *= back;
-        }
+        const int i = DOWN ? t : tl;
+        const float back = 1.0f / f16_row_scale(__uint_as_float(top[i < T ? i : 0]));   // a power of two
+        ag *= back;
+        au *= back;
       }
     } else {
-      uint32_t xoff[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int i = DOWN ? tl % TPB : b * 16 + tl, plane = DOWN ? tl / TPB : 0;
-        const int p = pair_of(i < T ? i : 0);
-        xoff[b] = i < T && plane < S ? uint32_t(row_of(p, plane) + c * 8) * 2 : kNoColumn;
-      }
-      struct Stage { W4Stage<FMT> g, u; uint4 x[NB][4]; };
+      const int i = DOWN ? tl % TPB : tl, plane = DOWN ? tl / TPB : 0;
+      const int p = pair_of(i < T ? i : 0);
+      const uint32_t xoff = i < T && plane < S ? uint32_t(row_of(p, plane) + c * 8) * 2 : kNoColumn;
+      struct Stage { W4Stage<FMT> g, u; uint4 x[4]; };
       auto load = [&](int i, Stage& st) {
         load_w(i, st.g, st.u);
         const __amdgpu_buffer_rsrc_t r = make_rsrc(xbase, i < n ? xbytes : 0);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            st.x[b][u] = buffer_load16(r, xoff[b] + u * 64, uint32_t(kq + i * KW) * kKStep * 2);
+        for (int u = 0; u < 4; ++u) st.x[u] = buffer_load16(r, xoff + u * 64, uint32_t(kq + i * KW) * kKStep * 2);
       };
       Stage st[DEPTH];
 #pragma unroll
@@ -657,32 +619,27 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
         for (int j = 0; j < DEPTH; ++j) {
           // past the last step codes and columns are zeros
           const int ks = kq + (i0 + j) * KW;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            if (!DOWN) to_operands<FMT>(st[j].x[b]);       // h is stored as operands
-          w4_step<FMT, NB>(st[j].g, ks, st[j].x, ag);
-          w4_step<FMT, NB>(st[j].u, ks, st[j].x, au);
+          if (!DOWN) to_operands<FMT>(st[j].x);            // h is stored as operands
+          w4_step<FMT>(st[j].g, ks, st[j].x, ag);
+          w4_step<FMT>(st[j].u, ks, st[j].x, au);
           load(i0 + j + DEPTH, st[j]);
           keep_order();
         }
       }
     }
     if (KW > 1) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        red[w][0][b][lane] = ag[b];
-        red[w][1][b][lane] = au[b];
-      }
+      red[w][0][lane] = ag;
+      red[w][1][lane] = au;
       lds_barrier();
     }
     if constexpr (DOWN) {
       if (kq == 0) {
-        v4f y[2] = {ag[0], au[0]};
+        v4f y[2] = {ag, au};
 #pragma unroll
         for (int v = 1; v < kGateWaves; ++v)
           if (v < KW) {
-            y[0] += red[w + v][0][0][lane];
-            y[1] += red[w + v][1][0][lane];
+            y[0] += red[w + v][0][lane];
+            y[1] += red[w + v][1][lane];
           }
         const int p = pair_of(tl < T ? tl : 0);
 #pragma unroll
@@ -703,14 +660,12 @@ __global__ void __launch_bounds__(512, NB == 1 ? 4 : 2) moe_rows_kernel(MoeArgs 
         }
       }
     } else if (kq == 0) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int i = b * 16 + tl, p = pair_of(i < T ? i : 0);
-        if (i >= T) continue;
-        v4f g = ag[b], u = au[b];                          // rows 4 c .. 4 c + 3 of pair p
+      const int p = pair_of(tl < T ? tl : 0);
+      if (tl < T) {
+        v4f g = ag, u = au;                                // rows 4 c .. 4 c + 3 of pair p
         for (int v = 1; v < KW; ++v) {
-          g += red[w + v][0][b][lane];
-          u += red[w + v][1][b][lane];
+          g += red[w + v][0][lane];
+          u += red[w + v][1][lane];
         }
         if (FMT == kFmtNVFP4) { g *= gs; u *= gs; }
         const int row = ft * 16 + c * 4;
@@ -743,13 +698,23 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
   for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
     const int m = i / per, row = i % per * 4;
     v4f y = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < a.top_k; ++j) {
-      const int p = m * a.top_k + j, id = a.ids[p];
-      if (id < 0 || id >= a.E) continue;
-      const v4f v = *reinterpret_cast<const v4f*>(a.o + int64_t(p) * a.N + row);
-      const float wt = a.weights[p];
+    for (int j0 = 0; j0 < a.top_k; j0 += 4) {              // four pairs' loads at once
+      int id[4];
+      float wt[4];
+      v4f v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = fmaf(wt, v[e], y[e]);
+      for (int j = 0; j < 4; ++j) {
+        const int p = m * a.top_k + (j0 + j < a.top_k ? j0 + j : j0);
+        id[j] = a.ids[p];
+        wt[j] = a.weights[p];
+        v[j] = *reinterpret_cast<const v4f*>(a.o + int64_t(p) * a.N + row);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j0 + j >= a.top_k || id[j] < 0 || id[j] >= a.E) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fmaf(wt[j], v[j][e], y[e]);
+      }
     }
     const int64_t at = int64_t(m) * a.ldy + row;
     if (OUT_F32)
@@ -795,7 +760,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     d.xoff = column ? uint32_t(((pl * a.P + d.pair) * int64_t(a.F) + c * 8) * 2) : kNoColumn;
   };
   const uint32_t h_bytes = uint32_t(int64_t(S) * a.P * a.F * 2);
-  struct Stage { W4Stage<FMT> w; uint4 x[1][4]; };                 // x unused with HL
+  struct Stage { W4Stage<FMT> w; uint4 x[4]; };                    // x unused with HL
   Stage st[DEPTH];
   constexpr bool F16 = HL && FMT == kFmtNVFP4;             // h becomes fp16
   uint32_t* const top = reinterpret_cast<uint32_t*>(wt + (a.P + 3) / 4 * 4);
@@ -815,7 +780,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     if constexpr (!HL) {
       const __amdgpu_buffer_rsrc_t r = make_rsrc(a.h, valid ? h_bytes : 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) s.x[0][q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
+      for (int q = 0; q < 4; ++q) s.x[q] = buffer_load16(r, ld.xoff + q * 64, ks * kKStep * 2);
     }
     if (++li >= ld.n && ld.n) {
       li = 0;
@@ -872,24 +837,24 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   if constexpr (F16) rows_to_f16<S, kDownWaves>(hl, row_b, a.F, a.P, top);
   if (HL) lds_barrier();
   int i = 0;
-  v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
   while (cu.n) {
 #pragma unroll
     for (int j = 0; j < DEPTH; ++j) {
       if constexpr (HL) {
-        uint4 x[1][4];
+        uint4 x[4];
         const int at = cu.ks0 + i < KS ? cu.ks0 + i : 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          x[0][q] = *reinterpret_cast<const uint4*>(hl + cu.row * row_b + (at * kKStep + q * 32 + c * 8) * 2);
-        w4_step<FMT, 1, F16>(st[j].w, cu.ks0 + i, x, acc);
+          x[q] = *reinterpret_cast<const uint4*>(hl + cu.row * row_b + (at * kKStep + q * 32 + c * 8) * 2);
+        w4_step<FMT, F16>(st[j].w, cu.ks0 + i, x, acc);
       } else {
-        w4_step<FMT, 1>(st[j].w, cu.ks0 + i, st[j].x, acc);
+        w4_step<FMT>(st[j].w, cu.ks0 + i, st[j].x, acc);
       }
       load(st[j]);
       keep_order();
       if (cu.n && ++i == cu.n) {
-        v4f y = acc[0];
+        v4f y = acc;
         if (FMT == kFmtNVFP4) y *= gs;
         if constexpr (F16) y *= 1.0f / f16_row_scale(__uint_as_float(top[cu.pair]));   // a power of two
         v4f sum = y;                                       // the planes' columns of a pair
@@ -899,7 +864,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
           for (int e = 0; e < 4; ++e) sum[e] += __shfl(y[e], lane + p * TPB);
         sum += v4f{bf_lo(bias.x), bf_hi(bias.x), bf_lo(bias.y), bf_hi(bias.y)};
         if (tl < cu.cnt) slot[(cu.kc * a.P + cu.pair) * 4 + c] = sum;
-        acc[0] = v4f{0.f, 0.f, 0.f, 0.f};
+        acc = v4f{0.f, 0.f, 0.f, 0.f};
         i = 0;
         u += kDownWaves;
         begin();
@@ -928,13 +893,15 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   }
 }
 
-template <int FMT, int S, int NB>
+template <int FMT, int S>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid(unsigned(a.F / 16 * a.KW / kGateWaves), unsigned(a.slots + (a.o ? 0 : 1)));
-  if (a.P <= 64)
-    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, NB, true, false>), grid, dim3(512), kGateXLds, s, a);
-  else
-    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, NB, false, false>), grid, dim3(512), kGateXLds, s, a);
+  const unsigned tiles = unsigned(a.F / 16 * a.KW / kGateWaves);
+  if (a.P <= 64) {
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, false, false>), dim3(tiles, unsigned(a.slots + 1)), dim3(512), kGateXLds, s, a);
+  } else {
+    hipLaunchKernelGGL((moe_plan_kernel<S>), dim3(1), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, false, true>), dim3(tiles, unsigned(a.slots)), dim3(512), kGateXLds, s, a);
+  }
 }
 
 // Waves that share a tile's K, for this many tiles at least.
@@ -948,14 +915,10 @@ template <int FMT, int S>
 static void down(MoeArgs a, hipStream_t s) {
   if (a.o) {
     const int experts = a.E < a.P ? a.E : a.P, tiles = (a.N + 31) / 32;
-    a.slots = experts + a.P / tokens_per_block(S);
     a.KW = waves_per_tile(int64_t(experts) * tiles);
     const int per = kGateWaves / a.KW;
-    const dim3 grid(unsigned((tiles + per - 1) / per), unsigned(a.slots));
-    if (a.P <= 64)
-      hipLaunchKernelGGL((moe_rows_kernel<FMT, S, 1, true, true>), grid, dim3(512), kGateXLds, s, a);
-    else
-      hipLaunchKernelGGL((moe_rows_kernel<FMT, S, 1, false, true>), grid, dim3(512), kGateXLds, s, a);
+    const dim3 grid(unsigned((tiles + per - 1) / per), unsigned(a.down_slots));
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, true, true>), grid, dim3(512), kGateXLds, s, a);
     const int64_t quads = int64_t(a.P) / a.top_k * (a.N / 4);
     hipLaunchKernelGGL((moe_join_kernel<S == 3>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, s, a);
     return;
@@ -994,16 +957,14 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     a.weights = weights + m0 * top_k;
     a.Y = static_cast<uint8_t*>(Y) + m0 * ldy * (f32 ? 4 : 2);
     const int experts = E < a.P ? E : a.P; // that may be asked for
-    const bool two = a.P > 8 * experts;    // more than a block of pairs is usual: two at a time
-    a.slots = experts + a.P / (two ? 32 : 16);
+    a.slots = experts + a.P / 16;
+    a.down_slots = experts + a.P / tokens_per_block(f32 ? 3 : 2);
     a.KW = waves_per_tile(int64_t(experts) * (F / 16));
     a.o = moe_by_pairs(experts, a.P, F, N) ? o : nullptr;
-#define SVDQ_GATE(FMT_)                                       \
-  do {                                                        \
-    if (f32 && two) gate_up<FMT_, 3, 2>(a, s);                \
-    else if (f32) gate_up<FMT_, 3, 1>(a, s);                  \
-    else if (two) gate_up<FMT_, 2, 2>(a, s);                  \
-    else gate_up<FMT_, 2, 1>(a, s);                           \
+#define SVDQ_GATE(FMT_)             \
+  do {                              \
+    if (f32) gate_up<FMT_, 3>(a, s); \
+    else gate_up<FMT_, 2>(a, s);    \
   } while (0)
     if (fmt_g == kFmtMXFP4) SVDQ_GATE(kFmtMXFP4);
     else if (fmt_g == kFmtINT4) SVDQ_GATE(kFmtINT4);

@@ -329,20 +329,20 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
     return;
   }
   int rt = blockIdx.x, i = 0;
-  v4f acc[1] = {zero};
+  v4f acc = zero;
   for (;;) {
 #pragma unroll
     for (int j = 0; j < kFewDepth; ++j) {
       const int ks = w + i * W;
-      uint4 x[1][4];
+      uint4 x[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) x[0][u] = *reinterpret_cast<const uint4*>(xp + (ks * kKStep + k_of<FMT>(c, u)) * 2);
-      w4_step<FMT, 1>(st[j], ks, x, acc);
+      for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(xp + (ks * kKStep + k_of<FMT>(c, u)) * 2);
+      w4_step<FMT>(st[j], ks, x, acc);
       load(st[j]);
       keep_order();
       if (++i == n) {
-        finish(rt, acc[0]);
-        acc[0] = zero;
+        finish(rt, acc);
+        acc = zero;
         i = 0;
         rt += gridDim.x;
         if (rt >= tiles) return;

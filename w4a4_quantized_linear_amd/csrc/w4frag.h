@@ -261,34 +261,25 @@ __device__ __forceinline__ void w4_half(const W4Stage<kFmtINT4> (&st)[T], int ha
   }
 }
 
-// A whole 128-K step of one tile; x[b][u] is the B operand of MFMA u.
-template <int FMT, int NB, bool F16 = false>
-__device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const uint4 (&x)[NB][4], v4f (&acc)[NB]) {
+// A whole 128-K step of one tile; x[u] is the B operand of MFMA u.
+template <int FMT, bool F16 = false>
+__device__ __forceinline__ void w4_step(const W4Stage<FMT>& st, int ks, const uint4 (&x)[4], v4f& acc) {
   const W4Stage<FMT> one[1] = {st};
-  v4f a[1][NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) a[0][b] = acc[b];
+  v4f a[1][1] = {{acc}};
   if constexpr (FMT == kFmtINT4) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint4 h[2][NB];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) h[u][b] = x[b][2 * half + u];
-      w4_half<1, NB>(one, half, h, a);
+      const uint4 h[2][1] = {{x[2 * half]}, {x[2 * half + 1]}};
+      w4_half<1, 1>(one, half, h, a);
     }
   } else {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      uint4 h[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) h[b] = x[b][u];
-      w4_mfma<FMT, 1, NB, F16>(one, ks, u, h, a);
+      const uint4 h[1] = {x[u]};
+      w4_mfma<FMT, 1, 1, F16>(one, ks, u, h, a);
     }
   }
-#pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = a[0][b];
+  acc = a[0][0];
 }
 
 // The factor that the sums of a packed weight still lack: NVFP4's tensor scale
