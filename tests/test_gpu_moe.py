@@ -317,6 +317,91 @@ def test_block_as_used(torch_dev, M):
             assert torch.equal(a, b), f"replay {r}"
 
 
+def test_experts_most(torch_dev):
+    """The most experts and choices, in two parts (64 tokens of 2048 pairs, and 6): four experts' weights,
+    each 128 times."""
+    torch, dev = torch_dev
+    mix = Mixture(torch, dev, 4, 512, 512, 32, "nvfp4", "int4", seed=12)
+    of = np.arange(512) % 4
+    M, k, many = 70, 32, torch.from_numpy(of).to(dev)
+    mix.E, mix.pg, mix.pd = 512, mix.pg[many], mix.pd[many]
+    for name in ("wg", "mg", "wd", "md", "bg", "bd"):
+        setattr(mix, name, getattr(mix, name)[of])
+    ids, wt = mix.route(M, k)
+    mix.check(torch, dev, _bits(mix.rng.standard_normal((M, 512))), ids, wt, "most")
+
+
+def test_experts_beyond_4_gib(torch_dev):
+    """Experts whose bytes lie behind 32-bit offsets give the bits that the same experts do at the front."""
+    torch, dev = torch_dev
+    gu, dn = sq.Layer("mxfp4", 4096, 4096, 0), sq.Layer("mxfp4", 2048, 512, 0)
+    g = torch.Generator(device=dev)
+    g.manual_seed(5)
+    pg, pd = (sq.pack_experts(l, torch.randn((2, l.N, l.K), generator=g, device=dev) * l.K ** -0.5)
+              for l in (gu, dn))
+    of = torch.arange(512, device=dev) % 2
+    pg, pd = pg[of], pd[of]
+    assert pg.numel() > 2 ** 32
+    for M in (3, 70):
+        X = torch.randn((M, 4096), generator=g, device=dev).bfloat16()
+        ids = torch.tensor([[0, 1]], dtype=torch.int32, device=dev).repeat(M, 1)
+        wt = torch.rand((M, 2), generator=g, device=dev)
+        a, b = (sq.moe(gu, pg, dn, pd, X, i, wt) for i in (ids, ids + 510))
+        assert torch.equal(a, b) and bool((a != 0).any())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
+def test_long_calls(torch_dev, fmt):
+    """Calls that go through the plan and the pairs' products in memory: a router whose logits take a
+    kernel of their own and the experts in a graph, replayed on new tokens (new choices) between eager
+    calls; two calls at once on two streams; non-finite tokens; a call that no expert has a token of."""
+    torch, dev = torch_dev
+    M, k, H, N, E = 96, 8, 512, 48, 400
+    mix = Mixture(torch, dev, 6, H, 512, N, fmt, fmt, seed=21)
+    router = dev_tensor(_bits(mix.rng.standard_normal((E, H)) * 2 / np.sqrt(H)), torch, dev)
+    assert sq.moe_route_bytes(M, H, E) > 0
+
+    def step(x, **kw):
+        ids, wt = sq.moe_route(x, router, k)
+        return ids, wt, mix.run(x, ids % 7, wt, 0, **kw)       # 6 is no expert
+
+    sx = dev_tensor(_bits(mix.rng.standard_normal((M, H))), torch, dev)
+    step(sx)
+    torch.cuda.synchronize()
+    ws = torch.zeros(sq.moe_bytes(mix.gu, mix.dn, M, k), dtype=torch.uint8, device=dev)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = step(sx, workspace=ws)
+    for r in range(4):
+        new = dev_tensor(_bits(mix.rng.standard_normal((M, H))), torch, dev)
+        sx.copy_(new)
+        g.replay()
+        eager = step(new)
+        torch.cuda.synchronize()
+        for a, b in zip(kept, eager):
+            assert torch.equal(a, b), f"replay {r}"
+        ws.fill_(0xFF)
+    ids, wt, want = eager[0] % 7, eager[1], eager[2]
+    mix.check(torch, dev, new.cpu().numpy(), ids.cpu().numpy(), wt.cpu().numpy(), f"long {fmt}")
+
+    half = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    both = []
+    for _ in range(5):
+        both += [mix.run(new, ids, wt, 0, stream=s) for s in half]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in both)
+
+    for bits in (0x7FC0, 0x7F80, -128):
+        bad = new.clone()
+        bad[60, 100] = bits
+        y = mix.run(bad, ids, wt, 0)
+        ok = [m for m in range(M) if m != 60]
+        assert torch.equal(y[ok], want[ok]) and not bool(torch.isfinite(y[60]).any())
+    y = mix.run(new, torch.full_like(ids, -1), torch.full_like(wt, float("nan")), 0)
+    assert bool((y == 0).all())
+
+
 def test_refusals(torch_dev):
     torch, dev = torch_dev
     mix = Mixture(torch, dev, 2, 512, 512, 32, "mxfp4", "mxfp4", seed=1)
@@ -336,6 +421,10 @@ def test_refusals(torch_dev):
         with pytest.raises(sq.SvdqError) as e:
             mix.run(X, ids, wt, **kw)
         assert e.value.status == status
+    for n in (0, 33):
+        with pytest.raises(sq.SvdqError) as e:
+            mix.run(X, torch.zeros((3, n), dtype=torch.int32, device=dev), torch.zeros((3, n), device=dev), 0)
+        assert e.value.status == 2 or n == 0               # no choices: no ids either
     router = torch.zeros((4, 512), dtype=torch.bfloat16, device=dev)
     for a, kw in (((X, router[:, :256], 2), {}), ((X, router.float(), 2), {}), ((X, router, 2), dict(bias=wt[0])),
                   ((X, router, 2), dict(ids=ids[:2])), ((X, router, 2), dict(weights=wt.double())),

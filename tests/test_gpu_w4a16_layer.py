@@ -196,6 +196,33 @@ def test_streams_graphs_and_repeats(torch_dev):
         assert torch.equal(sy, eager), f"replay {k}"
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
+def test_largest_layer(torch_dev, fmt):
+    """65536 x 65536 (codes of 2 GiB): its first and last rows against layers of those rows alone,
+    whose groups of weights are the same.  64 features are not zero, so a sum has at most 80 roundings
+    whatever its order, each 2^-24 of at most sum |w x| <= 64 x 5 x 5 (INT4: of (24 + |q|) s |x|
+    twice, s <= 5 / 7, q <= 7, which is below 54 x 5 x 64)."""
+    torch, dev = torch_dev
+    K = N = 65536
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    R, one = torch.randn((N, K), generator=g, device=dev).clamp_(-5, 5), torch.ones(K, device=dev)
+    X = torch.zeros((20, K), device=dev).bfloat16()
+    at = torch.linspace(0, K - 1, 64, device=dev).long()
+    X[:, at] = torch.randn((20, 64), generator=g, device=dev).clamp(-5, 5).bfloat16()
+    big, rows = sq.Layer(fmt, K, N, 0), sq.Layer(fmt, K, 32, 0)
+    w = sq.pack_weight(big, R, None, None, one, None)
+    ends = [(slice(i, i + 32), sq.pack_weight(rows, R[i:i + 32].contiguous(), None, None, one, None))
+            for i in (0, 32768, N - 32)]
+    del R
+    for M in (1, 20):
+        y = sq.linear_w4a16(big, w, X[:M].contiguous(), sq.EPI_OUT_F32)
+        for at, we in ends:
+            z = sq.linear_w4a16(rows, we, X[:M].contiguous(), sq.EPI_OUT_F32)
+            lim = 2 * 80 * 2.0 ** -24 * 64 * 5 * (54 if fmt == "int4" else 5)
+            assert float((y[:, at] - z).abs().max()) <= lim and float(z.abs().max()) > 4
+
+
 def test_refusals(torch_dev):
     torch, dev = torch_dev
     layer = sq.Layer("mxfp4", 1024, 64, 16)

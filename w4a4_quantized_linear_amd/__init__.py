@@ -376,7 +376,7 @@ def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi:
         if out.shape[0] != M:
             raise ValueError(f"out: {out.shape[0]} rows for {M} tokens")
     L = lib()
-    ws = _space(workspace, L.svdq_moe_bytes(pg, pd, M, top_k), dev)
+    ws = _space(workspace, L.svdq_moe_bytes(pg, pd, M, top_k) or 1, dev)   # 0: invalid, the call's to report
     st = L.svdq_moe(pg, wg_packed.data_ptr(), pd, wd_packed.data_ptr(), E, X.data_ptr(), M, ldx, ids.data_ptr(),
                     weights.data_ptr(), top_k, out.data_ptr(), ldy, epi, None if ws is None else ws.data_ptr(),
                     0 if ws is None else ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
