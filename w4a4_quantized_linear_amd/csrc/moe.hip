@@ -347,11 +347,12 @@ __device__ __forceinline__ int down_slots(int P) { return P > kDownMinSlots ? P 
 // pairs of kGatePlanWords words each, ended by blocks without pairs up to the grid's `slots`.
 constexpr int kGatePlan = 16384;       // in words
 constexpr int kGatePlanWords = 32;
+constexpr int kPlanLdsWords = 3 * kMoeMaxE + 2;
 template <int S, bool GATE>
-__device__ __forceinline__ void moe_plan(const MoeArgs& a) {
+__device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
   constexpr int TPB = tokens_per_block(S), THREADS = 512;
-  __shared__ int cursor[kMoeMaxE], base[kMoeMaxE], gbase[kMoeMaxE];
-  __shared__ int total, gtotal;
+  int *const cursor = lds, *const base = lds + kMoeMaxE, *const gbase = lds + 2 * kMoeMaxE;
+  int &total = lds[3 * kMoeMaxE], &gtotal = lds[3 * kMoeMaxE + 1];
   const int tid = threadIdx.x, lane = tid & 63;
   for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
   __syncthreads();
@@ -413,7 +414,8 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a) {
 
 template <int S>
 __global__ void __launch_bounds__(512) moe_plan_kernel(MoeArgs a) {
-  moe_plan<S, true>(a);
+  __shared__ int lds[kPlanLdsWords];
+  moe_plan<S, true>(a, lds);
 }
 
 // Rows in LDS (S planes x n rows of K bf16, row_b bytes apart) to fp16, in place, scaled by
@@ -476,7 +478,7 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // the plan for the down product.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
-constexpr int kGateXLds = 49152;       // beside 16 KiB, two workgroups a CU
+constexpr int kGateXLds = 81664;       // two workgroups a CU
 template <int FMT, int S, bool DOWN, bool PLANNED>
 __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
   constexpr int DEPTH = FMT != kFmtINT4 ? 3 : 2;           // registers for two workgroups a CU
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
   constexpr int COLS = DOWN ? TPB : 16;
   static_assert(PLANNED || !DOWN, "down blocks are planned");
   extern __shared__ uint4 xlds[];                          // kGateXLds bytes
-  __shared__ v4f red[kGateWaves][2][64];
+  v4f (*const red)[2][64] = reinterpret_cast<v4f(*)[2][64]>(xlds);   // after the rows of X
   constexpr bool F16 = FMT == kFmtNVFP4;                   // rows in LDS become fp16
   __shared__ uint32_t top[COLS];
   const int tid = threadIdx.x;
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
     mine = __shfl(words, (lane & 15) + (DOWN ? 4 : 2));
   } else {
     if (slot == a.slots) {
-      if (blockIdx.x == 0) moe_plan<S, false>(a);
+      if (blockIdx.x == 0) moe_plan<S, false>(a, reinterpret_cast<int*>(xlds));
       return;
     }
     const uint64_t below = (uint64_t(1) << lane) - 1;
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
       }
     }
     if (KW > 1) {
+      lds_barrier();
       red[w][0][lane] = ag;
       red[w][1][lane] = au;
       lds_barrier();
