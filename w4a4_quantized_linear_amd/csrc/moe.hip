@@ -328,8 +328,12 @@ struct MoeArgs {
   int H, F, N, E, top_k, P;            // gate/up: H -> 2 F, down: F -> N
   int d_int4;
   int slots, down_slots, KW;           // blocks of pairs at most; waves that share a tile's K
-  uint32_t epi;
+  int planes;                          // of h
+  uint32_t epi, inv_h, inv_f;          // segment_inverse of H and F
 };
+
+// i / (K / 512) as i * segment_inverse(K) >> 20, for i up to 16 rows of at most 128 segments.
+__host__ __device__ inline uint32_t segment_inverse(int K) { return ((1u << 20) + K / 512 - 1) / (K / 512); }
 
 // A column of an MFMA that no pair has: beyond every buffer, so its loads read nothing (zeros).
 constexpr uint32_t kNoColumn = 0x80000000u;
@@ -348,9 +352,10 @@ __device__ __forceinline__ int down_slots(int P) { return P > kDownMinSlots ? P 
 constexpr int kGatePlan = 16384;       // in words
 constexpr int kGatePlanWords = 32;
 constexpr int kPlanLdsWords = 3 * kMoeMaxE + 2;
-template <int S, bool GATE>
+template <bool GATE>
 __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
-  constexpr int TPB = tokens_per_block(S), THREADS = 512;
+  constexpr int THREADS = 512;
+  const int TPB = a.planes == 3 ? tokens_per_block(3) : tokens_per_block(2);
   int *const cursor = lds, *const base = lds + kMoeMaxE, *const gbase = lds + 2 * kMoeMaxE;
   int &total = lds[3 * kMoeMaxE], &gtotal = lds[3 * kMoeMaxE + 1];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -407,15 +412,15 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
     const int id = a.ids[p];
     if (id < 0 || id >= a.E) continue;
     const int i = atomicAdd(&cursor[id], 1);
-    for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[id] + i / TPB) * KC + k) + 4 + i % TPB] = p;
+    const int b = a.planes == 3 ? i / tokens_per_block(3) : i / tokens_per_block(2);
+    for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[id] + b) * KC + k) + 4 + i - b * TPB] = p;
     if (GATE) gate[kGatePlanWords * (gbase[id] + i / 16) + 2 + i % 16] = p;
   }
 }
 
-template <int S>
 __global__ void __launch_bounds__(512) moe_plan_kernel(MoeArgs a) {
   __shared__ int lds[kPlanLdsWords];
-  moe_plan<S, true>(a, lds);
+  moe_plan<true>(a, lds);
 }
 
 // Rows in LDS (S planes x n rows of K bf16, row_b bytes apart) to fp16, in place, scaled by
@@ -479,16 +484,15 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
 constexpr int kGateXLds = 81664;       // two workgroups a CU
-template <int FMT, int S, bool DOWN, bool PLANNED>
+template <int FMT, int S, bool PLANNED>
 __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
-  constexpr int DEPTH = FMT != kFmtINT4 ? 3 : 2;           // registers for two workgroups a CU
+  constexpr bool DOWN = S > 1;
   constexpr int TPB = tokens_per_block(S);
-  constexpr int COLS = DOWN ? TPB : 16;
   static_assert(PLANNED || !DOWN, "down blocks are planned");
   extern __shared__ uint4 xlds[];                          // kGateXLds bytes
   v4f (*const red)[2][64] = reinterpret_cast<v4f(*)[2][64]>(xlds);   // after the rows of X
   constexpr bool F16 = FMT == kFmtNVFP4;                   // rows in LDS become fp16
-  __shared__ uint32_t top[COLS];
+  __shared__ uint32_t top[TPB];
   const int tid = threadIdx.x;
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tl = lane & 15, c = lane >> 4;
@@ -502,26 +506,26 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
     mine = __shfl(words, (lane & 15) + (DOWN ? 4 : 2));
   } else {
     if (slot == a.slots) {
-      if (blockIdx.x == 0) moe_plan<S, false>(a, reinterpret_cast<int*>(xlds));
+      if (blockIdx.x == 0) moe_plan<false>(a, reinterpret_cast<int*>(xlds));
       return;
     }
     const uint64_t below = (uint64_t(1) << lane) - 1;
     const int id = lane < a.P ? a.ids[lane] : -1;
     uint64_t left = __ballot(id >= 0 && id < a.E), eq = 0;
-    int t0 = slot * COLS;                                  // the block's first pair among the expert's
+    int t0 = slot * TPB;                                  // the block's first pair among the expert's
     while (left) {
       ex = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
       eq = __ballot(id == ex);
-      const int blocks = (__popcll(eq) + COLS - 1) / COLS;
-      if (t0 < blocks * COLS) break;
-      t0 -= blocks * COLS;
+      const int blocks = (__popcll(eq) + TPB - 1) / TPB;
+      if (t0 < blocks * TPB) break;
+      t0 -= blocks * TPB;
       left &= ~eq;
     }
     if (!left) return;
     T = __popcll(eq);
     const int to = eq >> lane & 1 ? __popcll(eq & below) : T + __popcll(~eq & below);
     mine = __shfl(__builtin_amdgcn_ds_permute(to * 4, lane), (lane + t0) & 63);
-    T = T - t0 < COLS ? T - t0 : COLS;
+    T = T - t0 < TPB ? T - t0 : TPB;
   }
   ex = __builtin_amdgcn_readfirstlane(ex);
   auto pair_of = [&](int i) { return __shfl(mine, i); };
@@ -535,9 +539,9 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
   const W4Rows<FMT> rows(blob + (DOWN ? a.d_codes : a.g_codes), blob + (DOWN ? a.d_scales : a.g_scales), K,
                          DOWN ? a.Nd_pad : a.Ng_pad);
   const uint16_t* const xbase = DOWN ? a.h : a.X;
-  const uint32_t xbytes = uint32_t((DOWN ? int64_t(S) * a.P * a.F : int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2);
   const float gs = w4_tensor_scale<FMT>(blob + (DOWN ? a.d_amax : a.g_amax));
-  // column b * 16 + tl: element offset of its row of X (of h), or no pair
+  const uint32_t xbytes = uint32_t((DOWN ? int64_t(S) * a.P * a.F : int64_t(a.P / a.top_k - 1) * a.ldx + a.H) * 2);
+  // element offset of a pair's row of X (of h)
   auto row_of = [&](int p, int plane) -> int64_t { return DOWN ? (int64_t(plane) * a.P + p) * a.F : int64_t(p / a.top_k) * a.ldx; };
   {
     v4f ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
@@ -546,10 +550,48 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
       rows.load(rt0, ks, i < n, lane, g);
       rows.load(rt1, ks, i < n, lane, u);
     };
-    const int row_b = few_row_bytes(K), xrows = DOWN ? S * T : T;
-    if (xrows * row_b <= kGateXLds) {
-      // few pairs: their rows of X once into LDS.  A load of a step's columns costs the L1 as many
-      // cycles whatever the number of columns that are there.
+    // The block's rows of X (of h) go through LDS: a load of a step's columns from memory costs the L1
+    // as many cycles as sixteen, however many there are, for every wave.  Rows too long for it
+    // come in parts.
+    const int xrows = S * T;
+    uint8_t* const xl = reinterpret_cast<uint8_t*>(xlds);
+    // kc of K from k0 on; a wave's copies of 64 lanes x 16 bytes, `batch` in flight (an absent one,
+    // through a buffer of no bytes, still costs the L1 a load)
+    auto fill_by = [&](auto batch, int k0, int segs, int row_b, uint32_t inv) {
+      constexpr int N = decltype(batch)::value;
+      for (int g0 = w; g0 < xrows * segs; g0 += N * kGateWaves) {
+        uint4 v[N];
+        int at[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int g = g0 + j * kGateWaves;
+          const int r = int(uint32_t(g) * inv >> 20), seg = g - r * segs, plane = (S > 1 && r >= T) + (S > 2 && r >= 2 * T);
+          const int p = __builtin_amdgcn_readlane(mine, (r - plane * T) & 15);
+          v[j] = buffer_load16(make_rsrc(xbase, g < xrows * segs ? xbytes : 0), uint32_t(lane) * 16,
+                               uint32_t(row_of(p, plane) + k0 + seg * 512) * 2);
+          at[j] = r * row_b + seg * 1024;
+        }
+        keep_order();                                      // all loads before the first store
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (g0 + j * kGateWaves < xrows * segs) *reinterpret_cast<uint4*>(xl + at[j] + lane * 16) = v[j];
+      }
+    };
+    auto fill = [&](int k0, int kc, int row_b, uint32_t inv) {
+      if (xrows * kc <= 2 * kGateWaves * 512)
+        fill_by(std::integral_constant<int, 1>(), k0, kc / 512, row_b, inv);
+      else
+        fill_by(std::integral_constant<int, 8>(), k0, kc / 512, row_b, inv);
+    };
+    const int t = tl % TPB, pl = tl / TPB;
+    const int row = pl < S && t < T ? pl * T + t : 0;        // any where there is no column
+    auto operands = [&](const uint8_t* xp, int k, uint4 (&x)[4]) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        x[u] = *reinterpret_cast<const uint4*>(xp + (k + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
+    };
+    if (xrows * few_row_bytes(K) <= kGateXLds) {
+      const int row_b = few_row_bytes(K);
       constexpr int AHEAD = FMT == kFmtINT4 ? 3 : 4;
       W4Stage<FMT> sg[AHEAD], su[AHEAD];
 #pragma unroll
@@ -557,36 +599,16 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
         load_w(j, sg[j], su[j]);
         keep_order();
       }
-      uint8_t* const xl = reinterpret_cast<uint8_t*>(xlds);
-      // a wave's copies of 64 lanes x 16 bytes, eight in flight
-      const int segs = K / 512, all = xrows * segs;
-      for (int g0 = w; g0 < all; g0 += 8 * kGateWaves) {
-        uint4 v[8];
-        int r[8], sg[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int g = g0 + j * kGateWaves < all ? g0 + j * kGateWaves : g0;
-          r[j] = g / segs;
-          sg[j] = g - r[j] * segs;
-          const uint16_t* const src = xbase + row_of(pair_of(DOWN ? r[j] % T : r[j]), DOWN ? r[j] / T : 0);
-          v[j] = *reinterpret_cast<const uint4*>(src + sg[j] * 512 + lane * 8);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (g0 + j * kGateWaves < all) *reinterpret_cast<uint4*>(xl + r[j] * row_b + sg[j] * 1024 + lane * 16) = v[j];
-      }
-      if constexpr (F16) rows_to_f16<DOWN ? S : 1, kGateWaves>(xl, row_b, K, T, top);
+      fill(0, K, row_b, DOWN ? a.inv_f : a.inv_h);
+      if constexpr (F16) rows_to_f16<S, kGateWaves>(xl, row_b, K, T, top);
       lds_barrier();
-      const int t = tl % TPB, pl = tl / TPB;
-      const uint8_t* const xp = xl + (DOWN ? (pl < S && t < T ? pl * T + t : 0) : tl < T ? tl : T - 1) * row_b;
+      const uint8_t* const xp = xl + row * row_b;
       for (int i0 = 0; i0 < n; i0 += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
           const int ks = kq + (i0 + j < n ? i0 + j : n - 1) * KW;   // past the last step: codes are zeros
           uint4 x[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            x[u] = *reinterpret_cast<const uint4*>(xp + (ks * kKStep + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
+          operands(xp, ks * kKStep, x);
           w4_step<FMT, F16>(sg[j], ks, x, ag);
           w4_step<FMT, F16>(su[j], ks, x, au);
           load_w(i0 + j + AHEAD, sg[j], su[j]);
@@ -594,38 +616,37 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
         }
       }
       if constexpr (F16) {
-        const int i = DOWN ? t : tl;
-        const float back = 1.0f / f16_row_scale(__uint_as_float(top[i < T ? i : 0]));   // a power of two
+        const float back = 1.0f / f16_row_scale(__uint_as_float(top[t < T ? t : 0]));   // a power of two
         ag *= back;
         au *= back;
       }
     } else {
-      const int i = DOWN ? tl % TPB : tl, plane = DOWN ? tl / TPB : 0;
-      const int p = pair_of(i < T ? i : 0);
-      const uint32_t xoff = i < T && plane < S ? uint32_t(row_of(p, plane) + c * 8) * 2 : kNoColumn;
-      struct Stage { W4Stage<FMT> g, u; uint4 x[4]; };
-      auto load = [&](int i, Stage& st) {
-        load_w(i, st.g, st.u);
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(xbase, i < n ? xbytes : 0);
+      // a part is at least 2048 of K, so each of its waves has an even number of steps
+      constexpr int AHEAD = 2;
+      const int KC = (kGateXLds / xrows - 16) / 2 & ~1023, row_b = few_row_bytes(KC), per = KC / kKStep / KW;
+      const uint8_t* const xp = xl + row * row_b;
+      W4Stage<FMT> sg[AHEAD], su[AHEAD];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) st.x[u] = buffer_load16(r, xoff + u * 64, uint32_t(kq + i * KW) * kKStep * 2);
-      };
-      Stage st[DEPTH];
-#pragma unroll
-      for (int j = 0; j < DEPTH; ++j) {
-        load(j, st[j]);
+      for (int j = 0; j < AHEAD; ++j) {
+        load_w(j, sg[j], su[j]);
         keep_order();
       }
-      for (int i0 = 0; i0 < n; i0 += DEPTH) {
+      for (int k0 = 0, i = 0; k0 < K; k0 += KC) {
+        if (k0) lds_barrier();                             // the part before is read
+        const int kc = K - k0 < KC ? K - k0 : KC;
+        fill_by(std::integral_constant<int, 8>(), k0, kc / 512, row_b, segment_inverse(kc));
+        lds_barrier();
+        for (const int end = i + per < n ? i + per : n; i < end; i += AHEAD) {
 #pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {
-          // past the last step codes and columns are zeros
-          const int ks = kq + (i0 + j) * KW;
-          if (!DOWN) to_operands<FMT>(st[j].x);            // h is stored as operands
-          w4_step<FMT>(st[j].g, ks, st[j].x, ag);
-          w4_step<FMT>(st[j].u, ks, st[j].x, au);
-          load(i0 + j + DEPTH, st[j]);
-          keep_order();
+          for (int j = 0; j < AHEAD; ++j) {
+            const int ks = kq + (i + j < n ? i + j : n - 1) * KW;   // past the last step: codes are zeros
+            uint4 x[4];
+            operands(xp, ks * kKStep - k0, x);
+            w4_step<FMT>(sg[j], ks, x, ag);
+            w4_step<FMT>(su[j], ks, x, au);
+            load_w(i + j + AHEAD, sg[j], su[j]);
+            keep_order();
+          }
         }
       }
     }
@@ -682,13 +703,13 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           hv[e] = ((a.epi & SVDQ_EPI_GELU) ? gelu_erf(g[e]) : g[e] / (1.0f + expf(-g[e]))) * u[e];
-        uint4 pl[S];
-        split_planes<S>(hv, pl);
+        uint4 hp[3];
+        split_planes<3>(hv, hp);
         // in the order of the down product's operands
         const int kk = row & (kKStep - 1), at = row - kk + (a.d_int4 ? stored_at<kFmtINT4>(kk) : stored_at<kFmtMXFP4>(kk));
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-          *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + at) = make_uint2(pl[s].x, pl[s].y);
+        for (int s = 0; s < 3; ++s)
+          if (s < a.planes) *reinterpret_cast<uint2*>(a.h + (int64_t(s) * a.P + p) * a.F + at) = make_uint2(hp[s].x, hp[s].y);
       }
     }
   }
@@ -712,6 +733,7 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
         wt[j] = a.weights[p];
         v[j] = *reinterpret_cast<const v4f*>(a.o + int64_t(p) * a.N + row);
       }
+      keep_order();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j0 + j >= a.top_k || id[j] < 0 || id[j] >= a.E) continue;
@@ -819,8 +841,11 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
     for (int g0 = w; g0 < all; g0 += 8 * kDownWaves) {
       uint4 v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = reinterpret_cast<const uint4*>(a.h)[(g0 + j * kDownWaves < all ? g0 + j * kDownWaves : g0) * 64 + lane];
+      for (int j = 0; j < 8; ++j) {                        // past the end: through a buffer of no bytes
+        const int g = g0 + j * kDownWaves;
+        v[j] = buffer_load16(make_rsrc(a.h, g < all ? h_bytes : 0), uint32_t(lane) * 16, uint32_t(g) * 1024);
+      }
+      keep_order();                                        // all loads before the first store
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int g = g0 + j * kDownWaves;
@@ -896,14 +921,14 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   }
 }
 
-template <int FMT, int S>
+template <int FMT>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
   const unsigned tiles = unsigned(a.F / 16 * a.KW / kGateWaves);
   if (a.P <= 64) {
-    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, false, false>), dim3(tiles, unsigned(a.slots + 1)), dim3(512), kGateXLds, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, 1, false>), dim3(tiles, unsigned(a.slots + 1)), dim3(512), kGateXLds, s, a);
   } else {
-    hipLaunchKernelGGL((moe_plan_kernel<S>), dim3(1), dim3(512), 0, s, a);
-    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, false, true>), dim3(tiles, unsigned(a.slots)), dim3(512), kGateXLds, s, a);
+    hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, 1, true>), dim3(tiles, unsigned(a.slots)), dim3(512), kGateXLds, s, a);
   }
 }
 
@@ -921,7 +946,7 @@ static void down(MoeArgs a, hipStream_t s) {
     a.KW = waves_per_tile(int64_t(experts) * tiles);
     const int per = kGateWaves / a.KW;
     const dim3 grid(unsigned((tiles + per - 1) / per), unsigned(a.down_slots));
-    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, true, true>), grid, dim3(512), kGateXLds, s, a);
+    hipLaunchKernelGGL((moe_rows_kernel<FMT, S, true>), grid, dim3(512), kGateXLds, s, a);
     const int64_t quads = int64_t(a.P) / a.top_k * (a.N / 4);
     hipLaunchKernelGGL((moe_join_kernel<S == 3>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, s, a);
     return;
@@ -949,7 +974,9 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
   float* const o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMoePlanBytes + moe_h_bytes(M, top_k, F));
   a.ldx = ldx; a.ldy = ldy; a.Ng_pad = lg.N_pad; a.Nd_pad = ld.N_pad;
   a.H = H; a.F = F; a.N = N; a.E = E; a.top_k = top_k; a.epi = epi; a.d_int4 = fmt_d == kFmtINT4;
+  a.inv_h = segment_inverse(H); a.inv_f = segment_inverse(F);
   const bool f32 = (epi & SVDQ_EPI_OUT_F32) != 0;
+  a.planes = f32 ? 3 : 2;
   // a part's pairs fit the kernels' LDS and its rows of X one buffer
   const int64_t span = (int64_t(1) << 31) / (2 * ldx), most = kMoeMaxPairs / top_k, part = span < most ? span : most;
   for (int64_t m0 = 0; m0 < M; m0 += part) {
@@ -961,18 +988,12 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     a.Y = static_cast<uint8_t*>(Y) + m0 * ldy * (f32 ? 4 : 2);
     const int experts = E < a.P ? E : a.P; // that may be asked for
     a.slots = experts + a.P / 16;
-    a.down_slots = experts + a.P / tokens_per_block(f32 ? 3 : 2);
+    a.down_slots = experts + a.P / tokens_per_block(a.planes);
     a.KW = waves_per_tile(int64_t(experts) * (F / 16));
     a.o = moe_by_pairs(experts, a.P, F, N) ? o : nullptr;
-#define SVDQ_GATE(FMT_)             \
-  do {                              \
-    if (f32) gate_up<FMT_, 3>(a, s); \
-    else gate_up<FMT_, 2>(a, s);    \
-  } while (0)
-    if (fmt_g == kFmtMXFP4) SVDQ_GATE(kFmtMXFP4);
-    else if (fmt_g == kFmtINT4) SVDQ_GATE(kFmtINT4);
-    else SVDQ_GATE(kFmtNVFP4);
-#undef SVDQ_GATE
+    if (fmt_g == kFmtMXFP4) gate_up<kFmtMXFP4>(a, s);
+    else if (fmt_g == kFmtINT4) gate_up<kFmtINT4>(a, s);
+    else gate_up<kFmtNVFP4>(a, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 #define SVDQ_DOWN(FMT_)             \
