@@ -179,10 +179,11 @@ def test_experts(torch_dev, case):
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
 @pytest.mark.parametrize("M,k,E,H,Fh,N", [(12, 4, 36, 512, 2048, 4144), (24, 8, 40, 1536, 2048, 4096),
-                                           (6, 5, 24, 4096, 512, 512)])
+                                           (6, 5, 24, 4096, 512, 512), (3, 2, 2, 11264, 512, 64),
+                                           (40, 4, 6, 4608, 5632, 96), (64, 1, 1, 10240, 4608, 160)])
 def test_experts_large(torch_dev, fmt, M, k, E, H, Fh, N):
     """Sizes that take the other forms (pairs' products through memory for at most 64 pairs and for
-    more, few rows in LDS and many), against float64 on the GPU from the packed weights' own codes
+    more, few rows in LDS, many, and rows that come in parts), against float64 on the GPU from the packed weights' own codes
     and scales."""
     torch, dev = torch_dev
     g = torch.Generator(device=dev)

@@ -329,6 +329,7 @@ struct MoeArgs {
   int d_int4;
   int slots, down_slots, KW;           // blocks of pairs at most; waves that share a tile's K
   int planes;                          // of h
+  int cols, cols_inv;                  // unplanned gate/up: pairs a block, 65536 / cols rounded up
   uint32_t epi, inv_h, inv_f;          // segment_inverse of H and F
 };
 
@@ -512,20 +513,21 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
     const uint64_t below = (uint64_t(1) << lane) - 1;
     const int id = lane < a.P ? a.ids[lane] : -1;
     uint64_t left = __ballot(id >= 0 && id < a.E), eq = 0;
-    int t0 = slot * TPB;                                  // the block's first pair among the expert's
+    int t0 = slot;                                         // the block among the expert's
     while (left) {
       ex = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)left) - 1);
       eq = __ballot(id == ex);
-      const int blocks = (__popcll(eq) + TPB - 1) / TPB;
-      if (t0 < blocks * TPB) break;
-      t0 -= blocks * TPB;
+      const int blocks = (__popcll(eq) + a.cols - 1) * a.cols_inv >> 16;
+      if (t0 < blocks) break;
+      t0 -= blocks;
       left &= ~eq;
     }
     if (!left) return;
     T = __popcll(eq);
+    t0 *= a.cols;                                          // its first pair
     const int to = eq >> lane & 1 ? __popcll(eq & below) : T + __popcll(~eq & below);
     mine = __shfl(__builtin_amdgcn_ds_permute(to * 4, lane), (lane + t0) & 63);
-    T = T - t0 < TPB ? T - t0 : TPB;
+    T = T - t0 < a.cols ? T - t0 : a.cols;
   }
   ex = __builtin_amdgcn_readfirstlane(ex);
   auto pair_of = [&](int i) { return __shfl(mine, i); };
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
       for (int u = 0; u < 4; ++u)
         x[u] = *reinterpret_cast<const uint4*>(xp + (k + (DOWN ? u * 32 + c * 8 : k_of<FMT>(c, u))) * 2);
     };
-    if (xrows * few_row_bytes(K) <= kGateXLds) {
+    if (!PLANNED || xrows * few_row_bytes(K) <= kGateXLds) {
       const int row_b = few_row_bytes(K);
       constexpr int AHEAD = FMT == kFmtINT4 ? 3 : 4;
       W4Stage<FMT> sg[AHEAD], su[AHEAD];
@@ -621,9 +623,9 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
         au *= back;
       }
     } else {
-      // a part is at least 2048 of K, so each of its waves has an even number of steps
+      // a part is a multiple of 2048 of K, so each wave has an even number of its steps
       constexpr int AHEAD = 2;
-      const int KC = (kGateXLds / xrows - 16) / 2 & ~1023, row_b = few_row_bytes(KC), per = KC / kKStep / KW;
+      const int KC = (kGateXLds / xrows - 16) / 2 & ~2047, row_b = few_row_bytes(KC), per = KC / kKStep / KW;
       const uint8_t* const xp = xl + row * row_b;
       W4Stage<FMT> sg[AHEAD], su[AHEAD];
 #pragma unroll
@@ -836,22 +838,12 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
   };
   begin();
   if constexpr (HL) {
-    // a wave's copies of 64 lanes x 16 bytes, eight in flight
-    const int segs = a.F / 512, all = S * a.P * segs;
-    for (int g0 = w; g0 < all; g0 += 8 * kDownWaves) {
-      uint4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {                        // past the end: through a buffer of no bytes
-        const int g = g0 + j * kDownWaves;
-        v[j] = buffer_load16(make_rsrc(a.h, g < all ? h_bytes : 0), uint32_t(lane) * 16, uint32_t(g) * 1024);
-      }
-      keep_order();                                        // all loads before the first store
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int g = g0 + j * kDownWaves;
-        if (g < all) *reinterpret_cast<uint4*>(hl + g / segs * row_b + g % segs * 1024 + lane * 16) = v[j];
-      }
-    }
+    // a wave's copies of 64 lanes x 16 bytes, one after the other: together, the absent ones of few
+    // pairs cost more (9.0 against 8.6 us at one token, 4 of 32 experts, 2048 -> 2048)
+    const int segs = a.F / 512;
+    for (int g = w; g < S * a.P * segs; g += kDownWaves)
+      *reinterpret_cast<uint4*>(hl + g / segs * row_b + g % segs * 1024 + lane * 16) =
+          reinterpret_cast<const uint4*>(a.h)[g * 64 + lane];
   }
   // the pairs' weights; a pair without an expert adds zero
   for (int p = tid; p < a.P; p += 1024) {
@@ -924,7 +916,7 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
 template <int FMT>
 static void gate_up(const MoeArgs& a, hipStream_t s) {
   const unsigned tiles = unsigned(a.F / 16 * a.KW / kGateWaves);
-  if (a.P <= 64) {
+  if (a.cols) {
     hipLaunchKernelGGL((moe_rows_kernel<FMT, 1, false>), dim3(tiles, unsigned(a.slots + 1)), dim3(512), kGateXLds, s, a);
   } else {
     hipLaunchKernelGGL(moe_plan_kernel, dim3(1), dim3(512), 0, s, a);
@@ -987,7 +979,11 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     a.weights = weights + m0 * top_k;
     a.Y = static_cast<uint8_t*>(Y) + m0 * ldy * (f32 ? 4 : 2);
     const int experts = E < a.P ? E : a.P; // that may be asked for
-    a.slots = experts + a.P / 16;
+    // at most 64 pairs: no plan, if at least four rows of X fit the LDS whole
+    a.cols = kGateXLds / few_row_bytes(H) < 16 ? kGateXLds / few_row_bytes(H) : 16;
+    if (a.P > 64 || a.cols < 4) a.cols = 0;
+    a.cols_inv = a.cols ? (65535 + a.cols) / a.cols : 0;
+    a.slots = experts + a.P / (a.cols ? a.cols : 16);
     a.down_slots = experts + a.P / tokens_per_block(a.planes);
     a.KW = waves_per_tile(int64_t(experts) * (F / 16));
     a.o = moe_by_pairs(experts, a.P, F, N) ? o : nullptr;

@@ -43,36 +43,6 @@ __device__ __forceinline__ int stored_at(int kk) {           // kk: an element o
   return u * 32 + c * 8 + (kk & 7);
 }
 
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {   // a's upper half of lanes with b's lower
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {   // a's odd rows of 16 lanes with b's even rows
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap32(uint4& a, uint4& b) {
-  swap32(a.x, b.x); swap32(a.y, b.y); swap32(a.z, b.z); swap32(a.w, b.w);
-}
-__device__ __forceinline__ void swap16(uint4& a, uint4& b) {
-  swap16(a.x, b.x); swap16(a.y, b.y); swap16(a.z, b.z); swap16(a.w, b.w);
-}
-
-// A step of a row loaded in its natural order, x[v] of lane group c the elements 32 v + 8 c .. + 7
-// (64 bytes of a row at a time), to the MFMAs' operands: x[u] the elements k_of(c, u) .. + 7.
-template <int FMT>
-__device__ __forceinline__ void to_operands(uint4 (&x)[4]) {
-  if (FMT == kFmtINT4) {
-    swap32(x[0], x[1]); swap16(x[0], x[1]);
-    swap32(x[2], x[3]); swap16(x[2], x[3]);
-  } else {                                                   // a 4 x 4 transpose of registers and lane groups
-    swap32(x[0], x[2]); swap32(x[1], x[3]);
-    swap16(x[0], x[1]); swap16(x[2], x[3]);
-  }
-}
-
 // Codes and scales of one 16-row tile and 128-K step, as one lane holds them.
 template <int FMT>
 struct W4Stage {
