@@ -257,10 +257,14 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
 /* The experts' products of a mixture of experts, for few tokens:
  *     h[m, j] = act(X[m] Wg_e^T + bg_e) * (X[m] Wu_e^T + bu_e),   e = ids[m, j],
  *     Y[m]    = sum_j weights[m, j] (h[m, j] Wd_e^T + bd_e),
- * act = SiLU, or GELU (erf form) with SVDQ_EPI_GELU; the biases with SVDQ_EPI_BIAS.  Two
- * launches, each reading the weights of an expert only if a token asks for it.  Sums are
- * fp32 in a fixed order (the same call gives the same bits); h is not rounded to bf16 (it is
- * kept to 2^-18, or to fp32's own rounding with SVDQ_EPI_OUT_F32).
+ * act = SiLU, or GELU (erf form) with SVDQ_EPI_GELU; the biases with SVDQ_EPI_BIAS.  Two to
+ * four launches (long calls plan their blocks in one and add a token's pairs in another); the
+ * weights of an expert are read only if a token asks for it.  Sums are fp32 in a fixed order
+ * (the same call gives the same bits); h is not rounded to bf16 (it is kept to 2^-18, or to
+ * fp32's own rounding with SVDQ_EPI_OUT_F32).  With NVFP4 experts rows may be held in fp16,
+ * scaled by a power of two for each row: X is then exact but for what lies below 2^-28 of its
+ * row's largest element, off by at most 2^-39 of that, and h is kept to 2^-22 (2^-26 with
+ * SVDQ_EPI_OUT_F32).
  *   dg, wg_packed  one expert's gate and up projection as one layer, K = H inputs, N = 2 F
  *                  outputs, rows [gate | up]; E blobs of svdq_pack_weight, one after the
  *                  other, svdq_weight_bytes(dg) apart
@@ -272,8 +276,8 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
  *              expert on another device or a padded token)
  *   Y          device, M x N, row stride ldy, bf16, or float32 with SVDQ_EPI_OUT_F32
  *   workspace  device, at least svdq_moe_bytes(dg, dd, M, top_k) bytes, 256-byte aligned
- * Any M >= 0 is computed correctly (calls of more than 2048 pairs run in parts, two launches
- * each).  dg->N != 2 dd->K, E outside [1, 512] or top_k outside [1, 32] give SVDQ_ERR_SHAPE,
+ * Any M >= 0 is computed correctly (calls of more than 2048 pairs run in parts, launches of
+ * their own each).  dg->N != 2 dd->K, E outside [1, 512] or top_k outside [1, 32] give SVDQ_ERR_SHAPE,
  * a rank other than 0 or other flags SVDQ_ERR_FORMAT; other checks and errors as svdq_linear.
  * A token with non-finite features gives a non-finite row; no other row changes. */
 size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k);

@@ -26,7 +26,9 @@ diffusion inference in Diffusers" page; SVDQuant abstract, arXiv 2411.05007):
                   embedding on the layer output (the Nunchaku in Diffusers
                   page, section "Quantizing your own model").
 * w4a16.py     -- the 4-bit weight x 16-bit activation linear of the second
-                  kernel family (AWQ) on the Nunchaku in Diffusers page.
+                  kernel family (AWQ) on the Nunchaku in Diffusers page; and a
+                  whole layer (smoothing, low-rank branch) on 16-bit activations.
+* moe.py       -- the router and the 4-bit experts of a mixture of experts.
 * layer.py     -- the layer output of section 4.2:
                   X W = X_hat W_hat ~ X_hat L1 L2 + Q(X_hat) Q(R), plus bias and
                   an optional GELU, in float64; the error measure and bound of

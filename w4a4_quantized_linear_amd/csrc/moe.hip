@@ -149,7 +149,8 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, co
 // is chosen does not hang on the order of summation.
 //
 // One workgroup: a token.  Wave w takes experts w, w + 16, ..., four at a time, its lanes 8
-// consecutive K each; wave 0 then chooses.  Bound by the CU's fp64 conversions and FMAs.
+// consecutive K each; wave 0 then chooses.  Bound by the CU's fp64 conversions and FMAs: 1 x 2048 ->
+// 64, 7.6 us (10.4 us a call; 14.7 with the two kernels below).
 constexpr int kRouteOneWaves = 16;
 template <int PER>
 __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a) {
@@ -480,8 +481,15 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // of codes.  (Blocks of 32 pairs, which halve the reads of an expert with many, leave one workgroup
 // a CU: 67 against 62 us at 48 tokens, 8 of 24 experts, 3584 -> 2 x 1536.)
 // PLANNED: the blocks are in the plan.  Otherwise (gate/up of at most 64 pairs) every wave finds its
-// block by ballots, and the grid's last row (blockIdx.y == slots) holds one workgroup that writes
-// the plan for the down product.
+// block of up to a.cols pairs by ballots, which saves the plan's launch (4.5 us and what it costs the
+// host), and the grid's last row (blockIdx.y == slots) holds one workgroup that writes the plan for
+// the down product.
+//
+// Bound by the weights' bytes where experts have few pairs: MXFP4, 64 tokens, 6 of 64 experts, 4096 ->
+// 2 x 2048, gate/up 100 us for 571 MB (5.7 TB/s; a kernel that only reads reaches 6.0), down 55 us for
+// 285 MB (5.2 TB/s).  By L1 and LDS reads of the columns where they have many: 128 tokens, 4 of 16,
+// 2048 -> 2 x 1024, 21 and 29 us (experts of 32 pairs are read two and four times, from L2).  By
+// latency at one token: 4 of 32, 2048 -> 2 x 2048, 8.8 us for 18 MB.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 4096;
 constexpr int kGateXLds = 81664;       // two workgroups a CU
@@ -717,7 +725,8 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
   }
 }
 
-// Y[m] = sum_j w_j o[m, j], j in order; a pair without an expert adds nothing.
+// Y[m] = sum_j w_j o[m, j], j in order; a pair without an expert adds nothing.  4.3 us for 64 tokens of
+// 6 x 4096 (6.3 MB from L2): a launch's start and one round of loads.
 template <bool OUT_F32>
 __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
   const int per = a.N / 4, total = a.P / a.top_k * per;
@@ -755,7 +764,9 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
 // Down rows.  One workgroup: 16 output rows of all tokens, 16 waves.  A unit is one column block of
 // the plan and one of KC chunks of K; waves take every sixteenth unit, one pipeline running on from
 // unit to unit, and leave each pair's sums in a place of its own, so the sum over a token's experts
-// has one order.
+// has one order.  Bound by the latency of the first loads and by one CU's L1: 8.4 us at one token, 4 of
+// 32 experts, 2048 -> 2048 MXFP4 (9 MB); 19.5 us at 7 tokens, 5 of 60, 1024 -> 2560 NVFP4 (160
+// workgroups for 256 CUs; through memory instead 15.0 + 4.7 us and a launch more).
 constexpr int64_t kDownLds = 163840;   // HL: all of h in LDS where it fits (one workgroup a CU)
 
 template <int FMT, int S, bool HL>

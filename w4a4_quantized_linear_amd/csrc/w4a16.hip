@@ -3,9 +3,13 @@
 //   Y[m, n] = act( sum_k deQ(R)[n, k] x_hat[m, k] + sum_i L2[i, n] D[m, i] + b[n] ),
 //   x_hat = fp32(X / lambda),  D = X_hat L1.
 //
-// Two launches.  w4a16_prepare_kernel divides by lambda, splits x_hat into bf16
-// planes (w4frag.h) and forms D's partial sums, one per 512 of K;
-// w4a16_kernel streams the codes once per 16 columns.
+// What is to be read is the weights, so few tokens are bound by bytes in principle and by
+// latency in practice: 4096 x 4096 INT4 is 9 MB, 1.9 us at a copy's rate, and a launch that reads
+// 25 MB takes 7.8 us of which half is start and drain.  Two forms (layout.h, w4a16_plan):
+//   w4a16_few_kernel   all tokens' planes are columns of one MFMA: one launch.
+//   w4a16_wide_kernel  more: w4a16_prepare_kernel divides by lambda, splits x_hat into bf16
+//                      planes (w4frag.h) in the order of the B operands and forms D's partial
+//                      sums, one per 512 of K; the product; w4a16_join_kernel adds parts of K.
 #include <hip/hip_runtime.h>
 
 #include "svdq.h"
@@ -31,7 +35,8 @@ struct W4A16LinearArgs {
 constexpr int kPrepWaves = 8;          // 64 K each
 constexpr int kPrepTiles = 4;          // 16-rank tiles whose sums meet in LDS at a time
 
-// One workgroup: 16 tokens, 512 of K.
+// One workgroup: 16 tokens, 512 of K.  4.6 us for 8 tokens of 4096, 6.0 us for 33 of 12288: the
+// latency of one dependent chain (X and lambda, the division, the MFMAs, the exchange), not bytes.
 template <int S>
 __global__ void __launch_bounds__(512) w4a16_prepare_kernel(W4A16LinearArgs a) {
   __shared__ v4f red[kPrepWaves][kPrepTiles][64];
@@ -128,6 +133,10 @@ __device__ __forceinline__ void w4a16_store(const W4A16LinearArgs& a, int64_t m,
 // wave w the 128-K steps w, w + 8, ..., kFewDepth steps of codes in flight, the pipeline running
 // on from tile to tile.  The waves' sums meet in LDS (two buffers, so one barrier a tile); one
 // wave, another each tile, adds them and the up projection and writes the tile.
+//
+// Bound by start-up and latency: 6.0 us for 1 x 1024 -> 1024 MXFP4 rank 16, 9.5 us for 1 x 4096 ->
+// 4096 INT4 rank 32 (9.9 MB), 12.9 us for 5 x 2048 -> 8208 NVFP4 rank 64 (11 MB).  The two launches
+// that this replaces (x_hat and D prepared, then streamed) took 12.7 us at 1 x 4096 -> 4096.
 constexpr int kFewDepth = 4;
 constexpr int kFewGroups = 512;        // workgroups at most
 
@@ -355,6 +364,11 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
 // eight waves take every eighth 128-K step of the part with all NB column blocks, so a step's codes
 // are converted once and its columns are read once for T tiles, straight from L2 in whole 1 KiB
 // operands (two halves of a step in flight; no wave shares another's).  The waves' sums meet in LDS.
+//
+// Bound by the columns through L1 and L2, which T tiles share, and by latency: 8 x 4096 -> 16384 INT4
+// float32 13.8 us (36 MB, 2.6 TB/s), 33 x 12288 -> 4096 MXFP4 18.5 us (26.7 MB).  A kernel that reads
+// 16 columns a pass for each tile on its own took 44.7 and 69.2 us with its preparation (now 17.2 and
+// 26.1 us a call).
 template <int FMT, int NB, int T>
 __global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int S) {
   constexpr int W = kWideWaves;
