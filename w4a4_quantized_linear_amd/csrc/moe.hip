@@ -478,8 +478,8 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // The workgroup takes 8 / KW tiles and the blockIdx.y-th block: up to 16 pairs (DOWN: 16 / S, all
 // their planes being columns).  KW waves share a tile's K (every KW-th 128-K step each); KW is the
 // smallest that fills the GPU, since with few there is little exchange and a wave streams long runs
-// of codes.  (Blocks of 32 pairs, which halve the reads of an expert with many, leave one workgroup
-// a CU: 67 against 62 us at 48 tokens, 8 of 24 experts, 3584 -> 2 x 1536.)
+// of codes.  (Blocks of 32 pairs, which halve the reads of an expert with many, left one workgroup
+// a CU: 131 against 126 us the call at 48 tokens, 8 of 24 experts, 3584 -> 1536.)
 // PLANNED: the blocks are in the plan.  Otherwise (gate/up of at most 64 pairs) every wave finds its
 // block of up to a.cols pairs by ballots, which saves the plan's launch (4.5 us and what it costs the
 // host), and the grid's last row (blockIdx.y == slots) holds one workgroup that writes the plan for
