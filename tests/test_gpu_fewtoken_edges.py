@@ -1,0 +1,52 @@
+"""Corners of the few-token entry points on the GPU: the same bits from the same call where experts'
+blocks take different forms, equal and missing scores, the smallest magnitudes, precision that does
+not hang on the number of tokens."""
+import pytest
+
+import w4a4_quantized_linear_amd as sq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch_dev():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sq.lib()
+    assert sq.device_check(), "current device is not gfx950"
+    return torch, torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,k", [(33, 2), (70, 1), (200, 2), (900, 2), (1100, 2)])
+def test_nvfp4_experts_same_bits(torch_dev, M, k, f32):
+    """More than 64 pairs of NVFP4 experts at widths where a full block of pairs passes through the LDS
+    in parts and a shorter one whole (in fp16): repeats and replays of a graph equal the first call."""
+    torch, dev = torch_dev
+    g = torch.Generator(device=dev)
+    g.manual_seed(M)
+    E, H, Fh, N = 5, 2560, 4096, 64
+    gu, dn = sq.Layer("nvfp4", H, 2 * Fh, 0), sq.Layer("nvfp4", Fh, N, 0)
+    pg, pd = (sq.pack_experts(l, torch.randn((E, l.N, l.K), generator=g, device=dev) * l.K ** -0.5) for l in (gu, dn))
+    # magnitudes over 32 octaves: some lie below what fp16 holds beside the row's largest
+    X = torch.randn((M, H), generator=g, device=dev) * torch.exp2(-32 * torch.rand((M, H), generator=g, device=dev))
+    X, wt = X.bfloat16(), torch.rand((M, k), generator=g, device=dev)
+    ids = torch.rand((M, E), generator=g, device=dev).topk(k, 1)[1].int()
+
+    def call():
+        return sq.moe(gu, pg, dn, pd, X, ids, wt, sq.EPI_OUT_F32 if f32 else 0)
+
+    want = call()
+    assert bool(torch.isfinite(want).all()) and bool((want != 0).any())
+    for i in range(40):
+        assert torch.equal(call(), want), f"repeat {i}"
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        kept = call()
+    for i in range(10):
+        graph.replay()
+        other = call()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want) and torch.equal(other, want), f"replay {i}"

@@ -342,8 +342,9 @@ constexpr uint32_t kNoColumn = 0x80000000u;
 
 // The plan of moe_down_kernel: its units, kPlanWords words each: expert, pairs, K chunk, K chunks,
 // and the pairs (at most 16 / S of one expert, all their planes being columns of one MFMA); units
-// without pairs end every wave's sequence.  The pairs' order in a unit, which the atomics leave open,
-// does not reach the results: every pair has a column and a place of its own.
+// without pairs end every wave's sequence.  An expert's pairs stand in the order of their numbers, so
+// which of them share a block does not change from call to call: a full block and a shorter one may
+// form their sums differently (rows that do not fit the LDS whole come in parts).
 constexpr int kPlanWords = 16;
 constexpr int kDownWaves = 16;
 constexpr int kDownMinSlots = 256;     // pairs x K chunks that the LDS sums have room for at least
@@ -353,26 +354,61 @@ __device__ __forceinline__ int down_slots(int P) { return P > kDownMinSlots ? P 
 // pairs of kGatePlanWords words each, ended by blocks without pairs up to the grid's `slots`.
 constexpr int kGatePlan = 16384;       // in words
 constexpr int kGatePlanWords = 32;
-constexpr int kPlanLdsWords = 3 * kMoeMaxE + 2;
+constexpr int kPlanWaves = 8;
+constexpr int kPlanRounds = kMoeMaxPairs / (64 * kPlanWaves);
+constexpr int kPlanLdsWords = (kPlanWaves + 3) * kMoeMaxE + 2;
 template <bool GATE>
 __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
-  constexpr int THREADS = 512;
+  constexpr int THREADS = 64 * kPlanWaves;
   const int TPB = a.planes == 3 ? tokens_per_block(3) : tokens_per_block(2);
-  int *const cursor = lds, *const base = lds + kMoeMaxE, *const gbase = lds + 2 * kMoeMaxE;
-  int &total = lds[3 * kMoeMaxE], &gtotal = lds[3 * kMoeMaxE + 1];
-  const int tid = threadIdx.x, lane = tid & 63;
-  for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
+  // before[w]: an expert's pairs that wave w has met, then those of the waves before it
+  int *const before = lds, *const count = lds + kPlanWaves * kMoeMaxE, *const base = count + kMoeMaxE, *const gbase = base + kMoeMaxE;
+  int &total = gbase[kMoeMaxE], &gtotal = gbase[kMoeMaxE + 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int* const met = before + w * kMoeMaxE;
+  for (int e = lane; e < a.E; e += 64) met[e] = 0;
+  // a wave takes consecutive pairs, 64 a round; a pair's place among its expert's in the wave
+  const int rounds = (a.P + THREADS - 1) / THREADS, p0 = w * rounds * 64 + lane;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  int ex[kPlanRounds], at[kPlanRounds];
+#pragma unroll
+  for (int r = 0; r < kPlanRounds; ++r) {
+    const int p = p0 + r * 64, id = r < rounds && p < a.P ? a.ids[p] : -1;
+    ex[r] = id < a.E ? id : -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kPlanRounds; ++r) {
+    if (r >= rounds) break;
+    const bool valid = ex[r] >= 0;
+    uint64_t same = __ballot(valid);                       // lanes with this one's expert
+#pragma unroll
+    for (int b = 1; b < kMoeMaxE; b <<= 1) {
+      const uint64_t set = __ballot((ex[r] & b) != 0);
+      same &= ex[r] & b ? set : ~set;
+    }
+    keep_order();                                          // one wave's LDS operations are in order
+    const int met_before = valid ? met[ex[r]] : 0;
+    at[r] = met_before + __popcll(same & below);
+    keep_order();
+    if (valid && !(same & below)) met[ex[r]] = met_before + __popcll(same);
+  }
   __syncthreads();
-  for (int p = tid; p < a.P; p += THREADS) {
-    const int id = a.ids[p];
-    if (id >= 0 && id < a.E) atomicAdd(&cursor[id], 1);
+  for (int e = tid; e < a.E; e += THREADS) {
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < kPlanWaves; ++v) {
+      const int m = before[v * kMoeMaxE + e];
+      before[v * kMoeMaxE + e] = n;
+      n += m;
+    }
+    count[e] = n;
   }
   __syncthreads();
   if (tid < (GATE ? 128 : 64)) {                           // one wave for each kind of block
     const int size = tid < 64 ? TPB : 16;
     int blocks = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + lane, nb = e < a.E ? (cursor[e] + size - 1) / size : 0;
+      const int e = e0 + lane, nb = e < a.E ? (count[e] + size - 1) / size : 0;
       int sb = nb;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -391,7 +427,7 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
   while (!a.o && total * KC < kDownWaves && KC * 2 <= KS && KC * 2 * a.P <= slots) KC *= 2;
   int32_t* const gate = a.plan + kGatePlan;
   for (int e = tid; e < a.E; e += THREADS) {
-    const int cnt = cursor[e];
+    const int cnt = count[e];
     if (GATE)
       for (int b = 0; b * 16 < cnt; ++b)
         *reinterpret_cast<int2*>(gate + kGatePlanWords * (gbase[e] + b)) = make_int2(e, cnt - b * 16 < 16 ? cnt - b * 16 : 16);
@@ -407,16 +443,13 @@ __device__ __forceinline__ void moe_plan(const MoeArgs& a, int* lds) {
   if (GATE)
     for (int i = gtotal + tid; i < a.slots; i += THREADS)
       *reinterpret_cast<int2*>(gate + kGatePlanWords * i) = make_int2(0, 0);
-  __syncthreads();
-  for (int e = tid; e < a.E; e += THREADS) cursor[e] = 0;
-  __syncthreads();
-  for (int p = tid; p < a.P; p += THREADS) {
-    const int id = a.ids[p];
-    if (id < 0 || id >= a.E) continue;
-    const int i = atomicAdd(&cursor[id], 1);
+#pragma unroll
+  for (int r = 0; r < kPlanRounds; ++r) {
+    if (ex[r] < 0) continue;
+    const int p = p0 + r * 64, i = met[ex[r]] + at[r];
     const int b = a.planes == 3 ? i / tokens_per_block(3) : i / tokens_per_block(2);
-    for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[id] + b) * KC + k) + 4 + i - b * TPB] = p;
-    if (GATE) gate[kGatePlanWords * (gbase[id] + i / 16) + 2 + i % 16] = p;
+    for (int k = 0; k < KC; ++k) a.plan[kPlanWords * ((base[ex[r]] + b) * KC + k) + 4 + i - b * TPB] = p;
+    if (GATE) gate[kGatePlanWords * (gbase[ex[r]] + i / 16) + 2 + i % 16] = p;
   }
 }
 
