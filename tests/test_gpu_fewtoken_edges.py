@@ -50,3 +50,30 @@ def test_nvfp4_experts_same_bits(torch_dev, M, k, f32):
         other = call()
         torch.cuda.synchronize()
         assert torch.equal(kept, want) and torch.equal(other, want), f"replay {i}"
+
+
+def _bf16(torch, dev, rows):
+    """Rows of a few leading features, the others zero, 8 wide."""
+    t = torch.zeros((len(rows), 8), dtype=torch.float32)
+    for i, r in enumerate(rows):
+        t[i, :len(r)] = torch.tensor(r)
+    return t.bfloat16().to(dev)
+
+
+@pytest.mark.parametrize("M,E", [(1, 4), (1, 400), (300, 4), (300, 130)])
+def test_route_equal_scores_of_other_logits(torch_dev, M, E):
+    """The choice is by score (1 for the sigmoid of 40 and of 50, 0 for exp(-800) and exp(-900)), the
+    lower index first, with a bias of zeros as without one; one kernel (few tokens) and two."""
+    torch, dev = torch_dev
+    X = _bf16(torch, dev, [[1.0]] * M)
+    for sigmoid, logits, want in ((True, [1.0, 40.0, 50.0, 45.0], [1, 2, 3, 0]),
+                                  (False, [-800.0, 0.0, -900.0, -700.0], [1, 3, 0, 2])):
+        router = _bf16(torch, dev, [[-1000.0]] * (E - 4) + [[l] for l in logits])
+        if E > 4 and not sigmoid:
+            want = [E - 4 + 1, E - 4 + 3, 0, 1]              # every other score is 0: the lowest indices
+        elif E > 4:
+            want = [E - 4 + i for i in want]
+        for bias in (None, torch.zeros(E, device=dev)):
+            ids, w = sq.moe_route(X, router, 4, bias=bias, sigmoid=sigmoid, renorm=False)
+            assert ids.tolist() == [want] * M
+            assert w[:, :2].tolist() == [[1.0, 1.0 if sigmoid else 0.0]] * M

@@ -81,8 +81,8 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&
 }
 
 // One wave chooses one token's experts and writes their weights; l[i] and bias[i] are those of expert
-// 64 i + lane.  Each round takes the largest key left, the lowest index among equals; lane t keeps
-// the t-th choice.
+// 64 i + lane.  Each round takes the largest score + bias left, the lowest index among equals (scores
+// of other logits may be equal: a sigmoid of 40 and of 50 are both 1); lane t keeps the t-th choice.
 template <int PER>
 __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, const double (&l)[PER], const float (&bias)[PER],
                                                int lane) {
@@ -103,13 +103,12 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, co
       if (i * 64 + lane < a.E) sum += exp(l[i] - top);
     sum = wave_sum(sum);
   }
-  auto score = [&](double v) { return sig ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum; };
+  double p[PER];
   uint64_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = i * 64 + lane;
-    // without a bias the logits order the scores
-    key[i] = e < a.E ? order_of(a.bias ? score(l[i]) + double(bias[i]) : l[i]) : 0;
+    p[i] = sig ? 1.0 / (1.0 + exp(-l[i])) : exp(l[i] - top) / sum;
+    key[i] = i * 64 + lane < a.E ? order_of(p[i] + double(bias[i])) : 0;
   }
   int id = 0;
   double mine = 0.0;
@@ -119,7 +118,7 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, co
     double v = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (key[i] > best) { best = key[i]; at = i; v = l[i]; }
+      if (key[i] > best) { best = key[i]; at = i; v = p[i]; }
     const uint64_t most = wave_max(best);
     const uint64_t tied = __ballot(best == most);
     int from = __ffsll((unsigned long long)tied) - 1;
@@ -134,14 +133,13 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, co
     for (int i = 0; i < PER; ++i)
       if (lane == from && at == i) key[i] = 0;
   }
-  double p = lane < a.top_k ? score(mine) : 0.0;
   if (a.flags & SVDQ_ROUTE_RENORM) {
-    const double s = wave_sum(p);
-    p = s == 0.0 ? 0.0 : p / s;
+    const double s = wave_sum(mine);                       // 0 in lanes without a choice
+    mine = s == 0.0 ? 0.0 : mine / s;
   }
   if (lane < a.top_k) {
     a.ids[m * a.top_k + lane] = id;
-    a.weights[m * a.top_k + lane] = float(p * double(a.scale));
+    a.weights[m * a.top_k + lane] = float(mine * double(a.scale));
   }
 }
 
