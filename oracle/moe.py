@@ -32,8 +32,7 @@ def route(X_bits, Wr_bits, top_k: int, bias=None, sigmoid=False, renorm=True, sc
         logits = F.bf16_value(X_bits) @ F.bf16_value(Wr_bits).T
         p = 1.0 / (1.0 + np.exp(-logits)) if sigmoid else _softmax(logits)
         key = p if bias is None else p + np.asarray(bias, np.float64)
-    key = np.where(np.isnan(key), -np.inf, key)
-    ids = np.argsort(-key, axis=1, kind="stable")[:, :top_k]
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :top_k]          # NaN sorts last
     w = np.take_along_axis(p, ids, axis=1)
     if renorm:
         s = w.sum(axis=1, keepdims=True)

@@ -77,3 +77,18 @@ def test_route_equal_scores_of_other_logits(torch_dev, M, E):
             ids, w = sq.moe_route(X, router, 4, bias=bias, sigmoid=sigmoid, renorm=False)
             assert ids.tolist() == [want] * M
             assert w[:, :2].tolist() == [[1.0, 1.0 if sigmoid else 0.0]] * M
+
+
+@pytest.mark.parametrize("M,E", [(1, 5), (1, 300), (300, 5), (300, 130)])
+def test_route_nan_behind_minus_infinity(torch_dev, M, E):
+    """An expert whose score is NaN stands behind one that a bias of -infinity masks."""
+    torch, dev = torch_dev
+    X = _bf16(torch, dev, [[1.0]] * M)
+    nan, inf = float("nan"), float("inf")
+    router = _bf16(torch, dev, [[nan]] * (E - 5) + [[0.0], [nan], [1.0], [1.0], [nan]])
+    bias = torch.zeros(E, device=dev)
+    bias[E - 5 + 2] = -inf
+    want = [E - 5 + i for i in (3, 0, 2)] + ([1, 4] if E == 5 else [0, 1])
+    ids, w = sq.moe_route(X, router, 5, bias=bias, sigmoid=True, renorm=False)
+    assert ids.tolist() == [want] * M
+    assert bool(torch.isfinite(w[:, :3]).all()) and bool(torch.isnan(w[:, 3:]).all())

@@ -18,3 +18,9 @@ def test_equal_scores_of_other_logits(bias):
     assert ids.tolist() == [[1, 2, 3, 0]] and w[0, :3].tolist() == [1.0, 1.0, 1.0]
     ids, w = Mo.route(X, _bits([[-800.0], [0.0], [-900.0], [-700.0]]), 4, bias)
     assert ids.tolist() == [[1, 3, 0, 2]] and w[0, 2:].tolist() == [0.0, 0.0]
+
+
+def test_nan_behind_minus_infinity():
+    X, Wr = _bits([[1.0]]), _bits([[0.0], [np.nan], [1.0], [1.0], [np.nan]])
+    bias = np.array([0, 0, -np.inf, 0, 0], np.float32)
+    assert Mo.route(X, Wr, 5, bias, sigmoid=True)[0].tolist() == [[3, 0, 2, 1, 4]]

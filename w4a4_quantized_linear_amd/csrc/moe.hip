@@ -64,10 +64,10 @@ __device__ __forceinline__ double wave_sum(double v) {
   return lane_value(v, 63);
 }
 
-// A double's place among doubles as an unsigned number above 0 (NaN as -infinity, -0 as 0).
+// A double's place among doubles as an unsigned number above 0: NaN 1, below -infinity; -0 as 0.
 __device__ __forceinline__ uint64_t order_of(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v == v ? v + 0.0 : -__builtin_huge_val());
-  return u >> 63 ? ~u : u | (uint64_t(1) << 63);
+  const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
+  return !(v == v) ? 1 : u >> 63 ? ~u : u | (uint64_t(1) << 63);
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   const uint32_t hi = wave_max(uint32_t(v >> 32));
