@@ -260,11 +260,11 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
  * act = SiLU, or GELU (erf form) with SVDQ_EPI_GELU; the biases with SVDQ_EPI_BIAS.  Two to
  * four launches (long calls plan their blocks in one and add a token's pairs in another); the
  * weights of an expert are read only if a token asks for it.  Sums are fp32 in a fixed order
- * (the same call gives the same bits); h is not rounded to bf16 (it is kept to 2^-18, or to
- * fp32's own rounding with SVDQ_EPI_OUT_F32).  With NVFP4 experts rows may be held in fp16,
- * scaled by a power of two for each row: X is then exact but for what lies below 2^-28 of its
- * row's largest element, off by at most 2^-39 of that, and h is kept to 2^-22 (2^-26 with
- * SVDQ_EPI_OUT_F32).
+ * (the same call gives the same bits); h is not rounded to bf16: it is kept to 2^-18, or to
+ * fp32's own rounding with SVDQ_EPI_OUT_F32, but no finer than 2^-134 (half of bf16's smallest
+ * step).  With NVFP4 experts rows may be held in fp16, scaled by a power of two for each row: X
+ * is then exact but for what lies below 2^-28 of its row's largest element, off by at most 2^-39
+ * of that, and h is kept to 2^-22 (2^-26 with SVDQ_EPI_OUT_F32).
  *   dg, wg_packed  one expert's gate and up projection as one layer, K = H inputs, N = 2 F
  *                  outputs, rows [gate | up]; E blobs of svdq_pack_weight, one after the
  *                  other, svdq_weight_bytes(dg) apart

@@ -1,9 +1,16 @@
 """Corners of the few-token entry points on the GPU: the same bits from the same call where experts'
 blocks take different forms, equal and missing scores, the smallest magnitudes, precision that does
 not hang on the number of tokens."""
+import numpy as np
 import pytest
 
+import synth
 import w4a4_quantized_linear_amd as sq
+from oracle import formats as F
+from oracle import moe as Mo
+from oracle import quant as Q
+
+from _gpu_helpers import dev_tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +99,59 @@ def test_route_nan_behind_minus_infinity(torch_dev, M, E):
     ids, w = sq.moe_route(X, router, 5, bias=bias, sigmoid=True, renorm=False)
     assert ids.tolist() == [want] * M
     assert bool(torch.isfinite(w[:, :3]).all()) and bool(torch.isnan(w[:, 3:]).all())
+
+
+def _bits(a):
+    return synth.bf16_bits_from_f32(np.asarray(a, np.float32))
+
+
+def _values(R, fmt):
+    """Experts' dequantized weights and their magnitudes as they enter the kernels' sums."""
+    w, mag = np.empty(R.shape), np.empty(R.shape)
+    for e in range(len(R)):
+        gs = Q.nvfp4_global_scale(R[e]) if fmt == "nvfp4" else np.float32(1.0)
+        c, s = Q.quantize(R[e], fmt, gs)
+        w[e] = Q.dequantize(c, s, fmt, gs)
+        mag[e] = np.abs(w[e])
+        if fmt == "int4":
+            mag[e] = (np.abs(24 + c.astype(np.float64)) + 24) * np.repeat(F.fp16_value(s), 64, axis=1)
+    return w, mag
+
+
+def _sum_eps(K):
+    """Relative rounding of a product's sums: 5 roundings an MFMA, four MFMAs a 128 of K, and 40 more."""
+    return 2.0 ** -24 * (20 * (K // 128) + 40)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
+@pytest.mark.parametrize("M,k", [(1, 1), (9, 2), (70, 1)])
+@pytest.mark.parametrize("up", [9, 0])
+def test_experts_smallest_rows(torch_dev, fmt, M, k, up):
+    """Tokens of subnormal features, which gate biases and large weights (2^up of gate/up, 2^9 of down)
+    keep visible; with up = 0 h is subnormal too.  The experts' bound, 8 roundings of 2^-149, a
+    subnormal's, for each element of u and h, and 2^-134 for each of h: its bf16 planes' last place is
+    2^-133 however many there are, and the last plane rounds to the nearest."""
+    torch, dev = torch_dev
+    E, H, Fh, N = 3, 512, 512, 48
+    rng = np.random.default_rng(M + up)
+    Rg = (rng.standard_normal((E, 2 * Fh, H)) / np.sqrt(H) * 2.0 ** up).astype(np.float32)
+    Rd = (rng.standard_normal((E, N, Fh)) / np.sqrt(Fh) * 2.0 ** 9).astype(np.float32)
+    bg, bd = np.zeros((E, 2 * Fh), np.float32), np.zeros((E, N), np.float32)
+    bg[:, :Fh] = 4.0
+    gu, dn = sq.Layer(fmt, H, 2 * Fh, 0), sq.Layer(fmt, Fh, N, 0)
+    pg, pd = (sq.pack_experts(l, dev_tensor(R, torch, dev), dev_tensor(_bits(b), torch, dev))
+              for l, R, b in ((gu, Rg, bg), (dn, Rd, bd)))
+    # the largest are below 2^-126; multiples of 2^-133, bf16's last place there
+    X = rng.integers(-100, 101, (M, H)) * 2.0 ** -133
+    X[:, 7] = 2.0 ** -127
+    ids = np.argsort(rng.random((M, E)), axis=1)[:, :k].astype(np.int32)
+    wt = rng.random((M, k)).astype(np.float32)
+    (wg, mg), (wd, md) = _values(Rg, fmt), _values(Rd, fmt)
+    o, lim = Mo.experts(_bits(X), ids, wt, wg, bg, wd, bd, False, (mg, md), (_sum_eps(H), _sum_eps(Fh) + 2.0 ** -26))
+    least = (8 * 2.0 ** -149 * 4.0 + 2.0 ** -134) * np.abs(wd).sum(axis=2).max() * k
+    lim = lim * (1 + 2.0 ** -20) + 2.0 ** -24 * (k + 1) * (np.abs(o) + lim) + least
+    y = sq.moe(gu, pg, dn, pd, dev_tensor(_bits(X), torch, dev), dev_tensor(ids, torch, dev), dev_tensor(wt, torch, dev),
+               sq.EPI_BIAS | sq.EPI_OUT_F32).cpu().numpy().astype(np.float64)
+    assert np.abs(o).max() > 2.0 ** -126 and np.all(np.abs(o) + lim > 0)
+    assert np.median(lim) < 0.5 * np.median(np.abs(o))                # zeros would be beyond the bound
+    assert np.all(np.abs(y - o) <= lim), f"worst {np.max(np.abs(y - o) / lim):.2f}"

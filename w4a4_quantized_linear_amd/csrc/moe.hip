@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(512) moe_plan_kernel(MoeArgs a) {
 }
 
 // Rows in LDS (S planes x n rows of K bf16, row_b bytes apart) to fp16, in place, scaled by
-// f16_row_scale of each row's largest magnitude, whose bits go to top[0 .. n): the planes' sum becomes
+// 2^f16_row_power of each row's largest magnitude, whose bits go to top[0 .. n): the planes' sum becomes
 // fp16 hi (+ lo).  One wave takes a row.  The rows are written before; the caller's barrier follows.
 template <int S, int WAVES>
 __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n, uint32_t* top) {
@@ -477,7 +477,7 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
     }
     m = wave_max(m);
     if (lane == 0) top[r] = m;
-    const float s = f16_row_scale(__uint_as_float(m));
+    const int s = f16_row_power(__uint_as_float(m));
     for (int k = lane * 8; k < K; k += 512) {
       float v[8];
       unpack_bf8(*reinterpret_cast<const uint4*>(xl + r * row_b + k * 2), v);
@@ -489,7 +489,7 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
         for (int e = 0; e < 8; ++e) v[e] += l[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= s;
+      for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], s);
 #pragma unroll
       for (int p = 0; p < S; ++p) {
         const uint4 h = to_f16(v);
@@ -657,9 +657,12 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
         }
       }
       if constexpr (F16) {
-        const float back = 1.0f / f16_row_scale(__uint_as_float(top[t < T ? t : 0]));   // a power of two
-        ag *= back;
-        au *= back;
+        const int back = -f16_row_power(__uint_as_float(top[t < T ? t : 0]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ag[e] = ldexpf(ag[e], back);
+          au[e] = ldexpf(au[e], back);
+        }
       }
     } else {
       // a part is a multiple of 2048 of K, so each wave has an even number of its steps
@@ -917,8 +920,12 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a) {
       keep_order();
       if (cu.n && ++i == cu.n) {
         v4f y = acc;
+        if constexpr (F16) {
+          const int back = -f16_row_power(__uint_as_float(top[cu.pair]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = ldexpf(y[e], back);
+        }
         if (FMT == kFmtNVFP4) y *= gs;
-        if constexpr (F16) y *= 1.0f / f16_row_scale(__uint_as_float(top[cu.pair]));   // a power of two
         v4f sum = y;                                       // the planes' columns of a pair
 #pragma unroll
         for (int p = 1; p < S; ++p)

@@ -140,12 +140,12 @@ __device__ __forceinline__ uint4 nv_to_f16(uint32_t d, v2h s) {
                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 3) * s));
 }
 
-// fp16 activations of a row: the row times a power of two that brings its largest magnitude `top`
-// into [2^14, 2^15) (1 for zero, infinity and NaN).  A bf16 is then exact in fp16 down to 2^-28 of
-// the row's largest, and off by at most 2^-39 of it below; hi + lo hold an fp32 to 2^-22.
-__device__ __forceinline__ float f16_row_scale(float top) {
-  const int e = int(__float_as_uint(top) >> 23 & 0xFFu);
-  return e == 0 || e == 255 ? 1.0f : __uint_as_float(uint32_t(268 - e < 247 ? 268 - e : 247) << 23);
+// fp16 activations of a row: the row times the power of two 2^f16_row_power that brings its largest
+// magnitude `top` into [2^14, 2^15) (1 for zero, infinity and NaN).  A bf16 is then exact in fp16 down
+// to 2^-28 of the row's largest, and off by at most 2^-39 of it below; hi + lo hold an fp32 to 2^-22.
+// The power (-113 .. 147) is applied by ldexp: as a factor it would not fit fp32 for the smallest rows.
+__device__ __forceinline__ int f16_row_power(float top) {
+  return top > 0.f && top < __builtin_huge_valf() ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
 }
 __device__ __forceinline__ uint4 to_f16(const float (&v)[8]) {
   uint32_t r[4];
