@@ -209,7 +209,8 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
  * low-rank branch, the activations not quantized,
  *     Y = act( X_hat deQ(Q4(R))^T + (X_hat L1) L2 + b ),  X_hat = fp32(X / lambda),
  * on the same blob that svdq_linear takes.  Sums are fp32; X_hat enters as a sum of bf16
- * parts that holds it to 2^-18 (bf16 output) or to fp32's own rounding (SVDQ_EPI_OUT_F32).
+ * parts that holds it to 2^-18 (bf16 output) or to fp32's own rounding (SVDQ_EPI_OUT_F32),
+ * the sums of X_hat L1 to fp32's rounding with either (all no finer than 2^-134).
  * Up to 8 tokens (5 with float32 output) whose K x rank is small take one launch; others a
  * launch that prepares X_hat and X_hat L1, the product, and, where few output rows would leave
  * CUs idle, a launch that adds parts of K.  Any M >= 0 is computed correctly.  A row with a

@@ -155,3 +155,22 @@ def test_experts_smallest_rows(torch_dev, fmt, M, k, up):
     assert np.abs(o).max() > 2.0 ** -126 and np.all(np.abs(o) + lim > 0)
     assert np.median(lim) < 0.5 * np.median(np.abs(o))                # zeros would be beyond the bound
     assert np.all(np.abs(y - o) <= lim), f"worst {np.max(np.abs(y - o) / lim):.2f}"
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M,rank", [(1, 2), (5, 64), (8, 2), (8, 100), (9, 2), (40, 64)])
+def test_down_projection_keeps_its_bits(torch_dev, M, rank, f32):
+    """D = (1 + 2^-9 + 2^-20, 2^-9) exactly, and Y = D0 - D1 - 1 = 2^-20: every sum is exact in fp32, and
+    what is left needs more of D than two bf16 parts hold.  For few tokens, more, and either output."""
+    torch, dev = torch_dev
+    K, N = 512, 48
+    X, L1, L2 = np.zeros((M, K)), np.zeros((K, rank)), np.zeros((rank, N))
+    X[:, :3] = 1.0, 2.0 ** -9, 2.0 ** -20
+    L1[:3, 0], L1[1, 1] = 1.0, 1.0
+    L2[0], L2[1] = 1.0, -1.0
+    layer = sq.Layer("mxfp4", K, N, rank)
+    L1, L2, b = (dev_tensor(_bits(a), torch, dev) for a in (L1, L2, np.full(N, -1.0)))
+    w = sq.pack_weight(layer, torch.zeros((N, K), device=dev), L1, L2, torch.ones(K, device=dev), b)
+    y = sq.linear_w4a16(layer, w, dev_tensor(_bits(X), torch, dev),
+                        sq.EPI_LOWRANK | sq.EPI_BIAS | (sq.EPI_OUT_F32 if f32 else 0))
+    assert bool((y == 2.0 ** -20).all())

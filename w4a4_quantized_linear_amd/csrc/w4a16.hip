@@ -296,10 +296,10 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
         const float4* dq = reinterpret_cast<const float4*>(dsum + (tl < M ? tl : M - 1) * a.r_pad + r32 * 32 + c * 8);
         const float4 d0 = dq[0], d1 = dq[1];
         dv[0] = d0.x; dv[1] = d0.y; dv[2] = d0.z; dv[3] = d0.w; dv[4] = d1.x; dv[5] = d1.y; dv[6] = d1.z; dv[7] = d1.w;
-        uint4 p[S];
-        split_planes<S>(dv, p);
+        uint4 p[3];                                        // D to fp32's rounding for any number of tokens
+        split_planes<3>(dv, p);
 #pragma unroll
-        for (int i = 0; i < S; ++i) z = mfma_bf16(l2, p[i], z);
+        for (int i = 0; i < 3; ++i) z = mfma_bf16(l2, p[i], z);
       };
       if constexpr (RT != 0) {
 #pragma unroll
