@@ -211,14 +211,16 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
  * on the same blob that svdq_linear takes.  Sums are fp32; X_hat enters as a sum of bf16
  * parts that holds it to 2^-18 (bf16 output) or to fp32's own rounding (SVDQ_EPI_OUT_F32),
  * the sums of X_hat L1 to fp32's rounding with either (all no finer than 2^-134).
- * Up to 8 tokens (5 with float32 output) whose K x rank is small take one launch; others a
+ * Up to 8 tokens (5 with float32 output) take one launch where the parts of X_hat of all tokens
+ * fit a CU's LDS (M (2 K + 16) up to 68 KiB, with float32 output 45 KiB, and less with a low-rank
+ * branch) and K x rank is small (rank <= 64, K x rank <= 131072, rank rounded up to 32); others a
  * launch that prepares X_hat and X_hat L1, the product, and, where few output rows would leave
  * CUs idle, a launch that adds parts of K.  Any M >= 0 is computed correctly.  A row with a
  * non-finite element gives a non-finite row; no other row changes.
  *   X, Y, epi  as for svdq_linear (all SVDQ_EPI_* flags)
  *   workspace  device, at least svdq_w4a16_bytes(d, M) bytes, 256-byte aligned; every call
- *              writes what it reads of it.  A call that needs none (0 bytes: few tokens at a
- *              small K x rank) takes NULL.  Calls that may overlap (other streams, captured
+ *              writes what it reads of it.  NULL where that is 0 (no output type needs one
+ *              then), and only there.  Calls that may overlap (other streams, captured
  *              graphs that run at once) need workspaces of their own, here and below.
  * Checks and errors as svdq_linear. */
 size_t svdq_w4a16_bytes(const svdq_layer_desc* d, int64_t M);
