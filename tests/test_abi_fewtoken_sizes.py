@@ -45,3 +45,13 @@ def test_linear_w4a16_workspace(L, forced_device_error, M, K, rank, needed):
             assert call(None, 0) == (1 if needed else 6) and call(P, n) == 6
             if needed:
                 assert call(P, n - 1) == 5
+
+
+def test_moe_bytes_of_invalid_layers(L):
+    """0 for what svdq_moe refuses, as the other size queries."""
+    g, d = D(K=1024, N=1024, rank=0), D(K=512, N=256, rank=0)
+    assert L.svdq_moe_bytes(g, d, 4, 2) > 0
+    for bad_g in (D(fmt=0, K=1024, N=1024, rank=0), D(fmt=4, K=1024, N=1024, rank=0), D(K=1024, N=1024, rank=16)):
+        assert L.svdq_moe_bytes(bad_g, d, 4, 2) == 0
+    for bad_d in (D(fmt=0, K=512, N=256, rank=0), D(fmt=4, K=512, N=256, rank=0), D(K=512, N=256, rank=16)):
+        assert L.svdq_moe_bytes(g, bad_d, 4, 2) == 0

@@ -351,7 +351,9 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
 }
 
 size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k) {
-  if (!dg || !dd || !valid_moe_shape(dg, dd, M, top_k)) return 0;
+  if (!dg || !dd || !valid_moe_shape(dg, dd, M, top_k) || check_fmt(dg) != SVDQ_OK || check_fmt(dd) != SVDQ_OK ||
+      dg->rank != 0 || dd->rank != 0)
+    return 0;
   return moe_workspace(M, top_k, dd->K, dd->N);
 }
 
