@@ -74,10 +74,10 @@ extern "C" {
 typedef enum {
   SVDQ_OK = 0,
   SVDQ_ERR_NULL = 1,      /* a required pointer is NULL                         */
-  SVDQ_ERR_SHAPE = 2,     /* K, N, rank, M, ldx or ldy outside the stated set    */
+  SVDQ_ERR_SHAPE = 2,     /* a size, count or stride outside the stated set      */
   SVDQ_ERR_FORMAT = 3,    /* unknown format or epilogue flag                     */
   SVDQ_ERR_ALIGN = 4,     /* a pointer or stride is not aligned as required      */
-  SVDQ_ERR_WORKSPACE = 5, /* workspace smaller than svdq_act_bytes               */
+  SVDQ_ERR_WORKSPACE = 5, /* workspace smaller than the entry point's size query */
   SVDQ_ERR_DEVICE = 6,    /* no device, or the current device is not gfx950      */
   SVDQ_ERR_LAUNCH = 7,    /* a kernel launch failed                              */
   SVDQ_ERR_TOO_LARGE = 8  /* svdq_linear_noalloc: the layer's workspace exceeds its static scratch */
@@ -241,8 +241,8 @@ enum {
  *     weights[m, j] = scale * score[m, ids[m, j]]  (bias is in the choice only).
  * Logits, scores and the choice are computed in float64, so the choice does not hang on an
  * order of summation; weights are rounded to float32 once.  ids are always top_k different
- * experts in [0, E), also for a token with NaN or infinite features (whose weights are then
- * not finite).
+ * experts in [0, E), also for a token with NaN or infinite features (a softmax's scores are NaN
+ * then; a sigmoid's are 0, 1 or NaN, its logits being infinite or NaN).
  *   X        device, bf16 bits, M x K, row stride ldx (K <= ldx <= 2^24, multiple of 8)
  *   router   device, bf16 bits, E x K row-major; X and router 16-byte aligned
  *   bias     device, float32[E], or NULL
@@ -282,7 +282,7 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
  * Any M >= 0 is computed correctly (calls of more than 2048 pairs run in parts, launches of
  * their own each).  dg->N != 2 dd->K, E outside [1, 512] or top_k outside [1, 32] give SVDQ_ERR_SHAPE,
  * a rank other than 0 or other flags SVDQ_ERR_FORMAT; other checks and errors as svdq_linear.
- * A token with non-finite features gives a non-finite row; no other row changes. */
+ * A token with non-finite features and an expert gives a non-finite row; no other row changes. */
 size_t svdq_moe_bytes(const svdq_layer_desc* dg, const svdq_layer_desc* dd, int64_t M, int32_t top_k);
 svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svdq_layer_desc* dd,
                      const void* wd_packed, int32_t E, const uint16_t* X, int64_t M, int64_t ldx, const int32_t* ids,

@@ -174,3 +174,15 @@ def test_down_projection_keeps_its_bits(torch_dev, M, rank, f32):
     y = sq.linear_w4a16(layer, w, dev_tensor(_bits(X), torch, dev),
                         sq.EPI_LOWRANK | sq.EPI_BIAS | (sq.EPI_OUT_F32 if f32 else 0))
     assert bool((y == 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_route_infinite_features(torch_dev, M):
+    """Softmax scores are NaN, sigmoid scores 1, 0 and NaN (infinity times a router weight of 0)."""
+    torch, dev = torch_dev
+    X, router = _bf16(torch, dev, [[float("inf")]] * M), _bf16(torch, dev, [[-1.0], [0.0], [2.0], [-2.0], [1.0]])
+    ids, w = sq.moe_route(X, router, 5, sigmoid=True, renorm=False)
+    assert ids.tolist() == [[2, 4, 0, 3, 1]] * M
+    assert w[:, :4].tolist() == [[1.0, 1.0, 0.0, 0.0]] * M and bool(torch.isnan(w[:, 4]).all())
+    ids, w = sq.moe_route(X, router, 5)
+    assert ids.tolist() == [[0, 1, 2, 3, 4]] * M and bool(torch.isnan(w).all())

@@ -158,10 +158,10 @@ const char* svdq_status_str(svdq_status s) {
   switch (s) {
     case SVDQ_OK: return "ok";
     case SVDQ_ERR_NULL: return "a required pointer is NULL";
-    case SVDQ_ERR_SHAPE: return "unsupported shape (K % 512, N % 16, 0 <= rank <= 256, M, ldx/ldy)";
+    case SVDQ_ERR_SHAPE: return "unsupported shape (K % 512, N % 16, 0 <= rank <= 256, M, ldx/ldy, experts, top_k)";
     case SVDQ_ERR_FORMAT: return "unknown format or epilogue flag";
     case SVDQ_ERR_ALIGN: return "misaligned pointer or row stride";
-    case SVDQ_ERR_WORKSPACE: return "workspace smaller than svdq_act_bytes";
+    case SVDQ_ERR_WORKSPACE: return "workspace smaller than the entry point's size query (svdq_act_bytes, svdq_w4a16_bytes, ...)";
     case SVDQ_ERR_DEVICE: return "no device, or the current device is not gfx950 (MI355X)";
     case SVDQ_ERR_LAUNCH: return "kernel launch failed";
     case SVDQ_ERR_TOO_LARGE: return "layer needs more than the 64 MiB static scratch of svdq_linear_noalloc";
