@@ -186,3 +186,33 @@ def test_route_infinite_features(torch_dev, M):
     assert w[:, :4].tolist() == [[1.0, 1.0, 0.0, 0.0]] * M and bool(torch.isnan(w[:, 4]).all())
     ids, w = sq.moe_route(X, router, 5)
     assert ids.tolist() == [[0, 1, 2, 3, 4]] * M and bool(torch.isnan(w).all())
+
+
+@pytest.mark.parametrize("fg,fd", [("mxfp4", "int4"), ("int4", "nvfp4"), ("nvfp4", "mxfp4")])
+def test_experts_in_parts_within_the_bound(torch_dev, fg, fd):
+    """Wide experts of 37 and 39 pairs, whose full blocks pass through the LDS in parts and whose last ones
+    whole, against the oracle's bound for each element (76 pairs: 38 tokens, one with the same expert twice)."""
+    torch, dev = torch_dev
+    E, H, Fh, N, M, k = 2, 2560, 2560, 48, 38, 2
+    rng = np.random.default_rng(17)
+    Rg = (rng.standard_normal((E, 2 * Fh, H)) / np.sqrt(H)).astype(np.float32)
+    Rd = (rng.standard_normal((E, N, Fh)) / np.sqrt(Fh)).astype(np.float32)
+    bg, bd = _bits(rng.standard_normal((E, 2 * Fh)) * 0.1), _bits(rng.standard_normal((E, N)) * 0.1)
+    gu, dn = sq.Layer(fg, H, 2 * Fh, 0), sq.Layer(fd, Fh, N, 0)
+    pg, pd = (sq.pack_experts(l, dev_tensor(R, torch, dev), dev_tensor(b, torch, dev)) for l, R, b in ((gu, Rg, bg), (dn, Rd, bd)))
+    X = _bits(rng.standard_normal((M, H)))
+    ids = np.array([[0, 1]] * (M - 1) + [[1, 1]], np.int32)
+    wt = rng.random((M, k)).astype(np.float32)
+    (wg, mg), (wd, md) = _values(Rg, fg), _values(Rd, fd)
+    for f32 in (True, False):
+        o, lim = Mo.experts(X, ids, wt, wg, F.bf16_value(bg), wd, F.bf16_value(bd), False, (mg, md),
+                            (_sum_eps(H), _sum_eps(Fh) + (2.0 ** -26 if f32 else 2.0 ** -18)))
+        lim = lim * (1 + 2.0 ** -20) + 2.0 ** -24 * (k + 1) * (np.abs(o) + lim)
+        if not f32:
+            lim = lim + 2.0 ** -8 * (np.abs(o) + lim)
+        y = sq.moe(gu, pg, dn, pd, dev_tensor(X, torch, dev), dev_tensor(ids, torch, dev), dev_tensor(wt, torch, dev),
+                   sq.EPI_BIAS | (sq.EPI_OUT_F32 if f32 else 0)).float().cpu().numpy().astype(np.float64)
+        err = np.abs(y - o)
+        assert np.all(err <= lim), f"f32={f32}: worst {np.max(err / lim):.2f}"
+        if f32:                                              # no error shared by all outputs
+            assert err.sum() <= 1e-5 * np.abs(o).sum()
