@@ -55,3 +55,19 @@ def test_moe_bytes_of_invalid_layers(L):
         assert L.svdq_moe_bytes(bad_g, d, 4, 2) == 0
     for bad_d in (D(fmt=0, K=512, N=256, rank=0), D(fmt=4, K=512, N=256, rank=0), D(K=512, N=256, rank=16)):
         assert L.svdq_moe_bytes(g, bad_d, 4, 2) == 0
+
+
+@pytest.mark.parametrize("M,K,E,needed", [(1, 2560, 64, False), (1, 2568, 64, True), (1, 2560, 16, False), (1, 4096, 16, True),
+                                          (1, 1280, 128, False), (1, 1288, 128, True), (1, 4096, 8, False), (1, 4104, 8, True),
+                                          (256, 512, 160, False), (257, 512, 160, True), (1, 320, 512, False),
+                                          (1, 328, 512, True)])
+def test_route_workspace(L, forced_device_error, M, K, E, needed):
+    n = L.svdq_moe_route_bytes(M, K, E)
+    assert (n > 0) == needed and (n == 0 or n >= M * E * 8)
+
+    def call(ws, nbytes):
+        return L.svdq_moe_route(P, M, K, K, P, E, None, 4, 0, 1.0, P, P, ws, nbytes, None)
+
+    assert call(None, 0) == (1 if needed else 6) and call(P, n) == 6
+    if needed:
+        assert call(P, n - 1) == 5

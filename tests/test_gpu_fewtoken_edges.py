@@ -216,3 +216,15 @@ def test_experts_in_parts_within_the_bound(torch_dev, fg, fd):
         assert np.all(err <= lim), f"f32={f32}: worst {np.max(err / lim):.2f}"
         if f32:                                              # no error shared by all outputs
             assert err.sum() <= 1e-5 * np.abs(o).sum()
+
+
+@pytest.mark.parametrize("M,K,E,k", [(3, 2560, 64, 4), (3, 2568, 64, 4), (2, 4096, 8, 2), (2, 4104, 8, 2), (2, 1280, 128, 9),
+                                     (2, 1288, 128, 9), (256, 512, 160, 3), (257, 512, 160, 3), (1, 8192, 4, 4)])
+def test_route_on_both_sides_of_its_forms(torch_dev, M, K, E, k):
+    torch, dev = torch_dev
+    rng = np.random.default_rng(K + E)
+    X, Wr = _bits(rng.standard_normal((M, K))), _bits(rng.standard_normal((E, K)) * 2 / np.sqrt(K))
+    ids, w = sq.moe_route(dev_tensor(X, torch, dev), dev_tensor(Wr, torch, dev), k)
+    want, ww = Mo.route(X, Wr, k)
+    np.testing.assert_array_equal(ids.cpu().numpy(), want)
+    np.testing.assert_allclose(w.cpu().numpy(), ww, rtol=2.0 ** -23)

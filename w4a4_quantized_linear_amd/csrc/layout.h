@@ -54,14 +54,25 @@ constexpr int kMoeMaxPairs = 2048;
 // blocks of the gate/up product.
 constexpr size_t kMoePlanBytes = 65536 + 640 * 128;
 
-// svdq_moe_route: one kernel, a workgroup per token, while one CU's fp64 rate computes all of a
-// token's logits about as fast as a second launch costs and each token has a CU; otherwise the
-// logits are formed in tiles of 16 experts x 16 tokens, K split over
-// route_splits workgroups while there are CUs for them, and a second kernel chooses.
-constexpr int64_t kRouteOneMacs = 163840;
+// svdq_moe_route: one kernel, a workgroup per token, while one CU forms all of a token's logits about as
+// fast as a second launch costs and each token has a CU; otherwise the logits are formed in tiles of
+// 16 experts x 16 tokens, K split over route_splits workgroups while there are CUs for them, and a
+// second kernel chooses.  The one kernel's time goes by the rounds of 64 experts that its waves take,
+// K features each; up to 16 experts some waves have none, and K x E counts.  One kernel against two
+// (us a call in a graph; at 1, 64 and 250 tokens):
+//   E 64 (and 16, 32 within 10%)  K 1536  6.3 / 7.0   6.7 / 8.3   6.9 / 8.6
+//                                 K 2560  8.3 / 7.8   8.7 / 9.3   9.0 / 11.1
+//                                 K 3584 10.3 / 7.8  10.7 / 9.6  11.0 / 11.1
+//   E 128                         K 1024  8.4 / 7.4   8.9 / 8.6   9.3 / 8.6
+//                                 K 2048 12.5 / 8.2  12.9 / 9.1  13.4 / 10.6
+//   E 8                           K 4096  6.8 / 7.5   7.3 / 8.5   7.7 / 8.7
+//                                 K 8192 11.8 / 9.0  12.7 / 10.2 12.7 / 10.9
+// and at 300 tokens (a second round of workgroups) E 64 K 1024 9.8 / 9.2, K 2560 15.4 / 12.1.
+constexpr int64_t kRouteOneFeatures = 2560;
+constexpr int64_t kRouteOneMacs = 32768;
 constexpr int64_t kRouteOneTokens = 256;
 __host__ __device__ inline bool route_one(int64_t M, int K, int E) {
-  return M <= kRouteOneTokens && int64_t(E) * K <= kRouteOneMacs;
+  return M <= kRouteOneTokens && (int64_t((E + 63) / 64) * K <= kRouteOneFeatures || int64_t(E) * K <= kRouteOneMacs);
 }
 __host__ __device__ inline int route_splits(int64_t M, int K, int E) {
   const int64_t tiles = ((M + 15) / 16) * ((E + 15) / 16), z = 256 / (tiles > 0 ? tiles : 1);
