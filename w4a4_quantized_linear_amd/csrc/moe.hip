@@ -522,7 +522,7 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // 2048 -> 2 x 1024, 21 and 29 us (experts of 32 pairs are read two and four times, from L2).  By
 // latency at one token: 4 of 32, 2048 -> 2 x 2048, 8.8 us for 18 MB.
 constexpr int kGateWaves = 8;
-constexpr int kGateFill = 4096;
+constexpr int kGateFill = 2048;
 constexpr int kGateXLds = 81664;       // two workgroups a CU
 template <int FMT, int S, bool PLANNED>
 __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
@@ -973,7 +973,12 @@ static void gate_up(const MoeArgs& a, hipStream_t s) {
   }
 }
 
-// Waves that share a tile's K, for this many tiles at least.
+// Waves that share a tile's K: the fewest that make kGateFill waves (eight a CU) of the tiles that there
+// are at least.  Whole call (us, in a graph) with 1, 2, 4 and 8 of them for gate/up, 1 to 16 tokens, 4 or
+// 8 of 16 to 64 experts, 2048 -> 2 x 1024 MXFP4: 256 tiles 17.6 15.6 14.5 14.7, 512 19.9 17.9 16.6 17.5,
+// 1024 23.7 22.0 22.4 26.9, 2048 27.7 28.6 31.3 40.9, 4096 40.7 43.2 54.7 81.6; INT4 and NVFP4 alike,
+// and the down product by pairs (512 19.5 18.2 18.0 19.8, 1024 22.0 21.6 22.5 26.9, 2048 26.0 27.1 29.2
+// 34.9).
 static int waves_per_tile(int64_t tiles) {
   int kw = 1;
   while (kw < kGateWaves && tiles * kw < kGateFill) kw *= 2;
