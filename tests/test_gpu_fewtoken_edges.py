@@ -228,3 +228,35 @@ def test_route_on_both_sides_of_its_forms(torch_dev, M, K, E, k):
     want, ww = Mo.route(X, Wr, k)
     np.testing.assert_array_equal(ids.cpu().numpy(), want)
     np.testing.assert_allclose(w.cpu().numpy(), ww, rtol=2.0 ** -23)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
+@pytest.mark.parametrize("M,k,E", [(5, 3, 7), (50, 2, 4), (100, 2, 8), (112, 2, 8)])
+def test_experts_down_forms(torch_dev, fmt, M, k, E):
+    """The down product with h in LDS, with h too large for it, and either side of where pairs' products go
+    through memory (at 200 pairs for one output only): within the oracle's bound, with a workspace of just
+    the stated bytes inside a larger buffer that stays as it was."""
+    torch, dev = torch_dev
+    H, Fh, N = 512, 512, 80
+    rng = np.random.default_rng(M)
+    Rg = (rng.standard_normal((E, 2 * Fh, H)) / np.sqrt(H)).astype(np.float32)
+    Rd = (rng.standard_normal((E, N, Fh)) / np.sqrt(Fh)).astype(np.float32)
+    gu, dn = sq.Layer(fmt, H, 2 * Fh, 0), sq.Layer(fmt, Fh, N, 0)
+    pg, pd = (sq.pack_experts(l, dev_tensor(R, torch, dev)) for l, R in ((gu, Rg), (dn, Rd)))
+    X = _bits(rng.standard_normal((M, H)))
+    ids = np.argsort(rng.random((M, E)), axis=1)[:, :k].astype(np.int32)
+    wt = rng.random((M, k)).astype(np.float32)
+    (wg, mg), (wd, md) = _values(Rg, fmt), _values(Rd, fmt)
+    need = sq.moe_bytes(gu, dn, M, k)
+    for f32 in (True, False):
+        o, lim = Mo.experts(X, ids, wt, wg, None, wd, None, False, (mg, md),
+                            (_sum_eps(H), _sum_eps(Fh) + (2.0 ** -26 if f32 else 2.0 ** -18)))
+        lim = lim * (1 + 2.0 ** -20) + 2.0 ** -24 * (k + 1) * (np.abs(o) + lim)
+        if not f32:
+            lim = lim + 2.0 ** -8 * (np.abs(o) + lim)
+        around = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=dev)
+        y = sq.moe(gu, pg, dn, pd, dev_tensor(X, torch, dev), dev_tensor(ids, torch, dev), dev_tensor(wt, torch, dev),
+                   sq.EPI_OUT_F32 if f32 else 0, workspace=around[4096:4096 + need])
+        err = np.abs(y.float().cpu().numpy().astype(np.float64) - o)
+        assert np.all(err <= lim), f"f32={f32}: worst {np.max(err / lim):.2f}"
+        assert bool((around[:4096] == 0xA5).all()) and bool((around[4096 + need:] == 0xA5).all())

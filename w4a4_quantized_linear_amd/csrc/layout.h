@@ -89,15 +89,20 @@ __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + 
 __host__ __device__ inline size_t align256(size_t a) { return (a + 255) & ~size_t(255); }
 
 // svdq_moe's down product.  One kernel whose workgroups each take 16 rows of all tokens and add a
-// token's pairs in LDS, or (moe_by_pairs) pairs' products to memory and a kernel that adds them:
-// the first is bound by its L1, about 170 cycles for each column block and 128 of F, in N / 16
-// workgroups over 256 CUs; the second shares a block's columns between two row tiles and fills the
-// GPU whatever N is, for a launch more and the products' way through memory.
-constexpr int64_t kMoeDownSteps = 350;     // steps a CU from which the second is taken: at 512 (48 tokens,
-                                           // 4 of 8, 2048 -> 2048) 51.8 against 29 us, at 312 (7 tokens, 5 of
-                                           // 60, 1024 -> 2560) 19.5 against 15.0 and 4.7 us and a launch
-__host__ __device__ inline bool moe_by_pairs(int64_t experts, int64_t pairs, int F, int N) {
-  return (experts + pairs / 8) * (F / kKStep) * ((N / 16 + 255) / 256) > kMoeDownSteps;
+// token's pairs in LDS, or (moe_by_pairs) pairs' products to memory and a kernel that adds them: the
+// first takes a CU about 170 cycles for each block of pairs (16 / planes of one expert) and 128 of F, in
+// N / 16 workgroups over 256 CUs; the second shares a block's columns between two row tiles and fills
+// the GPU whatever N is, for a launch more and the products' way through memory.  One kernel against two,
+// whole calls (us, in a graph), by a CU's blocks x steps of 128:
+//   80 (50 tokens, 2 of 8, 512 -> 2048) MXFP4 24.6 / 22.8, NVFP4 27.7 / 27.1; float32 112: 28.3 / 26.0, 29.5 / 30.3
+//   112 (24, 4 of 16, 512 -> 4096)     MXFP4 25.0 / 23.7, NVFP4 27.4 / 28.5, INT4 26.6 / 27.2
+//   160 (8, 2 of 8, 2048 -> 4096)      MXFP4 22.4 / 20.9, NVFP4 27.8 / 24.9, INT4 25.3 / 23.8
+//   264 (6, 5 of 40, 1024 -> 2048)     MXFP4 26.1 / 24.7, NVFP4 32.5 / 29.5, INT4 31.9 / 30.6
+//   320 (8, 4 of 16, 2048 -> 2048)     MXFP4 32.8 / 23.4, NVFP4 34.4 / 27.5, INT4 35.8 / 25.9
+//   864 (400, 2 of 8, 1024 -> 4096)    MXFP4 134 / 78, NVFP4 144 / 100, INT4 142 / 97
+constexpr int64_t kMoeDownSteps = 140;     // steps a CU from which the second is taken
+__host__ __device__ inline bool moe_by_pairs(int64_t experts, int64_t pairs, int F, int N, int planes) {
+  return (experts + pairs / (16 / planes)) * (F / kKStep) * ((N / 16 + 255) / 256) > kMoeDownSteps;
 }
 __host__ __device__ inline int64_t moe_part_pairs(int64_t M, int top_k) {
   const int64_t pairs = M * top_k;
@@ -106,10 +111,11 @@ __host__ __device__ inline int64_t moe_part_pairs(int64_t M, int top_k) {
 __host__ __device__ inline size_t moe_h_bytes(int64_t M, int top_k, int F) {
   return align256(size_t(moe_part_pairs(M, top_k)) * F * 6);
 }
-// The plan, h's planes and, where any number of experts up to the pairs' may need them, the products.
+// The plan, h's planes and, where any number of experts up to the pairs' and either output may need them,
+// the products.
 __host__ __device__ inline size_t moe_workspace(int64_t M, int top_k, int F, int N) {
   const int64_t pairs = moe_part_pairs(M, top_k);
-  const bool by_pairs = moe_by_pairs(pairs < kMoeMaxE ? pairs : kMoeMaxE, pairs, F, N);
+  const bool by_pairs = moe_by_pairs(pairs < kMoeMaxE ? pairs : kMoeMaxE, pairs, F, N, 3);
   return kMoePlanBytes + moe_h_bytes(M, top_k, F) + (by_pairs ? align256(size_t(pairs) * N * 4) : 0);
 }
 

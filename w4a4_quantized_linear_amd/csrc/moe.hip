@@ -799,8 +799,8 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {
 // the plan and one of KC chunks of K; waves take every sixteenth unit, one pipeline running on from
 // unit to unit, and leave each pair's sums in a place of its own, so the sum over a token's experts
 // has one order.  Bound by the latency of the first loads and by one CU's L1: 8.4 us at one token, 4 of
-// 32 experts, 2048 -> 2048 MXFP4 (9 MB); 19.5 us at 7 tokens, 5 of 60, 1024 -> 2560 NVFP4 (160
-// workgroups for 256 CUs; through memory instead 15.0 + 4.7 us and a launch more).
+// 32 experts, 2048 -> 2048 MXFP4 (9 MB).  Calls with more steps go through memory (moe_by_pairs): 7
+// tokens, 5 of 60, 1024 -> 2560 NVFP4 takes 19.2 us here (160 workgroups for 256 CUs) and 11.6 + 3.8 there.
 constexpr int64_t kDownLds = 163840;   // HL: all of h in LDS where it fits (one workgroup a CU)
 
 template <int FMT, int S, bool HL>
@@ -1040,7 +1040,7 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
     a.slots = experts + a.P / (a.cols ? a.cols : 16);
     a.down_slots = experts + a.P / tokens_per_block(a.planes);
     a.KW = waves_per_tile(int64_t(experts) * (F / 16));
-    a.o = moe_by_pairs(experts, a.P, F, N) ? o : nullptr;
+    a.o = moe_by_pairs(experts, a.P, F, N, a.planes) ? o : nullptr;
     if (fmt_g == kFmtMXFP4) gate_up<kFmtMXFP4>(a, s);
     else if (fmt_g == kFmtINT4) gate_up<kFmtINT4>(a, s);
     else gate_up<kFmtNVFP4>(a, s);
