@@ -213,7 +213,7 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
  * the sums of X_hat L1 to fp32's rounding with either (all no finer than 2^-134).
  * Up to 8 tokens (5 with float32 output) take one launch where the parts of X_hat of all tokens
  * fit a CU's LDS (M (2 K + 16) up to 68 KiB, with float32 output 45 KiB, and less with a low-rank
- * branch) and K x rank is small (rank <= 64, K x rank <= 131072, rank rounded up to 32); others a
+ * branch) and K x rank is small (rank <= 64, K x rank <= 262144, rank rounded up to 32); others a
  * launch that prepares X_hat and X_hat L1, the product, and, where few output rows would leave
  * CUs idle, a launch that adds parts of K.  Any M >= 0 is computed correctly.  A row with a
  * non-finite element gives a non-finite row; no other row changes.

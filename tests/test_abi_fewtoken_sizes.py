@@ -29,8 +29,8 @@ def D(fmt=1, K=1024, N=512, rank=16):
 # (M, K, rank, whether a workspace is needed): 3 parts of M rows of 2 K + 16 bytes beside 16 KiB of sums
 # in 152 KiB; rank and K x rank; more tokens than one MFMA has columns for three parts of
 NEEDS = [(1, 22528, 0, False), (1, 23552, 0, True), (5, 4096, 0, False), (5, 4608, 0, False), (5, 5120, 0, True),
-         (8, 512, 0, True), (8, 4608, 0, True), (8, 8192, 0, True), (6, 512, 0, True), (1, 4096, 32, False),
-         (1, 4608, 32, True), (1, 2048, 64, False), (1, 2560, 64, True), (1, 512, 65, True), (1, 8192, 1, True)]
+         (8, 512, 0, True), (8, 4608, 0, True), (8, 8192, 0, True), (6, 512, 0, True), (1, 8192, 32, False),
+         (1, 8704, 32, True), (1, 4096, 64, False), (1, 4608, 64, True), (1, 512, 65, True), (1, 8704, 1, True)]
 
 
 @pytest.mark.parametrize("M,K,rank,needed", NEEDS)

@@ -9,8 +9,9 @@ import w4a4_quantized_linear_amd as sq
 from oracle import formats as F
 from oracle import moe as Mo
 from oracle import quant as Q
+from oracle import w4a16 as W
 
-from _gpu_helpers import dev_tensor
+from _gpu_helpers import dev_tensor, pack
 
 pytestmark = pytest.mark.gpu
 
@@ -260,3 +261,26 @@ def test_experts_down_forms(torch_dev, fmt, M, k, E):
         err = np.abs(y.float().cpu().numpy().astype(np.float64) - o)
         assert np.all(err <= lim), f"f32={f32}: worst {np.max(err / lim):.2f}"
         assert bool((around[:4096] == 0xA5).all()) and bool((around[4096 + need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4", "nvfp4"])
+@pytest.mark.parametrize("M,K,N,rank", [(1, 8192, 48, 32), (2, 8704, 48, 32), (1, 4096, 4112, 64), (3, 4608, 272, 50),
+                                        (2, 1024, 8208, 20), (1, 1024, 8208, 0), (4, 512, 16400, 64)])
+def test_linear_few_tokens_both_sides_of_its_forms(torch_dev, fmt, M, K, N, rank):
+    """Down projections that the kernel forms itself and that a launch prepares, one and more row tiles a
+    workgroup, against the oracle with the bound of the layer's tests."""
+    torch, dev = torch_dev
+    spec = synth.layer_spec("qkv", M=M, K=K, N=N, rank=rank, fmt=fmt, x_outliers=K // 100, w_outliers=K // 100, lora_rank=0)
+    L = synth.draw_layer(spec, seed=70 + M)
+    layer = sq.Layer(fmt, K, N, rank)
+    w, X = pack(layer, L, torch, dev), dev_tensor(L["X"], torch, dev)
+    o = W.layer_forward(L["X"], L["lam"], L["L1"] if rank else None, L["L2"] if rank else None, L["R"], L["b"], fmt)
+    for f32 in (True, False):
+        lim = (_sum_eps(K) + (2.0 ** -26 if f32 else 2.0 ** -18)) * (o["B"] + 3 * o["B_lr"] + np.abs(o["pre"]))
+        if not f32:
+            lim = lim + 2.0 ** -8 * (np.abs(o["Y"]) + lim)
+        y = sq.linear_w4a16(layer, w, X, sq.EPI_LOWRANK | sq.EPI_BIAS | (sq.EPI_OUT_F32 if f32 else 0))
+        err = np.abs(y.float().cpu().numpy().astype(np.float64) - o["Y"])
+        assert np.all(err <= lim), f"f32={f32}: worst {np.max(err / lim):.2f}"
+        if f32:                                              # no error shared by all outputs
+            assert err.sum() <= 1e-5 * np.abs(o["Y"]).sum()

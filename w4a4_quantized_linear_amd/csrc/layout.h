@@ -122,15 +122,30 @@ __host__ __device__ inline size_t moe_workspace(int64_t M, int top_k, int F, int
 // svdq_linear_w4a16: which form a call takes.  Few tokens (`few`): one kernel that holds
 // x_hat's S planes of all tokens in LDS beside the down projection's sums, when the columns of
 // one 16-column MFMA hold them and they fit; it forms the down projection itself (`own_d`) for
-// small K x rank, since every workgroup then reads all of L1.
+// up to four tiles of 16 ranks, which a wave's registers hold beside its pipeline, and a small
+// K x rank, since every workgroup then reads all of L1.  A prepare launch against an own down
+// projection (us a call in a graph, one token, N 512 / 2048 / 4096 / 8192 / 16384, NVFP4):
+//   L1 256 KB (K 2048 r 64)  10.8 11.1 12.5 14.0 17.6  /   8.3  8.4  9.2 12.1 15.0
+//   L1 448 KB (K 3584 r 64)  12.3 14.2 14.9 16.5 21.9  /  10.9 11.3 13.8 16.0 20.8
+//   L1 512 KB (K 8192 r 32)  15.4 17.5 18.2 22.1 30.5  /  13.1 16.1 16.8 20.8 29.6
+//   L1 576 KB (K 4608 r 64)  13.2 15.3 15.8 18.1 24.4  /  12.6 14.9 16.0 18.6 23.8
+//   L1 768 KB (K 6144 r 64)  14.5 16.7 17.1 20.3 27.2  /  14.8 18.1 18.7 21.7 27.9
+// (MXFP4, INT4, 5 tokens with float32 output and 8 tokens alike.)
 constexpr int kFewWaves = 8;
 constexpr int kFewMaxRank = 64;
-constexpr int kFewMaxL1Bytes = 262144;
+constexpr int kFewMaxL1Bytes = 524288;
 constexpr int64_t kFewLds = 155648;    // of 160 KiB
+// Workgroups at most: one a CU where each forms the down projection or only one fits a CU's LDS, else two.
+// 256 against 512 (us a call in a graph): own down projection, one token, 2048 -> 8192 rank 32, MXFP4
+// 9.1 / 10.1, INT4 9.5 / 13.3, NVFP4 9.9 / 10.7, -> 24576 13.8 / 14.2, 14.8 / 19.0, 15.5 / 15.8; 5
+// tokens float32, 2560 -> 16384, 115 KB of LDS, prepared, MXFP4 21.0 / 26.6; rank 0, one token, 2048 ->
+// 8208 MXFP4 6.7 / 6.1, -> 10240 6.8 / 7.4, -> 24576 10.2 / 9.2; prepared, 2048 -> 16384 15.7 / 13.9.
+constexpr int kFewGroups = 256;
 __host__ __device__ inline int few_row_bytes(int K) { return K * 2 + 16; }   // 16 skews the banks
 
 struct W4A16Plan {
   bool few, own_d;
+  int groups;
   int64_t lds;
 };
 __host__ __device__ inline W4A16Plan w4a16_plan(int K, int64_t r_pad, int64_t M, int S) {
@@ -140,6 +155,7 @@ __host__ __device__ inline W4A16Plan w4a16_plan(int K, int64_t r_pad, int64_t M,
   const int64_t sums = p.own_d && r_pad > 32 ? kFewWaves * r_pad / 16 * 1024 : 2 * kFewWaves * 1024;
   p.lds = S * M * few_row_bytes(K) + M * r_pad * 4 + sums;
   p.few = M <= 16 / S && p.lds <= kFewLds;
+  p.groups = (p.own_d && r_pad) || p.lds > 81920 ? kFewGroups : 2 * kFewGroups;
   return p;
 }
 

@@ -138,7 +138,6 @@ __device__ __forceinline__ void w4a16_store(const W4A16LinearArgs& a, int64_t m,
 // 4096 INT4 rank 32 (9.9 MB), 12.9 us for 5 x 2048 -> 8208 NVFP4 rank 64 (11 MB).  The two launches
 // that this replaces (x_hat and D prepared, then streamed) took 12.7 us at 1 x 4096 -> 4096.
 constexpr int kFewDepth = 4;
-constexpr int kFewGroups = 512;        // workgroups at most
 
 // RT: 16-rank tiles of OWN_D (0: no low-rank branch, or its sums are given)
 template <int FMT, int S, int RT>
@@ -553,7 +552,7 @@ hipError_t launch_linear_w4a16(int fmt, const uint8_t* wblob, const WeightLayout
     if (e != hipSuccess) return e;
   }
   if (plan.few) {
-    const int tiles = N / 16, per = (tiles + kFewGroups - 1) / kFewGroups;
+    const int tiles = N / 16, per = (tiles + plan.groups - 1) / plan.groups;
     const dim3 fgrid(unsigned((tiles + per - 1) / per));
     const int rt = plan.own_d ? a.r_pad / 16 : 0;   // 0, 2 or 4
 #define SVDQ_FEW_S(FMT_, S_)                                                                                \
