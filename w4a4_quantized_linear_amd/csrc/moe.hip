@@ -148,7 +148,7 @@ __device__ __forceinline__ void choose_experts(const RouteArgs& a, int64_t m, co
 //
 // One workgroup: a token.  Wave w takes experts w, w + 16, ..., four at a time, its lanes 8
 // consecutive K each; wave 0 then chooses.  Bound by the CU's fp64 conversions and FMAs: 1 x 2048 ->
-// 64, 7.6 us (10.4 us a call; 14.7 with the two kernels below).
+// 64, 7.5 us (10.4 us a call).
 constexpr int kRouteOneWaves = 16;
 template <int PER>
 __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a) {
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(1024) route_one_kernel(RouteArgs a) {
 // A tile of 16 experts x 16 tokens and one of Z parts of K on the fp64 MFMA (16x16x4): lane (r, c)
 // holds 8 consecutive K of expert and token r, so element e of both operands is one MFMA's K.  The
 // waves take every fourth 32 of K; their sums meet in LDS, the parts' in the next kernel.  Bound by
-// the fp64 units (1000 x 2888 -> 128: 23 us; tiles of 32 x 32, half the conversions an MFMA: 26 us).
+// the fp64 units (1000 x 2888 -> 128: 23.4 us, the MFMA busy 49% of a SIMD's time beside the conversions
+// of its operands; tiles of 32 x 32, half the conversions an MFMA: 26 us).
 typedef double v4d __attribute__((ext_vector_type(4)));
 __global__ void __launch_bounds__(256) route_logits_kernel(RouteArgs a) {
   constexpr int AHEAD = 4;                                 // steps of one batch of loads
@@ -510,17 +511,18 @@ __device__ __forceinline__ void rows_to_f16(uint8_t* xl, int row_b, int K, int n
 // their planes being columns).  KW waves share a tile's K (every KW-th 128-K step each); KW is the
 // smallest that fills the GPU, since with few there is little exchange and a wave streams long runs
 // of codes.  (Blocks of 32 pairs, which halve the reads of an expert with many, left one workgroup
-// a CU: 131 against 126 us the call at 48 tokens, 8 of 24 experts, 3584 -> 1536.)
-// PLANNED: the blocks are in the plan.  Otherwise (gate/up of at most 64 pairs) every wave finds its
-// block of up to a.cols pairs by ballots, which saves the plan's launch (4.5 us and what it costs the
-// host), and the grid's last row (blockIdx.y == slots) holds one workgroup that writes the plan for
-// the down product.
+// a CU and were 4% slower at 48 tokens, 8 of 24 experts, 3584 -> 1536.)
+// PLANNED: the blocks are in the plan.  Otherwise (gate/up of at most 64 pairs, a wave's lanes) every
+// wave finds its block of up to a.cols pairs by ballots, which saves the plan's launch, and the grid's
+// last row (blockIdx.y == slots) holds one workgroup that writes the plan for the down product.  Whole
+// calls by ballots and with a plan: 2 pairs 13.6 / 17.4 us, 16 22.9 / 26.2, 64 (16 tokens, 4 of 32, 2048
+// -> 2 x 1024 MXFP4) 37.0 / 39.8; INT4 and NVFP4 2 to 4 us likewise, but 16 tokens, 4 of 64, 4096 INT4 80.3 / 78.5.
 //
 // Bound by the weights' bytes where experts have few pairs: MXFP4, 64 tokens, 6 of 64 experts, 4096 ->
-// 2 x 2048, gate/up 100 us for 571 MB (5.7 TB/s; a kernel that only reads reaches 6.0), down 55 us for
-// 285 MB (5.2 TB/s).  By L1 and LDS reads of the columns where they have many: 128 tokens, 4 of 16,
-// 2048 -> 2 x 1024, 21 and 29 us (experts of 32 pairs are read two and four times, from L2).  By
-// latency at one token: 4 of 32, 2048 -> 2 x 2048, 8.8 us for 18 MB.
+// 2 x 2048, gate/up 100 us for 571 MB (5.7 TB/s; a kernel that only reads reaches 6.1), down 57 us for
+// 285 MB (5.0 TB/s).  By L1 and LDS reads of the columns where they have many: 128 tokens, 4 of 16,
+// 2048 -> 2 x 1024, 19 and 19 us (experts of 32 pairs are read two and four times, from L2).  By
+// latency at one token: 4 of 32, 2048 -> 2 x 2048, 8.5 us for 18 MB.
 constexpr int kGateWaves = 8;
 constexpr int kGateFill = 2048;
 constexpr int kGateXLds = 81664;       // two workgroups a CU
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(512, 4) moe_rows_kernel(MoeArgs a) {
   }
 }
 
-// Y[m] = sum_j w_j o[m, j], j in order; a pair without an expert adds nothing.  4.3 us for 64 tokens of
+// Y[m] = sum_j w_j o[m, j], j in order; a pair without an expert adds nothing.  5.3 us for 64 tokens of
 // 6 x 4096 (6.3 MB from L2): a launch's start and one round of loads.
 template <bool OUT_F32>
 __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a) {

@@ -4,8 +4,8 @@
 //   x_hat = fp32(X / lambda),  D = X_hat L1.
 //
 // What is to be read is the weights, so few tokens are bound by bytes in principle and by
-// latency in practice: 4096 x 4096 INT4 is 9 MB, 1.9 us at a copy's rate, and a launch that reads
-// 25 MB takes 7.8 us of which half is start and drain.  Two forms (layout.h, w4a16_plan):
+// latency in practice: 4096 x 4096 INT4 is 9 MB, 1.5 us at the rate of large reads, and a launch that
+// only reads 10 MB takes 6.0 us, one of 25 MB 7.8.  Two forms (layout.h, w4a16_plan):
 //   w4a16_few_kernel   all tokens' planes are columns of one MFMA: one launch.
 //   w4a16_wide_kernel  more: w4a16_prepare_kernel divides by lambda, splits x_hat into bf16
 //                      planes (w4frag.h) in the order of the B operands and forms D's partial
@@ -35,7 +35,7 @@ struct W4A16LinearArgs {
 constexpr int kPrepWaves = 8;          // 64 K each
 constexpr int kPrepTiles = 4;          // 16-rank tiles whose sums meet in LDS at a time
 
-// One workgroup: 16 tokens, 512 of K.  4.6 us for 8 tokens of 4096, 6.0 us for 33 of 12288: the
+// One workgroup: 16 tokens, 512 of K.  4.8 us for 8 tokens of 4096, 6.1 us for 33 of 12288: the
 // latency of one dependent chain (X and lambda, the division, the MFMAs, the exchange), not bytes.
 template <int S>
 __global__ void __launch_bounds__(512) w4a16_prepare_kernel(W4A16LinearArgs a) {
@@ -134,9 +134,11 @@ __device__ __forceinline__ void w4a16_store(const W4A16LinearArgs& a, int64_t m,
 // on from tile to tile.  The waves' sums meet in LDS (two buffers, so one barrier a tile); one
 // wave, another each tile, adds them and the up projection and writes the tile.
 //
-// Bound by start-up and latency: 6.0 us for 1 x 1024 -> 1024 MXFP4 rank 16, 9.5 us for 1 x 4096 ->
-// 4096 INT4 rank 32 (9.9 MB), 12.9 us for 5 x 2048 -> 8208 NVFP4 rank 64 (11 MB).  The two launches
-// that this replaces (x_hat and D prepared, then streamed) took 12.7 us at 1 x 4096 -> 4096.
+// Bound by start-up and latency (6.2 us for 1 x 1024 -> 1024 MXFP4 rank 16) and by the down projection,
+// whose L1 every workgroup reads: 9.5 us for 1 x 4096 -> 4096 INT4 rank 32 (9.9 MB of weights; 88 MB of
+// L2 reads, 67 of them L1's; in a graph 11.1 us, without the branch 6.5), 13.2 us for 5 x 2048 -> 8208
+// NVFP4 rank 64 (11 MB; 64 MB).  The two launches that this replaces (x_hat and D prepared, then
+// streamed) took 12.7 us at 1 x 4096 -> 4096.
 constexpr int kFewDepth = 4;
 
 // RT: 16-rank tiles of OWN_D (0: no low-rank branch, or its sums are given)
@@ -365,9 +367,9 @@ __global__ void __launch_bounds__(512) w4a16_few_kernel(W4A16LinearArgs a, int t
 // operands (two halves of a step in flight; no wave shares another's).  The waves' sums meet in LDS.
 //
 // Bound by the columns through L1 and L2, which T tiles share, and by latency: 8 x 4096 -> 16384 INT4
-// float32 13.8 us (36 MB, 2.6 TB/s), 33 x 12288 -> 4096 MXFP4 18.5 us (26.7 MB).  A kernel that reads
-// 16 columns a pass for each tile on its own took 44.7 and 69.2 us with its preparation (now 17.2 and
-// 26.1 us a call).
+// float32 13.8 us (36 MB of weights; 106 MB of L2 reads, 38 MB past it), 33 x 12288 -> 4096 MXFP4 18.6 us
+// (26.7 MB; 295 MB, 45 MB past it).  A kernel that reads 16 columns a pass for each tile on its own took
+// 44.7 and 69.2 us with its preparation (now 17.1 and 26.0 us a call).
 template <int FMT, int NB, int T>
 __global__ void __launch_bounds__(512) w4a16_wide_kernel(W4A16LinearArgs a, int S) {
   constexpr int W = kWideWaves;
