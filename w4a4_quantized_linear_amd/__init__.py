@@ -256,7 +256,7 @@ def linear_w4a16(layer: Layer, w_packed, X, epi: int = 0, out=None, workspace=No
     layer of any format for few tokens (X: M x K bf16); returns Y (M x N, bf16, or float32
     with EPI_OUT_F32)."""
     torch, dev = _torch(), X.device
-    if stream is not None or dev.index != torch.cuda.current_device():
+    if stream is not None or dev.index is None or dev.index != torch.cuda.current_device():
         return _elsewhere(dev, stream, lambda: linear_w4a16(layer, w_packed, X, epi, out, workspace))
     p, wb = _kept_desc(layer)
     ldx = _rows(X, "X", layer.K, dev, (torch.bfloat16, torch.int16))
@@ -290,7 +290,7 @@ def moe_route(X, router, top_k: int, bias=None, sigmoid: bool = False, renorm: b
     and weights (float32 M x top_k): softmax (or sigmoid) scores, divided by a token's sum with
     `renorm`, times `scale`."""
     torch, dev = _torch(), X.device
-    if stream is not None or dev.index != torch.cuda.current_device():
+    if stream is not None or dev.index is None or dev.index != torch.cuda.current_device():
         return _elsewhere(dev, stream, lambda: moe_route(X, router, top_k, bias, sigmoid, renorm, scale, ids, weights,
                                                          workspace))
     shape = router.shape
@@ -326,7 +326,7 @@ def pack_experts(layer: Layer, R, bias=None, stream=None):
     """E experts' weights of one layer shape (rank 0, lambda 1): R (E x N x K fp32), bias (E x N
     bf16 or None) -> E x weight_bytes(layer) uint8, as moe takes them."""
     torch, dev = _torch(), R.device
-    if stream is not None or dev.index != torch.cuda.current_device():
+    if stream is not None or dev.index is None or dev.index != torch.cuda.current_device():
         return _elsewhere(dev, stream, lambda: pack_experts(layer, R, bias))
     if layer.rank != 0 or R.dim() != 3 or tuple(R.shape[1:]) != (layer.N, layer.K):
         raise ValueError(f"expected rank 0 and weights E x {layer.N} x {layer.K}, got rank {layer.rank} and {tuple(R.shape)}")
@@ -353,7 +353,7 @@ def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi:
     down(act(gate) * up), act SiLU or, with EPI_GELU, GELU; returns Y (M x down.N, bf16, or
     float32 with EPI_OUT_F32)."""
     torch, dev = _torch(), X.device
-    if stream is not None or dev.index != torch.cuda.current_device():
+    if stream is not None or dev.index is None or dev.index != torch.cuda.current_device():
         return _elsewhere(dev, stream, lambda: moe(gate_up, wg_packed, down, wd_packed, X, ids, weights, epi, out,
                                                    workspace))
     (pg, gb), (pd, db) = _kept_desc(gate_up), _kept_desc(down)
