@@ -223,7 +223,8 @@ svdq_status svdq_gemm_w4a16(const svdq_layer_desc* d, const void* w_packed, cons
  * the faster call from some 50 tokens (MXFP4, 4096 -> 16384) to 200 (INT4, 4096 -> 4096).  A row
  * with a non-finite element (X_hat beyond bf16's largest counts as one) gives a non-finite
  * row; no other row changes.
- *   X, Y, epi  as for svdq_linear (all SVDQ_EPI_* flags)
+ *   X, Y, epi  as for svdq_linear (all SVDQ_EPI_* flags); Y's elements are none of X's (workgroups
+ *              read X while others write Y)
  *   workspace  device, at least svdq_w4a16_bytes(d, M) bytes, 256-byte aligned; every call
  *              writes what it reads of it.  NULL where that is 0 (no output type needs one
  *              then), and only there.  Calls that may overlap (other streams, captured
@@ -283,7 +284,8 @@ svdq_status svdq_moe_route(const uint16_t* X, int64_t M, int64_t ldx, int32_t K,
  *   ids, weights  device, int32 and float32, M x top_k (svdq_moe_route's, or any: the same
  *              expert twice counts twice; an id outside [0, E) adds nothing, for example an
  *              expert on another device or a padded token)
- *   Y          device, M x N, row stride ldy, bf16, or float32 with SVDQ_EPI_OUT_F32
+ *   Y          device, M x N, row stride ldy, bf16, or float32 with SVDQ_EPI_OUT_F32; its elements
+ *              are none of X's
  *   workspace  device, at least svdq_moe_bytes(dg, dd, M, top_k) bytes, 256-byte aligned
  * Any M >= 0 is computed correctly (calls of more than 2048 pairs run in parts, launches of
  * their own each).  dg->N != 2 dd->K, E outside [1, 512] or top_k outside [1, 32] give SVDQ_ERR_SHAPE,

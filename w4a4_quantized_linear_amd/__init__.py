@@ -186,7 +186,7 @@ def linear_noalloc(layer: Layer, w_packed, X, epi: int, out=None, stream=None):
 # ---- few tokens: 16-bit activations, experts ----
 #
 # These calls check what the C entry points cannot see of a tensor (type, device, shape,
-# inner stride, bytes of a packed weight) and raise ValueError.  They run on the device of
+# inner stride, bytes of a packed weight) and raise ValueError.  `out` shares no elements with X.  They run on the device of
 # their tensors, on `stream` or its current stream; what they allocate belongs to that stream.
 # A decoding step makes many of them on kernels of a few microseconds, so a call keeps to
 # plain attribute reads, raw addresses and one lookup of the layer's descriptor.
