@@ -297,6 +297,127 @@ svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svd
                      const float* weights, int32_t top_k, void* Y, int64_t ldy, uint32_t epi, void* workspace,
                      size_t ws_bytes, void* stream);
 
+/* ---- A key-value cache held in 4 bits, and the attention that reads it ----
+ *
+ * What stands between a QKV projection (svdq_gemm_qkv, or svdq_linear_w4a16 for few tokens) and
+ * the output projection.  A pool holds `pages` pages of `page` tokens, each with K and V of all
+ * heads, quantized per token and head by the Q4 rule above (the groups run along head_dim;
+ * NVFP4's tensor scale is 1).  The pool is pages x svdq_kv_page_bytes(d) device bytes, 64-byte
+ * aligned (a page's bytes are a multiple of 64), one per layer; its layout is opaque, but a page is the same bytes wherever it lies,
+ * and the bytes of one token are no other's.  Sequence b's token t is in page
+ * table[b ldt + t / page], at t % page.
+ *   d       fmt; heads K/V heads (1 .. 256); head_dim 64 or 128; page 16, 32, ... 1024 tokens
+ *   pool    may hold anything (NaN bits too) where no token was written
+ *   table   device, int32, batch x cols, row stride ldt; a place with a page outside [0, pages),
+ *           or behind the table's row, holds no token
+ *   lens    device, int32[batch]: tokens of each sequence, with the rows of this call
+ *   cu      device, int32[batch + 1], rising: sequence b's rows are cu[b] .. cu[b + 1] - 1 of
+ *           the M rows; NULL: one row each, M = batch.  Rows in front of cu[0] or from cu[batch]
+ *           on belong to no sequence: nothing of them is read or written
+ * Row j of the r rows of sequence b stands for token lens[b] - r + j.  table, lens and cu are
+ * read on the device only, so a captured graph follows them.
+ * Limits: pages <= 2^30, cols x page <= 2^30, batch <= 16384, M and batch x heads <= 2^22, row
+ * strides a multiple of 8 and at most 2^24, row pointers 16-byte aligned. */
+typedef struct {
+  int32_t fmt;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t page;
+} svdq_kv_desc;
+
+enum {
+  SVDQ_ROPE_HALVES = 1u,  /* svdq_kv_append: features p and p + pairs turn together, not 2 p and 2 p + 1 */
+  SVDQ_KV_FULL = 1u       /* svdq_kv_attention: a query also sees the tokens behind its own             */
+};
+
+/* Bytes of one page, 0 if the descriptor is invalid. */
+size_t svdq_kv_page_bytes(const svdq_kv_desc* d);
+
+/* New rows into the cache: for every row, its Q and K heads normalized and turned, K and V
+ * quantized into the token's place.
+ *     z = x / sqrt(mean of the head's x^2 + eps) * norm          (without norm_q / norm_k: x)
+ *     (z[i], z[j]) -> (z[i] c - z[j] s, z[i] s + z[j] c),  i, j = 2 p, 2 p + 1 (or p, p + pairs
+ *         with SVDQ_ROPE_HALVES), c, s = cos, sin of pos[axis[p]][row] freq[p], p < pairs;
+ *         features from 2 pairs on stay
+ * so several axes (time, height, width) share a head as the caller lays them out.  K is rounded
+ * to fp32, to bf16, then quantized; its norm and rotation are computed in float64, so its codes
+ * do not hang on an order of summation.  Q is computed in fp32 (the sines in float64) and written as
+ * bf16.  V is quantized as it is.  A NaN in K or V is stored as 0, an infinity as the largest bf16 of
+ * its sign: whatever a pool is given, no token's values are NaN or infinite.
+ *   K, V     device, bf16 bits, M x heads head_dim, row strides ldk, ldv (parts of one projection's
+ *            rows, say)
+ *   Q, Q_out device, bf16 bits, M x q_heads head_dim; may be the same rows.  q_heads 0: no Q
+ *   norm_q, norm_k  device, bf16 bits [head_dim], 16-byte aligned, or NULL each
+ *   eps      in [0, 1]
+ *   freq     device, float32[pairs] (pairs even, 0 .. head_dim / 2; 0: no rotation)
+ *   axis     device, int32[pairs], or NULL: all 0
+ *   pos      device, int32, axes x M, or NULL: every axis is the token's place in its sequence
+ * A row whose token has no place (lens[b] too small, a page outside the pool) is dropped; its Q is
+ * still written.  Two rows of a call with one place (a page in two sequences) are the caller's to avoid:
+ * either's codes may remain, or a mixture. */
+svdq_status svdq_kv_append(const svdq_kv_desc* d, void* pool, int64_t pages, const int32_t* table, int64_t ldt,
+                           int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch, int64_t M,
+                           const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, const uint16_t* Q,
+                           int64_t ldq, int32_t q_heads, uint16_t* Q_out, int64_t ldqo, const uint16_t* norm_q,
+                           const uint16_t* norm_k, float eps, const float* freq, const int32_t* axis, int32_t pairs,
+                           const int32_t* pos, int32_t axes, uint32_t flags, void* stream);
+
+/* The values the cache holds for the rows' tokens: K and V, M x heads head_dim, bf16 (nearest
+ * even), or float32 with SVDQ_EPI_OUT_F32, which is exact.  Rows of a sequence whose token has no place are zeros. */
+svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table, int64_t ldt,
+                         int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch, int64_t M, void* K,
+                         int64_t ldk, void* V, int64_t ldv, uint32_t flags, void* stream);
+
+/* Attention of the rows' queries over the cache: for each row and query head, with the K/V head
+ * h q = h q_heads / heads .. of it,
+ *     Y = sum_t p_t V_t / sum_t p_t,  p_t = exp(scale Q . K_t),  lse = log sum_t p_t
+ * over the tokens t < lens[b] that are there, up to the row's own (not with SVDQ_KV_FULL), and with
+ * window > 0 only the last `window` of those up to the row's own.  A row that sees nothing gives
+ * zeros and an lse of -infinity.  Scores and sums are fp32; p_t enters the sum over V rounded to
+ * 2^-11 of itself with NVFP4, else to 2^-16 where a sequence has at most 32 query rows a K/V head (tokens
+ * x q_heads / heads, on average) and to 2^-8 where it has more; the same call gives the same bits.
+ *   Q      device, bf16 bits, M x q_heads head_dim, row stride ldq; q_heads a multiple of heads
+ *   scale  > 0
+ *   Y      device, bf16 bits, M x q_heads head_dim; its elements are none of Q's
+ *   lse    device, float32, M x q_heads, or NULL
+ *   workspace  device, svdq_kv_attention_bytes(d, batch, M, q_heads) bytes, 256-byte aligned (NULL
+ *              where that is 0); every call writes what it reads of it
+ * A row with a NaN or an infinity in Q, or whose scores leave fp32's range, has no defined result; no other row changes.
+ * M x q_heads <= 2^27, q_heads <= 4096, and batch x (rows a sequence) x cols x page within what 32 bits count
+ * (2^37 tokens x 16 rows), else SVDQ_ERR_SHAPE. */
+size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t batch, int64_t M, int32_t q_heads);
+svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,
+                              int64_t ldt, int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch,
+                              int64_t M, const uint16_t* Q, int64_t ldq, int32_t q_heads, float scale, int32_t window,
+                              uint32_t flags, void* Y, int64_t ldy, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* Pages onto pages, in every one of `planes` layers' pools (plane_bytes apart, a multiple of 64; at least
+ * pages x svdq_kv_page_bytes(d); unused with one): page dst[i] becomes a copy of page src[i].  A sequence
+ * forks by sharing its full pages in two tables and copying the last, partly filled one; a pool is put in order
+ * likewise.  Freeing a page moves no bytes: it is the caller's bookkeeping.
+ *   src, dst  HOST, int32[n], read before the call returns (a captured graph keeps the values); pages in
+ *             range, no destination twice, no destination that is another pair's source, else SVDQ_ERR_SHAPE */
+svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
+                         const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/* The tokens that stay, moved together: token start[b] + i of sequence b's new place becomes its old
+ * token keep[b ldkeep + i], i < n_keep[b], in every one of `planes` layers' pools.  (Drafts that were
+ * accepted, tokens that eviction keeps.)  The sequence then has start[b] + n_keep[b] tokens; pages
+ * behind those are free.
+ *   table    device, batch x cols, ldt: where the tokens are
+ *   to       device, batch x cols_to, ldto: where they go, none of these pages in `table`; NULL: in place.
+ *            Tokens before start[b] do not move in either case
+ *   start    device, int32[batch], or NULL: 0
+ *   keep     device, int32, batch x most, row stride ldkeep: rising, and so keep[i] >= start + i in place
+ *   n_keep   device, int32[batch], at most `most` (more counts as `most`, less than 0 as 0)
+ * An index without a place, old or new, moves nothing.  In place, keep that does not rise, and pages that
+ * several sequences share, give unspecified tokens in the sequence's own places (nothing else). */
+svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
+                            const int32_t* table, int64_t ldt, int32_t cols, const int32_t* to, int64_t ldto,
+                            int32_t cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep, int32_t most,
+                            const int32_t* n_keep, int32_t batch, void* stream);
+
 /* Both launches; workspace >= svdq_act_bytes(d, M) bytes (device, 256-aligned). */
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X,
                         int64_t M, int64_t ldx, void* Y, int64_t ldy, uint32_t epi,

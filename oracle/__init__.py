@@ -29,6 +29,7 @@ diffusion inference in Diffusers" page; SVDQuant abstract, arXiv 2411.05007):
                   kernel family (AWQ) on the Nunchaku in Diffusers page; and a
                   whole layer (smoothing, low-rank branch) on 16-bit activations.
 * moe.py       -- the router and the 4-bit experts of a mixture of experts.
+* kv.py        -- a key-value cache held in 4 bits and the attention over it.
 * layer.py     -- the layer output of section 4.2:
                   X W = X_hat W_hat ~ X_hat L1 L2 + Q(X_hat) Q(R), plus bias and
                   an optional GELU, in float64; the error measure and bound of

@@ -13,7 +13,7 @@ import functools
 from dataclasses import dataclass
 
 from ._lib import (EPI_BIAS, EPI_GELU, EPI_LOWRANK, EPI_OUT_F32, INT4_G64, MXFP4, NVFP4, LIB_PATH,  # noqa: F401
-                   ROUTE_RENORM, ROUTE_SIGMOID, LayerDesc, SvdqError, check, lib)
+                   KV_FULL, ROPE_HALVES, ROUTE_RENORM, ROUTE_SIGMOID, KvDesc, LayerDesc, SvdqError, check, lib)
 
 FORMATS = {"mxfp4": MXFP4, "int4": INT4_G64, "nvfp4": NVFP4}
 GROUPS = {"mxfp4": 32, "int4": 64, "nvfp4": 16}
@@ -383,6 +383,231 @@ def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi:
     if st:
         check("svdq_moe", st)
     return out
+
+
+# ---- a key-value cache in 4 bits ----
+#
+# Checks, devices and streams as for the few-token calls.  A pool is a uint8 tensor of pages x
+# kv_page_bytes (for kv_copy and kv_compact also layers x pages x kv_page_bytes); table (batch x pages of a
+# sequence), lens (batch) and cu (batch + 1, or None: one row a sequence) are int32 tensors beside it.
+
+@dataclass(frozen=True)
+class KvLayout:
+    """A key-value cache: 4-bit format, K/V heads, features of a head (64, 128), tokens of a page
+    (16, 32, .. 1024)."""
+
+    fmt: str
+    heads: int
+    head_dim: int
+    page: int
+
+    def desc(self) -> KvDesc:
+        return KvDesc(FORMATS[self.fmt], self.heads, self.head_dim, self.page)
+
+
+@functools.lru_cache(maxsize=4096)
+def _kept_kv(kv: KvLayout):
+    p = ctypes.byref(kv.desc())
+    return p, int(lib().svdq_kv_page_bytes(p))
+
+
+def kv_page_bytes(kv: KvLayout) -> int:
+    """Bytes of one page (0: invalid)."""
+    return _kept_kv(kv)[1]
+
+
+def _here(dev, stream) -> bool:
+    return stream is None and dev.index is not None and dev.index == _torch().cuda.current_device()
+
+
+def _pool(t, page_bytes: int, dims: int):
+    torch = _torch()
+    shape = t.shape
+    if t.dtype != torch.uint8 or len(shape) not in range(2, dims + 1) or shape[-1] != page_bytes or not t.is_cuda:
+        raise ValueError(f"pool: expected pages x {page_bytes} bytes on a GPU, got {tuple(shape)} of {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("pool: expected contiguous bytes")
+
+
+def _int_rows(t, name: str, rows: int, device) -> int:
+    """Row stride of an int32 matrix."""
+    if t.dim() != 2 or t.shape[0] != rows or t.dtype != _torch().int32 or t.device != device:
+        raise ValueError(f"{name}: expected {rows} rows of int32 on {device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if rows > 1 else t.shape[1]
+
+
+def _cache_args(kv, pool, table, lens, cu, M: int):
+    """The arguments that calls on one layer's cache begin with."""
+    torch, dev = _torch(), pool.device
+    p, nbytes = _kept_kv(kv)
+    _pool(pool, nbytes, 2)
+    batch = lens.shape[0] if lens.dim() == 1 else -1
+    _flat(lens, "lens", (batch,), dev, torch.int32)
+    ldt = _int_rows(table, "table", batch, dev)
+    if cu is not None:
+        _flat(cu, "cu", (batch + 1,), dev, torch.int32)
+    elif M != batch:
+        raise ValueError(f"cu: needed for {M} rows of {batch} sequences")
+    return (p, pool.data_ptr(), pool.shape[0], table.data_ptr(), ldt, table.shape[1], lens.data_ptr(),
+            None if cu is None else cu.data_ptr(), batch, M)
+
+
+def kv_append(kv: KvLayout, pool, table, lens, K, V, cu=None, Q=None, q_out=None, norm_q=None, norm_k=None,
+              eps: float = 1e-6, freq=None, axis=None, pos=None, halves: bool = False, stream=None):
+    """Rows of K and V (M x heads head_dim bf16) into their places in the cache, K's heads normalized
+    (norm_k: bf16[head_dim]) and turned (freq: float32[pairs]; axis: int32[pairs] or None; pos: int32 axes x M, or
+    None for the tokens' places), Q (M x q_heads head_dim) likewise; returns Q's result (q_out), None without Q."""
+    torch, dev = _torch(), pool.device
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: kv_append(kv, pool, table, lens, K, V, cu, Q, q_out, norm_q, norm_k, eps,
+                                                         freq, axis, pos, halves))
+    M, D, bf16 = K.shape[0], kv.head_dim, (torch.bfloat16, torch.int16)
+    args = _cache_args(kv, pool, table, lens, cu, M)
+    ldk, ldv = _rows(K, "K", kv.heads * D, dev, bf16), _rows(V, "V", kv.heads * D, dev, bf16)
+    ldq = ldo = q_heads = pairs = axes = 0
+    if V.shape[0] != M:
+        raise ValueError(f"V: {V.shape[0]} rows for {M} of K")
+    if Q is not None:
+        if Q.dim() != 2 or Q.shape[1] == 0 or Q.shape[1] % D or Q.shape[0] != M:
+            raise ValueError(f"Q: expected {M} rows of heads x {D}, got {tuple(Q.shape)}")
+        q_heads = Q.shape[1] // D
+        ldq = _rows(Q, "Q", q_heads * D, dev, bf16)
+        if q_out is None:
+            q_out, ldo = torch.empty((M, q_heads * D), dtype=Q.dtype, device=dev), q_heads * D
+        else:
+            ldo = _rows(q_out, "q_out", q_heads * D, dev, bf16)
+            if q_out.shape[0] != M:
+                raise ValueError(f"q_out: {q_out.shape[0]} rows for {M}")
+    elif q_out is not None:
+        raise ValueError("q_out: given without Q")
+    for name, w in (("norm_q", norm_q), ("norm_k", norm_k)):
+        if w is not None:
+            _flat(w, name, (D,), dev, w.dtype if w.dtype == torch.int16 else torch.bfloat16)
+    if freq is not None:
+        pairs = freq.shape[0] if freq.dim() == 1 else -1
+        _flat(freq, "freq", (pairs,), dev, torch.float32)
+        if axis is not None:
+            _flat(axis, "axis", (pairs,), dev, torch.int32)
+        if pos is not None:
+            axes = pos.shape[0] if pos.dim() == 2 else -1
+            _flat(pos, "pos", (axes, M), dev, torch.int32)
+    elif axis is not None or pos is not None:
+        raise ValueError("axis, pos: given without freq")
+    st = lib().svdq_kv_append(*args, K.data_ptr(), ldk, V.data_ptr(), ldv, None if Q is None else Q.data_ptr(), ldq,
+                              q_heads, None if q_out is None else q_out.data_ptr(), ldo,
+                              None if norm_q is None else norm_q.data_ptr(),
+                              None if norm_k is None else norm_k.data_ptr(), eps,
+                              None if freq is None else freq.data_ptr(), None if axis is None else axis.data_ptr(),
+                              pairs, None if pos is None else pos.data_ptr(), axes, ROPE_HALVES if halves else 0,
+                              torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_kv_append", st)
+    return q_out
+
+
+def kv_read(kv: KvLayout, pool, table, lens, M: int, cu=None, f32: bool = False, stream=None):
+    """K and V (M x heads head_dim, bf16, or float32) that the cache holds for the M rows' tokens."""
+    torch, dev = _torch(), pool.device
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: kv_read(kv, pool, table, lens, M, cu, f32))
+    args, cols = _cache_args(kv, pool, table, lens, cu, M), kv.heads * kv.head_dim
+    K = torch.empty((M, cols), dtype=torch.float32 if f32 else torch.bfloat16, device=dev)
+    V = torch.empty_like(K)
+    st = lib().svdq_kv_read(*args, K.data_ptr(), cols, V.data_ptr(), cols, EPI_OUT_F32 if f32 else 0,
+                            torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_kv_read", st)
+    return K, V
+
+
+def kv_attention_bytes(kv: KvLayout, batch: int, M: int, q_heads: int) -> int:
+    """Workspace bytes of kv_attention (0: none needed, or invalid)."""
+    return int(lib().svdq_kv_attention_bytes(_kept_kv(kv)[0], int(batch), int(M), int(q_heads)))
+
+
+def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = None, window: int = 0, causal: bool = True,
+                 out=None, lse=False, workspace=None, stream=None):
+    """Attention of Q's rows (M x q_heads head_dim bf16) over the cache, scale 1 / sqrt(head_dim) unless given; returns
+    out (like Q), or with lse (True, or a float32 tensor M x q_heads) out and the rows' log sums."""
+    torch, dev = _torch(), pool.device
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: kv_attention(kv, pool, table, lens, Q, cu, scale, window, causal, out, lse,
+                                                            workspace))
+    D, bf16 = kv.head_dim, (torch.bfloat16, torch.int16)
+    if Q.dim() != 2 or Q.shape[1] % D:
+        raise ValueError(f"Q: expected rows of heads x {D}, got {tuple(Q.shape)}")
+    M, cols = Q.shape
+    q_heads = cols // D
+    args = _cache_args(kv, pool, table, lens, cu, M)
+    ldq = _rows(Q, "Q", cols, dev, bf16)
+    if out is None:
+        out, ldy = torch.empty((M, cols), dtype=Q.dtype, device=dev), cols
+    else:
+        ldy = _rows(out, "out", cols, dev, bf16)
+        if out.shape[0] != M:
+            raise ValueError(f"out: {out.shape[0]} rows for {M}")
+    if lse is True:
+        lse = torch.empty((M, q_heads), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    if lse is not None:
+        _flat(lse, "lse", (M, q_heads), dev, torch.float32)
+    L = lib()
+    ws = _space(workspace, L.svdq_kv_attention_bytes(args[0], args[8], M, q_heads), dev)
+    st = L.svdq_kv_attention(*args, Q.data_ptr(), ldq, q_heads, D ** -0.5 if scale is None else scale, window,
+                             0 if causal else KV_FULL, out.data_ptr(), ldy, None if lse is None else lse.data_ptr(),
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                             torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_kv_attention", st)
+    return out if lse is None else (out, lse)
+
+
+def kv_copy(kv: KvLayout, pool, src, dst, stream=None):
+    """Pages src (ints on the host) onto pages dst, in every layer of the pool ([layers x] pages x bytes); returns
+    the pool."""
+    dev = pool.device
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: kv_copy(kv, pool, src, dst))
+    p, nbytes = _kept_kv(kv)
+    _pool(pool, nbytes, 3)
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError(f"{n} sources for {len(dst)} destinations")
+    ids = (ctypes.c_int32 * n)(*src), (ctypes.c_int32 * n)(*dst)
+    pages = pool.shape[-2]
+    st = lib().svdq_kv_copy(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes, ids[0],
+                            ids[1], n, _torch()._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_kv_copy", st)
+    return pool
+
+
+def kv_compact(kv: KvLayout, pool, table, keep, n_keep, start=None, to=None, stream=None):
+    """Token start[b] + i of sequence b becomes its old token keep[b, i], i < n_keep[b], in every layer of the pool:
+    in place (keep rises), or from table's pages into those of `to`; returns the pool."""
+    torch, dev = _torch(), pool.device
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: kv_compact(kv, pool, table, keep, n_keep, start, to))
+    p, nbytes = _kept_kv(kv)
+    _pool(pool, nbytes, 3)
+    batch = n_keep.shape[0] if n_keep.dim() == 1 else -1
+    _flat(n_keep, "n_keep", (batch,), dev, torch.int32)
+    ldt, ldk = _int_rows(table, "table", batch, dev), _int_rows(keep, "keep", batch, dev)
+    ldto = 0 if to is None else _int_rows(to, "to", batch, dev)
+    if start is not None:
+        _flat(start, "start", (batch,), dev, torch.int32)
+    pages = pool.shape[-2]
+    st = lib().svdq_kv_compact(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes,
+                               table.data_ptr(), ldt, table.shape[1], None if to is None else to.data_ptr(), ldto,
+                               0 if to is None else to.shape[1], None if start is None else start.data_ptr(),
+                               keep.data_ptr(), ldk, keep.shape[1], n_keep.data_ptr(), batch,
+                               torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check("svdq_kv_compact", st)
+    return pool
 
 
 def _scales_out(torch, layer: Layer, rows: int, dev):

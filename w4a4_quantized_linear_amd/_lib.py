@@ -15,6 +15,8 @@ EPI_GELU = 4
 EPI_OUT_F32 = 8
 ROUTE_SIGMOID = 1
 ROUTE_RENORM = 2
+ROPE_HALVES = 1
+KV_FULL = 1
 
 STATUS = {0: "SVDQ_OK", 1: "SVDQ_ERR_NULL", 2: "SVDQ_ERR_SHAPE", 3: "SVDQ_ERR_FORMAT", 4: "SVDQ_ERR_ALIGN",
           5: "SVDQ_ERR_WORKSPACE", 6: "SVDQ_ERR_DEVICE", 7: "SVDQ_ERR_LAUNCH", 8: "SVDQ_ERR_TOO_LARGE"}
@@ -23,6 +25,10 @@ STATUS = {0: "SVDQ_OK", 1: "SVDQ_ERR_NULL", 2: "SVDQ_ERR_SHAPE", 3: "SVDQ_ERR_FO
 _P = ctypes.c_void_p
 _D = ctypes.c_void_p          # const svdq_layer_desc*
 _I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
+_U32 = ctypes.c_uint32
+_F32 = ctypes.c_float
+_CACHE = [_D, _P, _I64, _P, _I64, _I32, _P, _P, _I32, _I64]   # descriptor .. lens, cu, batch, M
 SIGNATURES = {
     "svdq_weight_bytes": (ctypes.c_size_t, [_D]),
     "svdq_act_bytes": (ctypes.c_size_t, [_D, _I64]),
@@ -41,6 +47,16 @@ SIGNATURES = {
     "svdq_moe_bytes": (ctypes.c_size_t, [_D, _D, _I64, ctypes.c_int32]),
     "svdq_moe": (ctypes.c_int, [_D, _P, _D, _P, ctypes.c_int32, _P, _I64, _I64, _P, _P, ctypes.c_int32, _P, _I64,
                                 ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
+    "svdq_kv_page_bytes": (ctypes.c_size_t, [_D]),
+    "svdq_kv_append": (ctypes.c_int, _CACHE + [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _F32, _P, _P, _I32,
+                                               _P, _I32, _U32, _P]),
+    "svdq_kv_read": (ctypes.c_int, _CACHE + [_P, _I64, _P, _I64, _U32, _P]),
+    "svdq_kv_attention_bytes": (ctypes.c_size_t, [_D, _I32, _I64, _I32]),
+    "svdq_kv_attention": (ctypes.c_int, _CACHE + [_P, _I64, _I32, _F32, _I32, _U32, _P, _I64, _P, _P, ctypes.c_size_t,
+                                                  _P]),
+    "svdq_kv_copy": (ctypes.c_int, [_D, _P, _I64, _I32, _I64, _P, _P, _I64, _P]),
+    "svdq_kv_compact": (ctypes.c_int, [_D, _P, _I64, _I32, _I64, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _I64, _I32, _P,
+                                       _I32, _P]),
     "svdq_linear": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
     "svdq_linear_noalloc": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P]),
     "svdq_unpack_weight": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P]),
@@ -54,6 +70,10 @@ SIGNATURES = {
 
 class LayerDesc(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("fmt", _I32), ("heads", _I32), ("head_dim", _I32), ("page", _I32)]
 
 
 class SvdqError(RuntimeError):

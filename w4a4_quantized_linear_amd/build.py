@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsvdq.so")
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "w4a16.hip", "moe.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "w4a16.hip", "moe.hip", "kv.hip", "kv_attention.hip"]
 ARCH = "gfx950"
 
 

@@ -2,10 +2,14 @@
 // Every check runs on the host before anything is enqueued; see include/svdq.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "svdq.h"
+#include "kv.h"
 #include "layout.h"
 
 namespace svdq {
@@ -40,6 +44,20 @@ hipError_t launch_moe(int fmt_g, const uint8_t* wg, const WeightLayout& lg, int 
                       const WeightLayout& ld, int H, int F, int N, int E, const uint16_t* X, int64_t M, int64_t ldx,
                       const int32_t* ids, const float* weights, int top_k, void* Y, int64_t ldy, uint32_t epi,
                       void* ws, hipStream_t s);
+hipError_t launch_kv_append(int fmt, int D, const KvCache& kc, const uint16_t* K, int64_t ldk, const uint16_t* V,
+                            int64_t ldv, const uint16_t* Q, int64_t ldq, int q_heads, uint16_t* Q_out, int64_t ldqo,
+                            const uint16_t* norm_q, const uint16_t* norm_k, float eps, const float* freq,
+                            const int32_t* axis, int pairs, const int32_t* pos, int axes, bool halves, hipStream_t s);
+hipError_t launch_kv_read(int fmt, int D, const KvCache& kc, void* K, int64_t ldk, void* V, int64_t ldv, bool f32,
+                          hipStream_t s);
+hipError_t launch_kv_attention(int fmt, int D, const KvCache& kc, const uint16_t* Q, int64_t ldq, int q_heads,
+                               float scale, int window, bool causal, uint16_t* Y, int64_t ldy, float* lse, float* part,
+                               hipStream_t s);
+hipError_t launch_kv_copy(uint8_t* pool, int planes, int64_t plane_bytes, int64_t page_bytes, const int32_t* src,
+                          const int32_t* dst, int64_t n, hipStream_t s);
+hipError_t launch_kv_compact(int fmt, int D, const KvCache& kc, int planes, int64_t plane_bytes, const int32_t* to,
+                             int64_t ldto, int cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep,
+                             const int32_t* n_keep, int most, bool in_place, hipStream_t s);
 hipError_t launch_unpack_weight(int fmt, int K, int N, int rank, const WeightLayout& wl, const uint8_t* blob,
                                 uint8_t* codes, void* scales, uint16_t* L1, uint16_t* L2, float* lam, uint16_t* bias,
                                 hipStream_t s);
@@ -148,6 +166,73 @@ svdq_status check_gemm_args(const svdq_layer_desc* d, const void* w_packed, cons
   return SVDQ_OK;
 }
 
+// Every page in range, no destination twice, and none of them a source of another pair.  Two bits a page would
+// be an allocation for a large pool, so the pairs are sorted instead where there are many.
+bool kv_pairs_valid(const int32_t* src, const int32_t* dst, int64_t n, int64_t pages) {
+  for (int64_t i = 0; i < n; ++i)
+    if (src[i] < 0 || src[i] >= pages || dst[i] < 0 || dst[i] >= pages) return false;
+  if (n <= 64) {
+    for (int64_t i = 0; i < n; ++i)
+      for (int64_t j = 0; j < n; ++j)
+        if (i != j && (dst[i] == dst[j] || dst[i] == src[j])) return false;
+    return true;
+  }
+  std::unique_ptr<int32_t[]> d(new (std::nothrow) int32_t[n]);
+  if (!d) return false;
+  std::copy(dst, dst + n, d.get());
+  std::sort(d.get(), d.get() + n);
+  for (int64_t i = 1; i < n; ++i)
+    if (d[i] == d[i - 1]) return false;
+  for (int64_t i = 0; i < n; ++i)
+    if (src[i] != dst[i] && std::binary_search(d.get(), d.get() + n, src[i])) return false;
+  return true;
+}
+
+svdq_status check_kv(const svdq_kv_desc* d) {
+  const int page = d->page;
+  if (d->heads < 1 || d->heads > kKvMaxHeads || (d->head_dim != 64 && d->head_dim != 128) || page < kKvTile ||
+      page > kKvMaxPage || (page & (page - 1)) != 0)
+    return SVDQ_ERR_SHAPE;
+  return d->fmt == SVDQ_MXFP4 || d->fmt == SVDQ_INT4_G64 || d->fmt == SVDQ_NVFP4 ? SVDQ_OK : SVDQ_ERR_FORMAT;
+}
+
+int64_t kv_page_bytes(const svdq_kv_desc* d) {
+  return int64_t(d->heads) * (d->page / kKvTile) * kv_tile_bytes(d->fmt, d->head_dim);
+}
+
+// The checks that every call on a cache shares, and the cache as the kernels take it.
+svdq_status check_cache(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table, int64_t ldt,
+                        int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch, int64_t M, KvCache* kc) {
+  const svdq_status s = check_kv(d);
+  if (s == SVDQ_ERR_SHAPE) return s;
+  if (pages < 1 || pages > kKvMaxPages || batch < 0 || batch > kKvMaxBatch || cols < 1 || ldt < cols ||
+      int64_t(cols) * d->page > kKvMaxTokens || M < 0 || M > kKvMaxRows || (cu == nullptr && M != batch) ||
+      (M > 0 && batch == 0) || int64_t(batch) * d->heads > kKvMaxRows)
+    return SVDQ_ERR_SHAPE;
+  if (s != SVDQ_OK) return s;
+  if (!aligned(pool, 64) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(cu, 4)) return SVDQ_ERR_ALIGN;
+  kc->pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  kc->table = table;
+  kc->lens = lens;
+  kc->cu = cu;
+  kc->page_bytes = kv_page_bytes(d);
+  kc->ldt = ldt;
+  kc->pages = int32_t(pages);
+  kc->cols = cols;
+  kc->batch = batch;
+  kc->M = int32_t(M);
+  kc->heads = d->heads;
+  kc->page_shift = 0;
+  while (kKvTile << kc->page_shift < d->page) ++kc->page_shift;
+  return SVDQ_OK;
+}
+
+// A matrix of M rows of `cols` 16-bit or (align 16 bytes all the same) 32-bit elements.
+svdq_status check_rows(const void* p, int64_t ld, int64_t cols) {
+  if (ld < cols || ld > kMaxLdx) return SVDQ_ERR_SHAPE;
+  return aligned(p, 16) && ld % 8 == 0 ? SVDQ_OK : SVDQ_ERR_ALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -158,7 +243,7 @@ const char* svdq_status_str(svdq_status s) {
   switch (s) {
     case SVDQ_OK: return "ok";
     case SVDQ_ERR_NULL: return "a required pointer is NULL";
-    case SVDQ_ERR_SHAPE: return "unsupported shape (K % 512, N % 16, 0 <= rank <= 256, M, ldx/ldy, experts, top_k)";
+    case SVDQ_ERR_SHAPE: return "unsupported shape (K % 512, N % 16, 0 <= rank <= 256, M, ldx/ldy, experts, top_k, heads, pages)";
     case SVDQ_ERR_FORMAT: return "unknown format or epilogue flag";
     case SVDQ_ERR_ALIGN: return "misaligned pointer or row stride";
     case SVDQ_ERR_WORKSPACE: return "workspace smaller than the entry point's size query (svdq_act_bytes, svdq_w4a16_bytes, ...)";
@@ -380,6 +465,141 @@ svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svd
   return launched(launch_moe(dg->fmt, static_cast<const uint8_t*>(wg_packed), lg, dd->fmt,
                              static_cast<const uint8_t*>(wd_packed), ld, dg->K, dd->K, dd->N, E, X, M, ldx, ids, weights,
                              top_k, Y, ldy, epi, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_kv_page_bytes(const svdq_kv_desc* d) {
+  return d && check_kv(d) == SVDQ_OK ? size_t(kv_page_bytes(d)) : 0;
+}
+
+svdq_status svdq_kv_append(const svdq_kv_desc* d, void* pool, int64_t pages, const int32_t* table, int64_t ldt,
+                           int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch, int64_t M,
+                           const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, const uint16_t* Q,
+                           int64_t ldq, int32_t q_heads, uint16_t* Q_out, int64_t ldqo, const uint16_t* norm_q,
+                           const uint16_t* norm_k, float eps, const float* freq, const int32_t* axis, int32_t pairs,
+                           const int32_t* pos, int32_t axes, uint32_t flags, void* stream) {
+  if (!d || !pool || (batch > 0 && (!table || !lens)) || (M > 0 && (!K || !V || (q_heads > 0 && (!Q || !Q_out)))) ||
+      (pairs > 0 && !freq))
+    return SVDQ_ERR_NULL;
+  KvCache kc;
+  svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
+  if (s == SVDQ_ERR_SHAPE) return s;
+  if (q_heads < 0 || q_heads > kKvMaxQHeads || pairs < 0 || pairs > d->head_dim / 2 || pairs % 2 != 0 || axes < 0 ||
+      axes > kKvMaxAxes || (pos && axes < 1) || !(eps >= 0.0f && eps <= 1.0f))
+    return SVDQ_ERR_SHAPE;
+  if (s == SVDQ_ERR_FORMAT || (flags & ~uint32_t(SVDQ_ROPE_HALVES)) != 0) return SVDQ_ERR_FORMAT;
+  const int64_t cols_kv = int64_t(d->heads) * d->head_dim, cols_q = int64_t(q_heads) * d->head_dim;
+  svdq_status r[4] = {check_rows(K, ldk, cols_kv), check_rows(V, ldv, cols_kv), SVDQ_OK, SVDQ_OK};
+  if (q_heads > 0) {
+    r[2] = check_rows(Q, ldq, cols_q);
+    r[3] = check_rows(Q_out, ldqo, cols_q);
+  }
+  for (svdq_status x : r)
+    if (x == SVDQ_ERR_SHAPE) return x;
+  for (svdq_status x : r)
+    if (x != SVDQ_OK) return x;
+  if (s != SVDQ_OK) return s;
+  if (!aligned(norm_q, 16) || !aligned(norm_k, 16) || !aligned(freq, 4) || !aligned(axis, 4) || !aligned(pos, 4))
+    return SVDQ_ERR_ALIGN;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  return launched(launch_kv_append(d->fmt, d->head_dim, kc, K, ldk, V, ldv, q_heads > 0 ? Q : nullptr, ldq, q_heads,
+                                   Q_out, ldqo, norm_q, norm_k, eps, freq, axis, pairs, pos, axes,
+                                   (flags & SVDQ_ROPE_HALVES) != 0, static_cast<hipStream_t>(stream)));
+}
+
+svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table, int64_t ldt,
+                         int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch, int64_t M, void* K,
+                         int64_t ldk, void* V, int64_t ldv, uint32_t flags, void* stream) {
+  if (!d || !pool || (batch > 0 && (!table || !lens)) || (M > 0 && (!K || !V))) return SVDQ_ERR_NULL;
+  KvCache kc;
+  svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
+  if (s == SVDQ_ERR_SHAPE) return s;
+  const int64_t cols_kv = int64_t(d->heads) * d->head_dim;
+  const svdq_status rk = check_rows(K, ldk, cols_kv), rv = check_rows(V, ldv, cols_kv);
+  if (rk == SVDQ_ERR_SHAPE || rv == SVDQ_ERR_SHAPE) return SVDQ_ERR_SHAPE;
+  if (s == SVDQ_ERR_FORMAT || (flags & ~uint32_t(SVDQ_EPI_OUT_F32)) != 0) return SVDQ_ERR_FORMAT;
+  if (s != SVDQ_OK || rk != SVDQ_OK || rv != SVDQ_OK) return SVDQ_ERR_ALIGN;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  return launched(launch_kv_read(d->fmt, d->head_dim, kc, K, ldk, V, ldv, (flags & SVDQ_EPI_OUT_F32) != 0,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t batch, int64_t M, int32_t q_heads) {
+  if (!d || check_kv(d) != SVDQ_OK || batch < 1 || batch > kKvMaxBatch || M < 1 || M > kKvMaxRows || q_heads < 1 ||
+      q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || M * q_heads > kKvMaxRowHeads)
+    return 0;
+  return kv_plan(d->head_dim, batch, M, q_heads, d->heads).bytes;
+}
+
+svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,
+                              int64_t ldt, int32_t cols, const int32_t* lens, const int32_t* cu, int32_t batch,
+                              int64_t M, const uint16_t* Q, int64_t ldq, int32_t q_heads, float scale, int32_t window,
+                              uint32_t flags, void* Y, int64_t ldy, float* lse, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  const size_t need = svdq_kv_attention_bytes(d, batch, M, q_heads);
+  if (!d || !pool || (batch > 0 && (!table || !lens)) || (M > 0 && (!Q || !Y)) || (need > 0 && !workspace))
+    return SVDQ_ERR_NULL;
+  KvCache kc;
+  svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
+  if (s == SVDQ_ERR_SHAPE) return s;
+  if (q_heads < 1 || q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || window < 0 ||
+      !(scale > 0.0f && scale <= 3.0e38f) || M * q_heads > kKvMaxRowHeads ||
+      !kv_units_fit(d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
+    return SVDQ_ERR_SHAPE;
+  const int64_t cols_q = int64_t(q_heads) * d->head_dim;
+  const svdq_status rq = check_rows(Q, ldq, cols_q), ry = check_rows(Y, ldy, cols_q);
+  if (rq == SVDQ_ERR_SHAPE || ry == SVDQ_ERR_SHAPE) return SVDQ_ERR_SHAPE;
+  if (s == SVDQ_ERR_FORMAT || (flags & ~uint32_t(SVDQ_KV_FULL)) != 0) return SVDQ_ERR_FORMAT;
+  if (s != SVDQ_OK || rq != SVDQ_OK || ry != SVDQ_OK || !aligned(lse, 4) || !aligned(workspace, 256))
+    return SVDQ_ERR_ALIGN;
+  if (ws_bytes < need) return SVDQ_ERR_WORKSPACE;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (M == 0) return SVDQ_OK;
+  return launched(launch_kv_attention(d->fmt, d->head_dim, kc, Q, ldq, q_heads, scale, window,
+                                      (flags & SVDQ_KV_FULL) == 0, static_cast<uint16_t*>(Y), ldy, lse,
+                                      static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
+                         const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+  if (!d || !pool || (n > 0 && (!src || !dst))) return SVDQ_ERR_NULL;
+  svdq_status s = check_kv(d);
+  if (s == SVDQ_ERR_SHAPE || pages < 1 || pages > kKvMaxPages || planes < 1 || planes > kKvMaxPlanes || n < 0 ||
+      n > pages)
+    return SVDQ_ERR_SHAPE;
+  if (s != SVDQ_OK) return s;
+  const int64_t page_bytes = kv_page_bytes(d);
+  if (planes > 1 && plane_bytes < pages * page_bytes) return SVDQ_ERR_SHAPE;
+  if (!kv_pairs_valid(src, dst, n, pages)) return SVDQ_ERR_SHAPE;
+  if (!aligned(pool, 64) || (planes > 1 && plane_bytes % 64 != 0)) return SVDQ_ERR_ALIGN;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (n == 0) return SVDQ_OK;
+  return launched(launch_kv_copy(static_cast<uint8_t*>(pool), planes, plane_bytes, page_bytes, src, dst, n,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
+                            const int32_t* table, int64_t ldt, int32_t cols, const int32_t* to, int64_t ldto,
+                            int32_t cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep, int32_t most,
+                            const int32_t* n_keep, int32_t batch, void* stream) {
+  if (!d || !pool || (batch > 0 && (!table || !n_keep || (most > 0 && !keep)))) return SVDQ_ERR_NULL;
+  KvCache kc;
+  svdq_status s = check_cache(d, pool, pages, table, ldt, cols, n_keep, nullptr, batch, batch, &kc);
+  if (s == SVDQ_ERR_SHAPE || planes < 1 || planes > kKvMaxPlanes || most < 0 || most > kKvMaxTokens || ldkeep < most ||
+      (to && (cols_to < 1 || ldto < cols_to || int64_t(cols_to) * d->page > kKvMaxTokens)))
+    return SVDQ_ERR_SHAPE;
+  if (s == SVDQ_ERR_FORMAT) return s;
+  if (planes > 1 && plane_bytes < pages * kc.page_bytes) return SVDQ_ERR_SHAPE;
+  if (s != SVDQ_OK || (planes > 1 && plane_bytes % 64 != 0) || !aligned(to, 4) || !aligned(start, 4) ||
+      !aligned(keep, 4))
+    return SVDQ_ERR_ALIGN;
+  if ((s = device_check()) != SVDQ_OK) return s;
+  if (batch == 0 || most == 0) return SVDQ_OK;
+  const bool in_place = to == nullptr || to == table;
+  return launched(launch_kv_compact(d->fmt, d->head_dim, kc, planes, plane_bytes, in_place ? table : to,
+                                    in_place ? ldt : ldto, in_place ? cols : cols_to, start, keep, ldkeep, n_keep,
+                                    most, in_place, static_cast<hipStream_t>(stream)));
 }
 
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,

@@ -1,0 +1,185 @@
+// A key-value cache held in 4 bits: its layout, and how the kernels find a row's place.
+//
+// The pool is a sequence of pages of `page` tokens.  A page holds its heads one after the other, a head its
+// tiles of 16 tokens, a tile
+//   K codes   16 rows of D / 2 bytes, two codes a byte, the even feature in the low nibble
+//   V codes   for each 4 tokens 16 pieces of 4 x D / 32 bytes: piece r holds D / 16 features of the 4 tokens, token
+//             by token.  MXFP4, NVFP4: features r D / 16 ..; INT4: 64 g + 4 r .. + 3 of every 64-group g in turn
+//   K scales  MXFP4, NVFP4: 16 rows of D / group bytes; INT4: for each group 16 fp16
+//   V scales  for each group 16 bytes (INT4: 16 fp16)
+// INT4 codes are stored as q + 8.  Scales are E8M0 bytes (MXFP4), fp16 (INT4), E4M3 bytes (NVFP4, tensor scale 1).
+//
+// Why so: with the tokens as rows of a 16x16x32 MFMA's A operand, lane (r, c) of a wave holds token r's features
+// c D / 4 .. + D / 4 (INT4: 16 of each group), 8 or 16 bytes of a K row.  The scores then lie in registers as lane
+// (query r, tokens 4 c .. 4 c + 3), which is the B operand of V^T P^T over 32 tokens if its k order is tokens 4 c .. of
+// one tile and of the next; the A operand's lane (feature piece r, c) needs the same 4 tokens' piece r: 8 or 16
+// bytes that lie together.  So a tile is four loads a lane, all of them whole lines, and neither K, V nor the
+// probabilities pass through LDS.
+#pragma once
+#include "common.h"
+
+namespace svdq {
+
+constexpr int kKvTile = 16;
+constexpr int64_t kKvMaxRows = int64_t(1) << 22;    // rows, batch x heads: workgroups of 256 in one grid dimension
+constexpr int kKvMaxBatch = 16384;
+constexpr int kKvMaxHeads = 256;
+constexpr int kKvMaxPlanes = 4096;
+constexpr int kKvMaxQHeads = 4096;
+constexpr int64_t kKvMaxRowHeads = int64_t(1) << 27;   // rows x query heads of an attention call
+constexpr int kKvMaxPage = 1024;
+constexpr int kKvMaxAxes = 16;
+constexpr int64_t kKvMaxPages = int64_t(1) << 30;
+constexpr int64_t kKvMaxTokens = int64_t(1) << 30;  // of one sequence's table
+
+__host__ __device__ constexpr int kv_group(int fmt) { return fmt == kFmtMXFP4 ? 32 : fmt == kFmtINT4 ? 64 : 16; }
+// Scale bytes of one token's K or V.
+__host__ __device__ constexpr int kv_scales(int fmt, int D) { return D / kv_group(fmt) * (fmt == kFmtINT4 ? 2 : 1); }
+__host__ __device__ constexpr int kv_tile_bytes(int fmt, int D) { return kKvTile * (D + 2 * kv_scales(fmt, D)); }
+
+// How a call of svdq_kv_attention is cut: `rows` query rows of a K/V head (a sequence's tokens x the heads that share
+// it) a workgroup, `jobs` such tiles at most; split: `ranges` workgroups a head share the units of all jobs.
+constexpr int kKvRangeGroups = 768;          // workgroups of a split call: three a CU
+struct KvPlan {
+  int rows, jobs, ranges;
+  bool split;
+  size_t bytes;
+};
+inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads) {
+  KvPlan p;
+  const int64_t group = q_heads / heads, each = (M * group + batch - 1) / (batch > 0 ? batch : 1);
+  p.rows = each <= 16 ? 16 : each <= 32 ? 32 : 128;
+  const int64_t jobs = (M * group + p.rows - 1) / p.rows + batch;
+  p.jobs = int(jobs);
+  p.split = p.rows < 128 || jobs * heads < 512;
+  p.ranges = p.split ? (kKvRangeGroups + heads - 1) / heads : 0;
+  p.bytes = p.split ? align256(size_t(p.ranges) * heads * 2 * p.rows * (D + 2) * 4) : 0;
+  return p;
+}
+
+// Whether the units of all jobs, of tables with `places` tokens each, can be counted in 32 bits.
+inline bool kv_units_fit(int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
+  const KvPlan p = kv_plan(D, batch, M, q_heads, heads);
+  return !p.split || p.jobs * (places / (p.rows < 128 ? 128 : 32) + 1) <= INT32_MAX - kKvRangeGroups;
+}
+
+// A cache and its sequences, as the kernels take them.  Places beyond a sequence's table or with a page outside
+// [0, pages) hold no token: writes to them are dropped, reads find nothing.
+struct KvCache {
+  uint8_t* pool;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* cu;               // rows of sequence b: cu[b] .. cu[b + 1]; NULL: one row each
+  int64_t page_bytes, ldt;
+  int32_t pages, cols, batch, M, heads, page_shift;   // a page has 1 << page_shift tiles
+
+  __device__ __forceinline__ int capacity() const { return cols << (page_shift + 4); }
+  // Tokens, first row and rows of sequence b.
+  __device__ __forceinline__ void sequence(int b, int& len, int& row, int& rows) const {
+    len = max(lens[b], 0);
+    if (cu == nullptr) {
+      row = b;
+      rows = 1;
+    } else {
+      row = min(max(cu[b], 0), M);
+      rows = max(min(cu[b + 1], M) - row, 0);
+    }
+  }
+  // The page of a place (tile) of sequence b, -1 if there is none.
+  __device__ __forceinline__ int page_of(int b, int tile) const {
+    const int at = tile >> page_shift;
+    if (tile < 0 || at >= cols) return -1;
+    const int p = table[b * ldt + at];
+    return p >= 0 && p < pages ? p : -1;
+  }
+};
+
+// The sequence of row m, by the whole wave: the last b with cu[b] <= m; -1 behind the last row.
+__device__ __forceinline__ int kv_sequence_of(const int32_t* cu, int batch, int m, int lane) {
+  if (cu[batch] <= m || cu[0] > m) return -1;
+  int lo = 0, n = batch;                                    // the answer is in lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 63) / 64, i = lane * step;
+    const uint64_t le = __ballot(i < n && cu[lo + i] <= m);
+    const int k = 63 - __builtin_clzll(le | 1);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// ---- 4-bit codes of K and V (tensor scale 1) ----
+
+// Finite bf16 of x: NaN becomes 0, infinities (and what rounds to them) the largest of their sign.
+__device__ __forceinline__ float kv_finite_bf16(float x) {
+  const float b = bf_lo(f2bf(x));
+  return x != x ? 0.f : fminf(fmaxf(b, -3.38953138925e38f), 3.38953138925e38f);
+}
+
+// Scale of a group whose largest magnitude is amax: its bits in the pool, and the number that x is divided by.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_scale(float amax, float& div) {
+  if constexpr (FMT == kFmtMXFP4) {
+    const uint32_t b = e8m0_of_amax(amax);
+    div = scale_operand(b);
+    return b;
+  } else if constexpr (FMT == kFmtINT4) {
+    const _Float16 s = static_cast<_Float16>(fminf(amax / 7.0f, 65504.0f));
+    div = float(s);
+    return __builtin_bit_cast(uint16_t, s);
+  } else {
+    const uint32_t b = e4m3_rne(amax / 6.0f);
+    div = e4m3_value(b);
+    return b;
+  }
+}
+// Byte of two codes, x0 in the low nibble.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_encode(float x0, float x1, float div) {
+  if constexpr (FMT == kFmtMXFP4) {
+    return cvt_fp4x2_div<0>(0, x0, x1, div) & 0xFFu;
+  } else if constexpr (FMT == kFmtINT4) {
+    if (div == 0.f) return 0x88u;
+    const float a = fminf(fmaxf(__builtin_rintf(x0 / div), -8.f), 7.f);
+    const float b = fminf(fmaxf(__builtin_rintf(x1 / div), -8.f), 7.f);
+    return uint32_t(int(a) + 8) | uint32_t(int(b) + 8) << 4;
+  } else {
+    const float a = div == 0.f ? copysignf(0.f, x0) : x0 / div;
+    const float b = div == 0.f ? copysignf(0.f, x1) : x1 / div;
+    return cvt_fp4x2<0>(0, a, b) & 0xFFu;
+  }
+}
+// The two values of a byte, given the scale's bits.
+template <int FMT>
+__device__ __forceinline__ v2f kv_decode(uint32_t byte, uint32_t scale) {
+  if constexpr (FMT == kFmtMXFP4) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(byte, scale_operand(scale), 0);
+  } else if constexpr (FMT == kFmtINT4) {
+    const float s = float(__builtin_bit_cast(_Float16, uint16_t(scale)));
+    return v2f{(int(byte & 15) - 8) * s, (int(byte >> 4) - 8) * s};
+  } else {
+    const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(byte, 1.0f, 0);
+    const float s = e4m3_value(scale);
+    return v2f{v.x * s, v.y * s};
+  }
+}
+
+// Where, in a tile, the byte of features d, d + 1 (d even) of token t lies, and the scale of d's group.
+template <int FMT, int D>
+__device__ __forceinline__ int kv_k_code(int t, int d) { return t * (D / 2) + d / 2; }
+template <int FMT, int D>
+__device__ __forceinline__ int kv_v_code(int t, int d) {
+  const int r = FMT == kFmtINT4 ? (d & 63) >> 2 : d / (D / 16);
+  const int byte = FMT == kFmtINT4 ? (d >> 6) * 2 + ((d & 3) >> 1) : (d % (D / 16)) / 2;
+  return 8 * D + ((t >> 2) * 16 + r) * (D / 8) + (t & 3) * (D / 32) + byte;
+}
+template <int FMT, int D>
+__device__ __forceinline__ int kv_k_scale(int t, int g) {
+  return 16 * D + (FMT == kFmtINT4 ? (g * 16 + t) * 2 : t * (D / kv_group(FMT)) + g);
+}
+template <int FMT, int D>
+__device__ __forceinline__ int kv_v_scale(int t, int g) {
+  return 16 * (D + kv_scales(FMT, D)) + (FMT == kFmtINT4 ? (g * 16 + t) * 2 : g * 16 + t);
+}
+
+}  // namespace svdq
