@@ -48,48 +48,65 @@ struct KvStage {
 };
 
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&d)[N]) {
+__device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t t, uint32_t off, uint32_t more, uint32_t (&d)[N]) {
   if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint4 v = buffer_load16(t, off, more);
     d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
   } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    d[0] = v.x; d[1] = v.y;
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(t, off, more, 0);
+    d[0] = uint32_t(v[0]); d[1] = uint32_t(v[1]);
   }
 }
 
-// One tile's data of a lane; `tile` is the same for the whole wave.
+// A lane's offsets in a tile.
 template <int FMT, int D>
-__device__ __forceinline__ void load_tile(const uint8_t* tile, int r, int c, KvStage<FMT, D>& st) {
-  constexpr int KS = 16 * D, VS = 16 * (D + kv_scales(FMT, D));
+struct KvLane {
+  uint32_t k, ks, v, vs;
+  __device__ __forceinline__ KvLane(uint32_t r, uint32_t c) {
+    v = (c * 16 + r) * (D / 8);
+    if constexpr (FMT == kFmtINT4) {
+      k = r * (D / 2) + c * 8;
+      ks = vs = c * 8;
+    } else {
+      constexpr int G = kv_group(FMT);
+      k = r * (D / 2) + c * (D / 8);
+      ks = r * (D / G) + c * (D / 4) / G;
+      vs = r * (D / 16) / G * 16 + 4 * c;
+    }
+  }
+};
+
+// One tile's data of a lane.  The tile is the whole wave's, as a buffer of its bytes (of none where its page is not
+// there: zeros), so a load is scalar registers, one of four lane offsets and a constant.
+template <int FMT, int D>
+__device__ __forceinline__ void load_tile(__amdgpu_buffer_rsrc_t t, const KvLane<FMT, D>& at, KvStage<FMT, D>& st) {
+  constexpr uint32_t KS = 16 * D, VS = 16 * (D + kv_scales(FMT, D));
   if constexpr (FMT == kFmtINT4) {
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
-      const uint2 v = *reinterpret_cast<const uint2*>(tile + r * (D / 2) + g * 32 + c * 8);
-      st.k[2 * g] = v.x;
-      st.k[2 * g + 1] = v.y;
-      const uint2 s = *reinterpret_cast<const uint2*>(tile + KS + (g * 16 + 4 * c) * 2);
-      st.ks[2 * g] = s.x;
-      st.ks[2 * g + 1] = s.y;
-      const uint2 z = *reinterpret_cast<const uint2*>(tile + VS + (g * 16 + 4 * c) * 2);
-      st.vs[2 * g] = z.x;
-      st.vs[2 * g + 1] = z.y;
+      uint32_t x[2];
+      load_words(t, at.k, g * 32, x);
+      st.k[2 * g] = x[0];
+      st.k[2 * g + 1] = x[1];
+      load_words(t, at.ks, KS + g * 32, x);
+      st.ks[2 * g] = x[0];
+      st.ks[2 * g + 1] = x[1];
+      load_words(t, at.vs, VS + g * 32, x);
+      st.vs[2 * g] = x[0];
+      st.vs[2 * g + 1] = x[1];
     }
   } else {
-    load_words(tile + r * (D / 2) + c * (D / 8), st.k);
-    if constexpr (FMT == kFmtMXFP4) {
-      st.ks[0] = tile[KS + r * (D / 32) + c * (D / 4) / 32];
-      st.vs[0] = *reinterpret_cast<const uint32_t*>(tile + VS + r * (D / 16) / 32 * 16 + 4 * c);
-    } else {
-      if constexpr (D == 128)
-        st.ks[0] = *reinterpret_cast<const uint16_t*>(tile + KS + r * 8 + 2 * c);
-      else
-        st.ks[0] = tile[KS + r * 4 + c];
-      st.vs[0] = *reinterpret_cast<const uint32_t*>(tile + VS + r * (D / 16) / 16 * 16 + 4 * c);
-    }
+    load_words(t, at.k, 0, st.k);
+    if constexpr (FMT == kFmtNVFP4 && D == 128)
+      st.ks[0] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(t, at.ks, KS, 0));
+    else
+      st.ks[0] = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(t, at.ks, KS, 0));
+    st.vs[0] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(t, at.vs, VS, 0));
   }
-  load_words(tile + 8 * D + (c * 16 + r) * (D / 8), st.v);
+  load_words(t, at.v, 8 * D, st.v);
 }
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // Tokens of a tile outside [first, behind): their V scales are made 0 (what lies in the pool there may be
 // anything, and a probability of 0 times an infinity or a NaN would not be 0).
@@ -161,48 +178,60 @@ __device__ __forceinline__ uint32_t v_pair(const KvStage<FMT, D>& st, const v2h 
 }
 constexpr uint32_t kLowHalves = 0x05040100u, kHighHalves = 0x07060302u;
 
-// O^T += V^T P^T over a step for every feature tile; p[n][x] is the B operand of column tile n, plane x, and with
-// INT4 of group g in p[n][g PL + x].
-template <int FMT, int D, int NQ, int PL, int NP>
-__device__ __forceinline__ void add_values(const KvStage<FMT, D> (&st)[2], const uint4 (&p)[NQ][NP],
-                                           v4f (&o)[NQ][D / 16]) {
+// O^T += V^T P^T over a step for every feature tile, e the probabilities of a lane's 8 tokens.  INT4: a group's scales
+// multiply its probabilities, so they are rounded once, and off is -8 times their sums.
+template <int FMT, int D, int NQ, int PL>
+__device__ __forceinline__ void add_values(const KvStage<FMT, D> (&st)[2], const float (&e)[NQ][8], v4f (&o)[NQ][D / 16],
+                                           v4f (&off)[NQ][D / 64]) {
   if constexpr (FMT == kFmtINT4) {
-    // token pairs: low and high nibbles of their pieces, then bytes of the two tokens side by side
-    uint32_t w[2][2][D / 16][2];                            // tile, tokens 0 1 / 2 3, two features' bytes, nibble
+    const uint4 m8 = make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u);          // bf16 -8
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int g = 0; g < D / 64; ++g) {
+      uint4 p[NQ][PL];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t lo[2], hi[2];
-        if constexpr (D == 128) {
+      for (int n = 0; n < NQ; ++n) {
+        float x[8];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            lo[i] = st[t].v[2 * h + i] & 0x0F0F0F0Fu;
-            hi[i] = (st[t].v[2 * h + i] >> 4) & 0x0F0F0F0Fu;
-          }
-          w[t][h][0][0] = __builtin_amdgcn_perm(lo[1], lo[0], 0x05010400u);
-          w[t][h][0][1] = __builtin_amdgcn_perm(hi[1], hi[0], 0x05010400u);
-          w[t][h][1][0] = __builtin_amdgcn_perm(lo[1], lo[0], 0x07030602u);
-          w[t][h][1][1] = __builtin_amdgcn_perm(hi[1], hi[0], 0x07030602u);
-        } else {
-          lo[0] = st[t].v[h] & 0x0F0F0F0Fu;
-          hi[0] = (st[t].v[h] >> 4) & 0x0F0F0F0Fu;
-          w[t][h][0][0] = __builtin_amdgcn_perm(lo[0], lo[0], 0x03010200u);
-          w[t][h][0][1] = __builtin_amdgcn_perm(hi[0], hi[0], 0x03010200u);
-        }
+        for (int i = 0; i < 8; ++i)
+          x[i] = e[n][i] * f16_value(st[i >> 2].vs[2 * g + ((i & 3) >> 1)] >> (16 * (i & 1)));
+        split_planes<PL>(x, p[n]);
+#pragma unroll
+        for (int y = 0; y < PL; ++y) off[n][g] = mfma_bf16(m8, p[n][y], off[n][g]);
+      }
+      uint32_t w[4][2];                                     // token pairs: two features' bytes of both, by nibble
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const KvStage<FMT, D>& z = st[t >> 1];
+        const uint32_t x = D == 128 ? __builtin_amdgcn_perm(z.v[D / 64 * (t & 1) + D / 128], z.v[D / 64 * (t & 1)],
+                                                            g ? 0x07030602u : 0x05010400u)
+                                    : __builtin_amdgcn_perm(z.v[t & 1], z.v[t & 1], 0x03010200u);
+        w[t][0] = x & 0x0F0F0F0Fu;
+        w[t][1] = (x >> 4) & 0x0F0F0F0Fu;
       }
 #pragma unroll
-    for (int g = 0; g < D / 64; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {                         // feature 64 g + 4 r + e: byte e / 2, nibble e % 2
-        const uint4 a = make_uint4(fp8_pair(w[0][0][g][e & 1], e >> 1), fp8_pair(w[0][1][g][e & 1], e >> 1),
-                                   fp8_pair(w[1][0][g][e & 1], e >> 1), fp8_pair(w[1][1][g][e & 1], e >> 1));
+      for (int f = 0; f < 4; ++f) {                         // feature 64 g + 4 r + f: byte f / 2, nibble f % 2
+        const uint4 a = make_uint4(fp8_pair(w[0][f & 1], f >> 1), fp8_pair(w[1][f & 1], f >> 1),
+                                   fp8_pair(w[2][f & 1], f >> 1), fp8_pair(w[3][f & 1], f >> 1));
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int x = 0; x < PL; ++x) o[n][4 * g + e] = mfma16<FMT>(a, p[n][g * PL + x], o[n][4 * g + e]);
+          for (int y = 0; y < PL; ++y) o[n][4 * g + f] = mfma_bf16(a, p[n][y], o[n][4 * g + f]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   } else {
+    uint4 p[NQ][PL];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      if constexpr (FMT == kFmtNVFP4) {
+        p[n][0] = to_f16(e[n]);
+      } else {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = e[n][i];
+        split_planes<PL>(x, p[n]);
+      }
+    }
     v2h nv[2][2];
     if constexpr (FMT == kFmtNVFP4) {
 #pragma unroll
@@ -227,6 +256,7 @@ __device__ __forceinline__ void add_values(const KvStage<FMT, D> (&st)[2], const
 #pragma unroll
           for (int y = 0; y < PL; ++y) o[n][2 * B + i] = mfma16<FMT>(a, p[n][y], o[n][2 * B + i]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
     one(std::integral_constant<int, 0>{});
     one(std::integral_constant<int, 1>{});
@@ -274,99 +304,109 @@ struct KvSeq {
   int len, row, rows, tiles, lo, units;       // lo: first token that any row sees, a multiple of 32
 };
 template <int R, int U, bool SPLIT>
-__device__ __forceinline__ KvSeq kv_seq(const KvCache& kc, const KvAttn& a, int b) {
+__device__ __forceinline__ KvSeq kv_seq(const KvCache& kc, const KvAttn& a, int len, int row, int rows) {
   KvSeq s;
-  kc.sequence(b, s.len, s.row, s.rows);
-  s.tiles = (int64_t(s.rows) * a.group + R - 1) / R;
-  const int64_t first = a.window > 0 ? int64_t(s.len) - s.rows + 1 - a.window : 0;
-  s.lo = int(first > 0 ? first : 0) & ~31;
-  const int seen = max(min(s.len, kc.capacity()) - s.lo, 0);
+  s.len = len;
+  s.row = row;
+  s.rows = rows;
+  s.tiles = (rows * a.group + R - 1) / R;
+  const int first = a.window > 0 ? len - rows + 1 - a.window : 0;
+  s.lo = (first > 0 ? first : 0) & ~31;
+  const int seen = max(min(len, kc.capacity()) - s.lo, 0);
   s.units = SPLIT ? max((seen + U - 1) / U, 1) : 1;
   return s;
 }
+// The same of sequence b, which all lanes ask for: scalar loads.
+template <int R, int U, bool SPLIT>
+__device__ __forceinline__ KvSeq kv_seq_of(const KvCache& kc, const KvAttn& a, int b) {
+  typedef const __attribute__((address_space(4))) int32_t* Words;
+  const Words lens = (Words)(uintptr_t)kc.lens, cu = (Words)(uintptr_t)kc.cu;
+  b = uni(b);
+  const int len = max(lens[b], 0);
+  if (kc.cu == nullptr) return kv_seq<R, U, SPLIT>(kc, a, len, b, 1);
+  const int row = min(max(cu[b], 0), kc.M);
+  return kv_seq<R, U, SPLIT>(kc, a, len, row, max(min(cu[b + 1], kc.M) - row, 0));
+}
 
-// Inclusive sum over the wave's lanes.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int x = 1; x < 64; x *= 2) {
-    const int u = __shfl_up(v, x);
-    if (lane >= x) v += u;
-  }
+// Inclusive sum over the wave's lanes: within rows of 16 by shifts, then the rows' last lanes on to those after.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);    // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);    // row_bcast:31 into rows 2 and 3
   return v;
 }
 
-// Over the batch, by a workgroup of NT threads: the units of all jobs (SPLIT; else jobs).  With at >= 0 also the
-// sequence that unit `at` falls into (-1: none) and the units before it; at may depend on the total.
+// The work of all sequences in units (SPLIT: of jobs x tokens; else jobs), and the sequence that unit `at`
+// falls into with the units before it (b = -1: none).  A batch of up to 64 is one wave's scan, which each
+// wave does for itself; a larger one goes through the workgroup in chunks of NT.
 struct KvFound {
   int b, before;
 };
 template <int R, int U, bool SPLIT, int NT>
-__device__ __forceinline__ int kv_total(const KvCache& kc, const KvAttn& a, int* sh, int& mine) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int total = 0;
-  for (int base = 0; base < kc.batch; base += NT) {
-    const int b = base + threadIdx.x;
-    int v = 0;
-    if (b < kc.batch) {
-      const KvSeq s = kv_seq<R, U, SPLIT>(kc, a, b);
-      v = s.tiles * s.units;
-    }
-    v = wave_scan(v, lane);
-    if (NT > 64) {
-      if (base) __syncthreads();
-      if (lane == 63) sh[wave] = v;
-      __syncthreads();
-      int before = 0, all = 0;
+struct KvScan {
+  const KvCache& kc;
+  const KvAttn& a;
+  int* sh;                                     // 16 words of LDS
+  int v = 0, end = 0, total = 0;
+
+  __device__ __forceinline__ int units_of(int b) const {
+    if (b >= kc.batch) return 0;
+    int len, row, rows;
+    kc.sequence(b, len, row, rows);
+    const KvSeq s = kv_seq<R, U, SPLIT>(kc, a, len, row, rows);
+    return s.tiles * s.units;
+  }
+  // This thread's inclusive sum in the chunk at `base`, the chunks before it being `before`; adds the chunk to it.
+  __device__ __forceinline__ int chunk(int base, int& before) {
+    v = units_of(base + int(threadIdx.x));
+    const int sum = wave_scan(v), wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63) sh[wave] = sum;
+    __syncthreads();
+    int lower = 0, all = 0;
 #pragma unroll
-      for (int w = 0; w < NT / 64; ++w) {
-        before += w < wave ? sh[w] : 0;
-        all += sh[w];
-      }
-      mine = total + before + v;
-      total += all;
-    } else {
-      mine = total + v;
-      total += __shfl(v, 63);
+    for (int w = 0; w < NT / 64; ++w) {
+      lower += w < wave ? sh[w] : 0;
+      all += sh[w];
     }
+    const int e = before + lower + sum;
+    before += all;
+    return e;
   }
-  return total;
-}
-// mine: this thread's inclusive sum of the last (for a batch of up to NT, the only) chunk.
-template <int R, int U, bool SPLIT, int NT>
-__device__ __forceinline__ KvFound kv_find(const KvCache& kc, const KvAttn& a, int at, int* sh, int mine) {
-  if (threadIdx.x == 0) sh[8] = -1;
-  __syncthreads();
-  int total = 0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int base = 0; base < kc.batch; base += NT) {
-    const int b = base + threadIdx.x;
-    int v = 0;
-    if (b < kc.batch) {
-      const KvSeq s = kv_seq<R, U, SPLIT>(kc, a, b);
-      v = s.tiles * s.units;
+  __device__ __forceinline__ int count() {
+    if (kc.batch <= 64) {
+      v = units_of(threadIdx.x & 63);
+      end = wave_scan(v);
+      return total = __builtin_amdgcn_readlane(end, 63);
     }
-    int end = mine;
-    if (kc.batch > NT) {
-      const int scan = wave_scan(v, lane);
-      __syncthreads();
-      if (lane == 63) sh[wave] = scan;
-      __syncthreads();
-      int before = 0, all = 0;
-      for (int w = 0; w < NT / 64; ++w) {
-        before += w < wave ? sh[w] : 0;
-        all += sh[w];
-      }
-      end = total + before + scan;
-      total += all;
-    }
-    if (at >= end - v && at < end) {
-      sh[8] = b;
-      sh[9] = end - v;
-    }
+    for (int base = 0; base < kc.batch; base += NT) end = chunk(base, total);
+    return total = __builtin_amdgcn_readfirstlane(total);
   }
-  __syncthreads();
-  return {__builtin_amdgcn_readfirstlane(sh[8]), __builtin_amdgcn_readfirstlane(sh[9])};
-}
+  __device__ __forceinline__ KvFound find(int at) {
+    if (kc.batch <= 64) {
+      const uint64_t in = __ballot(at < end);
+      if (in == 0) return {-1, 0};
+      const int lane = __builtin_ctzll(in);
+      return {lane, __builtin_amdgcn_readlane(end - v, lane)};
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh[8] = -1;
+    int before = 0;
+    for (int base = 0; base < kc.batch; base += NT) {
+      const int e = kc.batch <= NT ? end : chunk(base, before);
+      __syncthreads();
+      if (at >= e - v && at < e) {
+        sh[8] = base + int(threadIdx.x);
+        sh[9] = e - v;
+      }
+    }
+    __syncthreads();
+    return {__builtin_amdgcn_readfirstlane(sh[8]), __builtin_amdgcn_readfirstlane(sh[9])};
+  }
+};
 
 // Units that a range takes: the total over the ranges, and no fewer than `least`.
 __device__ __forceinline__ int units_a_range(int total, int ranges, int least) {
@@ -375,7 +415,7 @@ __device__ __forceinline__ int units_a_range(int total, int ranges, int least) {
 constexpr int kLeastUnits = 2;
 
 template <int FMT, int D, int NQ, int WQ, int WK, int PLANES, bool SPLIT>
-__global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, KvAttn a) {
+__global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && D == 128) ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
   using TL = KvTiles<NQ, WQ, WK>;
   constexpr int R = TL::R, U = TL::U, NT = 64 * WQ * WK, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1;
   constexpr int PL = FMT == kFmtNVFP4 ? 1 : PLANES;            // fp16 needs no second plane
@@ -387,52 +427,59 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
   const int r = lane & 15, c = lane >> 4, wq = wave / WK, wk = wave % WK;
   const int h = blockIdx.x % kc.heads, range = blockIdx.x / kc.heads;
 
-  int mine = 0;
-  const int total = kv_total<R, U, SPLIT, NT>(kc, a, sh, mine);
+  KvScan<R, U, SPLIT, NT> scan{kc, a, sh};
+  const int total = scan.count();
   const int per = SPLIT ? units_a_range(total, a.ranges, kLeastUnits) : 1;
-  const int64_t first = int64_t(range) * per;
-  if (first >= total) return;
-  const KvFound f = kv_find<R, U, SPLIT, NT>(kc, a, int(first), sh, mine);
-  int left = min(per, total - int(first)), b = f.b;
+  const int64_t first64 = int64_t(range) * per;
+  if (first64 >= total) return;
+  const int first = int(first64);
+  const KvFound f = scan.find(first);
+  int left = min(per, total - first), b = f.b;
   if (b < 0) return;
-  KvSeq s = kv_seq<R, U, SPLIT>(kc, a, b);
-  int job = (int(first) - f.before) / s.units, unit = (int(first) - f.before) % s.units;
+  KvSeq s = kv_seq_of<R, U, SPLIT>(kc, a, b);
+  int job = (first - f.before) / s.units, unit = (first - f.before) % s.units;
 
   while (left > 0) {
     while (job >= s.tiles) {                                  // the next sequence with rows
       if (++b >= kc.batch) return;
-      s = kv_seq<R, U, SPLIT>(kc, a, b);
+      s = kv_seq_of<R, U, SPLIT>(kc, a, b);
       job = 0;
       unit = 0;
     }
     const int n_units = min(left, s.units - unit);
     const int tile_rows = SPLIT ? job : s.tiles - 1 - job;    // long causal tiles first
-    const int64_t row0 = int64_t(tile_rows) * R + wq * 16 * NQ;
-    const int64_t rows = int64_t(s.rows) * a.group;
-    const int capacity = kc.capacity();
+    const int row0 = tile_rows * R + wq * 16 * NQ, rows = s.rows * a.group;
+    const int there_all = min(s.len, kc.capacity());
 
-    // Query rows, and the tokens [lo, hi) that each sees.
+    // The tokens [first, behind) that a query row's token sees; of the wave's rows the outermost and innermost.
+    auto first_of = [&](int token) { return a.window > 0 ? max(s.len - s.rows + token - a.window + 1, 0) : 0; };
+    auto behind_of = [&](int token) {
+      return a.causal ? min(max(s.len - s.rows + token + 1, 0), there_all) : there_all;
+    };
+    const int token_a = min(row0, rows - 1) / a.group, token_z = min(row0 + 16 * NQ, rows) - 1 < 0
+                                                                     ? 0 : (min(row0 + 16 * NQ, rows) - 1) / a.group;
+    const int first_all = first_of(token_a), first_max = first_of(token_z);
+    const int last_all = row0 < rows ? behind_of(token_z) : 0, last_min = behind_of(token_a);
+
+    int qr = r, qc = c;                                       // opaque likewise
+    asm volatile("" : "+v"(qr), "+v"(qc));
     uint4 q[NQ][D / 32];
     float k2[NQ];
     int lo[NQ], hi[NQ];
     v4f s0[FMT == kFmtINT4 ? NQ : 1][FMT == kFmtINT4 ? NG : 1];
-    int first_all = INT32_MAX, last_all = 0, first_max = 0, last_min = INT32_MAX;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int64_t i = row0 + n * 16 + r;
+      const int i = row0 + n * 16 + qr;
       const bool there = i < rows;
-      const int token = there ? int(i / a.group) : 0, head = there ? int(i % a.group) : 0;
-      const uint16_t* row = a.Q + int64_t(s.row + token) * a.ldq + int64_t(h * a.group + head) * D;
+      const int token = there ? int(unsigned(i) / unsigned(a.group)) : 0, head = there ? i - token * a.group : 0;
+      const uint16_t* row = a.Q + int64_t(s.row + token) * a.ldq + (h * a.group + head) * D;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) q[n][j] = there ? q_operand<FMT, D>(row, c, j) : make_uint4(0, 0, 0, 0);
-      const int at = s.len - s.rows + token;                  // the query's place
-      hi[n] = !there ? 0 : a.causal ? min(max(at + 1, 0), min(s.len, capacity)) : min(s.len, capacity);
-      lo[n] = a.window > 0 ? max(at - a.window + 1, 0) : 0;
-      if (!there) lo[n] = 0;
-      first_all = min(first_all, hi[n] > 0 ? lo[n] : INT32_MAX);
-      last_all = max(last_all, hi[n]);
-      first_max = max(first_max, lo[n]);
-      last_min = min(last_min, there ? hi[n] : INT32_MAX);
+      for (int j = 0; j < D / 32; ++j) q[n][j] = there ? q_operand<FMT, D>(row, qc, j) : make_uint4(0, 0, 0, 0);
+      hi[n] = there ? behind_of(token) : 0;
+      lo[n] = there ? first_of(token) : 0;
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
       k2[n] = a.scale2;
       if constexpr (FMT == kFmtNVFP4) {
         float v[D / 32][8], top = 0.f;
@@ -461,20 +508,8 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
         }
       }
     }
-    // Over the 16 rows of a column tile (lanes c hold the same).
-#pragma unroll
-    for (int x = 1; x < 16; x *= 2) {
-      first_all = min(first_all, __shfl_xor(first_all, x));
-      last_all = max(last_all, __shfl_xor(last_all, x));
-      first_max = max(first_max, __shfl_xor(first_max, x));
-      last_min = min(last_min, __shfl_xor(last_min, x));
-    }
-    first_all = __builtin_amdgcn_readfirstlane(first_all);
-    last_all = __builtin_amdgcn_readfirstlane(last_all);
-    first_max = __builtin_amdgcn_readfirstlane(first_max);
-    last_min = __builtin_amdgcn_readfirstlane(last_min);
 
-    v4f o[NQ][DT], off[FMT == kFmtINT4 ? NQ : 1][NG];
+    v4f o[NQ][DT], off[NQ][D / 64];
     float m[NQ], l[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -496,11 +531,12 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
     const int steps = end > t0 ? (end - t0 + STRIDE - 1) / STRIDE : 0;
     const uint8_t* base = kc.pool + (int64_t(TB) << kc.page_shift) * h;
     const int mask = (1 << kc.page_shift) - 1;
+    const KvLane<FMT, D> at(r, c);
 
     // Pages of 32 steps, one a lane (a step's two tiles in lanes 2 i, 2 i + 1), loaded 32 steps ahead.
     auto pages_from = [&](int i) {
-      const int64_t tile = (int64_t(t0) + int64_t(i + (lane >> 1)) * STRIDE) / 16 + (lane & 1);
-      return tile * 16 < end ? kc.page_of(b, int(tile)) : -1;
+      const int tile = (t0 >> 4) + (i + (lane >> 1)) * (STRIDE / 16) + (lane & 1);
+      return tile * 16 < end ? kc.page_of(b, tile) : -1;
     };
     int pages = -1, next_pages = steps > 0 ? pages_from(0) : -1;
     auto fetch = [&](int i, KvStage<FMT, D> (&st)[2], int (&ok)[2]) {
@@ -513,7 +549,8 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
       for (int x = 0; x < 2; ++x) {
         const int p = __builtin_amdgcn_readlane(pages, (i & 31) * 2 + x);
         ok[x] = p >= 0;
-        load_tile<FMT, D>(base + int64_t(p >= 0 ? p : 0) * kc.page_bytes + int64_t((tile + x) & mask) * TB, r, c, st[x]);
+        const uint8_t* from = base + int64_t(p >= 0 ? p : 0) * kc.page_bytes + uint32_t((tile + x) & mask) * uint32_t(TB);
+        load_tile<FMT, D>(make_rsrc(from, p >= 0 ? TB : 0), at, st[x]);
       }
     };
 
@@ -521,10 +558,10 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
       // Scores: lane (query r, tokens t + 16 i + 4 c + e).
       float z[NQ][2][4];
       const bool whole = t + 32 <= last_min && t >= first_max && ok[0] && ok[1];
-      if (t + 32 > last_all || t < first_all || !ok[0] || !ok[1]) {
+      if (t + 32 > last_all || t < first_all) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          clear_outside<FMT, D>(first_all - t - 16 * i, ok[i] ? last_all - t - 16 * i : 0, c, st[i]);
+          clear_outside<FMT, D>(first_all - t - 16 * i, last_all - t - 16 * i, c, st[i]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -561,6 +598,7 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
             for (int e = 0; e < 4; ++e) z[n][i][e] = x[n][e];
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -595,47 +633,19 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
             for (int g = 0; g < NG; ++g) off[n][g] *= x;
         }
       }
-      // Probabilities, and their operands.
-      uint4 p[NQ][NG * PL];
+      // Probabilities.
+      float e[NQ][8];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float e[8];
         const float base2 = FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], k2[n], -base2));
-          l[n] += e[i];
-        }
-        if constexpr (FMT == kFmtNVFP4) {
-          p[n][0] = to_f16(e);
-        } else if constexpr (FMT == kFmtINT4) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = e[i] * f16_value(st[i >> 2].vs[2 * g + ((i & 3) >> 1)] >> (16 * (i & 1)));
-            uint4 planes[PL];
-            split_planes<PL>(x, planes);
-#pragma unroll
-            for (int y = 0; y < PL; ++y) p[n][g * PL + y] = planes[y];
-          }
-        } else {
-          uint4 planes[PL];
-          split_planes<PL>(e, planes);
-#pragma unroll
-          for (int y = 0; y < PL; ++y) p[n][y] = planes[y];
+          e[n][i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], k2[n], -base2));
+          l[n] += e[n][i];
         }
       }
-      add_values<FMT, D, NQ, PL>(st, p, o);
-      if constexpr (FMT == kFmtINT4) {
-        const uint4 m8 = make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int y = 0; y < PL; ++y) off[n][g] = mfma_bf16(m8, p[n][g * PL + y], off[n][g]);
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      add_values<FMT, D, NQ, PL>(st, e, o, off);
     };
 
     if (steps > 0) {
@@ -653,10 +663,13 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
 
     // Results of the segment: a whole job's rows are written, a part's go to the workspace.
     const bool all = !SPLIT || (unit == 0 && n_units == s.units);
+    int tid = threadIdx.x;                                    // opaque: what follows from it is not kept in registers
+    asm volatile("" : "+v"(tid));                             // over the steps
+    const int er = tid & 15, ec = (tid >> 4) & 3;
     float* part = SPLIT ? a.part + ((int64_t(range) * kc.heads + h) * 2 + (unit > 0 ? 0 : 1)) * (R * (D + 2)) : nullptr;
     auto emit = [&](int in_tile, int d, auto& v, float mm, float ll) {        // features d .. of row in_tile
       constexpr int N = sizeof(v) / sizeof(float);
-      const int64_t i = int64_t(tile_rows) * R + in_tile;
+      const int i = tile_rows * R + in_tile;
       if (i >= rows) return;
       if (!all) {
         if (d == 0) {
@@ -667,8 +680,8 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
         for (int e = 0; e < N; ++e) part[2 * R + in_tile * D + d + e] = v[e];
         return;
       }
-      const int token = s.row + int(i / a.group), head = h * a.group + int(i % a.group);
-      kv_store<N>(a, token, head, D, d, v, mm, ll);
+      const int token = int(unsigned(i) / unsigned(a.group));
+      kv_store<N>(a, s.row + token, h * a.group + i - token * a.group, D, d, v, mm, ll);
     };
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -683,24 +696,24 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float v[4] = {o[n][d][i], o[n][d + 1][i], o[n][d + 2][i], o[n][d + 3][i]};
-            emit(wq * 16 * NQ + n * 16 + r, o_feature<FMT, D>(c, d, i), v, mm, l[n]);
+            emit(wq * 16 * NQ + n * 16 + er, o_feature<FMT, D>(ec, d, i), v, mm, l[n]);
           }
       } else {
         __syncthreads();                                      // the rows before are read
-        float* mine_o = merge_o + (wk * 16 + r) * OS;
+        float* mine_o = merge_o + (wk * 16 + er) * OS;
 #pragma unroll
         for (int d = 0; d < DT; d += 4)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(mine_o + o_feature<FMT, D>(c, d, i)) =
+            *reinterpret_cast<float4*>(mine_o + o_feature<FMT, D>(ec, d, i)) =
                 make_float4(o[n][d][i], o[n][d + 1][i], o[n][d + 2][i], o[n][d + 3][i]);
-        if (c == 0) {
-          merge_m[wk][r] = mm;
-          merge_l[wk][r] = l[n];
+        if (ec == 0) {
+          merge_m[wk][er] = mm;
+          merge_l[wk][er] = l[n];
         }
         __syncthreads();
         constexpr int TPR = NT / 16, FPT = D / TPR;           // threads a row, features a thread
-        const int row = threadIdx.x / TPR, d = threadIdx.x % TPR * FPT;
+        const int row = tid / TPR, d = tid % TPR * FPT;
         float mx = merge_m[0][row], ll = 0.f, v[FPT] = {};
 #pragma unroll
         for (int w = 1; w < WK; ++w) mx = fmaxf(mx, merge_m[w][row]);
@@ -723,57 +736,65 @@ __global__ void __launch_bounds__(64 * WQ * WK) kv_attention_kernel(KvCache kc, 
   }
 }
 
-// Joins the parts of split jobs: a workgroup takes the first range border inside a job (and only that), 4 of its
-// rows; wave w adds parts w, w + 4, ...
+// Joins the parts of split jobs: a workgroup takes the first range border inside a job (and only that) and one
+// row of it; D / 8 threads take a row's features, so 2048 / D parts are read at a time.
 template <int D, int R, int U>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
-  constexpr int F = D / 16;
+  constexpr int F = 8, TPR = D / F, NP = 256 / TPR;
   __shared__ int sh[16];
-  __shared__ float sm[4][4], sl[4][4], so[4][4][D];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float sm[NP], sl[NP], so[NP][D];
   const int h = blockIdx.x % kc.heads, border = blockIdx.x / kc.heads + 1;
-  int mine = 0;
-  const int total = kv_total<R, U, true, 256>(kc, a, sh, mine);
+  KvScan<R, U, true, 256> scan{kc, a, sh};
+  const int total = scan.count();
   const int per = units_a_range(total, a.ranges, kLeastUnits);
   const int64_t at = int64_t(border) * per;
   if (at >= total) return;
-  const KvFound f = kv_find<R, U, true, 256>(kc, a, int(at), sh, mine);
+  const KvFound f = scan.find(int(at));
   if (f.b < 0) return;
-  const KvSeq s = kv_seq<R, U, true>(kc, a, f.b);
+  const KvSeq s = kv_seq_of<R, U, true>(kc, a, f.b);
   const int job = (int(at) - f.before) / s.units, start = f.before + job * s.units;
   if (start == at || start < at - per) return;
+  const int row = blockIdx.y, i = job * R + row;
+  if (i >= s.rows * a.group) return;
   const int last = (start + s.units - 1) / per;              // ranges border - 1 .. last hold parts
-  const int row = blockIdx.y * 4 + (lane >> 4), d = (lane & 15) * F;
-  const int64_t i = int64_t(job) * R + row;
-  const bool there = i < int64_t(s.rows) * a.group;
+  const int x = threadIdx.x / TPR, d = threadIdx.x % TPR * F;
   float m = kLowest, l = 0.f, v[F] = {};
-  if (there)
-    for (int g = border - 1 + wave; g <= last; g += 4) {
-      const float* part = a.part + ((int64_t(g) * kc.heads + h) * 2 + (g == border - 1 ? 1 : 0)) * (R * (D + 2));
-      const float pm = part[row], pl = part[R + row], now = fmaxf(m, pm);
-      const float x = __builtin_amdgcn_exp2f(m - now), y = __builtin_amdgcn_exp2f(pm - now);
-      const float* o = part + 2 * R + row * D + d;
+  for (int g = border - 1 + x; g <= last; g += NP) {
+    const float* part = a.part + ((int64_t(g) * kc.heads + h) * 2 + (g == border - 1 ? 1 : 0)) * (R * (D + 2));
+    const float4* o = reinterpret_cast<const float4*>(part + 2 * R + row * D + d);
+    const float4 o0 = o[0], o1 = o[1];
+    const float pm = part[row], pl = part[R + row], now = fmaxf(m, pm);
+    const float y = __builtin_amdgcn_exp2f(m - now), z = __builtin_amdgcn_exp2f(pm - now);
+    const float w[F] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
-      for (int e = 0; e < F; ++e) v[e] = v[e] * x + o[e] * y;
-      l = l * x + pl * y;
-      m = now;
-    }
-  sm[wave][lane >> 4] = m;
-  sl[wave][lane >> 4] = l;
-#pragma unroll
-  for (int e = 0; e < F; ++e) so[wave][lane >> 4][d + e] = v[e];
-  __syncthreads();
-  if (wave != 0 || !there) return;
-#pragma unroll
-  for (int w = 1; w < 4; ++w) {
-    const float pm = sm[w][lane >> 4], now = fmaxf(m, pm);
-    const float x = __builtin_amdgcn_exp2f(m - now), y = __builtin_amdgcn_exp2f(pm - now);
-#pragma unroll
-    for (int e = 0; e < F; ++e) v[e] = v[e] * x + so[w][lane >> 4][d + e] * y;
-    l = l * x + sl[w][lane >> 4] * y;
+    for (int e = 0; e < F; ++e) v[e] = v[e] * y + w[e] * z;
+    l = l * y + pl * z;
     m = now;
   }
-  kv_store<F>(a, s.row + i / a.group, h * a.group + int(i % a.group), D, d, v, m, l);
+  if (d == 0) {
+    sm[x] = m;
+    sl[x] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < F; ++e) so[x][d + e] = v[e];
+  __syncthreads();
+  // Feature threadIdx.x of all partial sums, in order; F threads' results go out together.
+  if (threadIdx.x >= TPR) return;
+  m = sm[0];
+#pragma unroll
+  for (int w = 1; w < NP; ++w) m = fmaxf(m, sm[w]);
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < F; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < NP; ++w) {
+    const float z = __builtin_amdgcn_exp2f(sm[w] - m);
+    l += sl[w] * z;
+#pragma unroll
+    for (int e = 0; e < F; ++e) v[e] += so[w][d + e] * z;
+  }
+  const int token = int(unsigned(i) / unsigned(a.group));
+  kv_store<F>(a, s.row + token, h * a.group + i - token * a.group, D, d, v, m, l);
 }
 
 template <int FMT, int D, int NQ, int WQ, int WK, int PL>
@@ -784,7 +805,10 @@ void attend(const KvCache& kc, const KvAttn& a, bool split, int jobs, hipStream_
     return;
   }
   kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), NT, 0, s>>>(kc, a);
-  if (a.ranges > 1) kv_join_kernel<D, R, U><<<dim3((a.ranges - 1) * kc.heads, R / 4), 256, 0, s>>>(kc, a);
+  if (a.ranges > 1) {
+    const int64_t rows = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group;      // of a job, at most
+    kv_join_kernel<D, R, U><<<dim3((a.ranges - 1) * kc.heads, unsigned(rows < R ? rows : R)), 256, 0, s>>>(kc, a);
+  }
 }
 
 template <int FMT, int D>
