@@ -54,9 +54,11 @@ def test_sizes(L):
     assert L.svdq_kv_page_bytes(None) == 0 and L.svdq_kv_page_bytes(D(fmt=4)) == 0
     for bad in BAD_DESC:
         assert L.svdq_kv_page_bytes(D(**bad)) == 0
-    n = L.svdq_kv_attention_bytes(D(), 3, 3, 16)
-    assert n > 0 and n % 256 == 0 and L.svdq_kv_attention_bytes(D(), 1, 100000, 16) == 0   # enough tiles: not split
-    for bad in ((0, 1, 16), (16385, 1, 16), (1, 0, 16), (1, 1, 6), (1, 1, 0), (1, 1 << 23, 16), (1, 1 << 22, 1024)):
+    n = L.svdq_kv_attention_bytes(D(), 100, 3, 3, 16)
+    assert n > 0 and n % 256 == 0 and L.svdq_kv_attention_bytes(D(), 5000, 1, 100000, 16) == 0   # enough tiles: not split
+    assert L.svdq_kv_attention_bytes(D(), 4, 3, 3, 16) == 0                     # short tables: a job is one workgroup's
+    for bad in ((0, 1, 1, 16), (1 << 26, 1, 1, 16), (100, 0, 1, 16), (100, 16385, 1, 16), (100, 1, 0, 16), (100, 1, 1, 6),
+                (100, 1, 1, 0), (100, 1, 1 << 23, 16), (100, 1, 1 << 22, 1024)):
         assert L.svdq_kv_attention_bytes(D(), *bad) == 0
 
 
@@ -96,15 +98,15 @@ def test_read_validation(L, forced_device_error):
 
 
 def test_attention_validation(L, forced_device_error):
-    n = L.svdq_kv_attention_bytes(D(), 5, 40, 16)
+    n = L.svdq_kv_attention_bytes(D(), 80, 5, 40, 16)
     # d, pool, pages, table, ldt, cols, lens, cu, batch, M, Q, ldq, q_heads, scale, window, flags, Y, ldy, lse, ws,
     # bytes, stream
-    call = caller(L.svdq_kv_attention, [D(), P, 100, P, 8, 8, P, P, 5, 40, P, 2048, 16, 0.1, 0, 0, P, 2048, P, P, n, None])
+    call = caller(L.svdq_kv_attention, [D(), P, 100, P, 80, 80, P, P, 5, 40, P, 2048, 16, 0.1, 0, 0, P, 2048, P, P, n, None])
     assert n > 0 and call() == 6 and call(_15=1, _18=None, _14=7) == 6
     assert call(_9=0, _10=None, _16=None, _19=None, _20=0) == 6
     for i in (0, 1, 3, 6, 10, 16, 19):
         assert call(**{f"_{i}": None}) == 1, i
-    for bad in BAD_CACHE + [dict(_11=2040), dict(_17=2040), dict(_12=6, _20=BIG), dict(_12=0), dict(_13=0.0),
+    for bad in [b for b in BAD_CACHE if b != dict(_4=7)] + [dict(_4=79), dict(_11=2040), dict(_17=2040), dict(_12=6, _20=BIG), dict(_12=0), dict(_13=0.0),
                             dict(_13=-1.0), dict(_13=float("nan")), dict(_13=float("inf")), dict(_14=-1),
                             dict(_8=16000, _4=1 << 25, _5=1 << 25, _20=BIG)] + [dict(_0=D(**b)) for b in BAD_DESC]:
         assert call(**bad) == 2, bad

@@ -181,11 +181,13 @@ SHAPES = {
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("name", list(SHAPES))
-def test_attention(td, fmt, D, name):
+@pytest.mark.parametrize("table", ["own", "long"])
+def test_attention(td, fmt, D, name, table):
+    """Tables as long as the longest sequence, and long ones, whose calls are cut into ranges that are joined."""
     torch, dev = td
     q_lens, lens, Hq, H, page = SHAPES[name]
     kv = sq.KvLayout(fmt, H, D, page)
-    c = Cache(torch, dev, kv, lens, len(name) + D)
+    c = Cache(torch, dev, kv, lens, len(name) + D, cols=4096 // page if table == "long" else None)
     M = sum(q_lens)
     Qv = c.bf16(c.rng.standard_normal((M, Hq, D)) * 1.5)
     q = c.dev_bf16(Qv.reshape(M, -1))
@@ -206,8 +208,9 @@ def test_attention_long(td, fmt):
     """One long sequence over many ranges, its join, and a batch beyond one scan's 256."""
     torch, dev = td
     kv = sq.KvLayout(fmt, 1, 64, 64)
-    for lens, Hq in (([70001], 2), ([3, 40000, 5], 1), ([int(n) for n in np.random.default_rng(3).integers(0, 50, 600)], 2)):
-        c = Cache(torch, dev, kv, lens, 9)
+    short = [int(n) for n in np.random.default_rng(3).integers(0, 50, 600)]
+    for lens, Hq, cols in (([70001], 2, None), ([3, 40000, 5], 1, None), (short, 2, None), (short, 2, 100)):
+        c = Cache(torch, dev, kv, lens, 9, cols=cols)
         Qv = c.bf16(c.rng.standard_normal((len(lens), Hq, 64)))
         out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(len(lens), -1)), lse=True)
         check_attention(c, Qv, out, lse, [1] * len(lens), lens, Hq, 0.125, True, 0, f"{fmt} {len(lens)}",
@@ -219,11 +222,11 @@ def test_attention_many_sequences_of_rows(td, fmt):
     """More than 256 sequences of several rows (the scan's chunks), prompts among them, in both kinds of plan."""
     torch, dev = td
     rng = np.random.default_rng(8)
-    for B, most, H, Hq in ((300, 3, 1, 2), (270, 90, 2, 4)):
+    for B, most, H, Hq, cols in ((300, 3, 1, 2, None), (300, 3, 1, 2, 80), (270, 90, 2, 4, None), (270, 90, 1, 4, 10)):
         q_lens = [int(x) for x in rng.integers(0, most + 1, B)]
         lens = [int(x + y) for x, y in zip(q_lens, rng.integers(0, 40, B))]
         kv = sq.KvLayout(fmt, H, 64, 16)
-        c = Cache(torch, dev, kv, lens, B)
+        c = Cache(torch, dev, kv, lens, B, cols=cols)
         M = sum(q_lens)
         Qv = c.bf16(c.rng.standard_normal((M, Hq, 64)))
         out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(M, -1)),
@@ -307,15 +310,15 @@ def test_attention_strides_and_rows_outside(td, fmt):
     torch, dev = td
     kv = sq.KvLayout(fmt, 2, 64, 32)
     q_lens, lens, Hq = [2, 1, 40], [70, 33, 900], 4
-    for q_lens in ([2, 1, 4], [2, 1, 130]):
-        c = Cache(torch, dev, kv, lens, 7)
+    for q_lens, cols in (([2, 1, 4], None), ([2, 1, 4], 200), ([2, 1, 130], None)):
+        c = Cache(torch, dev, kv, lens, 7, cols=cols)
         M = sum(q_lens) + 5
         Qv = c.bf16(c.rng.standard_normal((M, Hq, 64)))
         wide = torch.full((M, Hq * 64 + 24), float("nan"), device=dev).bfloat16()
         q = wide[:, 8:8 + Hq * 64]
         q.copy_(c.dev_bf16(Qv.reshape(M, -1)))
         cu = i32(2 + np.r_[0, np.cumsum(q_lens)], dev, torch)
-        n = sq.kv_attention_bytes(kv, 3, M, Hq)
+        n = sq.kv_attention_bytes(kv, c.cols, 3, M, Hq)
         space = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=dev)
         out = torch.full((M, Hq * 64 + 16), 5.0, device=dev).bfloat16()
         y = out[:, 8:8 + Hq * 64]
@@ -343,7 +346,7 @@ def test_attention_strides_and_rows_outside(td, fmt):
 def test_attention_refusals(td):
     torch, dev = td
     kv = sq.KvLayout("mxfp4", 2, 64, 16)
-    c = Cache(torch, dev, kv, [20, 30], 3)
+    c = Cache(torch, dev, kv, [20, 30], 3, cols=100)
     n32, q = i32([20, 30], dev, torch), torch.zeros((2, 256), device=dev).bfloat16()
     ok = lambda **kw: sq.kv_attention(kv, c.pool, c.table, n32, **{"Q": q, **kw})
     ok()

@@ -218,7 +218,7 @@ def test_graph_follows_lengths(td):
                     break
     table, lens = i32(tab, dev, torch), i32([501, 41, 901], dev, torch)
     row = torch.randn((3, (8 + 4) * 128), device=dev).bfloat16()
-    ws = [torch.empty(sq.kv_attention_bytes(kv, 3, 3, 8), dtype=torch.uint8, device=dev) for _ in range(2)]
+    ws = [torch.empty(sq.kv_attention_bytes(kv, 40, 3, 3, 8), dtype=torch.uint8, device=dev) for _ in range(2)]
 
     def step(pool, w):
         q = sq.kv_append(kv, pool, table, lens, row[:, 1024:1280], row[:, 1280:], Q=row[:, :1024])

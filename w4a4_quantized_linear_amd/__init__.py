@@ -522,9 +522,9 @@ def kv_read(kv: KvLayout, pool, table, lens, M: int, cu=None, f32: bool = False,
     return K, V
 
 
-def kv_attention_bytes(kv: KvLayout, batch: int, M: int, q_heads: int) -> int:
-    """Workspace bytes of kv_attention (0: none needed, or invalid)."""
-    return int(lib().svdq_kv_attention_bytes(_kept_kv(kv)[0], int(batch), int(M), int(q_heads)))
+def kv_attention_bytes(kv: KvLayout, cols: int, batch: int, M: int, q_heads: int) -> int:
+    """Workspace bytes of kv_attention for tables of `cols` pages (0: none needed, or invalid)."""
+    return int(lib().svdq_kv_attention_bytes(_kept_kv(kv)[0], int(cols), int(batch), int(M), int(q_heads)))
 
 
 def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = None, window: int = 0, causal: bool = True,
@@ -555,7 +555,7 @@ def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = Non
     if lse is not None:
         _flat(lse, "lse", (M, q_heads), dev, torch.float32)
     L = lib()
-    ws = _space(workspace, L.svdq_kv_attention_bytes(args[0], args[8], M, q_heads), dev)
+    ws = _space(workspace, L.svdq_kv_attention_bytes(args[0], args[5], args[8], M, q_heads), dev)
     st = L.svdq_kv_attention(*args, Q.data_ptr(), ldq, q_heads, D ** -0.5 if scale is None else scale, window,
                              0 if causal else KV_FULL, out.data_ptr(), ldy, None if lse is None else lse.data_ptr(),
                              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),

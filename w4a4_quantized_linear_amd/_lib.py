@@ -51,7 +51,7 @@ SIGNATURES = {
     "svdq_kv_append": (ctypes.c_int, _CACHE + [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _P, _F32, _P, _P, _I32,
                                                _P, _I32, _U32, _P]),
     "svdq_kv_read": (ctypes.c_int, _CACHE + [_P, _I64, _P, _I64, _U32, _P]),
-    "svdq_kv_attention_bytes": (ctypes.c_size_t, [_D, _I32, _I64, _I32]),
+    "svdq_kv_attention_bytes": (ctypes.c_size_t, [_D, _I32, _I32, _I64, _I32]),
     "svdq_kv_attention": (ctypes.c_int, _CACHE + [_P, _I64, _I32, _F32, _I32, _U32, _P, _I64, _P, _P, ctypes.c_size_t,
                                                   _P]),
     "svdq_kv_copy": (ctypes.c_int, [_D, _P, _I64, _I32, _I64, _P, _P, _I64, _P]),

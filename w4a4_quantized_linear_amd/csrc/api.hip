@@ -525,11 +525,12 @@ svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages,
                                  static_cast<hipStream_t>(stream)));
 }
 
-size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t batch, int64_t M, int32_t q_heads) {
+size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t cols, int32_t batch, int64_t M, int32_t q_heads) {
   if (!d || check_kv(d) != SVDQ_OK || batch < 1 || batch > kKvMaxBatch || M < 1 || M > kKvMaxRows || q_heads < 1 ||
-      q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || M * q_heads > kKvMaxRowHeads)
+      q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || M * q_heads > kKvMaxRowHeads ||
+      cols < 1 || int64_t(cols) * d->page > kKvMaxTokens)
     return 0;
-  return kv_plan(d->head_dim, batch, M, q_heads, d->heads).bytes;
+  return kv_plan(d->fmt, d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page).bytes;
 }
 
 svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,
@@ -537,7 +538,7 @@ svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t p
                               int64_t M, const uint16_t* Q, int64_t ldq, int32_t q_heads, float scale, int32_t window,
                               uint32_t flags, void* Y, int64_t ldy, float* lse, void* workspace, size_t ws_bytes,
                               void* stream) {
-  const size_t need = svdq_kv_attention_bytes(d, batch, M, q_heads);
+  const size_t need = svdq_kv_attention_bytes(d, cols, batch, M, q_heads);
   if (!d || !pool || (batch > 0 && (!table || !lens)) || (M > 0 && (!Q || !Y)) || (need > 0 && !workspace))
     return SVDQ_ERR_NULL;
   KvCache kc;
@@ -545,7 +546,7 @@ svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t p
   if (s == SVDQ_ERR_SHAPE) return s;
   if (q_heads < 1 || q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || window < 0 ||
       !(scale > 0.0f && scale <= 3.0e38f) || M * q_heads > kKvMaxRowHeads ||
-      !kv_units_fit(d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
+      !kv_units_fit(d->fmt, d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
     return SVDQ_ERR_SHAPE;
   const int64_t cols_q = int64_t(q_heads) * d->head_dim;
   const svdq_status rq = check_rows(Q, ldq, cols_q), ry = check_rows(Y, ldy, cols_q);

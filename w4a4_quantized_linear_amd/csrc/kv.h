@@ -39,28 +39,29 @@ __host__ __device__ constexpr int kv_tile_bytes(int fmt, int D) { return kKvTile
 
 // How a call of svdq_kv_attention is cut: `rows` query rows of a K/V head (a sequence's tokens x the heads that share
 // it) a workgroup, `jobs` such tiles at most; split: `ranges` workgroups a head share the units of all jobs.
-constexpr int kKvRangeGroups = 768;          // workgroups of a split call: three a CU
+constexpr int64_t kKvWhole = 1024;           // tokens of a table up to which a job is one workgroup's
 struct KvPlan {
   int rows, jobs, ranges;
   bool split;
   size_t bytes;
 };
-inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads) {
+inline KvPlan kv_plan(int fmt, int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
   KvPlan p;
   const int64_t group = q_heads / heads, each = (M * group + batch - 1) / (batch > 0 ? batch : 1);
   p.rows = each <= 16 ? 16 : each <= 32 ? 32 : 128;
   const int64_t jobs = (M * group + p.rows - 1) / p.rows + batch;
   p.jobs = int(jobs);
-  p.split = p.rows < 128 || jobs * heads < 512;
-  p.ranges = p.split ? (kKvRangeGroups + heads - 1) / heads : 0;
+  p.split = p.rows < 128 ? places > kKvWhole : jobs * heads < 512;
+  const int a_cu = p.rows == 16 ? 3 : 2;
+  p.ranges = p.split ? (256 * a_cu + heads - 1) / heads : 0;
   p.bytes = p.split ? align256(size_t(p.ranges) * heads * 2 * p.rows * (D + 2) * 4) : 0;
   return p;
 }
 
 // Whether the units of all jobs, of tables with `places` tokens each, can be counted in 32 bits.
-inline bool kv_units_fit(int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
-  const KvPlan p = kv_plan(D, batch, M, q_heads, heads);
-  return !p.split || p.jobs * (places / (p.rows < 128 ? 128 : 32) + 1) <= INT32_MAX - kKvRangeGroups;
+inline bool kv_units_fit(int fmt, int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
+  const KvPlan p = kv_plan(fmt, D, batch, M, q_heads, heads, places);
+  return !p.split || p.jobs * (places / (p.rows < 128 ? 128 : 32) + 1) <= INT32_MAX - 4096;
 }
 
 // A cache and its sequences, as the kernels take them.  Places beyond a sequence's table or with a page outside
@@ -73,7 +74,7 @@ struct KvCache {
   int64_t page_bytes, ldt;
   int32_t pages, cols, batch, M, heads, page_shift;   // a page has 1 << page_shift tiles
 
-  __device__ __forceinline__ int capacity() const { return cols << (page_shift + 4); }
+  __host__ __device__ __forceinline__ int capacity() const { return cols << (page_shift + 4); }
   // Tokens, first row and rows of sequence b.
   __device__ __forceinline__ void sequence(int b, int& len, int& row, int& rows) const {
     len = max(lens[b], 0);

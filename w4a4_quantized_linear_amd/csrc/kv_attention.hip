@@ -385,6 +385,18 @@ struct KvScan {
     for (int base = 0; base < kc.batch; base += NT) end = chunk(base, total);
     return total = __builtin_amdgcn_readfirstlane(total);
   }
+  // Units before sequence b.
+  __device__ __forceinline__ int before(int b) {
+    if (kc.batch <= 64) return __builtin_amdgcn_readlane(end - v, b);
+    int sum = 0;
+    for (int base = 0; base <= b; base += NT) {
+      const int e = kc.batch <= NT ? end : chunk(base, sum);
+      __syncthreads();
+      if (base + int(threadIdx.x) == b) sh[9] = e - v;
+    }
+    __syncthreads();
+    return uni(sh[9]);
+  }
   __device__ __forceinline__ KvFound find(int at) {
     if (kc.batch <= 64) {
       const uint64_t in = __ballot(at < end);
@@ -415,7 +427,7 @@ __device__ __forceinline__ int units_a_range(int total, int ranges, int least) {
 constexpr int kLeastUnits = 2;
 
 template <int FMT, int D, int NQ, int WQ, int WK, int PLANES, bool SPLIT>
-__global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && D == 128) ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
+__global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
   using TL = KvTiles<NQ, WQ, WK>;
   constexpr int R = TL::R, U = TL::U, NT = 64 * WQ * WK, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1;
   constexpr int PL = FMT == kFmtNVFP4 ? 1 : PLANES;            // fp16 needs no second plane
@@ -478,23 +490,61 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && 
       hi[n] = there ? behind_of(token) : 0;
       lo[n] = there ? first_of(token) : 0;
     }
+    // This wave's steps: 32 tokens from s.lo + 32 (unit WK + wk) on, every WK-th; those before every row's window
+    // are left out.
+    constexpr int STRIDE = 32 * WK;
+    int t0 = s.lo + unit * U + 32 * wk;
+    const int end = min(SPLIT ? s.lo + (unit + n_units) * U : INT32_MAX, last_all);
+    if (first_all > t0 && end > t0) t0 += (min(first_all, end) - t0) / STRIDE * STRIDE;
+    const int steps = end > t0 ? (end - t0 + STRIDE - 1) / STRIDE : 0;
+    const uint8_t* base = kc.pool + (int64_t(TB) << kc.page_shift) * h;
+    const int mask = (1 << kc.page_shift) - 1;
+    const KvLane<FMT, D> at(r, c);
+
+    // Pages of 32 steps, one a lane (a step's two tiles in lanes 2 i, 2 i + 1), loaded 32 steps ahead.
+    auto pages_from = [&](int i) {
+      const int tile = (t0 >> 4) + (i + (lane >> 1)) * (STRIDE / 16) + (lane & 1);
+      return tile * 16 < end ? kc.page_of(b, tile) : -1;
+    };
+    int pages = -1, next_pages = pages_from(0);
+    auto fetch = [&](int i, KvStage<FMT, D> (&st)[2], int (&ok)[2]) {
+      if ((i & 31) == 0) {
+        pages = next_pages;
+        next_pages = pages_from(i + 32);
+      }
+      const int tile = (t0 >> 4) + i * (STRIDE / 16);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int p = __builtin_amdgcn_readlane(pages, (i & 31) * 2 + x);
+        ok[x] = p >= 0;
+        const uint8_t* from = base + int64_t(p >= 0 ? p : 0) * kc.page_bytes + uint32_t((tile + x) & mask) * uint32_t(TB);
+        load_tile<FMT, D>(make_rsrc(from, p >= 0 ? TB : 0), at, st[x]);
+      }
+    };
+    KvStage<FMT, D> now[2], next[2];
+    int now_ok[2], next_ok[2];
+    fetch(0, now, now_ok);                                    // without a step: of no pages, so no bytes
+    __builtin_amdgcn_sched_barrier(0);                        // these loads are on their way before Q is waited for
+
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       k2[n] = a.scale2;
       if constexpr (FMT == kFmtNVFP4) {
-        float v[D / 32][8], top = 0.f;
+        u16x2 top = {0, 0};                                   // the largest magnitude's bits
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+          for (uint32_t x : {q[n][j].x, q[n][j].y, q[n][j].z, q[n][j].w})
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu));
+        const int e2 = f16_row_power(rowgroup_max(__uint_as_float(uint32_t(top.x > top.y ? top.x : top.y) << 16)));
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          unpack_bf8(q[n][j], v[j]);
+          float v[8];
+          unpack_bf8(q[n][j], v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[j][e]));
-        }
-        const int e2 = f16_row_power(rowgroup_max(top));
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[j][e] = ldexpf(v[j][e], e2);
-          q[n][j] = to_f16(v[j]);
+          for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
+          q[n][j] = to_f16(v);
+          __builtin_amdgcn_sched_barrier(0);
         }
         k2[n] = ldexpf(k2[n], -e2);
       }
@@ -521,38 +571,6 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && 
 #pragma unroll
         for (int g = 0; g < NG; ++g) off[n][g] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-
-    // This wave's steps: 32 tokens from s.lo + 32 (unit WK + wk) on, every WK-th; those before every row's window
-    // are left out.
-    constexpr int STRIDE = 32 * WK;
-    int t0 = s.lo + unit * U + 32 * wk;
-    const int end = min(SPLIT ? s.lo + (unit + n_units) * U : INT32_MAX, last_all);
-    if (first_all > t0 && end > t0) t0 += (min(first_all, end) - t0) / STRIDE * STRIDE;
-    const int steps = end > t0 ? (end - t0 + STRIDE - 1) / STRIDE : 0;
-    const uint8_t* base = kc.pool + (int64_t(TB) << kc.page_shift) * h;
-    const int mask = (1 << kc.page_shift) - 1;
-    const KvLane<FMT, D> at(r, c);
-
-    // Pages of 32 steps, one a lane (a step's two tiles in lanes 2 i, 2 i + 1), loaded 32 steps ahead.
-    auto pages_from = [&](int i) {
-      const int tile = (t0 >> 4) + (i + (lane >> 1)) * (STRIDE / 16) + (lane & 1);
-      return tile * 16 < end ? kc.page_of(b, tile) : -1;
-    };
-    int pages = -1, next_pages = steps > 0 ? pages_from(0) : -1;
-    auto fetch = [&](int i, KvStage<FMT, D> (&st)[2], int (&ok)[2]) {
-      if ((i & 31) == 0) {
-        pages = next_pages;
-        next_pages = pages_from(i + 32);
-      }
-      const int tile = (t0 >> 4) + i * (STRIDE / 16);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int p = __builtin_amdgcn_readlane(pages, (i & 31) * 2 + x);
-        ok[x] = p >= 0;
-        const uint8_t* from = base + int64_t(p >= 0 ? p : 0) * kc.page_bytes + uint32_t((tile + x) & mask) * uint32_t(TB);
-        load_tile<FMT, D>(make_rsrc(from, p >= 0 ? TB : 0), at, st[x]);
-      }
-    };
 
     auto step = [&](int t, KvStage<FMT, D> (&st)[2], const int (&ok)[2]) {
       // Scores: lane (query r, tokens t + 16 i + 4 c + e).
@@ -648,16 +666,13 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && 
       add_values<FMT, D, NQ, PL>(st, e, o, off);
     };
 
-    if (steps > 0) {
-      KvStage<FMT, D> st[2][2];
-      int ok[2][2];
-      fetch(0, st[0], ok[0]);
-      for (int i = 0; i < steps; i += 2) {
-        if (i + 1 < steps) fetch(i + 1, st[1], ok[1]);
-        step(t0 + i * STRIDE, st[0], ok[0]);
-        if (i + 1 >= steps) break;
-        if (i + 2 < steps) fetch(i + 2, st[0], ok[0]);
-        step(t0 + (i + 1) * STRIDE, st[1], ok[1]);
+    for (int i = 0; i < steps; ++i) {
+      fetch(i + 1, next, next_ok);                            // behind the last step: no bytes
+      step(t0 + i * STRIDE, now, now_ok);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        now[x] = next[x];
+        now_ok[x] = next_ok[x];
       }
     }
 
@@ -736,89 +751,116 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 && !(FMT == kFmtINT4 && 
   }
 }
 
-// Joins the parts of split jobs: a workgroup takes the first range border inside a job (and only that) and one
-// row of it; D / 8 threads take a row's features, so 2048 / D parts are read at a time.
-template <int D, int R, int U>
+constexpr int kJoinGroups = 2048;        // workgroups of a join at most, if jobs x heads are not more
+
+// Joins the parts of split jobs.  A workgroup takes a job (BY_SEQ, where a sequence is one: the sequence's; else the
+// one inside which a range border is the first) and its rows: D / 8 threads take a row's features, and of the
+// 2048 / D such groups as many share a row as the parts keep busy.
+template <int D, int R, int U, bool BY_SEQ>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   constexpr int F = 8, TPR = D / F, NP = 256 / TPR;
   __shared__ int sh[16];
   __shared__ float sm[NP], sl[NP], so[NP][D];
-  const int h = blockIdx.x % kc.heads, border = blockIdx.x / kc.heads + 1;
+  const int h = blockIdx.x % kc.heads, index = blockIdx.x / kc.heads;
   KvScan<R, U, true, 256> scan{kc, a, sh};
   const int total = scan.count();
   const int per = units_a_range(total, a.ranges, kLeastUnits);
-  const int64_t at = int64_t(border) * per;
-  if (at >= total) return;
-  const KvFound f = scan.find(int(at));
-  if (f.b < 0) return;
-  const KvSeq s = kv_seq_of<R, U, true>(kc, a, f.b);
-  const int job = (int(at) - f.before) / s.units, start = f.before + job * s.units;
-  if (start == at || start < at - per) return;
-  const int row = blockIdx.y, i = job * R + row;
-  if (i >= s.rows * a.group) return;
-  const int last = (start + s.units - 1) / per;              // ranges border - 1 .. last hold parts
-  const int x = threadIdx.x / TPR, d = threadIdx.x % TPR * F;
-  float m = kLowest, l = 0.f, v[F] = {};
-  for (int g = border - 1 + x; g <= last; g += NP) {
-    const float* part = a.part + ((int64_t(g) * kc.heads + h) * 2 + (g == border - 1 ? 1 : 0)) * (R * (D + 2));
-    const float4* o = reinterpret_cast<const float4*>(part + 2 * R + row * D + d);
-    const float4 o0 = o[0], o1 = o[1];
-    const float pm = part[row], pl = part[R + row], now = fmaxf(m, pm);
-    const float y = __builtin_amdgcn_exp2f(m - now), z = __builtin_amdgcn_exp2f(pm - now);
-    const float w[F] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-#pragma unroll
-    for (int e = 0; e < F; ++e) v[e] = v[e] * y + w[e] * z;
-    l = l * y + pl * z;
-    m = now;
+  int b, job, start;
+  KvSeq s;
+  if constexpr (BY_SEQ) {
+    b = index;
+    job = 0;
+    start = scan.before(b);
+    s = kv_seq_of<R, U, true>(kc, a, b);
+  } else {
+    const int64_t at = int64_t(index + 1) * per;
+    if (at >= total) return;
+    const KvFound f = scan.find(int(at));
+    if (f.b < 0) return;
+    b = f.b;
+    s = kv_seq_of<R, U, true>(kc, a, b);
+    job = (int(at) - f.before) / s.units;
+    start = f.before + job * s.units;
+    if (start == at || start < at - per) return;
   }
-  if (d == 0) {
-    sm[x] = m;
-    sl[x] = l;
+  const int first = start / per, last = (start + s.units - 1) / per;     // ranges that hold parts
+  if (first == last) return;
+  const int d = threadIdx.x % TPR * F, slot = threadIdx.x / TPR;
+  const int rows = min(s.rows * a.group - job * R, R);
+  int shift = 0;                                             // 1 << shift slots share a row, parts / 2 or as many as there are
+  while ((2 << shift) < last - first + 1 && (1 << shift) < NP) ++shift;
+  const int x = slot & ((1 << shift) - 1), at_once = NP >> shift;
+  for (int base = int(blockIdx.y) * at_once; base < rows; base += int(gridDim.y) * at_once) {
+    const int row = base + (slot >> shift);
+    float m = kLowest, l = 0.f, v[F] = {};
+    if (row < rows)
+      for (int g = first + x; g <= last; g += 1 << shift) {
+        // the first range begins the job (a part of kind 1), the others go on with it
+        const float* part = a.part + ((int64_t(g) * kc.heads + h) * 2 + (g == first ? 1 : 0)) * (R * (D + 2));
+        const float4* o = reinterpret_cast<const float4*>(part + 2 * R + row * D + d);
+        const float4 o0 = o[0], o1 = o[1];
+        const float pm = part[row], pl = part[R + row], now = fmaxf(m, pm);
+        const float y = __builtin_amdgcn_exp2f(m - now), z = __builtin_amdgcn_exp2f(pm - now);
+        const float w[F] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+        for (int e = 0; e < F; ++e) v[e] = v[e] * y + w[e] * z;
+        l = l * y + pl * z;
+        m = now;
+      }
+    if (shift > 0) {
+      __syncthreads();                                       // the rows before are read
+      if (d == 0) {
+        sm[slot] = m;
+        sl[slot] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < F; ++e) so[slot][d + e] = v[e];
+      __syncthreads();
+      if (x == 0)
+        for (int w = 1; w < 1 << shift; ++w) {
+          const float pm = sm[slot + w], now = fmaxf(m, pm);
+          const float y = __builtin_amdgcn_exp2f(m - now), z = __builtin_amdgcn_exp2f(pm - now);
+#pragma unroll
+          for (int e = 0; e < F; ++e) v[e] = v[e] * y + so[slot + w][d + e] * z;
+          l = l * y + sl[slot + w] * z;
+          m = now;
+        }
+    }
+    if (x == 0 && row < rows) {
+      const int i = job * R + row, token = int(unsigned(i) / unsigned(a.group));
+      kv_store<F>(a, s.row + token, h * a.group + i - token * a.group, D, d, v, m, l);
+    }
   }
-#pragma unroll
-  for (int e = 0; e < F; ++e) so[x][d + e] = v[e];
-  __syncthreads();
-  // Feature threadIdx.x of all partial sums, in order; F threads' results go out together.
-  if (threadIdx.x >= TPR) return;
-  m = sm[0];
-#pragma unroll
-  for (int w = 1; w < NP; ++w) m = fmaxf(m, sm[w]);
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < F; ++e) v[e] = 0.f;
-#pragma unroll
-  for (int w = 0; w < NP; ++w) {
-    const float z = __builtin_amdgcn_exp2f(sm[w] - m);
-    l += sl[w] * z;
-#pragma unroll
-    for (int e = 0; e < F; ++e) v[e] += so[w][d + e] * z;
-  }
-  const int token = int(unsigned(i) / unsigned(a.group));
-  kv_store<F>(a, s.row + token, h * a.group + i - token * a.group, D, d, v, m, l);
 }
 
 template <int FMT, int D, int NQ, int WQ, int WK, int PL>
-void attend(const KvCache& kc, const KvAttn& a, bool split, int jobs, hipStream_t s) {
-  constexpr int NT = 64 * WQ * WK, R = KvTiles<NQ, WQ, WK>::R, U = KvTiles<NQ, WQ, WK>::U;
-  if (!split) {
-    kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(unsigned(jobs) * kc.heads), NT, 0, s>>>(kc, a);
-    return;
-  }
-  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), NT, 0, s>>>(kc, a);
-  if (a.ranges > 1) {
-    const int64_t rows = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group;      // of a job, at most
-    kv_join_kernel<D, R, U><<<dim3((a.ranges - 1) * kc.heads, unsigned(rows < R ? rows : R)), 256, 0, s>>>(kc, a);
-  }
+void attend_whole(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
+  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(unsigned(jobs) * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
+}
+template <int FMT, int D, int NQ, int WQ, int WK, int PL>
+void attend_split(const KvCache& kc, const KvAttn& a, hipStream_t s) {
+  constexpr int R = KvTiles<NQ, WQ, WK>::R, U = KvTiles<NQ, WQ, WK>::U;
+  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
+  if (a.ranges < 2) return;
+  const bool by_seq = kc.cu == nullptr && a.group <= R;      // a sequence is one job
+  const int jobs_h = (by_seq ? kc.batch : a.ranges - 1) * kc.heads;
+  const int64_t rows = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group, most = rows < R ? rows : R;
+  const int64_t fill = kJoinGroups / jobs_h;
+  const unsigned y = unsigned(fill < 1 ? 1 : fill < most ? fill : most);
+  if (by_seq)
+    kv_join_kernel<D, R, U, true><<<dim3(jobs_h, y), 256, 0, s>>>(kc, a);
+  else
+    kv_join_kernel<D, R, U, false><<<dim3(jobs_h, y), 256, 0, s>>>(kc, a);
 }
 
 template <int FMT, int D>
 void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_t s) {
   if (p.rows == 16)
-    attend<FMT, D, 1, 1, 4, 2>(kc, a, p.split, p.jobs, s);
+    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, p.jobs, s);
   else if (p.rows == 32)
-    attend<FMT, D, 2, 1, 4, 2>(kc, a, p.split, p.jobs, s);
+    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s);
   else
-    attend<FMT, D, 2, 4, 1, 1>(kc, a, p.split, p.jobs, s);
+    p.split ? attend_split<FMT, D, 2, 4, 1, 1>(kc, a, s) : attend_whole<FMT, D, 2, 4, 1, 1>(kc, a, p.jobs, s);
 }
 
 }  // namespace
@@ -826,7 +868,7 @@ void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_
 hipError_t launch_kv_attention(int fmt, int D, const KvCache& kc, const uint16_t* Q, int64_t ldq, int q_heads,
                                float scale, int window, bool causal, uint16_t* Y, int64_t ldy, float* lse, float* part,
                                hipStream_t s) {
-  const KvPlan p = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads);
+  const KvPlan p = kv_plan(fmt, D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
   const KvAttn a = {Q, Y, lse, part, ldq, ldy, q_heads / kc.heads, q_heads, window, causal ? 1 : 0, p.ranges,
                     scale * 1.44269504088896341f};
   if (fmt == kFmtMXFP4)
