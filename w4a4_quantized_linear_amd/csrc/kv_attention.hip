@@ -44,7 +44,7 @@ template <int FMT, int D>
 struct KvStage {
   static constexpr int W = D / 32;                       // dwords of K or V a lane has of a tile
   uint32_t k[W], v[W];
-  uint32_t ks[FMT == kFmtINT4 ? D / 32 : 1], vs[FMT == kFmtINT4 ? D / 32 : 1];
+  uint32_t ks[1], vs[FMT == kFmtINT4 ? 2 : 1];           // scales (INT4: all in vs, see kv_scales4)
 };
 
 template <int N>
@@ -63,16 +63,11 @@ template <int FMT, int D>
 struct KvLane {
   uint32_t k, ks, v, vs;
   __device__ __forceinline__ KvLane(uint32_t r, uint32_t c) {
+    constexpr int G = kv_group(FMT);
     v = (c * 16 + r) * (D / 8);
-    if constexpr (FMT == kFmtINT4) {
-      k = r * (D / 2) + c * 8;
-      ks = vs = c * 8;
-    } else {
-      constexpr int G = kv_group(FMT);
-      k = r * (D / 2) + c * (D / 8);
-      ks = r * (D / G) + c * (D / 4) / G;
-      vs = r * (D / 16) / G * 16 + 4 * c;
-    }
+    k = r * (D / 2) + c * (D / 8);
+    ks = r * (D / G) + c * (D / 4) / G;
+    vs = FMT == kFmtINT4 ? r % (D / 32) * 32 + c * 8 : r * (D / 16) / G * 16 + 4 * c;
   }
 };
 
@@ -81,22 +76,10 @@ struct KvLane {
 template <int FMT, int D>
 __device__ __forceinline__ void load_tile(__amdgpu_buffer_rsrc_t t, const KvLane<FMT, D>& at, KvStage<FMT, D>& st) {
   constexpr uint32_t KS = 16 * D, VS = 16 * (D + kv_scales(FMT, D));
+  load_words(t, at.k, 0, st.k);
   if constexpr (FMT == kFmtINT4) {
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-      uint32_t x[2];
-      load_words(t, at.k, g * 32, x);
-      st.k[2 * g] = x[0];
-      st.k[2 * g + 1] = x[1];
-      load_words(t, at.ks, KS + g * 32, x);
-      st.ks[2 * g] = x[0];
-      st.ks[2 * g + 1] = x[1];
-      load_words(t, at.vs, VS + g * 32, x);
-      st.vs[2 * g] = x[0];
-      st.vs[2 * g + 1] = x[1];
-    }
+    load_words(t, at.vs, KS, st.vs);
   } else {
-    load_words(t, at.k, 0, st.k);
     if constexpr (FMT == kFmtNVFP4 && D == 128)
       st.ks[0] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(t, at.ks, KS, 0));
     else
@@ -104,6 +87,19 @@ __device__ __forceinline__ void load_tile(__amdgpu_buffer_rsrc_t t, const KvLane
     st.vs[0] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(t, at.vs, VS, 0));
   }
   load_words(t, at.v, 8 * D, st.v);
+}
+
+// INT4: the scales of tokens 4 c .. 4 c + 3, kind K of group 0, of group 1, V of group 0, of group 1 (a head of 64
+// features: K, V), lie in lanes r % 4 (% 2) of the quads; every lane gets a word of piece `kind`.
+template <int D>
+__device__ __forceinline__ uint32_t kv_scales4(uint32_t x, int kind) {
+  constexpr int Q0 = 0x00, Q1 = 0x55, Q2 = 0xAA, Q3 = 0xFF;            // quad_perm: lane 0, 1, 2, 3 of the quad
+  switch (kind) {
+    case 0: return uint32_t(__builtin_amdgcn_mov_dpp(int(x), Q0, 0xF, 0xF, true));
+    case 1: return uint32_t(__builtin_amdgcn_mov_dpp(int(x), Q1, 0xF, 0xF, true));
+    case 2: return uint32_t(__builtin_amdgcn_mov_dpp(int(x), Q2, 0xF, 0xF, true));
+    default: return uint32_t(__builtin_amdgcn_mov_dpp(int(x), Q3, 0xF, 0xF, true));
+  }
 }
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -116,11 +112,8 @@ __device__ __forceinline__ void clear_outside(int first, int behind, int c, KvSt
 #pragma unroll
   for (int i = 0; i < 4; ++i) keep[i] = 4 * c + i >= first && 4 * c + i < behind ? 0xFFFFFFFFu : 0u;
   if constexpr (FMT == kFmtINT4) {
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-      st.vs[2 * g] &= (keep[0] & 0xFFFFu) | (keep[1] & 0xFFFF0000u);
-      st.vs[2 * g + 1] &= (keep[2] & 0xFFFFu) | (keep[3] & 0xFFFF0000u);
-    }
+    st.vs[0] &= (keep[0] & 0xFFFFu) | (keep[1] & 0xFFFF0000u);
+    st.vs[1] &= (keep[2] & 0xFFFFu) | (keep[3] & 0xFFFF0000u);
   } else {
     st.vs[0] &= (keep[0] & 0xFFu) | (keep[1] & 0xFF00u) | (keep[2] & 0xFF0000u) | (keep[3] & 0xFF000000u);
   }
@@ -134,6 +127,20 @@ __device__ __forceinline__ uint32_t fp8_pair(uint32_t d, bool high) {       // b
 template <int FMT>
 __device__ __forceinline__ v4f mfma16(const uint4& a, const uint4& b, v4f c) {
   return FMT == kFmtNVFP4 ? mfma_f16(a, b, c) : mfma_bf16(a, b, c);
+}
+
+// INT4 heads of 128 features: a lane loads 32 features that lie together, all of one group, but a group's MFMAs
+// need every lane.  Lanes c and c + 2 trade halves: afterwards words 0, 1 are of group 0 and 2, 3 of group 1.
+template <int FMT, int D>
+__device__ __forceinline__ void trade_groups(KvStage<FMT, D>& st) {
+  if constexpr (FMT == kFmtINT4 && D == 128) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const auto x = __builtin_amdgcn_permlane32_swap(st.k[i], st.k[2 + i], false, false);
+      st.k[i] = x[0];
+      st.k[2 + i] = x[1];
+    }
+  }
 }
 
 // A operand of K's MFMA j.
@@ -154,7 +161,8 @@ __device__ __forceinline__ uint4 k_operand(const KvStage<FMT, D>& st, int j) {
 template <int FMT, int D>
 __device__ __forceinline__ uint4 q_operand(const uint16_t* row, int c, int j) {
   if constexpr (FMT == kFmtINT4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + (j >> 1) * 64 + c * 16 + (j & 1) * 8);
+    const int piece = D == 64 ? c : (c & 1) * 2 + (c >> 1);                // of the group's four
+    const uint4 v = *reinterpret_cast<const uint4*>(row + (j >> 1) * 64 + piece * 16 + (j & 1) * 8);
     return make_uint4(__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
                       __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u));
   } else {
@@ -188,12 +196,15 @@ __device__ __forceinline__ void add_values(const KvStage<FMT, D> (&st)[2], const
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
       uint4 p[NQ][PL];
+      uint32_t sv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sv[i] = kv_scales4<D>(st[i >> 1].vs[i & 1], D / 64 + g);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          x[i] = e[n][i] * f16_value(st[i >> 2].vs[2 * g + ((i & 3) >> 1)] >> (16 * (i & 1)));
+          x[i] = e[n][i] * f16_value(sv[i >> 1] >> (16 * (i & 1)));
         split_planes<PL>(x, p[n]);
 #pragma unroll
         for (int y = 0; y < PL; ++y) off[n][g] = mfma_bf16(m8, p[n][y], off[n][g]);
@@ -585,6 +596,12 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
       for (int i = 0; i < 2; ++i) {
         if constexpr (FMT == kFmtINT4) {
           uint4 ka[D / 32];
+          uint32_t sk[NG][2];
+          trade_groups<FMT, D>(st[i]);
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) sk[g][w] = kv_scales4<D>(st[i].vs[w], g);
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) ka[j] = k_operand<FMT, D>(st[i], j);
 #pragma unroll
@@ -597,7 +614,7 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
               x = mfma_bf16(ka[2 * g + 1], q[n][2 * g + 1], x);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                z[n][i][e] = fmaf(x[e], f16_value(st[i].ks[2 * g + (e >> 1)] >> (16 * (e & 1))), z[n][i][e]);
+                z[n][i][e] = fmaf(x[e], f16_value(sk[g][e >> 1] >> (16 * (e & 1))), z[n][i][e]);
             }
           }
         } else {
