@@ -349,7 +349,8 @@ size_t svdq_kv_page_bytes(const svdq_kv_desc* d);
  *   Q, Q_out device, bf16 bits, M x q_heads head_dim; may be the same rows.  q_heads 0: no Q
  *   norm_q, norm_k  device, bf16 bits [head_dim], 16-byte aligned, or NULL each
  *   eps      in [0, 1]
- *   freq     device, float32[pairs] (pairs even, 0 .. head_dim / 2; 0: no rotation)
+ *   freq     device, float32[pairs] (pairs even, with SVDQ_ROPE_HALVES a multiple of 8, 0 .. head_dim / 2;
+ *            0: no rotation)
  *   axis     device, int32[pairs], or NULL: all 0
  *   pos      device, int32, axes x M, or NULL: every axis is the token's place in its sequence
  * A row whose token has no place (lens[b] too small, a page outside the pool) is dropped; its Q is

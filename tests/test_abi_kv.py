@@ -69,13 +69,14 @@ def test_append_validation(L, forced_device_error):
                                      P, 64, P, 3, 1, None])
     assert call() == 6 and call(_9=0, _10=None, _12=None, _14=None, _17=None) == 6
     assert call(_16=0, _14=None, _17=None) == 6 and call(_24=0, _22=None, _23=None, _25=None) == 6
+    assert call(_24=12, _27=0) == 6 and call(_24=24) == 6
     assert call(_19=None) == 6 and call(_20=None, _23=None, _25=None) == 6 and call(_7=None, _9=5) == 6
     for i in (0, 1, 3, 6, 10, 12, 14, 17, 22):
         assert call(**{f"_{i}": None}) == 1, i
     for bad in BAD_DESC:
         assert call(_0=D(**bad)) == 2
     for bad in BAD_CACHE + [dict(_11=504), dict(_13=504), dict(_15=1016), dict(_18=1016), dict(_11=(1 << 24) + 8),
-                            dict(_16=-1), dict(_24=-2), dict(_24=66), dict(_24=7), dict(_26=0), dict(_26=17),
+                            dict(_16=-1), dict(_24=-2), dict(_24=66), dict(_24=7, _27=0), dict(_24=68), dict(_24=12), dict(_26=0), dict(_26=17),
                             dict(_21=-1.0), dict(_21=2.0), dict(_21=float("nan"))]:
         assert call(**bad) == 2, bad
     assert call(_0=D(fmt=0)) == 3 and call(_27=2) == 3

@@ -90,7 +90,7 @@ def _heads(rng, M, H, D):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D,pairs,axes,halves,norm,far", [
     (128, 64, 1, True, True, False), (128, 64, 3, False, True, False), (64, 32, 2, True, False, False),
-    (64, 16, 1, False, True, False), (128, 32, 4, True, True, True), (64, 6, 1, True, False, True), (128, 0, 0, False, True, False)])
+    (64, 16, 1, False, True, False), (128, 32, 4, True, True, True), (64, 24, 1, True, False, True), (64, 6, 1, False, False, True), (128, 0, 0, False, True, False)])
 def test_append_norm_and_rotation(td, fmt, D, pairs, axes, halves, norm, far):
     """K's codes equal the oracle's; Q is within bf16's half step and fp32's rounding of a norm and a rotation."""
     torch, dev = td

@@ -483,7 +483,7 @@ svdq_status svdq_kv_append(const svdq_kv_desc* d, void* pool, int64_t pages, con
   KvCache kc;
   svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
   if (s == SVDQ_ERR_SHAPE) return s;
-  if (q_heads < 0 || q_heads > kKvMaxQHeads || pairs < 0 || pairs > d->head_dim / 2 || pairs % 2 != 0 || axes < 0 ||
+  if (q_heads < 0 || q_heads > kKvMaxQHeads || pairs < 0 || pairs > d->head_dim / 2 || pairs % ((flags & SVDQ_ROPE_HALVES) ? 8 : 2) != 0 || axes < 0 ||
       axes > kKvMaxAxes || (pos && axes < 1) || !(eps >= 0.0f && eps <= 1.0f))
     return SVDQ_ERR_SHAPE;
   if (s == SVDQ_ERR_FORMAT || (flags & ~uint32_t(SVDQ_ROPE_HALVES)) != 0) return SVDQ_ERR_FORMAT;

@@ -134,22 +134,6 @@ __device__ __forceinline__ uint32_t kv_scale(float amax, float& div) {
     return b;
   }
 }
-// Byte of two codes, x0 in the low nibble.
-template <int FMT>
-__device__ __forceinline__ uint32_t kv_encode(float x0, float x1, float div) {
-  if constexpr (FMT == kFmtMXFP4) {
-    return cvt_fp4x2_div<0>(0, x0, x1, div) & 0xFFu;
-  } else if constexpr (FMT == kFmtINT4) {
-    if (div == 0.f) return 0x88u;
-    const float a = fminf(fmaxf(__builtin_rintf(x0 / div), -8.f), 7.f);
-    const float b = fminf(fmaxf(__builtin_rintf(x1 / div), -8.f), 7.f);
-    return uint32_t(int(a) + 8) | uint32_t(int(b) + 8) << 4;
-  } else {
-    const float a = div == 0.f ? copysignf(0.f, x0) : x0 / div;
-    const float b = div == 0.f ? copysignf(0.f, x1) : x1 / div;
-    return cvt_fp4x2<0>(0, a, b) & 0xFFu;
-  }
-}
 // The two values of a byte, given the scale's bits.
 template <int FMT>
 __device__ __forceinline__ v2f kv_decode(uint32_t byte, uint32_t scale) {

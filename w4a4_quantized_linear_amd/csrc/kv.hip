@@ -1,22 +1,47 @@
 // svdq_kv_append, svdq_kv_read, svdq_kv_copy and svdq_kv_compact: what fills a 4-bit key-value cache, reads it
 // back and moves its pages and tokens.  Layout: kv.h.
+#include <type_traits>
+
 #include "kv.h"
 
 namespace svdq {
 
 namespace {
 
-// max of v over the W (8, 16, 32) lanes of an aligned group
+// v of the lane that differs in bit log2(X) of its number (X = 1, 2) or, X = 4, 8, of its mirror in 8, 16 lanes,
+// which serves a reduction in rising order of X as well; X = -8: of the lane 8 further on of 16.
+template <int X>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  constexpr int ctrl = X == 1 ? 0xB1 : X == 2 ? 0x4E : X == 4 ? 0x141 : X == 8 ? 0x140 : 0x128;
+  return uint32_t(__builtin_amdgcn_mov_dpp(int(v), ctrl, 0xF, 0xF, true));
+}
+template <int X>
+__device__ __forceinline__ float partner_of(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return __uint_as_float(partner<X>(u));
+}
+template <int X>
+__device__ __forceinline__ double partner_of(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __float_as_uint(partner_of<X>(__uint_as_float(uint32_t(u))));
+  const uint32_t hi = __float_as_uint(partner_of<X>(__uint_as_float(uint32_t(u >> 32))));
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+
+// max and sum of v over the W lanes of an aligned group
 template <int W>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int x = 1; x < W; x *= 2) v = fmaxf(v, __shfl_xor(v, x));
+  if constexpr (W > 1) v = fmaxf(v, partner_of<1>(v));
+  if constexpr (W > 2) v = fmaxf(v, partner_of<2>(v));
+  if constexpr (W > 4) v = fmaxf(v, partner_of<4>(v));
   return v;
 }
 template <int W, typename T>
 __device__ __forceinline__ T group_sum(T v) {
-#pragma unroll
-  for (int x = 1; x < W; x *= 2) v += __shfl_xor(v, x);
+  v += partner_of<1>(v);
+  v += partner_of<2>(v);
+  v += partner_of<4>(v);
+  if constexpr (W > 8) v += partner_of<8>(v);
   return v;
 }
 
@@ -37,40 +62,108 @@ struct KvAppend {
   KvRope rope;
 };
 
-// A lane's two neighbouring features turned.  Neighbours: they are a pair.  Halves: feature d pairs with d + pairs,
-// which the lane pairs / 2 further on holds.
-template <int LPH, typename T>
-__device__ __forceinline__ void turn(T& a, T& b, const KvRope& r, int sub, bool turned, T c0, T s0, T c1, T s1) {
+// A row's sines as a lane needs them: of pairs 4 l .. + 3 (neighbours) or of features 8 l .. + 7 (halves).
+template <typename T>
+struct KvSines {
+  T c[8], s[8];
+};
+
+// A lane's 8 features turned.  Neighbours: they are 4 pairs.  Halves: feature d pairs with d + pairs, which lane
+// l + pairs / 8 of the head holds.
+template <int L, typename T>
+__device__ __forceinline__ void turn(T (&x)[8], const KvRope& r, int l, const KvSines<T>& t) {
   if (!r.halves) {
-    if (turned) {
-      const T u = a * c0 - b * s0;
-      b = a * s0 + b * c0;
-      a = u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * l + j >= r.pairs) continue;
+      const T u = x[2 * j] * t.c[j] - x[2 * j + 1] * t.s[j];
+      x[2 * j + 1] = x[2 * j] * t.s[j] + x[2 * j + 1] * t.c[j];
+      x[2 * j] = u;
     }
     return;
   }
-  const bool second = 2 * sub >= r.pairs;
-  const int from = second ? sub - r.pairs / 2 : sub + r.pairs / 2;
-  const T a2 = __shfl(a, from, LPH), b2 = __shfl(b, from, LPH);
-  if (turned) {
-    a = second ? a2 * s0 + a * c0 : a * c0 - a2 * s0;
-    b = second ? b2 * s1 + b * c1 : b * c1 - b2 * s1;
+  const int step = r.pairs / 8, from = l < step ? l + step : l < 2 * step ? l - step : l;
+  const T sign = l < step ? T(-1) : T(1);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const T other = L == 16 && step == 8 ? partner_of<-8>(x[j]) : __shfl(x[j], from, L);
+    const T u = x[j] * t.c[j] + sign * (other * t.s[j]);     // (a c - b s, b c + a s)
+    x[j] = l < 2 * step ? u : x[j];
   }
 }
 
-// A workgroup takes a row m, its waves the row's heads in turn: K's, V's, Q's.  A lane holds two neighbouring
-// features, so D / 2 lanes a head.  K's norm and rotation are in 64 bits, so that its codes, which are
-// choices, do not hang on an order of summation or on a sine's last bit; the angle pos x freq is a 64-bit
-// product, which holds far positions.  Q's are in 32 bits with the same sines.  Bound by memory for prompts
-// (Q in and out is most of it), by the chain lengths -> table -> row -> store for single tokens.
+// a / b for the codes, b > 0: div_refined on the group's one correctly rounded reciprocal, with a's sign, which
+// -0 would lose.  Where that is not the correctly rounded quotient (it is below 2^-40), the code is 0.
+__device__ __forceinline__ float kv_div(float a, float b, float rb) { return copysignf(div_refined(a, b, rb), a); }
+
+// 8 codes of a lane's 8 finite bf16 values, given the number they are divided by: a dword, in order.
+template <int FMT>
+__device__ __forceinline__ uint32_t kv_encode8(const float (&x)[8], float div) {
+  uint32_t d = 0;
+  if constexpr (FMT == kFmtMXFP4) {
+    d = cvt_fp4x2_div<0>(d, x[0], x[1], div);
+    d = cvt_fp4x2_div<1>(d, x[2], x[3], div);
+    d = cvt_fp4x2_div<2>(d, x[4], x[5], div);
+    d = cvt_fp4x2_div<3>(d, x[6], x[7], div);
+  } else {
+    const float rd = div == 0.f ? 0.f : 1.0f / div;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = kv_div(x[i], div, rd);     // 0 with x's sign where div is 0
+    if constexpr (FMT == kFmtINT4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d |= uint32_t(int(fminf(fmaxf(__builtin_rintf(v[i]), -8.f), 7.f)) + 8) << (4 * i);
+    } else {
+      d = cvt_fp4x2<0>(d, v[0], v[1]);
+      d = cvt_fp4x2<1>(d, v[2], v[3]);
+      d = cvt_fp4x2<2>(d, v[4], v[5]);
+      d = cvt_fp4x2<3>(d, v[6], v[7]);
+    }
+  }
+  return d;
+}
+
+// 1 / sqrt(x) to about 2^-52, x > 0: the hardware's estimate (at least 2^-20) by two of Newton's steps.
+__device__ __forceinline__ double rsqrt64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = fma(0.5 * y, fma(-x * y, y, 1.0), y);
+  return y;
+}
+
+// A wave takes units of one row: 8 features a lane, so D / 8 lanes a head, and 4 heads (of 64 features: 8) of K, V
+// or Q at once; all units of a row, or every `parts`-th where few rows would leave CUs idle.  The inputs of the next
+// units are on their way while one is worked on.  A row's sines are computed once by its wave, pair p in lane p.
+// K's norm and rotation are in 64 bits, so that its codes, which are choices, do not hang on an order of summation
+// or on a sine's last bit; the angle pos x freq is a 64-bit product, which holds far positions.  Q's are
+// in 32 bits with the same sines.
+// 9165 rows, 32 + 2 x 8 heads of 128, NVFP4, norm and three axes (209 MB): with a feature pair a lane, IEEE divisions
+// and 64-bit quotients it was bound by its instructions, 98 us.
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(KvCache kc, KvAppend a) {
-  constexpr int LPH = D / 2, HPW = 64 / LPH, G = kv_group(FMT);
-  const int lane = threadIdx.x & 63, sub = lane % LPH;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + blockIdx.y * 4, waves = gridDim.y * 4;
-  const int m = blockIdx.x;
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend a, int parts) {
+  constexpr int L = D / 8, HPW = 64 / L, G = kv_group(FMT), AHEAD = 2;
+  const int lane = threadIdx.x & 63, l = lane % L;
+  const int wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = wave / parts, part = wave - m * parts;
+  if (m >= kc.M) return;
+  const int kv_units = (kc.heads + HPW - 1) / HPW, units = 2 * kv_units + (a.q_heads + HPW - 1) / HPW;
+
+  auto load = [&](int u) -> uint4 {
+    const bool is_k = u < kv_units, is_q = u >= 2 * kv_units;
+    const int h = (is_q ? u - 2 * kv_units : is_k ? u : u - kv_units) * HPW + lane / L;
+    const uint16_t* src = is_q ? a.Q + int64_t(m) * a.ldq : is_k ? a.K + int64_t(m) * a.ldk : a.V + int64_t(m) * a.ldv;
+    if (u >= units || h >= (is_q ? a.q_heads : kc.heads)) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4*>(src + h * D + 8 * l);
+  };
   const int b = kc.cu == nullptr ? m : kv_sequence_of(kc.cu, kc.batch, m, lane);
   if (b < 0) return;
+  uint4 in[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) in[i] = load(part + i * parts);
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (a.norm_q) wq = *reinterpret_cast<const uint4*>(a.norm_q + 8 * l);
+  if (a.norm_k) wk = *reinterpret_cast<const uint4*>(a.norm_k + 8 * l);
   int len, row, rows;
   kc.sequence(b, len, row, rows);
   const int t = len - rows + (m - row);                        // the row's place
@@ -81,74 +174,123 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvCache kc, KvAppend a) 
            int64_t((t >> 4) & ((1 << kc.page_shift) - 1)) * kv_tile_bytes(FMT, D);
   const int64_t head_bytes = int64_t(kv_tile_bytes(FMT, D)) << kc.page_shift;
 
-  double c0 = 1, s0 = 0, c1 = 1, s1 = 0;
-  bool turned = false;
+  KvSines<double> sines;
   const KvRope& r = a.rope;
   if (r.pairs > 0) {
-    const int p0 = r.halves ? (2 * sub) % r.pairs : sub, p1 = r.halves ? (2 * sub + 1) % r.pairs : sub;
-    turned = 2 * sub < 2 * r.pairs;
-    if (turned) {
-      auto angle = [&](int p) {
+    double s = 0, c = 1;
+    if (lane < r.pairs) {
 #pragma clang fp contract(off)
-        const int ax = r.axis == nullptr ? 0 : r.axis[p];
-        int pos = t;
-        if (r.pos != nullptr) pos = ax >= 0 && ax < r.axes ? r.pos[int64_t(ax) * kc.M + m] : 0;
-        return double(pos) * double(r.freq[p]);
-      };
-      sincos(angle(p0), &s0, &c0);
-      if (r.halves) sincos(angle(p1), &s1, &c1);
+      const int ax = r.axis == nullptr ? 0 : r.axis[lane];
+      int pos = t;
+      if (r.pos != nullptr) pos = ax >= 0 && ax < r.axes ? r.pos[int64_t(ax) * kc.M + m] : 0;
+      const double angle = double(pos) * double(r.freq[lane]);
+      sincos(angle, &s, &c);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!r.halves && j >= 4) {
+        sines.c[j] = 1;
+        sines.s[j] = 0;
+        continue;
+      }
+      const int p = r.halves ? 8 * l + j : 4 * l + j, from = p >= r.pairs ? p - r.pairs : p;
+      sines.c[j] = __shfl(c, from & 63);
+      sines.s[j] = __shfl(s, from & 63);
     }
   }
-
-  const int kv_units = (kc.heads + HPW - 1) / HPW, q_units = (a.q_heads + HPW - 1) / HPW;
-  for (int u = wave; u < 2 * kv_units + q_units; u += waves) {
-    const bool is_k = u < kv_units, is_q = u >= 2 * kv_units;
-    const int heads = is_q ? a.q_heads : kc.heads;
-    const int h = (is_q ? u - 2 * kv_units : is_k ? u : u - kv_units) * HPW + lane / LPH;
-    const bool there = h < heads;
-    const uint16_t* src = is_q ? a.Q + int64_t(m) * a.ldq : is_k ? a.K + int64_t(m) * a.ldk : a.V + int64_t(m) * a.ldv;
-    const uint32_t in = there ? *reinterpret_cast<const uint32_t*>(src + h * D + 2 * sub) : 0;
-    if (is_q) {
-      float x = bf_lo(in), y = bf_hi(in);
-      if (a.norm_q != nullptr) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.norm_q + 2 * sub);
-        const float k = 1.0f / sqrtf(group_sum<LPH>(x * x + y * y) / D + a.eps);
-        x = x * k * bf_lo(w);
-        y = y * k * bf_hi(w);
-      }
-      turn<LPH, float>(x, y, r, sub, turned, float(c0), float(s0), float(c1), float(s1));
-      if (there) *reinterpret_cast<uint32_t*>(a.Q_out + int64_t(m) * a.ldqo + h * D + 2 * sub) = cvt_bf2(x, y);
-      continue;
+  // K's units, V's, Q's, in loops of their own: the 64-bit sines are K's alone.
+  int u = part;
+  auto next = [&]() -> uint4 {
+    const uint4 now = in[0];
+#pragma unroll
+    for (int i = 0; i + 1 < AHEAD; ++i) in[i] = in[i + 1];
+    in[AHEAD - 1] = load(u + AHEAD * parts);
+    return now;
+  };
+  auto keep = [&](auto kind, float (&x)[8], int h) {             // kind 0: K, 1: V
+    constexpr bool is_k = decltype(kind)::value == 0;
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = kv_finite_bf16(x[j]);
+      top = fmaxf(top, fabsf(x[j]));
     }
-    float x = bf_lo(in), y = bf_hi(in);
-    if (is_k) {
-      double z = x, v = y;
-      if (a.norm_k != nullptr) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.norm_k + 2 * sub);
-        const double k = sqrt(group_sum<LPH>(z * z + v * v) / D + double(a.eps));
-        z = z / k * bf_lo(w);
-        v = v / k * bf_hi(w);
-      }
-      turn<LPH, double>(z, v, r, sub, turned, c0, s0, c1, s1);
-      x = float(z);
-      y = float(v);
-    }
-    x = kv_finite_bf16(x);
-    y = kv_finite_bf16(y);
     float div;
-    const uint32_t s = kv_scale<FMT>(group_max<G / 2>(fmaxf(fabsf(x), fabsf(y))), div);
-    const uint32_t code = kv_encode<FMT>(x, y, div);
-    if (!there || page < 0) continue;
+    const uint32_t s = kv_scale<FMT>(group_max<G / 8>(top), div);
+    const uint32_t codes = kv_encode8<FMT>(x, div);
+    if (h >= kc.heads || page < 0) return;
     uint8_t* to = tile + h * head_bytes;
-    const int ti = t & 15, g = 2 * sub / G;
-    to[is_k ? kv_k_code<FMT, D>(ti, 2 * sub) : kv_v_code<FMT, D>(ti, 2 * sub)] = uint8_t(code);
-    if (sub % (G / 2) == 0) {
+    const int ti = t & 15, g = 8 * l / G;
+    if constexpr (is_k) {
+      *reinterpret_cast<uint32_t*>(to + kv_k_code<FMT, D>(ti, 8 * l)) = codes;
+    } else if constexpr (FMT != kFmtINT4 && D == 128) {
+      *reinterpret_cast<uint32_t*>(to + kv_v_code<FMT, D>(ti, 8 * l)) = codes;
+    } else {                                                     // two pieces of 4 features
+      *reinterpret_cast<uint16_t*>(to + kv_v_code<FMT, D>(ti, 8 * l)) = uint16_t(codes);
+      *reinterpret_cast<uint16_t*>(to + kv_v_code<FMT, D>(ti, 8 * l + 4)) = uint16_t(codes >> 16);
+    }
+    if (l % (G / 8) == 0) {
       uint8_t* at = to + (is_k ? kv_k_scale<FMT, D>(ti, g) : kv_v_scale<FMT, D>(ti, g));
       if constexpr (FMT == kFmtINT4)
         *reinterpret_cast<uint16_t*>(at) = uint16_t(s);
       else
         *at = uint8_t(s);
     }
+  };
+
+  for (; u < kv_units; u += parts) {
+    float x[8];
+    unpack_bf8(next(), x);
+    if (a.norm_k != nullptr || r.pairs > 0) {
+      double z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = x[j];
+      if (a.norm_k != nullptr) {
+        double sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma(z[j], z[j], sum);
+        const double mean = group_sum<L>(sum) * (1.0 / D) + double(a.eps);
+        // a row of zeros with eps 0, or of infinities: as the definition has it
+        const double k = mean > 0 && mean < __builtin_huge_val() ? rsqrt64(mean) : 1 / sqrt(mean);
+        float w[8];
+        unpack_bf8(wk, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = z[j] * k * w[j];
+      }
+      if (r.pairs > 0) turn<L, double>(z, r, l, sines);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = float(z[j]);
+    }
+    keep(std::integral_constant<int, 0>{}, x, u * HPW + lane / L);
+  }
+  for (; u < 2 * kv_units; u += parts) {
+    float x[8];
+    unpack_bf8(next(), x);
+    keep(std::integral_constant<int, 1>{}, x, (u - kv_units) * HPW + lane / L);
+  }
+  KvSines<float> sines32;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    sines32.c[j] = float(sines.c[j]);
+    sines32.s[j] = float(sines.s[j]);
+  }
+  for (; u < units; u += parts) {
+    float x[8];
+    unpack_bf8(next(), x);
+    if (a.norm_q != nullptr) {
+      float sum = 0.f, w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+      const float k = __builtin_amdgcn_rsqf(group_sum<L>(sum) * (1.0f / D) + a.eps);
+      unpack_bf8(wq, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = x[j] * k * w[j];
+    }
+    if (r.pairs > 0) turn<L, float>(x, r, l, sines32);
+    const int h = (u - 2 * kv_units) * HPW + lane / L;
+    if (h < a.q_heads)
+      *reinterpret_cast<uint4*>(a.Q_out + int64_t(m) * a.ldqo + h * D + 8 * l) =
+          make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
   }
 }
 
@@ -334,6 +476,8 @@ void by_format(int fmt, int D, A&&... args) {
     D == 64 ? F<kFmtNVFP4, 64>::run(args...) : F<kFmtNVFP4, 128>::run(args...);
 }
 
+constexpr int64_t kAppendWaves = 4096;       // waves of an append, if it has units for them
+
 // Workgroups a row: one, or more where few rows leave CUs idle, each wave then taking fewer heads.
 int row_parts(int64_t M, int units) {
   const int64_t want = 512 / (M > 0 ? M : 1), most = (units + 3) / 4;
@@ -343,8 +487,9 @@ int row_parts(int64_t M, int units) {
 template <int FMT, int D>
 struct Append {
   static void run(const KvCache& kc, const KvAppend& a, hipStream_t s) {
-    const int hpw = 128 / D, units = 2 * ((kc.heads + hpw - 1) / hpw) + (a.q_heads + hpw - 1) / hpw;
-    kv_append_kernel<FMT, D><<<dim3(kc.M, row_parts(kc.M, units)), 256, 0, s>>>(kc, a);
+    const int hpw = 512 / D, units = 2 * ((kc.heads + hpw - 1) / hpw) + (a.q_heads + hpw - 1) / hpw;
+    const int64_t fill = kAppendWaves / kc.M, parts = fill < 1 ? 1 : fill < units ? fill : units;
+    kv_append_kernel<FMT, D><<<unsigned((kc.M * parts + 3) / 4), 256, 0, s>>>(kc, a, int(parts));
   }
 };
 template <int FMT, int D>
