@@ -361,26 +361,40 @@ struct KvCompact {
   const int32_t* keep;
   const int32_t* n_keep;
   int64_t ldto, ldkeep, plane_bytes;
-  int32_t cols_to, most;
+  int32_t cols_to, most, planes, parts;
 };
 
-// A wave fills a tile of the new places of one sequence, head and layer: it gathers the tile's 16 tokens and
-// writes whole pieces.  In place a workgroup walks a sequence's tiles in order, four at a time, all loads
-// before the stores: the tokens that are kept come in rising order, so those of later tiles lie behind
-// every place written so far.
-template <int FMT, int D, bool IN_PLACE>
+// What a wave moves of one tile: lane (token lane / 4, quarter lane % 4) of K, lane (4 tokens lane / 16, piece lane % 16)
+// of V, lane (token lane % 16, groups lane / 16 + 4 j) of the scales.
+template <int FMT, int D>
+struct KvMoved {
+  static constexpr int DW = D / 32, NG = D / kv_group(FMT), NS = (NG + 3) / 4;
+  uint32_t k[DW], v[4], sk[NS], sv[NS];
+};
+
+// A wave fills a tile of the new places of one sequence: it finds where the tile's 16 tokens come from once, then
+// gathers and writes the tile of every head and layer (of a part of them where there are few tiles), the next one's
+// loads on their way before the stores.  With a tile of one head a wave the four dependent loads in front (count,
+// index, page, bytes) cost as much as the bytes: 18000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) took 72 us.  In place a
+// workgroup walks a sequence's tiles in order, four at a time, all loads of a head before its stores: the tokens that
+// are kept come in rising order, so those of later tiles lie behind every place written so far.
+enum { kApart = 0, kInPlace = 1, kInPlaceByWave = 2 };
+template <int FMT, int D, int HOW>
 __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a) {
-  constexpr int TB = kv_tile_bytes(FMT, D), DW = D / 32;
+  using Moved = KvMoved<FMT, D>;
+  constexpr int TB = kv_tile_bytes(FMT, D), DW = Moved::DW, NG = Moved::NG, NS = Moved::NS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.x / kc.heads, h = blockIdx.x % kc.heads;
-  uint8_t* pool = kc.pool + blockIdx.z * a.plane_bytes + (int64_t(TB) << kc.page_shift) * h;
+  constexpr int TILES = HOW == kInPlaceByWave ? 1 : 4;        // of a sequence at once
+  const int b = blockIdx.x / a.parts, part = (blockIdx.x % a.parts) * (4 / TILES) + (TILES == 1 ? wave : 0);
+  const int step = a.parts * (4 / TILES);
+  const int64_t head_bytes = int64_t(TB) << kc.page_shift;
   const int start = a.start == nullptr ? 0 : max(a.start[b], 0);
   const int n = min(max(a.n_keep[b], 0), a.most);
   if (n == 0) return;
   const int64_t end = int64_t(start) + n;
-  const int mask = (1 << kc.page_shift) - 1;
-  for (int64_t at = int64_t(start / 16) + blockIdx.y * 4; at * 16 < end; at += gridDim.y * 4) {
-    const int64_t tile = at + wave;
+  const int mask = (1 << kc.page_shift) - 1, all = a.planes * kc.heads;
+  for (int64_t at = int64_t(start / 16) + blockIdx.y * TILES; at * 16 < end; at += gridDim.y * TILES) {
+    const int64_t tile = at + (TILES == 1 ? 0 : wave);
     // Token lane % 16 of the tile: where it comes from, as a tile's offset in the pool and a place in it.
     int64_t from = -1;
     int place = 0;
@@ -391,77 +405,93 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
       if (p >= 0) from = int64_t(p) * kc.page_bytes + int64_t((old >> 4) & mask) * TB;
       place = old & 15;
     }
-    uint8_t* to = nullptr;
+    int64_t to = -1;
     if (tile * 16 < end && (tile >> kc.page_shift) < a.cols_to) {
       const int p = a.to[b * a.ldto + (tile >> kc.page_shift)];
-      if (p >= 0 && p < kc.pages) to = pool + int64_t(p) * kc.page_bytes + (tile & mask) * TB;
+      if (p >= 0 && p < kc.pages) to = int64_t(p) * kc.page_bytes + (tile & mask) * TB;
     }
-    if (to == nullptr) from = -1;
-    // K: lane (token lane / 4, quarter lane % 4).  V: lane (4 tokens lane / 16, piece lane % 16).  Scales one by
-    // one: lane (token lane % 16, groups lane / 16 + 4 j).
-    uint32_t k[DW], v[4];
+    if (to < 0) from = -1;
+    // Offsets of the lane's pieces; -1: not moved.
     const int kt = lane >> 2;
     const int64_t kf = __shfl(from, kt);
-    const int kp = __shfl(place, kt);
-    if (kf >= 0) {
-      const uint32_t* s = reinterpret_cast<const uint32_t*>(pool + kf + kp * (D / 2) + (lane & 3) * (D / 8));
-#pragma unroll
-      for (int j = 0; j < DW; ++j) k[j] = s[j];
-    }
     int64_t vf[4];
+    const int kp = __shfl(place, kt) * (D / 2) + (lane & 3) * (D / 8);
     int vp[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       vf[j] = __shfl(from, (lane >> 4) * 4 + j);
-      vp[j] = __shfl(place, (lane >> 4) * 4 + j);
-      if (vf[j] >= 0) {
-        const uint8_t* s = pool + vf[j] + 8 * D + ((vp[j] >> 2) * 16 + (lane & 15)) * (D / 8) + (vp[j] & 3) * DW;
-        if constexpr (DW >= 4)
-          v[j] = *reinterpret_cast<const uint32_t*>(s);
-        else
-          v[j] = *reinterpret_cast<const uint16_t*>(s);
-      }
+      const int p = __shfl(place, (lane >> 4) * 4 + j);
+      vp[j] = 8 * D + ((p >> 2) * 16 + (lane & 15)) * (D / 8) + (p & 3) * DW;
     }
-    constexpr int NG = D / kv_group(FMT);
-    uint32_t sk[(NG + 3) / 4], sv[(NG + 3) / 4];
-    const int64_t sf = from;                                  // of token lane % 16
+    auto load = [&](int x, Moved& m) {
+      if (x >= all) return;
+      const uint8_t* base = kc.pool + (x / kc.heads) * a.plane_bytes + (x % kc.heads) * head_bytes;
+      if (kf >= 0) {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(base + kf + kp);
 #pragma unroll
-    for (int j = 0; j < (NG + 3) / 4; ++j) {
-      const int g = (lane >> 4) + 4 * j;
-      if (sf >= 0 && g < NG) {
-        const uint8_t *x = pool + sf + kv_k_scale<FMT, D>(place, g), *y = pool + sf + kv_v_scale<FMT, D>(place, g);
-        sk[j] = FMT == kFmtINT4 ? *reinterpret_cast<const uint16_t*>(x) : *x;
-        sv[j] = FMT == kFmtINT4 ? *reinterpret_cast<const uint16_t*>(y) : *y;
-      }
-    }
-    if constexpr (IN_PLACE) __syncthreads();
-    if (kf >= 0) {
-      uint32_t* d = reinterpret_cast<uint32_t*>(to + kt * (D / 2) + (lane & 3) * (D / 8));
-#pragma unroll
-      for (int j = 0; j < DW; ++j) d[j] = k[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (vf[j] >= 0) {
-        uint8_t* d = to + 8 * D + lane * (D / 8) + j * DW;
-        if constexpr (DW >= 4)
-          *reinterpret_cast<uint32_t*>(d) = v[j];
-        else
-          *reinterpret_cast<uint16_t*>(d) = uint16_t(v[j]);
+        for (int j = 0; j < DW; ++j) m.k[j] = s[j];
       }
 #pragma unroll
-    for (int j = 0; j < (NG + 3) / 4; ++j) {
-      const int g = (lane >> 4) + 4 * j;
-      if (sf >= 0 && g < NG) {
-        uint8_t *x = to + kv_k_scale<FMT, D>(lane & 15, g), *y = to + kv_v_scale<FMT, D>(lane & 15, g);
-        if constexpr (FMT == kFmtINT4) {
-          *reinterpret_cast<uint16_t*>(x) = uint16_t(sk[j]);
-          *reinterpret_cast<uint16_t*>(y) = uint16_t(sv[j]);
-        } else {
-          *x = uint8_t(sk[j]);
-          *y = uint8_t(sv[j]);
+      for (int j = 0; j < 4; ++j)
+        if (vf[j] >= 0) {
+          const uint8_t* s = base + vf[j] + vp[j];
+          m.v[j] = DW >= 4 ? *reinterpret_cast<const uint32_t*>(s) : *reinterpret_cast<const uint16_t*>(s);
+        }
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int g = (lane >> 4) + 4 * j;
+        if (from >= 0 && g < NG) {
+          const uint8_t *y = base + from + kv_k_scale<FMT, D>(place, g), *z = base + from + kv_v_scale<FMT, D>(place, g);
+          m.sk[j] = FMT == kFmtINT4 ? *reinterpret_cast<const uint16_t*>(y) : *y;
+          m.sv[j] = FMT == kFmtINT4 ? *reinterpret_cast<const uint16_t*>(z) : *z;
         }
       }
+    };
+    auto store = [&](int x, const Moved& m) {
+      uint8_t* base = kc.pool + (x / kc.heads) * a.plane_bytes + (x % kc.heads) * head_bytes + to;
+      if (kf >= 0) {
+        uint32_t* d = reinterpret_cast<uint32_t*>(base + kt * (D / 2) + (lane & 3) * (D / 8));
+#pragma unroll
+        for (int j = 0; j < DW; ++j) d[j] = m.k[j];
+      }
+      uint8_t* dv = base + 8 * D + lane * (D / 8);
+      if (vf[0] >= 0 && vf[1] >= 0 && vf[2] >= 0 && vf[3] >= 0) {
+        if constexpr (DW >= 4)
+          *reinterpret_cast<uint4*>(dv) = make_uint4(m.v[0], m.v[1], m.v[2], m.v[3]);
+        else
+          *reinterpret_cast<uint2*>(dv) = make_uint2(m.v[0] | m.v[1] << 16, m.v[2] | m.v[3] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (vf[j] >= 0) {
+            if constexpr (DW >= 4)
+              *reinterpret_cast<uint32_t*>(dv + j * DW) = m.v[j];
+            else
+              *reinterpret_cast<uint16_t*>(dv + j * DW) = uint16_t(m.v[j]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int g = (lane >> 4) + 4 * j;
+        if (from >= 0 && g < NG) {
+          uint8_t *y = base + kv_k_scale<FMT, D>(lane & 15, g), *z = base + kv_v_scale<FMT, D>(lane & 15, g);
+          if constexpr (FMT == kFmtINT4) {
+            *reinterpret_cast<uint16_t*>(y) = uint16_t(m.sk[j]);
+            *reinterpret_cast<uint16_t*>(z) = uint16_t(m.sv[j]);
+          } else {
+            *y = uint8_t(m.sk[j]);
+            *z = uint8_t(m.sv[j]);
+          }
+        }
+      }
+    };
+    Moved now, next;
+    load(part, now);
+    for (int x = part; x < all; x += step) {
+      load(x + step, next);
+      if constexpr (HOW == kInPlace) __syncthreads();          // every wave has what it reads of x
+      store(x, now);
+      now = next;
     }
   }
 }
@@ -499,16 +529,24 @@ struct Read {
     kv_read_kernel<FMT, D><<<dim3(kc.M, row_parts(kc.M, units)), 256, 0, s>>>(kc, K, ldk, V, ldv, f32);
   }
 };
+constexpr int kCompactFew = 64;             // tokens that one wave moves in place
+constexpr int64_t kCompactGroups = 2048;    // workgroups of a compaction, if it has heads and layers for them
+
 template <int FMT, int D>
 struct Compact {
-  static void run(const KvCache& kc, const KvCompact& a, int planes, bool in_place, hipStream_t s) {
-    const int x = kc.batch * kc.heads;
-    if (in_place) {
-      kv_compact_kernel<FMT, D, true><<<dim3(x, 1, planes), 256, 0, s>>>(kc, a);
-    } else {
-      const int64_t tiles = a.most / 16 + 2, y = (tiles + 3) / 4;
-      kv_compact_kernel<FMT, D, false><<<dim3(x, unsigned(y < 65535 ? y : 65535), planes), 256, 0, s>>>(kc, a);
-    }
+  static void run(const KvCache& kc, KvCompact a, bool in_place, hipStream_t s) {
+    const int64_t tiles = a.most / 16 + 2, all = int64_t(a.planes) * kc.heads;
+    const bool by_wave = in_place && a.most <= kCompactFew;
+    const int64_t y = in_place ? 1 : tiles < 4 * 65535 ? (tiles + 3) / 4 : 65535, most = by_wave ? (all + 3) / 4 : all;
+    const int64_t fill = kCompactGroups / (kc.batch * y);
+    a.parts = int(fill < 1 ? 1 : fill < most ? fill : most);
+    const dim3 grid(unsigned(kc.batch) * a.parts, unsigned(y));
+    if (by_wave)
+      kv_compact_kernel<FMT, D, kInPlaceByWave><<<grid, 256, 0, s>>>(kc, a);
+    else if (in_place)
+      kv_compact_kernel<FMT, D, kInPlace><<<grid, 256, 0, s>>>(kc, a);
+    else
+      kv_compact_kernel<FMT, D, kApart><<<grid, 256, 0, s>>>(kc, a);
   }
 };
 
@@ -550,8 +588,8 @@ hipError_t launch_kv_copy(uint8_t* pool, int planes, int64_t plane_bytes, int64_
 hipError_t launch_kv_compact(int fmt, int D, const KvCache& kc, int planes, int64_t plane_bytes, const int32_t* to,
                              int64_t ldto, int cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep,
                              const int32_t* n_keep, int most, bool in_place, hipStream_t s) {
-  const KvCompact a = {to, start, keep, n_keep, ldto, ldkeep, plane_bytes, cols_to, most};
-  by_format<Compact>(fmt, D, kc, a, planes, in_place, s);
+  const KvCompact a = {to, start, keep, n_keep, ldto, ldkeep, plane_bytes, cols_to, most, planes, 1};
+  by_format<Compact>(fmt, D, kc, a, in_place, s);
   return hipGetLastError();
 }
 
