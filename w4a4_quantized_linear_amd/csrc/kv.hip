@@ -334,25 +334,27 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvCache kc, void* K, int64
 
 // Pairs of pages, by value: the host's list is the caller's again when the call returns, and no copy of it has to
 // reach the GPU first.
-constexpr int kCopyPairs = 256;
+constexpr int kCopyPairs = 480;              // 3840 of a kernel's 4096 bytes of arguments
 struct KvPairs {
   int32_t src[kCopyPairs], dst[kCopyPairs];
 };
 
-// A workgroup copies 16 KiB of one page of one layer: four 16-byte loads a lane in flight.
+// A workgroup copies an even share, up to 16 KiB, of one page of one layer: four 16-byte loads a lane in flight.
 constexpr int kCopyChunk = 16384;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __global__ void __launch_bounds__(256) kv_copy_kernel(uint8_t* pool, int64_t plane_bytes, int64_t page_bytes, KvPairs p) {
   uint8_t* plane = pool + blockIdx.z * plane_bytes;
-  const uint4* src = reinterpret_cast<const uint4*>(plane + p.src[blockIdx.y] * page_bytes);
-  uint4* dst = reinterpret_cast<uint4*>(plane + p.dst[blockIdx.y] * page_bytes);
-  const int64_t n = page_bytes / 16, at = int64_t(blockIdx.x) * (kCopyChunk / 16) + threadIdx.x;
-  uint4 v[4];
+  const u32x4* src = reinterpret_cast<const u32x4*>(plane + p.src[blockIdx.y] * page_bytes);
+  u32x4* dst = reinterpret_cast<u32x4*>(plane + p.dst[blockIdx.y] * page_bytes);
+  const int n = int(page_bytes / 16), share = (n + gridDim.x - 1) / gridDim.x;
+  const int at = blockIdx.x * share + threadIdx.x, end = min(n, int(blockIdx.x + 1) * share);
+  u32x4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (at + i * 256 < n) v[i] = src[at + i * 256];
+    if (at + i * 256 < end) v[i] = __builtin_nontemporal_load(src + at + i * 256);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (at + i * 256 < n) dst[at + i * 256] = v[i];
+    if (at + i * 256 < end) __builtin_nontemporal_store(v[i], dst + at + i * 256);
 }
 
 struct KvCompact {
