@@ -421,9 +421,8 @@ def _here(dev, stream) -> bool:
 
 
 def _pool(t, page_bytes: int, dims: int):
-    torch = _torch()
-    shape = t.shape
-    if t.dtype != torch.uint8 or len(shape) not in range(2, dims + 1) or shape[-1] != page_bytes or not t.is_cuda:
+    torch, shape = _torch(), t.shape
+    if t.dtype is not torch.uint8 or not 2 <= len(shape) <= dims or shape[-1] != page_bytes or not t.is_cuda:
         raise ValueError(f"pool: expected pages x {page_bytes} bytes on a GPU, got {tuple(shape)} of {t.dtype} on {t.device}")
     if not t.is_contiguous():
         raise ValueError("pool: expected contiguous bytes")
@@ -431,27 +430,44 @@ def _pool(t, page_bytes: int, dims: int):
 
 def _int_rows(t, name: str, rows: int, device) -> int:
     """Row stride of an int32 matrix."""
-    if t.dim() != 2 or t.shape[0] != rows or t.dtype != _torch().int32 or t.device != device:
-        raise ValueError(f"{name}: expected {rows} rows of int32 on {device}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or t.dtype is not _torch().int32 or t.device != device:
+        raise ValueError(f"{name}: expected {rows} rows of int32 on {device}, got {tuple(shape)} of {t.dtype} on {t.device}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if rows > 1 else t.shape[1]
+    return ld if rows > 1 else shape[1]
 
 
 def _cache_args(kv, pool, table, lens, cu, M: int):
     """The arguments that calls on one layer's cache begin with."""
-    torch, dev = _torch(), pool.device
+    i32, dev = _torch().int32, pool.device
     p, nbytes = _kept_kv(kv)
     _pool(pool, nbytes, 2)
-    batch = lens.shape[0] if lens.dim() == 1 else -1
-    _flat(lens, "lens", (batch,), dev, torch.int32)
+    shape = lens.shape
+    batch = shape[0] if len(shape) == 1 else -1
+    if batch < 0 or lens.dtype is not i32 or lens.device != dev or not lens.is_contiguous():
+        _flat(lens, "lens", (batch,), dev, i32)
     ldt = _int_rows(table, "table", batch, dev)
     if cu is not None:
-        _flat(cu, "cu", (batch + 1,), dev, torch.int32)
+        _flat(cu, "cu", (batch + 1,), dev, i32)
     elif M != batch:
         raise ValueError(f"cu: needed for {M} rows of {batch} sequences")
     return (p, pool.data_ptr(), pool.shape[0], table.data_ptr(), ldt, table.shape[1], lens.data_ptr(),
             None if cu is None else cu.data_ptr(), batch, M)
+
+
+def _bf16_rows(t, name: str, rows: int, cols: int, device) -> int:
+    """Row stride of `rows` rows of bf16 (or their bits)."""
+    torch = _torch()
+    if t.dtype is torch.bfloat16 and t.shape == (rows, cols) and t.device == device:
+        ld, inner = t.stride()
+        if inner == 1:
+            return ld if rows > 1 else (cols + 7) // 8 * 8
+    ld = _rows(t, name, cols, device, (torch.bfloat16, torch.int16))
+    if t.shape[0] != rows:
+        raise ValueError(f"{name}: {t.shape[0]} rows for {rows}")
+    return ld
 
 
 def kv_append(kv: KvLayout, pool, table, lens, K, V, cu=None, Q=None, q_out=None, norm_q=None, norm_k=None,
@@ -463,44 +479,46 @@ def kv_append(kv: KvLayout, pool, table, lens, K, V, cu=None, Q=None, q_out=None
     if not _here(dev, stream):
         return _elsewhere(dev, stream, lambda: kv_append(kv, pool, table, lens, K, V, cu, Q, q_out, norm_q, norm_k, eps,
                                                          freq, axis, pos, halves))
-    M, D, bf16 = K.shape[0], kv.head_dim, (torch.bfloat16, torch.int16)
+    M, D = K.shape[0], kv.head_dim
+    cols = kv.heads * D
     args = _cache_args(kv, pool, table, lens, cu, M)
-    ldk, ldv = _rows(K, "K", kv.heads * D, dev, bf16), _rows(V, "V", kv.heads * D, dev, bf16)
+    ldk, ldv = _bf16_rows(K, "K", M, cols, dev), _bf16_rows(V, "V", M, cols, dev)
     ldq = ldo = q_heads = pairs = axes = 0
-    if V.shape[0] != M:
-        raise ValueError(f"V: {V.shape[0]} rows for {M} of K")
+    pq = po = pnq = pnk = pf = pa = pp = None
     if Q is not None:
-        if Q.dim() != 2 or Q.shape[1] == 0 or Q.shape[1] % D or Q.shape[0] != M:
+        cols = Q.shape[1] if Q.dim() == 2 else 0
+        q_heads = cols // D
+        if cols == 0 or cols % D:
             raise ValueError(f"Q: expected {M} rows of heads x {D}, got {tuple(Q.shape)}")
-        q_heads = Q.shape[1] // D
-        ldq = _rows(Q, "Q", q_heads * D, dev, bf16)
+        ldq, pq = _bf16_rows(Q, "Q", M, cols, dev), Q.data_ptr()
         if q_out is None:
-            q_out, ldo = torch.empty((M, q_heads * D), dtype=Q.dtype, device=dev), q_heads * D
+            q_out, ldo = torch.empty((M, cols), dtype=Q.dtype, device=dev), cols
         else:
-            ldo = _rows(q_out, "q_out", q_heads * D, dev, bf16)
-            if q_out.shape[0] != M:
-                raise ValueError(f"q_out: {q_out.shape[0]} rows for {M}")
+            ldo = _bf16_rows(q_out, "q_out", M, cols, dev)
+        po = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out: given without Q")
-    for name, w in (("norm_q", norm_q), ("norm_k", norm_k)):
-        if w is not None:
-            _flat(w, name, (D,), dev, w.dtype if w.dtype == torch.int16 else torch.bfloat16)
+    if norm_q is not None:
+        _flat(norm_q, "norm_q", (D,), dev, norm_q.dtype if norm_q.dtype is torch.int16 else torch.bfloat16)
+        pnq = norm_q.data_ptr()
+    if norm_k is not None:
+        _flat(norm_k, "norm_k", (D,), dev, norm_k.dtype if norm_k.dtype is torch.int16 else torch.bfloat16)
+        pnk = norm_k.data_ptr()
     if freq is not None:
         pairs = freq.shape[0] if freq.dim() == 1 else -1
         _flat(freq, "freq", (pairs,), dev, torch.float32)
+        pf = freq.data_ptr()
         if axis is not None:
             _flat(axis, "axis", (pairs,), dev, torch.int32)
+            pa = axis.data_ptr()
         if pos is not None:
             axes = pos.shape[0] if pos.dim() == 2 else -1
             _flat(pos, "pos", (axes, M), dev, torch.int32)
+            pp = pos.data_ptr()
     elif axis is not None or pos is not None:
         raise ValueError("axis, pos: given without freq")
-    st = lib().svdq_kv_append(*args, K.data_ptr(), ldk, V.data_ptr(), ldv, None if Q is None else Q.data_ptr(), ldq,
-                              q_heads, None if q_out is None else q_out.data_ptr(), ldo,
-                              None if norm_q is None else norm_q.data_ptr(),
-                              None if norm_k is None else norm_k.data_ptr(), eps,
-                              None if freq is None else freq.data_ptr(), None if axis is None else axis.data_ptr(),
-                              pairs, None if pos is None else pos.data_ptr(), axes, ROPE_HALVES if halves else 0,
+    st = lib().svdq_kv_append(*args, K.data_ptr(), ldk, V.data_ptr(), ldv, pq, ldq, q_heads, po, ldo, pnq, pnk, eps, pf, pa,
+                              pairs, pp, axes, ROPE_HALVES if halves else 0,
                               torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
         check("svdq_kv_append", st)
@@ -535,19 +553,17 @@ def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = Non
     if not _here(dev, stream):
         return _elsewhere(dev, stream, lambda: kv_attention(kv, pool, table, lens, Q, cu, scale, window, causal, out, lse,
                                                             workspace))
-    D, bf16 = kv.head_dim, (torch.bfloat16, torch.int16)
-    if Q.dim() != 2 or Q.shape[1] % D:
-        raise ValueError(f"Q: expected rows of heads x {D}, got {tuple(Q.shape)}")
-    M, cols = Q.shape
+    D, shape = kv.head_dim, Q.shape
+    if len(shape) != 2 or shape[1] % D:
+        raise ValueError(f"Q: expected rows of heads x {D}, got {tuple(shape)}")
+    M, cols = shape
     q_heads = cols // D
     args = _cache_args(kv, pool, table, lens, cu, M)
-    ldq = _rows(Q, "Q", cols, dev, bf16)
+    ldq = _bf16_rows(Q, "Q", M, cols, dev)
     if out is None:
         out, ldy = torch.empty((M, cols), dtype=Q.dtype, device=dev), cols
     else:
-        ldy = _rows(out, "out", cols, dev, bf16)
-        if out.shape[0] != M:
-            raise ValueError(f"out: {out.shape[0]} rows for {M}")
+        ldy = _bf16_rows(out, "out", M, cols, dev)
     if lse is True:
         lse = torch.empty((M, q_heads), dtype=torch.float32, device=dev)
     elif lse is False:
@@ -576,10 +592,10 @@ def kv_copy(kv: KvLayout, pool, src, dst, stream=None):
     n = len(src)
     if len(dst) != n:
         raise ValueError(f"{n} sources for {len(dst)} destinations")
-    ids = (ctypes.c_int32 * n)(*src), (ctypes.c_int32 * n)(*dst)
+    array = ctypes.c_int32 * n
     pages = pool.shape[-2]
-    st = lib().svdq_kv_copy(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes, ids[0],
-                            ids[1], n, _torch()._C._cuda_getCurrentRawStream(dev.index))
+    st = lib().svdq_kv_copy(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes,
+                            array(*src), array(*dst), n, _torch()._C._cuda_getCurrentRawStream(dev.index))
     if st:
         check("svdq_kv_copy", st)
     return pool

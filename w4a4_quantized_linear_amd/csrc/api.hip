@@ -530,7 +530,7 @@ size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t cols, int32_t batc
       q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || M * q_heads > kKvMaxRowHeads ||
       cols < 1 || int64_t(cols) * d->page > kKvMaxTokens)
     return 0;
-  return kv_plan(d->fmt, d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page).bytes;
+  return kv_plan(d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page).bytes;
 }
 
 svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,
@@ -546,7 +546,7 @@ svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t p
   if (s == SVDQ_ERR_SHAPE) return s;
   if (q_heads < 1 || q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || window < 0 ||
       !(scale > 0.0f && scale <= 3.0e38f) || M * q_heads > kKvMaxRowHeads ||
-      !kv_units_fit(d->fmt, d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
+      !kv_units_fit(d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
     return SVDQ_ERR_SHAPE;
   const int64_t cols_q = int64_t(q_heads) * d->head_dim;
   const svdq_status rq = check_rows(Q, ldq, cols_q), ry = check_rows(Y, ldy, cols_q);

@@ -39,29 +39,44 @@ __host__ __device__ constexpr int kv_tile_bytes(int fmt, int D) { return kKvTile
 
 // How a call of svdq_kv_attention is cut: `rows` query rows of a K/V head (a sequence's tokens x the heads that share
 // it) a workgroup, `jobs` such tiles at most; split: `ranges` workgroups a head share the units of all jobs.
+//
+// Rows by what a sequence has on average, and 128 where there are 256 such tiles (then a wave's 32 rows see all
+// tokens, 4 waves side by side; with fewer, a tile's tokens are shared out).  us in a graph, MXFP4, 8 heads x 4
+// queries of 128, 16 sequences of 2000 tokens, new tokens each: 16 rows / 32 / 128
+//   q 2 21.0 / 21.3 / 61    q 12 29.1 / 28.7 / 64    q 32 - / 41.5 / 66    q 64 - / 74 / 68    q 256 - / 242 / 182
+// and one sequence of 8192: q 8 17.5 / 17.4 / 228, q 256 - / 78 / 225, q 512 - / 130 / 225 (128 tiles), and of 16000
+// 4 sequences, 2 x 8 heads: q 512 - / 420 / 428 (256 tiles).
+// Split where tokens are many for the tiles: one query a sequence, ragged, whole against split at 512, 1024, 2048, 4096
+// tokens: 8 tiles 7.2 / 8.7, 9.6 / 9.1, 14.5 / 9.4, 23.5 / 10.4; 128 tiles 7.6 / 10.9, 10.0 / 12.5, 14.8 / 13.4,
+// 23.8 / 18.4; 512 tiles 13.0 / 15.2, 18.4 / 21.2, 27.3 / 25.3, 44.2 / 34.9 (INT4 and NVFP4 alike); with 32 rows at
+// 256 tiles of 2000 tokens 28.7 / 31.5, 128 tiles 28.1 / 24.8.
+// Ranges: three workgroups a CU (1, 2, 3, 4 a CU: 64 x 8192 MXFP4 76.9 63.7 59.7 63.4, 3 x 131072 38.7 35.0 35.7
+// 38.2, INT4 64 x 8192 89.3 75.7 69.0 72.7), two where a wave has 32 rows and registers for two.
 constexpr int64_t kKvWhole = 1024;           // tokens of a table up to which a job is one workgroup's
+constexpr int64_t kKvWholeMany = 1536;       // the same from 64 jobs on
 struct KvPlan {
   int rows, jobs, ranges;
   bool split;
   size_t bytes;
 };
-inline KvPlan kv_plan(int fmt, int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
+inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
   KvPlan p;
   const int64_t group = q_heads / heads, each = (M * group + batch - 1) / (batch > 0 ? batch : 1);
-  p.rows = each <= 16 ? 16 : each <= 32 ? 32 : 128;
-  const int64_t jobs = (M * group + p.rows - 1) / p.rows + batch;
+  auto tiles = [&](int rows) { return (M * group + rows - 1) / rows + batch; };
+  p.rows = each <= 16 ? 16 : (tiles(128) - batch) * heads >= 256 ? 128 : 32;
+  const int64_t jobs = tiles(p.rows);
   p.jobs = int(jobs);
-  p.split = p.rows < 128 ? places > kKvWhole : jobs * heads < 512;
-  const int a_cu = p.rows == 16 ? 3 : 2;
-  p.ranges = p.split ? (256 * a_cu + heads - 1) / heads : 0;
+  p.split = p.rows < 128 && places > (jobs * heads >= 64 ? kKvWholeMany : kKvWhole) &&
+            (p.rows == 16 || jobs * heads < 384);
+  p.ranges = p.split ? (256 * (p.rows == 16 ? 3 : 2) + heads - 1) / heads : 0;
   p.bytes = p.split ? align256(size_t(p.ranges) * heads * 2 * p.rows * (D + 2) * 4) : 0;
   return p;
 }
 
 // Whether the units of all jobs, of tables with `places` tokens each, can be counted in 32 bits.
-inline bool kv_units_fit(int fmt, int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
-  const KvPlan p = kv_plan(fmt, D, batch, M, q_heads, heads, places);
-  return !p.split || p.jobs * (places / (p.rows < 128 ? 128 : 32) + 1) <= INT32_MAX - 4096;
+inline bool kv_units_fit(int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
+  const KvPlan p = kv_plan(D, batch, M, q_heads, heads, places);
+  return !p.split || p.jobs * (places / 128 + 1) <= INT32_MAX - 4096;
 }
 
 // A cache and its sequences, as the kernels take them.  Places beyond a sequence's table or with a page outside

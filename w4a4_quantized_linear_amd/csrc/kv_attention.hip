@@ -363,11 +363,15 @@ struct KvScan {
   int* sh;                                     // 16 words of LDS
   int v = 0, end = 0, total = 0;
 
-  __device__ __forceinline__ int units_of(int b) const {
-    if (b >= kc.batch) return 0;
+  __device__ __forceinline__ KvSeq seq(int b) const {
     int len, row, rows;
     kc.sequence(b, len, row, rows);
-    const KvSeq s = kv_seq<R, U, SPLIT>(kc, a, len, row, rows);
+    return kv_seq<R, U, SPLIT>(kc, a, len, row, rows);
+  }
+  __device__ __forceinline__ int tiles_of(int b) const { return b < kc.batch ? seq(b).tiles : 0; }
+  __device__ __forceinline__ int units_of(int b) const {
+    if (b >= kc.batch) return 0;
+    const KvSeq s = seq(b);
     return s.tiles * s.units;
   }
   // This thread's inclusive sum in the chunk at `base`, the chunks before it being `before`; adds the chunk to it.
@@ -770,10 +774,11 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
 
 constexpr int kJoinGroups = 2048;        // workgroups of a join at most, if jobs x heads are not more
 
-// Joins the parts of split jobs.  A workgroup takes a job (BY_SEQ, where a sequence is one: the sequence's; else the
-// one inside which a range border is the first) and its rows: D / 8 threads take a row's features, and of the
-// 2048 / D such groups as many share a row as the parts keep busy.
-template <int D, int R, int U, bool BY_SEQ>
+// Joins the parts of split jobs.  A workgroup takes a job and its rows: D / 8 threads take a row's features, and of the
+// 2048 / D such groups as many share a row as the parts keep busy.  How it finds its job: by number, in a batch whose
+// scan is one wave's; by sequence, where each is one job; else as the one inside which a range border is the first.
+enum { kByJob = 0, kBySeq = 1, kByBorder = 2 };
+template <int D, int R, int U, int HOW>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   constexpr int F = 8, TPR = D / F, NP = 256 / TPR;
   __shared__ int sh[16];
@@ -784,7 +789,15 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   const int per = units_a_range(total, a.ranges, kLeastUnits);
   int b, job, start;
   KvSeq s;
-  if constexpr (BY_SEQ) {
+  if constexpr (HOW == kByJob) {
+    const int tiles = scan.tiles_of(int(threadIdx.x) & 63), sum = wave_scan(tiles);
+    const uint64_t in = __ballot(index < sum);
+    if (in == 0) return;
+    b = __builtin_ctzll(in);
+    job = index - __builtin_amdgcn_readlane(sum - tiles, b);
+    s = kv_seq_of<R, U, true>(kc, a, b);
+    start = scan.before(b) + job * s.units;
+  } else if constexpr (HOW == kBySeq) {
     b = index;
     job = 0;
     start = scan.before(b);
@@ -855,29 +868,31 @@ void attend_whole(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
   kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(unsigned(jobs) * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
 }
 template <int FMT, int D, int NQ, int WQ, int WK, int PL>
-void attend_split(const KvCache& kc, const KvAttn& a, hipStream_t s) {
+void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
   constexpr int R = KvTiles<NQ, WQ, WK>::R, U = KvTiles<NQ, WQ, WK>::U;
   kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
   if (a.ranges < 2) return;
-  const bool by_seq = kc.cu == nullptr && a.group <= R;      // a sequence is one job
-  const int jobs_h = (by_seq ? kc.batch : a.ranges - 1) * kc.heads;
-  const int64_t rows = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group, most = rows < R ? rows : R;
-  const int64_t fill = kJoinGroups / jobs_h;
-  const unsigned y = unsigned(fill < 1 ? 1 : fill < most ? fill : most);
-  if (by_seq)
-    kv_join_kernel<D, R, U, true><<<dim3(jobs_h, y), 256, 0, s>>>(kc, a);
+  const int64_t most = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group, rows = most < R ? most : R;
+  const int how = kc.batch <= 64 ? kByJob : kc.cu == nullptr && a.group <= R ? kBySeq : kByBorder;
+  const int x = (how == kByJob ? jobs : how == kBySeq ? kc.batch : a.ranges - 1) * kc.heads;
+  const int fill = kJoinGroups / x;
+  const dim3 grid(x, unsigned(fill < 1 ? 1 : fill < rows ? fill : rows));
+  if (how == kByJob)
+    kv_join_kernel<D, R, U, kByJob><<<grid, 256, 0, s>>>(kc, a);
+  else if (how == kBySeq)
+    kv_join_kernel<D, R, U, kBySeq><<<grid, 256, 0, s>>>(kc, a);
   else
-    kv_join_kernel<D, R, U, false><<<dim3(jobs_h, y), 256, 0, s>>>(kc, a);
+    kv_join_kernel<D, R, U, kByBorder><<<grid, 256, 0, s>>>(kc, a);
 }
 
 template <int FMT, int D>
 void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_t s) {
   if (p.rows == 16)
-    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, p.jobs, s);
+    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, p.jobs, s);
   else if (p.rows == 32)
-    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s);
+    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s);
   else
-    p.split ? attend_split<FMT, D, 2, 4, 1, 1>(kc, a, s) : attend_whole<FMT, D, 2, 4, 1, 1>(kc, a, p.jobs, s);
+    attend_whole<FMT, D, 2, 4, 1, 1>(kc, a, p.jobs, s);
 }
 
 }  // namespace
@@ -885,7 +900,7 @@ void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_
 hipError_t launch_kv_attention(int fmt, int D, const KvCache& kc, const uint16_t* Q, int64_t ldq, int q_heads,
                                float scale, int window, bool causal, uint16_t* Y, int64_t ldy, float* lse, float* part,
                                hipStream_t s) {
-  const KvPlan p = kv_plan(fmt, D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
+  const KvPlan p = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
   const KvAttn a = {Q, Y, lse, part, ldq, ldy, q_heads / kc.heads, q_heads, window, causal ? 1 : 0, p.ranges,
                     scale * 1.44269504088896341f};
   if (fmt == kFmtMXFP4)
