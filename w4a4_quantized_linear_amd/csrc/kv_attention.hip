@@ -186,6 +186,15 @@ __device__ __forceinline__ uint32_t v_pair(const KvStage<FMT, D>& st, const v2h 
 }
 constexpr uint32_t kLowHalves = 0x05040100u, kHighHalves = 0x07060302u;
 
+// INT4: bytes of group g's features of tokens 2 t and 2 t + 1, one beside the other.
+template <int D>
+__device__ __forceinline__ uint32_t value_pair(const KvStage<kFmtINT4, D>& st, int t, int g) {
+  if constexpr (D == 128)
+    return __builtin_amdgcn_perm(st.v[2 * t + 1], st.v[2 * t], g ? 0x07030602u : 0x05010400u);
+  else
+    return __builtin_amdgcn_perm(st.v[t], st.v[t], 0x03010200u);
+}
+
 // O^T += V^T P^T over a step for every feature tile, e the probabilities of a lane's 8 tokens.  INT4: a group's scales
 // multiply its probabilities, so they are rounded once, and off is -8 times their sums.
 template <int FMT, int D, int NQ, int PL>
@@ -212,10 +221,7 @@ __device__ __forceinline__ void add_values(const KvStage<FMT, D> (&st)[2], const
       uint32_t w[4][2];                                     // token pairs: two features' bytes of both, by nibble
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const KvStage<FMT, D>& z = st[t >> 1];
-        const uint32_t x = D == 128 ? __builtin_amdgcn_perm(z.v[D / 64 * (t & 1) + D / 128], z.v[D / 64 * (t & 1)],
-                                                            g ? 0x07030602u : 0x05010400u)
-                                    : __builtin_amdgcn_perm(z.v[t & 1], z.v[t & 1], 0x03010200u);
+        const uint32_t x = value_pair<D>(st[t >> 1], t & 1, g);
         w[t][0] = x & 0x0F0F0F0Fu;
         w[t][1] = (x >> 4) & 0x0F0F0F0Fu;
       }
@@ -337,6 +343,138 @@ __device__ __forceinline__ KvSeq kv_seq_of(const KvCache& kc, const KvAttn& a, i
   if (kc.cu == nullptr) return kv_seq<R, U, SPLIT>(kc, a, len, b, 1);
   const int row = min(max(cu[b], 0), kc.M);
   return kv_seq<R, U, SPLIT>(kc, a, len, row, max(min(cu[b + 1], kc.M) - row, 0));
+}
+
+// The query rows of a sequence on one K/V head, and the tokens [first, behind) that they see.
+struct KvSpan {
+  int first, behind, first_most, behind_least;                // outermost and innermost of a run of rows
+};
+struct KvRows {
+  int rows, place0, there, window, causal, group;             // place0: the first row's place in its sequence
+  __device__ __forceinline__ KvRows(const KvCache& kc, const KvAttn& a, const KvSeq& s)
+      : rows(s.rows * a.group), place0(s.len - s.rows), there(min(s.len, kc.capacity())), window(a.window),
+        causal(a.causal), group(a.group) {}
+  __device__ __forceinline__ int first(int token) const { return window > 0 ? max(place0 + token - window + 1, 0) : 0; }
+  __device__ __forceinline__ int behind(int token) const {
+    return causal ? min(max(place0 + token + 1, 0), there) : there;
+  }
+  __device__ __forceinline__ KvSpan span(int row, int n) const {
+    if (row >= rows) return {0, 0, 0, 0};
+    const int a = row / group, z = (min(row + n, rows) - 1) / group;
+    return {first(a), behind(z), first(z), behind(a)};
+  }
+};
+
+// A wave's 16 NQ query rows from row0 on, as they lie, and what each sees; rows that are not there are zeros that see nothing.
+template <int FMT, int D, int NQ>
+__device__ __forceinline__ void load_queries(const KvAttn& a, const KvSeq& s, const KvRows& rows, int row0, int h, int r,
+                                             int c, uint4 (&q)[NQ][D / 32], int (&lo)[NQ], int (&hi)[NQ]) {
+  asm volatile("" : "+v"(r), "+v"(c));                        // opaque: its addresses are not kept in registers
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int i = row0 + n * 16 + r;
+    const bool there = i < rows.rows;
+    const int token = there ? int(unsigned(i) / unsigned(a.group)) : 0, head = there ? i - token * a.group : 0;
+    const uint16_t* row = a.Q + int64_t(s.row + token) * a.ldq + (h * a.group + head) * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) q[n][j] = there ? q_operand<FMT, D>(row, c, j) : make_uint4(0, 0, 0, 0);
+    hi[n] = there ? rows.behind(token) : 0;
+    lo[n] = there ? rows.first(token) : 0;
+  }
+}
+
+// The rows as operands (NVFP4: fp16, scaled by a power of two), the factor of their scores, and what INT4's sums start at.
+template <int FMT, int D, int NQ, int NG>
+__device__ __forceinline__ void finish_queries(const KvAttn& a, uint4 (&q)[NQ][D / 32], float (&k2)[NQ],
+                                               v4f (&s0)[NQ][NG]) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    k2[n] = a.scale2;
+    if constexpr (FMT == kFmtNVFP4) {
+      u16x2 top = {0, 0};                                     // the largest magnitude's bits
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (uint32_t x : {q[n][j].x, q[n][j].y, q[n][j].z, q[n][j].w})
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu));
+      const int e2 = f16_row_power(rowgroup_max(__uint_as_float(uint32_t(top.x > top.y ? top.x : top.y) << 16)));
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        float v[8];
+        unpack_bf8(q[n][j], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
+        q[n][j] = to_f16(v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      k2[n] = ldexpf(k2[n], -e2);
+    }
+    if constexpr (FMT == kFmtINT4) {
+      const uint4 m8 = make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u);        // bf16 -8
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        v4f z = {0.f, 0.f, 0.f, 0.f};
+        z = mfma_bf16(m8, q[n][2 * g], z);
+        s0[n][g] = mfma_bf16(m8, q[n][2 * g + 1], z);
+      }
+    }
+  }
+}
+
+// Scores z[n][tile][token] of tokens t + 16 tile + 4 c + token; those that a row does not see become -infinity.
+template <int NQ>
+__device__ __forceinline__ void mask_scores(float (&z)[NQ][2][4], int t, int c, const bool (&ok)[2], const int (&lo)[NQ],
+                                            const int (&hi)[NQ]) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = t + 16 * i + 4 * c + e;
+        if (!(ok[i] && at < hi[n] && at >= lo[n])) z[n][i][e] = -__builtin_huge_valf();
+      }
+}
+
+// The running maxima, moved where a score exceeds one by kGrow.
+template <int D, int NQ, bool OFF>
+__device__ __forceinline__ void new_maxima(const float (&z)[NQ][2][4], const float (&k2)[NQ], float (&m)[NQ], float (&l)[NQ],
+                                           v4f (&o)[NQ][D / 16], v4f (&off)[NQ][D / 64]) {
+  bool grow = false;
+  float top[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    top[n] = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
+                   fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3]))) * k2[n];
+    grow |= top[n] > m[n] + kGrow;
+  }
+  if (!__any(grow)) return;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const float now = fmaxf(m[n], rowgroup_max(top[n]));
+    const float x = __builtin_amdgcn_exp2f(m[n] - now);
+    m[n] = now;
+    l[n] *= x;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[n][d] *= x;
+    if constexpr (OFF)
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) off[n][g] *= x;
+  }
+}
+
+template <int FMT, int NQ>
+__device__ __forceinline__ void probabilities(const float (&z)[NQ][2][4], const float (&k2)[NQ], const float (&m)[NQ],
+                                              float (&l)[NQ], float (&e)[NQ][8]) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const float base2 = FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[n][i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], k2[n], -base2));
+      l[n] += e[n][i];
+    }
+  }
 }
 
 // Inclusive sum over the wave's lanes: within rows of 16 by shifts, then the rows' last lanes on to those after.
@@ -475,42 +613,21 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
     }
     const int n_units = min(left, s.units - unit);
     const int tile_rows = SPLIT ? job : s.tiles - 1 - job;    // long causal tiles first
-    const int row0 = tile_rows * R + wq * 16 * NQ, rows = s.rows * a.group;
-    const int there_all = min(s.len, kc.capacity());
-
-    // The tokens [first, behind) that a query row's token sees; of the wave's rows the outermost and innermost.
-    auto first_of = [&](int token) { return a.window > 0 ? max(s.len - s.rows + token - a.window + 1, 0) : 0; };
-    auto behind_of = [&](int token) {
-      return a.causal ? min(max(s.len - s.rows + token + 1, 0), there_all) : there_all;
-    };
-    const int token_a = min(row0, rows - 1) / a.group, token_z = min(row0 + 16 * NQ, rows) - 1 < 0
-                                                                     ? 0 : (min(row0 + 16 * NQ, rows) - 1) / a.group;
-    const int first_all = first_of(token_a), first_max = first_of(token_z);
-    const int last_all = row0 < rows ? behind_of(token_z) : 0, last_min = behind_of(token_a);
-
-    int qr = r, qc = c;                                       // opaque likewise
-    asm volatile("" : "+v"(qr), "+v"(qc));
+    const int row0 = tile_rows * R + wq * 16 * NQ;
+    const KvRows rows(kc, a, s);
+    const KvSpan span = rows.span(row0, 16 * NQ);
     uint4 q[NQ][D / 32];
     float k2[NQ];
     int lo[NQ], hi[NQ];
-    v4f s0[FMT == kFmtINT4 ? NQ : 1][FMT == kFmtINT4 ? NG : 1];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int i = row0 + n * 16 + qr;
-      const bool there = i < rows;
-      const int token = there ? int(unsigned(i) / unsigned(a.group)) : 0, head = there ? i - token * a.group : 0;
-      const uint16_t* row = a.Q + int64_t(s.row + token) * a.ldq + (h * a.group + head) * D;
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) q[n][j] = there ? q_operand<FMT, D>(row, qc, j) : make_uint4(0, 0, 0, 0);
-      hi[n] = there ? behind_of(token) : 0;
-      lo[n] = there ? first_of(token) : 0;
-    }
+    v4f s0[NQ][NG];
+    load_queries<FMT, D, NQ>(a, s, rows, row0, h, r, c, q, lo, hi);
+
     // This wave's steps: 32 tokens from s.lo + 32 (unit WK + wk) on, every WK-th; those before every row's window
     // are left out.
     constexpr int STRIDE = 32 * WK;
     int t0 = s.lo + unit * U + 32 * wk;
-    const int end = min(SPLIT ? s.lo + (unit + n_units) * U : INT32_MAX, last_all);
-    if (first_all > t0 && end > t0) t0 += (min(first_all, end) - t0) / STRIDE * STRIDE;
+    const int end = min(SPLIT ? s.lo + (unit + n_units) * U : INT32_MAX, span.behind);
+    if (span.first > t0 && end > t0) t0 += (min(span.first, end) - t0) / STRIDE * STRIDE;
     const int steps = end > t0 ? (end - t0 + STRIDE - 1) / STRIDE : 0;
     const uint8_t* base = kc.pool + (int64_t(TB) << kc.page_shift) * h;
     const int mask = (1 << kc.page_shift) - 1;
@@ -522,7 +639,7 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
       return tile * 16 < end ? kc.page_of(b, tile) : -1;
     };
     int pages = -1, next_pages = pages_from(0);
-    auto fetch = [&](int i, KvStage<FMT, D> (&st)[2], int (&ok)[2]) {
+    auto fetch = [&](int i, KvStage<FMT, D> (&st)[2], bool (&ok)[2]) {
       if ((i & 31) == 0) {
         pages = next_pages;
         next_pages = pages_from(i + 32);
@@ -537,43 +654,11 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
       }
     };
     KvStage<FMT, D> now[2], next[2];
-    int now_ok[2], next_ok[2];
+    bool now_ok[2], next_ok[2];
     fetch(0, now, now_ok);                                    // without a step: of no pages, so no bytes
     __builtin_amdgcn_sched_barrier(0);                        // these loads are on their way before Q is waited for
 
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      k2[n] = a.scale2;
-      if constexpr (FMT == kFmtNVFP4) {
-        u16x2 top = {0, 0};                                   // the largest magnitude's bits
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-          for (uint32_t x : {q[n][j].x, q[n][j].y, q[n][j].z, q[n][j].w})
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu));
-        const int e2 = f16_row_power(rowgroup_max(__uint_as_float(uint32_t(top.x > top.y ? top.x : top.y) << 16)));
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          float v[8];
-          unpack_bf8(q[n][j], v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
-          q[n][j] = to_f16(v);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        k2[n] = ldexpf(k2[n], -e2);
-      }
-      if constexpr (FMT == kFmtINT4) {
-        const uint4 m8 = make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u);      // bf16 -8
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          v4f z = {0.f, 0.f, 0.f, 0.f};
-          z = mfma_bf16(m8, q[n][2 * g], z);
-          s0[n][g] = mfma_bf16(m8, q[n][2 * g + 1], z);
-        }
-      }
-    }
-
+    finish_queries<FMT, D, NQ>(a, q, k2, s0);
     v4f o[NQ][DT], off[NQ][D / 64];
     float m[NQ], l[NQ];
 #pragma unroll
@@ -587,14 +672,13 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
         for (int g = 0; g < NG; ++g) off[n][g] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    auto step = [&](int t, KvStage<FMT, D> (&st)[2], const int (&ok)[2]) {
+    auto step = [&](int t, KvStage<FMT, D> (&st)[2], const bool (&ok)[2]) {
       // Scores: lane (query r, tokens t + 16 i + 4 c + e).
       float z[NQ][2][4];
-      const bool whole = t + 32 <= last_min && t >= first_max && ok[0] && ok[1];
-      if (t + 32 > last_all || t < first_all) {
+      if (t + 32 > span.behind || t < span.first) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          clear_outside<FMT, D>(first_all - t - 16 * i, last_all - t - 16 * i, c, st[i]);
+          clear_outside<FMT, D>(span.first - t - 16 * i, span.behind - t - 16 * i, c, st[i]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -638,51 +722,10 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (!whole) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = t + 16 * i + 4 * c + e;
-              if (!(ok[i] && at < hi[n] && at >= lo[n])) z[n][i][e] = -__builtin_huge_valf();
-            }
-      }
-      // New maxima.
-      bool grow = false;
-      float top[NQ];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        top[n] = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
-                       fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3]))) * k2[n];
-        grow |= top[n] > m[n] + kGrow;
-      }
-      if (__any(grow)) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const float now = fmaxf(m[n], rowgroup_max(top[n]));
-          const float x = __builtin_amdgcn_exp2f(m[n] - now);
-          m[n] = now;
-          l[n] *= x;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[n][d] *= x;
-          if constexpr (FMT == kFmtINT4)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) off[n][g] *= x;
-        }
-      }
-      // Probabilities.
+      if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
+      new_maxima<D, NQ, FMT == kFmtINT4>(z, k2, m, l, o, off);
       float e[NQ][8];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        const float base2 = FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[n][i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], k2[n], -base2));
-          l[n] += e[n][i];
-        }
-      }
+      probabilities<FMT, NQ>(z, k2, m, l, e);
       __builtin_amdgcn_sched_barrier(0);
       add_values<FMT, D, NQ, PL>(st, e, o, off);
     };
@@ -706,7 +749,7 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
     auto emit = [&](int in_tile, int d, auto& v, float mm, float ll) {        // features d .. of row in_tile
       constexpr int N = sizeof(v) / sizeof(float);
       const int i = tile_rows * R + in_tile;
-      if (i >= rows) return;
+      if (i >= rows.rows) return;
       if (!all) {
         if (d == 0) {
           part[in_tile] = mm;
@@ -769,6 +812,236 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
       unit = 0;
       ++job;
     }
+  }
+}
+
+// Prompts: the same with what the waves of a workgroup share done once.  Four waves of 32 rows walk the tokens in chunks
+// of 64; of a chunk each wave makes one tile's operands 16-bit and puts them in LDS in operand order (K's of a
+// tile, its half of V's of a step of 32 tokens), the next chunk's while this one is worked on, with a barrier a chunk.
+// Then a wave's vector instructions are the softmax's and a quarter of the conversions.  2048 queries x 32 heads on
+// 8192 tokens, 8 heads of 128, MXFP4 (241 GFLOP): a wave converting for itself 312 us.
+template <int FMT, int D>
+struct KvShared {
+  uint4 k[2][4][D / 32][64];
+  uint2 v[2][2][D / 16][64][2];
+  uint2 s[2][4][FMT == kFmtINT4 ? D / 4 / 2 : 1];              // INT4: a tile's scales, as in the pool
+};
+
+template <int FMT, int D>
+__device__ __forceinline__ void share_tile(KvStage<FMT, D>& st, int tile, int lane, KvShared<FMT, D>& sh, int half) {
+  trade_groups<FMT, D>(st);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) sh.k[half][tile][j][lane] = k_operand<FMT, D>(st, j);
+  auto put = [&](int dt, uint32_t lo, uint32_t hi) { sh.v[half][tile >> 1][dt][lane][tile & 1] = make_uint2(lo, hi); };
+  if constexpr (FMT == kFmtINT4) {
+    if ((lane & 15) < D / 32) sh.s[half][tile][(lane & 15) * 4 + (lane >> 4)] = make_uint2(st.vs[0], st.vs[1]);
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+      uint32_t w[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t x = value_pair<D>(st, t, g);
+        w[t][0] = x & 0x0F0F0F0Fu;
+        w[t][1] = (x >> 4) & 0x0F0F0F0Fu;
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) put(4 * g + f, fp8_pair(w[0][f & 1], f >> 1), fp8_pair(w[1][f & 1], f >> 1));
+    }
+  } else {
+    v2h nv[2] = {};
+    if constexpr (FMT == kFmtNVFP4) {
+      nv[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(st.vs[0], 1.0f, false);
+      nv[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(st.vs[0], 1.0f, true);
+    }
+    auto one = [&](auto byte) {
+      constexpr int B = decltype(byte)::value;
+      const uint32_t x[4] = {v_pair<FMT, D, 0, B>(st, nv), v_pair<FMT, D, 1, B>(st, nv), v_pair<FMT, D, 2, B>(st, nv),
+                             v_pair<FMT, D, 3, B>(st, nv)};
+      put(2 * B, __builtin_amdgcn_perm(x[1], x[0], kLowHalves), __builtin_amdgcn_perm(x[3], x[2], kLowHalves));
+      put(2 * B + 1, __builtin_amdgcn_perm(x[1], x[0], kHighHalves), __builtin_amdgcn_perm(x[3], x[2], kHighHalves));
+    };
+    one(std::integral_constant<int, 0>{});
+    one(std::integral_constant<int, 1>{});
+    if constexpr (D == 128) {
+      one(std::integral_constant<int, 2>{});
+      one(std::integral_constant<int, 3>{});
+    }
+  }
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a) {
+  constexpr int NQ = 2, R = 128, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1, TB = kv_tile_bytes(FMT, D);
+  __shared__ KvShared<FMT, D> shared;
+  __shared__ int words[16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  const int h = blockIdx.x % kc.heads, index = blockIdx.x / kc.heads;
+  KvScan<R, 32, false, 256> scan{kc, a, words};
+  const int total = scan.count();
+  if (index >= total) return;
+  const KvFound f = scan.find(index);
+  if (f.b < 0) return;
+  const KvSeq s = kv_seq_of<R, 32, false>(kc, a, f.b);
+  const int tile_rows = s.tiles - 1 - (index - f.before);      // long causal tiles first
+  const KvRows rows(kc, a, s);
+  const int wg0 = tile_rows * R, row0 = wg0 + wave * 32;
+
+  uint4 q[NQ][D / 32];
+  float k2[NQ];
+  int lo[NQ], hi[NQ];
+  v4f s0[NQ][NG];
+  load_queries<FMT, D, NQ>(a, s, rows, row0, h, r, c, q, lo, hi);
+  const KvSpan span = rows.span(row0, 32), wg = rows.span(wg0, R);
+  const int t0 = wg.first & ~63, chunks = wg.behind > t0 ? (wg.behind - t0 + 63) / 64 : 0;
+  const uint8_t* base = kc.pool + (int64_t(TB) << kc.page_shift) * h;
+  const int mask = (1 << kc.page_shift) - 1;
+  const KvLane<FMT, D> at(r, c);
+
+  // This wave's tile of every chunk: pages of 64 chunks, one a lane.
+  auto pages_from = [&](int i) {
+    const int tile = (t0 >> 4) + (i + lane) * 4 + wave;
+    return tile * 16 < wg.behind ? kc.page_of(f.b, tile) : -1;
+  };
+  int pages = -1, next_pages = pages_from(0);
+  KvStage<FMT, D> st;
+  auto fetch = [&](int i) {
+    if ((i & 63) == 0) {
+      pages = next_pages;
+      next_pages = pages_from(i + 64);
+    }
+    const int p = __builtin_amdgcn_readlane(pages, i & 63), tile = (t0 >> 4) + i * 4 + wave;
+    const uint8_t* from = base + int64_t(p >= 0 ? p : 0) * kc.page_bytes + uint32_t(tile & mask) * uint32_t(TB);
+    load_tile<FMT, D>(make_rsrc(from, p >= 0 ? TB : 0), at, st);
+    return p >= 0;
+  };
+  // The fetched tile of chunk i to LDS; a tile that is not there leaves a mark.
+  auto share = [&](int i, bool there) {
+    const int t = t0 + i * 64 + wave * 16;
+    if (t + 16 > wg.behind || t < wg.first) clear_outside<FMT, D>(wg.first - t, wg.behind - t, c, st);
+    share_tile<FMT, D>(st, wave, lane, shared, i & 1);
+    if (lane == 0) words[8 + (i & 1) * 4 + wave] = there;
+  };
+
+  bool there = fetch(0);
+  finish_queries<FMT, D, NQ>(a, q, k2, s0);
+  v4f o[NQ][DT], off[NQ][D / 64];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = kLowest;
+    l[n] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[n][d] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) off[n][g] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  __syncthreads();                                             // words were the scan's
+  if (chunks > 0) share(0, there);
+  if (chunks > 1) there = fetch(1);
+  for (int i = 0; i < chunks; ++i) {
+    __syncthreads();                                           // chunk i is there, and the other half is read
+    const int half = i & 1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int t = t0 + i * 64 + x * 32;
+      if (t + 32 <= span.first || t >= span.behind) continue;
+      const bool ok[2] = {__builtin_amdgcn_readfirstlane(words[8 + half * 4 + 2 * x]) != 0,
+                          __builtin_amdgcn_readfirstlane(words[8 + half * 4 + 2 * x + 1]) != 0};
+      float z[NQ][2][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        v4f acc[NQ][NG];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) acc[n][g] = FMT == kFmtINT4 ? s0[n][g] : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 ka = shared.k[half][2 * x + y][j][lane];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            acc[n][FMT == kFmtINT4 ? j / 2 : 0] = mfma16<FMT>(ka, q[n][j], acc[n][FMT == kFmtINT4 ? j / 2 : 0]);
+        }
+        if constexpr (FMT == kFmtINT4) {
+          uint2 sk[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) sk[g] = shared.s[half][2 * x + y][g * 4 + c];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              z[n][y][e] = 0.f;
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                z[n][y][e] = fmaf(acc[n][g][e], f16_value((e < 2 ? sk[g].x : sk[g].y) >> (16 * (e & 1))), z[n][y][e]);
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[n][y][e] = acc[n][0][e];
+        }
+      }
+      if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
+      new_maxima<D, NQ, FMT == kFmtINT4>(z, k2, m, l, o, off);
+      float e[NQ][8];
+      probabilities<FMT, NQ>(z, k2, m, l, e);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint4 p[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) w[y] = e[n][y];
+          if constexpr (FMT == kFmtINT4) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint2 sv = shared.s[half][2 * x + y][(NG + g) * 4 + c];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) w[4 * y + b] *= f16_value((b < 2 ? sv.x : sv.y) >> (16 * (b & 1)));
+            }
+          }
+          if constexpr (FMT == kFmtNVFP4) {
+            p[n] = to_f16(w);
+          } else {
+            uint4 one[1];
+            split_planes<1>(w, one);
+            p[n] = one[0];
+          }
+          if constexpr (FMT == kFmtINT4)
+            off[n][g] = mfma_bf16(make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u), p[n], off[n][g]);
+        }
+#pragma unroll
+        for (int d = 0; d < DT / NG; ++d) {
+          const uint4 va = *reinterpret_cast<const uint4*>(&shared.v[half][x][g * (DT / NG) + d][lane][0]);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) o[n][g * (DT / NG) + d] = mfma16<FMT>(va, p[n], o[n][g * (DT / NG) + d]);
+        }
+      }
+    }
+    if (i + 1 < chunks) {
+      share(i + 1, there);
+      if (i + 2 < chunks) there = fetch(i + 2);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    l[n] = rowgroup_sum(l[n]);
+    const int i = row0 + n * 16 + r;
+    if (i >= rows.rows) continue;
+    const int token = int(unsigned(i) / unsigned(a.group));
+#pragma unroll
+    for (int d = 0; d < DT; d += 4)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = o[n][d + y][e] + (FMT == kFmtINT4 ? off[n][d >> 2][e] : 0.f);
+        kv_store<4>(a, s.row + token, h * a.group + i - token * a.group, D, o_feature<FMT, D>(c, d, e), v,
+                    FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n], l[n]);
+      }
   }
 }
 
@@ -892,7 +1165,7 @@ void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_
   else if (p.rows == 32)
     p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s);
   else
-    attend_whole<FMT, D, 2, 4, 1, 1>(kc, a, p.jobs, s);
+    kv_prompt_kernel<FMT, D><<<dim3(unsigned(p.jobs) * kc.heads), 256, 0, s>>>(kc, a);
 }
 
 }  // namespace
