@@ -436,45 +436,48 @@ __device__ __forceinline__ void mask_scores(float (&z)[NQ][2][4], int t, int c, 
       }
 }
 
-// The running maxima, moved where a score exceeds one by kGrow.
-template <int D, int NQ, bool OFF>
-__device__ __forceinline__ void new_maxima(const float (&z)[NQ][2][4], const float (&k2)[NQ], float (&m)[NQ], float (&l)[NQ],
-                                           v4f (&o)[NQ][D / 16], v4f (&off)[NQ][D / 64]) {
+// Probabilities e of the scores z, relative to the running maxima, which move where a score exceeds one by kGrow; l, O
+// and off with them.  The scores are brought to the exponent first and their largest sought there: what a matrix
+// instruction gives would cost one more operation each on its way into a maximum.
+template <int FMT, int D, int NQ>
+__device__ __forceinline__ void probabilities(const float (&z)[NQ][2][4], const float (&k2)[NQ], float (&m)[NQ],
+                                              float (&l)[NQ], v4f (&o)[NQ][D / 16], v4f (&off)[NQ][D / 64],
+                                              float (&e)[NQ][8]) {
+  constexpr float kUp = FMT == kFmtNVFP4 ? 11.0f : 0.0f;      // powers of two that probabilities are kept larger by
   bool grow = false;
-  float top[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    top[n] = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
-                   fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3]))) * k2[n];
-    grow |= top[n] > m[n] + kGrow;
+    const float base = m[n] - kUp;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
+    grow |= fmaxf(fmaxf(fmaxf(e[n][0], e[n][1]), fmaxf(e[n][2], e[n][3])),
+                  fmaxf(fmaxf(e[n][4], e[n][5]), fmaxf(e[n][6], e[n][7]))) > kGrow + kUp;
   }
-  if (!__any(grow)) return;
+  if (__any(grow)) {
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const float now = fmaxf(m[n], rowgroup_max(top[n]));
-    const float x = __builtin_amdgcn_exp2f(m[n] - now);
-    m[n] = now;
-    l[n] *= x;
+    for (int n = 0; n < NQ; ++n) {
+      const float top = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
+                              fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3])));
+      const float now = fmaxf(m[n], rowgroup_max(top) * k2[n]), x = __builtin_amdgcn_exp2f(m[n] - now);
+      m[n] = now;
+      l[n] *= x;
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) o[n][d] *= x;
-    if constexpr (OFF)
+      for (int d = 0; d < D / 16; ++d) o[n][d] *= x;
+      if constexpr (FMT == kFmtINT4)
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g) off[n][g] *= x;
-  }
-}
-
-template <int FMT, int NQ>
-__device__ __forceinline__ void probabilities(const float (&z)[NQ][2][4], const float (&k2)[NQ], const float (&m)[NQ],
-                                              float (&l)[NQ], float (&e)[NQ][8]) {
+        for (int g = 0; g < D / 64; ++g) off[n][g] *= x;
+      const float base = now - kUp;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const float base2 = FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e[n][i] = __builtin_amdgcn_exp2f(fmaf(z[n][i >> 2][i & 3], k2[n], -base2));
-      l[n] += e[n][i];
+      for (int i = 0; i < 8; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
     }
   }
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[n][i] = __builtin_amdgcn_exp2f(e[n][i]);
+      l[n] += e[n][i];
+    }
 }
 
 // Inclusive sum over the wave's lanes: within rows of 16 by shifts, then the rows' last lanes on to those after.
@@ -723,9 +726,8 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
       }
       __builtin_amdgcn_sched_barrier(0);
       if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
-      new_maxima<D, NQ, FMT == kFmtINT4>(z, k2, m, l, o, off);
       float e[NQ][8];
-      probabilities<FMT, NQ>(z, k2, m, l, e);
+      probabilities<FMT, D, NQ>(z, k2, m, l, o, off, e);
       __builtin_amdgcn_sched_barrier(0);
       add_values<FMT, D, NQ, PL>(st, e, o, off);
     };
@@ -984,9 +986,8 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
         }
       }
       if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
-      new_maxima<D, NQ, FMT == kFmtINT4>(z, k2, m, l, o, off);
       float e[NQ][8];
-      probabilities<FMT, NQ>(z, k2, m, l, e);
+      probabilities<FMT, D, NQ>(z, k2, m, l, o, off, e);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         uint4 p[NQ];
