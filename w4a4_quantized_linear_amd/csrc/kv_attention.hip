@@ -421,14 +421,14 @@ __device__ __forceinline__ void finish_queries(const KvAttn& a, uint4 (&q)[NQ][D
   }
 }
 
-// Scores z[n][tile][token] of tokens t + 16 tile + 4 c + token; those that a row does not see become -infinity.
-template <int NQ>
-__device__ __forceinline__ void mask_scores(float (&z)[NQ][2][4], int t, int c, const bool (&ok)[2], const int (&lo)[NQ],
+// Scores z[n][tile][token] of tokens t + 16 tile + 4 c + token, T tiles; those that a row does not see become -infinity.
+template <int NQ, int T>
+__device__ __forceinline__ void mask_scores(float (&z)[NQ][T][4], int t, int c, const bool (&ok)[T], const int (&lo)[NQ],
                                             const int (&hi)[NQ]) {
 #pragma unroll
   for (int n = 0; n < NQ; ++n)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < T; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int at = t + 16 * i + 4 * c + e;
@@ -436,28 +436,36 @@ __device__ __forceinline__ void mask_scores(float (&z)[NQ][2][4], int t, int c, 
       }
 }
 
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N]) {
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+  return top;
+}
+
 // Probabilities e of the scores z, relative to the running maxima, which move where a score exceeds one by kGrow; l, O
 // and off with them.  The scores are brought to the exponent first and their largest sought there: what a matrix
 // instruction gives would cost one more operation each on its way into a maximum.
-template <int FMT, int D, int NQ>
-__device__ __forceinline__ void probabilities(const float (&z)[NQ][2][4], const float (&k2)[NQ], float (&m)[NQ],
+template <int FMT, int D, int NQ, int T>
+__device__ __forceinline__ void probabilities(const float (&z)[NQ][T][4], const float (&k2)[NQ], float (&m)[NQ],
                                               float (&l)[NQ], v4f (&o)[NQ][D / 16], v4f (&off)[NQ][D / 64],
-                                              float (&e)[NQ][8]) {
+                                              float (&e)[NQ][4 * T]) {
   constexpr float kUp = FMT == kFmtNVFP4 ? 11.0f : 0.0f;      // powers of two that probabilities are kept larger by
   bool grow = false;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float base = m[n] - kUp;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
-    grow |= fmaxf(fmaxf(fmaxf(e[n][0], e[n][1]), fmaxf(e[n][2], e[n][3])),
-                  fmaxf(fmaxf(e[n][4], e[n][5]), fmaxf(e[n][6], e[n][7]))) > kGrow + kUp;
+    for (int i = 0; i < 4 * T; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
+    grow |= largest(e[n]) > kGrow + kUp;
   }
   if (__any(grow)) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const float top = fmaxf(fmaxf(fmaxf(z[n][0][0], z[n][0][1]), fmaxf(z[n][0][2], z[n][0][3])),
-                              fmaxf(fmaxf(z[n][1][0], z[n][1][1]), fmaxf(z[n][1][2], z[n][1][3])));
+      float top = z[n][0][0];
+#pragma unroll
+      for (int i = 1; i < 4 * T; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
       const float now = fmaxf(m[n], rowgroup_max(top) * k2[n]), x = __builtin_amdgcn_exp2f(m[n] - now);
       m[n] = now;
       l[n] *= x;
@@ -468,13 +476,13 @@ __device__ __forceinline__ void probabilities(const float (&z)[NQ][2][4], const 
         for (int g = 0; g < D / 64; ++g) off[n][g] *= x;
       const float base = now - kUp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
+      for (int i = 0; i < 4 * T; ++i) e[n][i] = fmaf(z[n][i >> 2][i & 3], k2[n], -base);
     }
   }
 #pragma unroll
   for (int n = 0; n < NQ; ++n)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4 * T; ++i) {
       e[n][i] = __builtin_amdgcn_exp2f(e[n][i]);
       l[n] += e[n][i];
     }
@@ -725,9 +733,9 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
+      if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ, 2>(z, t, c, ok, lo, hi);
       float e[NQ][8];
-      probabilities<FMT, D, NQ>(z, k2, m, l, o, off, e);
+      probabilities<FMT, D, NQ, 2>(z, k2, m, l, o, off, e);
       __builtin_amdgcn_sched_barrier(0);
       add_values<FMT, D, NQ, PL>(st, e, o, off);
     };
@@ -943,16 +951,14 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
   if (chunks > 1) there = fetch(1);
   for (int i = 0; i < chunks; ++i) {
     __syncthreads();                                           // chunk i is there, and the other half is read
-    const int half = i & 1;
+    const int half = i & 1, t = t0 + i * 64;
+    if (t + 64 > span.first && t < span.behind) {
+      bool ok[4];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = t0 + i * 64 + x * 32;
-      if (t + 32 <= span.first || t >= span.behind) continue;
-      const bool ok[2] = {__builtin_amdgcn_readfirstlane(words[8 + half * 4 + 2 * x]) != 0,
-                          __builtin_amdgcn_readfirstlane(words[8 + half * 4 + 2 * x + 1]) != 0};
-      float z[NQ][2][4];
+      for (int y = 0; y < 4; ++y) ok[y] = uni(words[8 + half * 4 + y]) != 0;
+      float z[NQ][4][4];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < 4; ++y) {
         v4f acc[NQ][NG];
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -960,7 +966,7 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
           for (int g = 0; g < NG; ++g) acc[n][g] = FMT == kFmtINT4 ? s0[n][g] : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint4 ka = shared.k[half][2 * x + y][j][lane];
+          const uint4 ka = shared.k[half][y][j][lane];
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
             acc[n][FMT == kFmtINT4 ? j / 2 : 0] = mfma16<FMT>(ka, q[n][j], acc[n][FMT == kFmtINT4 ? j / 2 : 0]);
@@ -968,7 +974,7 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
         if constexpr (FMT == kFmtINT4) {
           uint2 sk[NG];
 #pragma unroll
-          for (int g = 0; g < NG; ++g) sk[g] = shared.s[half][2 * x + y][g * 4 + c];
+          for (int g = 0; g < NG; ++g) sk[g] = shared.s[half][y][g * 4 + c];
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -985,42 +991,45 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
             for (int e = 0; e < 4; ++e) z[n][y][e] = acc[n][0][e];
         }
       }
-      if (!(t + 32 <= span.behind_least && t >= span.first_most && ok[0] && ok[1])) mask_scores<NQ>(z, t, c, ok, lo, hi);
-      float e[NQ][8];
-      probabilities<FMT, D, NQ>(z, k2, m, l, o, off, e);
+      if (!(t + 64 <= span.behind_least && t >= span.first_most && ok[0] && ok[1] && ok[2] && ok[3]))
+        mask_scores<NQ, 4>(z, t, c, ok, lo, hi);
+      float e[NQ][16];
+      probabilities<FMT, D, NQ, 4>(z, k2, m, l, o, off, e);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint4 p[NQ];
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float w[8];
+        for (int g = 0; g < NG; ++g) {
+          uint4 p[NQ];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) w[y] = e[n][y];
-          if constexpr (FMT == kFmtINT4) {
+          for (int n = 0; n < NQ; ++n) {
+            float w[8];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint2 sv = shared.s[half][2 * x + y][(NG + g) * 4 + c];
+            for (int y = 0; y < 8; ++y) w[y] = e[n][8 * x + y];
+            if constexpr (FMT == kFmtINT4) {
 #pragma unroll
-              for (int b = 0; b < 4; ++b) w[4 * y + b] *= f16_value((b < 2 ? sv.x : sv.y) >> (16 * (b & 1)));
+              for (int y = 0; y < 2; ++y) {
+                const uint2 sv = shared.s[half][2 * x + y][(NG + g) * 4 + c];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) w[4 * y + b] *= f16_value((b < 2 ? sv.x : sv.y) >> (16 * (b & 1)));
+              }
             }
+            if constexpr (FMT == kFmtNVFP4) {
+              p[n] = to_f16(w);
+            } else {
+              uint4 one[1];
+              split_planes<1>(w, one);
+              p[n] = one[0];
+            }
+            if constexpr (FMT == kFmtINT4)
+              off[n][g] = mfma_bf16(make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u), p[n], off[n][g]);
           }
-          if constexpr (FMT == kFmtNVFP4) {
-            p[n] = to_f16(w);
-          } else {
-            uint4 one[1];
-            split_planes<1>(w, one);
-            p[n] = one[0];
+#pragma unroll
+          for (int d = 0; d < DT / NG; ++d) {
+            const uint4 va = *reinterpret_cast<const uint4*>(&shared.v[half][x][g * (DT / NG) + d][lane][0]);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) o[n][g * (DT / NG) + d] = mfma16<FMT>(va, p[n], o[n][g * (DT / NG) + d]);
           }
-          if constexpr (FMT == kFmtINT4)
-            off[n][g] = mfma_bf16(make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u), p[n], off[n][g]);
         }
-#pragma unroll
-        for (int d = 0; d < DT / NG; ++d) {
-          const uint4 va = *reinterpret_cast<const uint4*>(&shared.v[half][x][g * (DT / NG) + d][lane][0]);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][g * (DT / NG) + d] = mfma16<FMT>(va, p[n], o[n][g * (DT / NG) + d]);
-        }
-      }
     }
     if (i + 1 < chunks) {
       share(i + 1, there);
