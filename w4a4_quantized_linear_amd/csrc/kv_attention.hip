@@ -505,12 +505,17 @@ __device__ __forceinline__ int wave_scan(int v) {
 struct KvFound {
   int b, before;
 };
+constexpr int kLeastUnits = 2;           // of a range
+constexpr int kShortUnits = 8;           // of a range, up to which a range is part of one job
+
 template <int R, int U, bool SPLIT, int NT>
 struct KvScan {
   const KvCache& kc;
   const KvAttn& a;
   int* sh;                                     // 16 words of LDS
   int v = 0, end = 0, total = 0;
+  int per = 1;                                 // units of a range
+  bool short_ranges = false;                   // a range is part of one job; then v and end count ranges
 
   __device__ __forceinline__ KvSeq seq(int b) const {
     int len, row, rows;
@@ -549,7 +554,32 @@ struct KvScan {
     for (int base = 0; base < kc.batch; base += NT) end = chunk(base, total);
     return total = __builtin_amdgcn_readfirstlane(total);
   }
-  // Units before sequence b.
+  // Cuts the units into ranges.  Evenly, so that a range may end one job and begin others; but where ranges are
+  // short, what a second job costs (its rows, pages and first tokens one after the other, some 5 us) is more than an
+  // uneven cut: then a job is cut into as many ranges as it has `per` units, if all of them are no more than the
+  // workgroups there are (16 sequences of 400 .. 4000 tokens, 8 heads: 17.0 us evenly).
+  __device__ __forceinline__ void cut(int ranges) {
+    per = max((total + ranges - 1) / ranges, kLeastUnits);
+    if (kc.batch > 64 || per > kShortUnits) return;
+    const int b = threadIdx.x & 63;
+    int tiles = 0, units = 1;
+    if (b < kc.batch) {
+      const KvSeq s = seq(b);
+      tiles = s.tiles;
+      units = s.units;
+    }
+    for (int p = per; p <= 2 * per; ++p) {
+      const int n = tiles * ((units + p - 1) / p), sum = wave_scan(n);
+      if (__builtin_amdgcn_readlane(sum, 63) <= ranges) {
+        v = n;
+        end = sum;
+        per = p;
+        short_ranges = true;
+        return;
+      }
+    }
+  }
+  // Units (short ranges: ranges) before sequence b.
   __device__ __forceinline__ int before(int b) {
     if (kc.batch <= 64) return __builtin_amdgcn_readlane(end - v, b);
     int sum = 0;
@@ -584,12 +614,6 @@ struct KvScan {
   }
 };
 
-// Units that a range takes: the total over the ranges, and no fewer than `least`.
-__device__ __forceinline__ int units_a_range(int total, int ranges, int least) {
-  return max((total + ranges - 1) / ranges, least);
-}
-constexpr int kLeastUnits = 2;
-
 template <int FMT, int D, int NQ, int WQ, int WK, int PLANES, bool SPLIT>
 __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
   using TL = KvTiles<NQ, WQ, WK>;
@@ -605,15 +629,25 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
 
   KvScan<R, U, SPLIT, NT> scan{kc, a, sh};
   const int total = scan.count();
-  const int per = SPLIT ? units_a_range(total, a.ranges, kLeastUnits) : 1;
-  const int64_t first64 = int64_t(range) * per;
-  if (first64 >= total) return;
+  if constexpr (SPLIT) scan.cut(a.ranges);
+  const int per = SPLIT ? scan.per : 1;
+  const int64_t first64 = scan.short_ranges ? range : int64_t(range) * per;
+  if (!scan.short_ranges && first64 >= total) return;
   const int first = int(first64);
   const KvFound f = scan.find(first);
   int left = min(per, total - first), b = f.b;
   if (b < 0) return;
   KvSeq s = kv_seq_of<R, U, SPLIT>(kc, a, b);
-  int job = (first - f.before) / s.units, unit = (first - f.before) % s.units;
+  int job, unit;
+  if (scan.short_ranges) {
+    const int each = (s.units + per - 1) / per;               // ranges of a job
+    job = (first - f.before) / each;
+    unit = ((first - f.before) % each) * per;
+    left = min(per, s.units - unit);
+  } else {
+    job = (first - f.before) / s.units;
+    unit = (first - f.before) % s.units;
+  }
 
   while (left > 0) {
     while (job >= s.tiles) {                                  // the next sequence with rows
@@ -1069,7 +1103,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   const int h = blockIdx.x % kc.heads, index = blockIdx.x / kc.heads;
   KvScan<R, U, true, 256> scan{kc, a, sh};
   const int total = scan.count();
-  const int per = units_a_range(total, a.ranges, kLeastUnits);
+  scan.cut(a.ranges);
+  const int per = scan.per;
   int b, job, start;
   KvSeq s;
   if constexpr (HOW == kByJob) {
@@ -1079,7 +1114,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
     b = __builtin_ctzll(in);
     job = index - __builtin_amdgcn_readlane(sum - tiles, b);
     s = kv_seq_of<R, U, true>(kc, a, b);
-    start = scan.before(b) + job * s.units;
+    start = scan.before(b);
+    if (!scan.short_ranges) start += job * s.units;
   } else if constexpr (HOW == kBySeq) {
     b = index;
     job = 0;
@@ -1096,7 +1132,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
     start = f.before + job * s.units;
     if (start == at || start < at - per) return;
   }
-  const int first = start / per, last = (start + s.units - 1) / per;     // ranges that hold parts
+  int first = start / per, last = (start + s.units - 1) / per;          // ranges that hold parts
+  if (scan.short_ranges) {
+    const int each = (s.units + per - 1) / per;
+    first = start + job * each;
+    last = first + each - 1;
+  }
   if (first == last) return;
   const int d = threadIdx.x % TPR * F, slot = threadIdx.x / TPR;
   const int rows = min(s.rows * a.group - job * R, R);
