@@ -513,7 +513,7 @@ struct KvScan {
   const KvCache& kc;
   const KvAttn& a;
   int* sh;                                     // 16 words of LDS
-  int v = 0, end = 0, total = 0;
+  int v = 0, end = 0, total = 0, tiles = 0, units = 1;
   int per = 1;                                 // units of a range
   bool short_ranges = false;                   // a range is part of one job; then v and end count ranges
 
@@ -522,7 +522,6 @@ struct KvScan {
     kc.sequence(b, len, row, rows);
     return kv_seq<R, U, SPLIT>(kc, a, len, row, rows);
   }
-  __device__ __forceinline__ int tiles_of(int b) const { return b < kc.batch ? seq(b).tiles : 0; }
   __device__ __forceinline__ int units_of(int b) const {
     if (b >= kc.batch) return 0;
     const KvSeq s = seq(b);
@@ -547,7 +546,13 @@ struct KvScan {
   }
   __device__ __forceinline__ int count() {
     if (kc.batch <= 64) {
-      v = units_of(threadIdx.x & 63);
+      const int b = threadIdx.x & 63;
+      if (b < kc.batch) {
+        const KvSeq s = seq(b);
+        tiles = s.tiles;
+        units = s.units;
+      }
+      v = tiles * units;
       end = wave_scan(v);
       return total = __builtin_amdgcn_readlane(end, 63);
     }
@@ -560,16 +565,9 @@ struct KvScan {
   // workgroups there are (16 sequences of 400 .. 4000 tokens, 8 heads: 17.0 us evenly).
   __device__ __forceinline__ void cut(int ranges) {
     per = max((total + ranges - 1) / ranges, kLeastUnits);
-    if (kc.batch > 64 || per > kShortUnits) return;
-    const int b = threadIdx.x & 63;
-    int tiles = 0, units = 1;
-    if (b < kc.batch) {
-      const KvSeq s = seq(b);
-      tiles = s.tiles;
-      units = s.units;
-    }
+    if (kc.batch == 1 || kc.batch > 64 || per > kShortUnits) return;
     for (int p = per; p <= 2 * per; ++p) {
-      const int n = tiles * ((units + p - 1) / p), sum = wave_scan(n);
+      const int n = tiles * int(unsigned(units + p - 1) / unsigned(p)), sum = wave_scan(n);
       if (__builtin_amdgcn_readlane(sum, 63) <= ranges) {
         v = n;
         end = sum;
@@ -1108,11 +1106,11 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   int b, job, start;
   KvSeq s;
   if constexpr (HOW == kByJob) {
-    const int tiles = scan.tiles_of(int(threadIdx.x) & 63), sum = wave_scan(tiles);
+    const int sum = wave_scan(scan.tiles);
     const uint64_t in = __ballot(index < sum);
     if (in == 0) return;
     b = __builtin_ctzll(in);
-    job = index - __builtin_amdgcn_readlane(sum - tiles, b);
+    job = index - __builtin_amdgcn_readlane(sum - scan.tiles, b);
     s = kv_seq_of<R, U, true>(kc, a, b);
     start = scan.before(b);
     if (!scan.short_ranges) start += job * s.units;
