@@ -412,12 +412,15 @@ svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32
  *   start    device, int32[batch], or NULL: 0
  *   keep     device, int32, batch x most, row stride ldkeep: rising, and so keep[i] >= start + i in place
  *   n_keep   device, int32[batch], at most `most` (more counts as `most`, less than 0 as 0)
+ *   workspace  device, svdq_kv_compact_bytes(d, planes, batch, most, to == NULL) bytes, 256-byte aligned (NULL
+ *            where that is 0: apart, for few tokens, or with sequences, heads and layers enough)
  * An index without a place, old or new, moves nothing.  In place, keep that does not rise, and pages that
- * several sequences share, give unspecified tokens in the sequence's own places (nothing else). */
+ * several sequences share, give unspecified tokens in the sequences' own places (nothing else). */
+size_t svdq_kv_compact_bytes(const svdq_kv_desc* d, int32_t planes, int32_t batch, int32_t most, int32_t in_place);
 svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
                             const int32_t* table, int64_t ldt, int32_t cols, const int32_t* to, int64_t ldto,
                             int32_t cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep, int32_t most,
-                            const int32_t* n_keep, int32_t batch, void* stream);
+                            const int32_t* n_keep, int32_t batch, void* workspace, size_t ws_bytes, void* stream);
 
 /* Both launches; workspace >= svdq_act_bytes(d, M) bytes (device, 256-aligned). */
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X,

@@ -143,7 +143,7 @@ def test_compact_validation(L, forced_device_error):
     per = L.svdq_kv_page_bytes(D())
     # d, pool, pages, planes, plane_bytes, table, ldt, cols, to, ldto, cols_to, start, keep, ldkeep, most, n_keep, batch,
     # stream
-    call = caller(L.svdq_kv_compact, [D(), P, 100, 2, 100 * per, P, 8, 8, P + 256, 6, 6, P, P, 50, 50, P, 5, None])
+    call = caller(L.svdq_kv_compact, [D(), P, 100, 2, 100 * per, P, 8, 8, P + 256, 6, 6, P, P, 50, 50, P, 5, None, 0, None])
     assert call() == 6 and call(_8=None, _9=0, _10=0) == 6 and call(_11=None) == 6 and call(_14=0, _12=None) == 6
     assert call(_16=0, _5=None, _15=None, _12=None) == 6
     for i in (0, 1, 5, 12, 15):
@@ -152,6 +152,14 @@ def test_compact_validation(L, forced_device_error):
             dict(_2=0), dict(_3=0), dict(_4=100 * per - 64), dict(_6=7), dict(_7=0), dict(_9=5), dict(_10=0),
             dict(_13=49), dict(_14=-1), dict(_16=-1), dict(_16=16385)]:
         assert call(**bad) == 2, bad
+    n = L.svdq_kv_compact_bytes(D(), 2, 5, 5000, 1)
+    assert n >= 5 * 5000 * 2 * 4 * 2 * 68 and n % 256 == 0 and L.svdq_kv_compact_bytes(D(), 2, 5, 5000, 0) == 0
+    assert L.svdq_kv_compact_bytes(D(), 2, 5, 64, 1) == 0 and L.svdq_kv_compact_bytes(D(), 100, 5, 5000, 1) == 0
+    for bad in ((None, 2, 5, 500, 1), (D(fmt=0), 2, 5, 500, 1), (D(), 0, 5, 500, 1), (D(), 2, 0, 500, 1), (D(), 2, 5, 0, 1)):
+        assert L.svdq_kv_compact_bytes(*bad) == 0
+    long = dict(_8=None, _9=0, _10=0, _13=5000, _14=5000)
+    assert call(**long) == 1 and call(**long, _17=P) == 5 and call(**long, _17=P, _18=n - 1) == 5
+    assert call(**long, _17=P, _18=n) == 6 and call(**long, _17=P + 64, _18=n) == 4 and call(**{**long, "_8": P, "_9": 8, "_10": 8}, _17=P, _18=0) == 5
     assert call(_0=D(fmt=0)) == 3
     for bad in (dict(_1=P + 16), dict(_4=100 * per + 32), dict(_5=P + 2), dict(_8=P + 2), dict(_11=P + 2), dict(_12=P + 2),
                 dict(_15=P + 2)):

@@ -114,10 +114,24 @@ def test_compact_bounds(td, fmt):
     assert torch.equal(c.pool, before)
     sq.kv_compact(kv, c.pool, c.table, i32([[5, 9]], dev, torch), i32([2], dev, torch), start=i32([200], dev, torch))
     assert torch.equal(c.pool, before)                                 # new places behind the table
+    few = Cache(torch, dev, kv, [40, 90, 500], 14)                     # a wave's tiles, in two layers
+    pool, keep = torch.stack([few.pool, few.pool]), np.array([[3, 5, 6] + [9] * 47, np.r_[20:70], np.r_[7:400:8]])
+    sq.kv_compact(kv, pool, few.table, i32(keep, dev, torch), i32([3, 50, 50], dev, torch), start=i32([2, 15, 0], dev, torch))
+    for layer in range(2):
+        k, _ = sq.kv_read(kv, pool[layer], few.table, i32([40, 90, 500], dev, torch), 630, cu=i32([0, 40, 130, 630], dev, torch), f32=True)
+        want = few.kh[:, 0].astype(np.float32).copy()
+        want[2:5], want[40 + 15:40 + 65], want[130:180] = few.kh[keep[0, :3], 0], few.kh[40 + keep[1], 0], few.kh[130 + keep[2], 0]
+        assert np.array_equal(k.cpu().numpy(), want)
     lens = [5000]
     c = Cache(torch, dev, kv, lens, 13)
+    n = sq.kv_compact_bytes(kv, 1, 1, 3333)
+    space = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=dev)
     keep = np.sort(c.rng.choice(5000, 3333, replace=False))
+    other = c.pool.clone()
+    sq.kv_compact(kv, other, c.table, i32(keep[None], dev, torch), i32([3333], dev, torch), workspace=space[256:256 + n])
+    assert n > 0 and int((space[:256] != 0xA5).sum()) == 0 and int((space[256 + n:] != 0xA5).sum()) == 0
     sq.kv_compact(kv, c.pool, c.table, i32(keep[None], dev, torch), i32([3333], dev, torch))
+    assert torch.equal(other, c.pool)
     k, v = sq.kv_read(kv, c.pool, c.table, i32([3333], dev, torch), 3333, cu=i32([0, 3333], dev, torch), f32=True)
     assert np.array_equal(k.cpu().numpy(), c.kh[keep, 0].astype(np.float32))
     assert np.array_equal(v.cpu().numpy(), c.vh[keep, 0].astype(np.float32))
@@ -251,3 +265,34 @@ def test_graph_follows_lengths(td):
     other = sq.kv_attention(kv, eager, table, lens, row[:, :1024], stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(other, sq.kv_attention(kv, eager, table, lens, row[:, :1024]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_compact_walks(td, fmt):
+    """In place with workgroups enough to walk: 40 sequences, 2 heads, 7 layers; the workspace form (fewer layers) on the
+    same tokens gives the same bytes; and the tokens are numpy's."""
+    torch, dev = td
+    kv = sq.KvLayout(fmt, 2, 64, 32)
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(1, 400, 40)]
+    c = Cache(torch, dev, kv, lens, 15)
+    start = np.array([int(rng.integers(0, n)) for n in lens])
+    kept = [np.sort(rng.choice(np.arange(s, n), int(rng.integers(0, n - s + 1)), replace=False)) for s, n in zip(start, lens)]
+    keep = np.zeros((40, 400), int)
+    for b, k in enumerate(kept):
+        keep[b, :len(k)] = k
+    args = (c.table, i32(keep, dev, torch), i32([len(k) for k in kept], dev, torch))
+    many = torch.stack([c.pool] * 7)
+    assert sq.kv_compact_bytes(kv, 7, 40, 400) == 0 and sq.kv_compact_bytes(kv, 1, 40, 400) > 0
+    sq.kv_compact(kv, many, *args, start=i32(start, dev, torch))
+    one = c.pool.clone()
+    sq.kv_compact(kv, one, *args, start=i32(start, dev, torch))
+    for layer in many:
+        assert torch.equal(layer, one)
+    M = sum(lens)
+    k, v = sq.kv_read(kv, one, c.table, i32(lens, dev, torch), M, cu=i32(c.cu, dev, torch), f32=True)
+    for got, held in ((k, c.kh), (v, c.vh)):
+        want = held.reshape(M, -1).astype(np.float32).copy()
+        for b, kk in enumerate(kept):
+            want[c.cu[b] + start[b]:c.cu[b] + start[b] + len(kk)] = held.reshape(M, -1)[c.cu[b] + kk]
+        assert np.array_equal(got.cpu().numpy(), want)

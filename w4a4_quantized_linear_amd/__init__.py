@@ -601,12 +601,17 @@ def kv_copy(kv: KvLayout, pool, src, dst, stream=None):
     return pool
 
 
-def kv_compact(kv: KvLayout, pool, table, keep, n_keep, start=None, to=None, stream=None):
+def kv_compact_bytes(kv: KvLayout, planes: int, batch: int, most: int, in_place: bool = True) -> int:
+    """Workspace bytes of kv_compact for lists of `most` tokens (0: none needed, or invalid)."""
+    return int(lib().svdq_kv_compact_bytes(_kept_kv(kv)[0], int(planes), int(batch), int(most), int(in_place)))
+
+
+def kv_compact(kv: KvLayout, pool, table, keep, n_keep, start=None, to=None, workspace=None, stream=None):
     """Token start[b] + i of sequence b becomes its old token keep[b, i], i < n_keep[b], in every layer of the pool:
     in place (keep rises), or from table's pages into those of `to`; returns the pool."""
     torch, dev = _torch(), pool.device
     if not _here(dev, stream):
-        return _elsewhere(dev, stream, lambda: kv_compact(kv, pool, table, keep, n_keep, start, to))
+        return _elsewhere(dev, stream, lambda: kv_compact(kv, pool, table, keep, n_keep, start, to, workspace))
     p, nbytes = _kept_kv(kv)
     _pool(pool, nbytes, 3)
     batch = n_keep.shape[0] if n_keep.dim() == 1 else -1
@@ -615,12 +620,14 @@ def kv_compact(kv: KvLayout, pool, table, keep, n_keep, start=None, to=None, str
     ldto = 0 if to is None else _int_rows(to, "to", batch, dev)
     if start is not None:
         _flat(start, "start", (batch,), dev, torch.int32)
-    pages = pool.shape[-2]
-    st = lib().svdq_kv_compact(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes,
-                               table.data_ptr(), ldt, table.shape[1], None if to is None else to.data_ptr(), ldto,
-                               0 if to is None else to.shape[1], None if start is None else start.data_ptr(),
-                               keep.data_ptr(), ldk, keep.shape[1], n_keep.data_ptr(), batch,
-                               torch._C._cuda_getCurrentRawStream(dev.index))
+    pages, planes, most = pool.shape[-2], pool.shape[0] if pool.dim() == 3 else 1, keep.shape[1]
+    pt, pto = table.data_ptr(), None if to is None else to.data_ptr()
+    L = lib()
+    ws = _space(workspace, L.svdq_kv_compact_bytes(p, planes, batch, most, pto is None or pto == pt), dev)
+    st = L.svdq_kv_compact(p, pool.data_ptr(), pages, planes, pages * nbytes, pt, ldt, table.shape[1], pto, ldto,
+                           0 if to is None else to.shape[1], None if start is None else start.data_ptr(),
+                           keep.data_ptr(), ldk, most, n_keep.data_ptr(), batch, None if ws is None else ws.data_ptr(),
+                           0 if ws is None else ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
         check("svdq_kv_compact", st)
     return pool

@@ -56,7 +56,8 @@ SIGNATURES = {
                                                   _P]),
     "svdq_kv_copy": (ctypes.c_int, [_D, _P, _I64, _I32, _I64, _P, _P, _I64, _P]),
     "svdq_kv_compact": (ctypes.c_int, [_D, _P, _I64, _I32, _I64, _P, _I64, _I32, _P, _I64, _I32, _P, _P, _I64, _I32, _P,
-                                       _I32, _P]),
+                                       _I32, _P, ctypes.c_size_t, _P]),
+    "svdq_kv_compact_bytes": (ctypes.c_size_t, [_D, _I32, _I32, _I32, _I32]),
     "svdq_linear": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P, ctypes.c_size_t, _P]),
     "svdq_linear_noalloc": (ctypes.c_int, [_D, _P, _P, _I64, _I64, _P, _I64, ctypes.c_uint32, _P]),
     "svdq_unpack_weight": (ctypes.c_int, [_D, _P, _P, _P, _P, _P, _P, _P, _P]),

@@ -57,7 +57,7 @@ hipError_t launch_kv_copy(uint8_t* pool, int planes, int64_t plane_bytes, int64_
                           const int32_t* dst, int64_t n, hipStream_t s);
 hipError_t launch_kv_compact(int fmt, int D, const KvCache& kc, int planes, int64_t plane_bytes, const int32_t* to,
                              int64_t ldto, int cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep,
-                             const int32_t* n_keep, int most, bool in_place, hipStream_t s);
+                             const int32_t* n_keep, int most, bool in_place, void* space, hipStream_t s);
 hipError_t launch_unpack_weight(int fmt, int K, int N, int rank, const WeightLayout& wl, const uint8_t* blob,
                                 uint8_t* codes, void* scales, uint16_t* L1, uint16_t* L2, float* lam, uint16_t* bias,
                                 hipStream_t s);
@@ -580,27 +580,38 @@ svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32
                                  static_cast<hipStream_t>(stream)));
 }
 
+size_t svdq_kv_compact_bytes(const svdq_kv_desc* d, int32_t planes, int32_t batch, int32_t most, int32_t in_place) {
+  if (!d || check_kv(d) != SVDQ_OK || planes < 1 || planes > kKvMaxPlanes || batch < 1 || batch > kKvMaxBatch ||
+      most < 1 || most > kKvMaxTokens || in_place == 0)
+    return 0;
+  const int64_t slab = kv_compact_slab(d->fmt, d->head_dim, batch, int64_t(planes) * d->heads, most);
+  return align256(size_t(slab) * batch * kv_compact_tiles(most) * kv_tile_bytes(d->fmt, d->head_dim));
+}
+
 svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
                             const int32_t* table, int64_t ldt, int32_t cols, const int32_t* to, int64_t ldto,
                             int32_t cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep, int32_t most,
-                            const int32_t* n_keep, int32_t batch, void* stream) {
-  if (!d || !pool || (batch > 0 && (!table || !n_keep || (most > 0 && !keep)))) return SVDQ_ERR_NULL;
+                            const int32_t* n_keep, int32_t batch, void* workspace, size_t ws_bytes, void* stream) {
+  const bool in_place = to == nullptr || to == table;
+  const size_t need = svdq_kv_compact_bytes(d, planes, batch, most, in_place);
+  if (!d || !pool || (batch > 0 && (!table || !n_keep || (most > 0 && !keep))) || (need > 0 && !workspace))
+    return SVDQ_ERR_NULL;
   KvCache kc;
   svdq_status s = check_cache(d, pool, pages, table, ldt, cols, n_keep, nullptr, batch, batch, &kc);
   if (s == SVDQ_ERR_SHAPE || planes < 1 || planes > kKvMaxPlanes || most < 0 || most > kKvMaxTokens || ldkeep < most ||
       (to && (cols_to < 1 || ldto < cols_to || int64_t(cols_to) * d->page > kKvMaxTokens)))
     return SVDQ_ERR_SHAPE;
   if (s == SVDQ_ERR_FORMAT) return s;
-  if (planes > 1 && plane_bytes < pages * kc.page_bytes) return SVDQ_ERR_SHAPE;
+  if (planes > 1 && plane_bytes < pages * kv_page_bytes(d)) return SVDQ_ERR_SHAPE;
   if (s != SVDQ_OK || (planes > 1 && plane_bytes % 64 != 0) || !aligned(to, 4) || !aligned(start, 4) ||
-      !aligned(keep, 4))
+      !aligned(keep, 4) || !aligned(workspace, 256))
     return SVDQ_ERR_ALIGN;
+  if (ws_bytes < need) return SVDQ_ERR_WORKSPACE;
   if ((s = device_check()) != SVDQ_OK) return s;
   if (batch == 0 || most == 0) return SVDQ_OK;
-  const bool in_place = to == nullptr || to == table;
   return launched(launch_kv_compact(d->fmt, d->head_dim, kc, planes, plane_bytes, in_place ? table : to,
                                     in_place ? ldt : ldto, in_place ? cols : cols_to, start, keep, ldkeep, n_keep,
-                                    most, in_place, static_cast<hipStream_t>(stream)));
+                                    most, in_place, workspace, static_cast<hipStream_t>(stream)));
 }
 
 svdq_status svdq_linear(const svdq_layer_desc* d, const void* w_packed, const uint16_t* X, int64_t M, int64_t ldx,

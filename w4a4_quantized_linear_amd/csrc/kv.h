@@ -37,6 +37,22 @@ __host__ __device__ constexpr int kv_group(int fmt) { return fmt == kFmtMXFP4 ? 
 __host__ __device__ constexpr int kv_scales(int fmt, int D) { return D / kv_group(fmt) * (fmt == kFmtINT4 ? 2 : 1); }
 __host__ __device__ constexpr int kv_tile_bytes(int fmt, int D) { return kKvTile * (D + 2 * kv_scales(fmt, D)); }
 
+// svdq_kv_compact in place.  Up to kKvCompactFew tokens a wave walks a sequence's tiles.  More are walked by a workgroup
+// where the batch's heads and layers are workgroups enough or the walk is short, else they go through a workspace, `slab`
+// heads at a time (0: none).  Half of L tokens kept, 8 heads of 128 in 4 layers, NVFP4, walk / workspace (us):
+//   128 walks (4 sequences) L 500 13.1 / 20.3, L 5000 91.0 / 46.3    32 walks L 20000 341 / 47.6    1 walk L 100000 1702 / 19.2
+//   256 walks L 500 12.4 / 22.6, L 5000 93.4 / 91.2                  512 walks L 5000 143 / 180
+constexpr int kKvCompactFew = 64;
+constexpr int kKvCompactShort = 384;
+constexpr int64_t kKvCompactWalks = 256;
+constexpr int64_t kKvCompactSpace = int64_t(64) << 20;     // bytes, unless one head's tokens are more
+inline int64_t kv_compact_tiles(int64_t most) { return most / 16 + 2; }
+inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most) {
+  if (most <= kKvCompactShort || batch * all >= kKvCompactWalks) return 0;
+  const int64_t slab = kKvCompactSpace / (batch * kv_compact_tiles(most) * kv_tile_bytes(fmt, D));
+  return int(slab < 1 ? 1 : slab < all ? slab : all);
+}
+
 // How a call of svdq_kv_attention is cut: `rows` query rows of a K/V head (a sequence's tokens x the heads that share
 // it) a workgroup, `jobs` such tiles at most; split: `ranges` workgroups a head share the units of all jobs.
 //

@@ -363,7 +363,9 @@ struct KvCompact {
   const int32_t* keep;
   const int32_t* n_keep;
   int64_t ldto, ldkeep, plane_bytes;
-  int32_t cols_to, most, planes, parts;
+  int32_t cols_to, most, parts;
+  uint8_t* space;                  // of kThrough and kBack: tiles of the heads x0 .. x1 - 1 (of all layers), batch x tiles each
+  int32_t x0, x1, tiles;
 };
 
 // What a wave moves of one tile: lane (token lane / 4, quarter lane % 4) of K, lane (4 tokens lane / 16, piece lane % 16)
@@ -380,7 +382,7 @@ struct KvMoved {
 // index, page, bytes) cost as much as the bytes: 18000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) took 72 us.  In place a
 // workgroup walks a sequence's tiles in order, four at a time, all loads of a head before its stores: the tokens that
 // are kept come in rising order, so those of later tiles lie behind every place written so far.
-enum { kApart = 0, kInPlace = 1, kInPlaceByWave = 2 };
+enum { kApart = 0, kInPlace = 1, kInPlaceByWave = 2, kThrough = 3, kBack = 4 };
 template <int FMT, int D, int HOW>
 __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a) {
   using Moved = KvMoved<FMT, D>;
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
   const int n = min(max(a.n_keep[b], 0), a.most);
   if (n == 0) return;
   const int64_t end = int64_t(start) + n;
-  const int mask = (1 << kc.page_shift) - 1, all = a.planes * kc.heads;
+  const int mask = (1 << kc.page_shift) - 1, all = a.x1;
   for (int64_t at = int64_t(start / 16) + blockIdx.y * TILES; at * 16 < end; at += gridDim.y * TILES) {
     const int64_t tile = at + (TILES == 1 ? 0 : wave);
     // Token lane % 16 of the tile: where it comes from, as a tile's offset in the pool and a place in it.
@@ -413,6 +415,14 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
       if (p >= 0 && p < kc.pages) to = int64_t(p) * kc.page_bytes + (tile & mask) * TB;
     }
     if (to < 0) from = -1;
+    const int64_t spare = (int64_t(b) * a.tiles + (tile - start / 16)) * TB;
+    if constexpr (HOW == kThrough) to = spare;
+    if constexpr (HOW == kBack) {
+      if (from >= 0) from = spare;
+      place = lane & 15;
+    }
+    auto pool_of = [&](int x) { return kc.pool + (x / kc.heads) * a.plane_bytes + (x % kc.heads) * head_bytes; };
+    auto space_of = [&](int x) { return a.space + int64_t(x - a.x0) * (int64_t(a.tiles) * TB) * (gridDim.x / a.parts); };
     // Offsets of the lane's pieces; -1: not moved.
     const int kt = lane >> 2;
     const int64_t kf = __shfl(from, kt);
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
     }
     auto load = [&](int x, Moved& m) {
       if (x >= all) return;
-      const uint8_t* base = kc.pool + (x / kc.heads) * a.plane_bytes + (x % kc.heads) * head_bytes;
+      const uint8_t* base = HOW == kBack ? space_of(x) : pool_of(x);
       if (kf >= 0) {
         const uint32_t* s = reinterpret_cast<const uint32_t*>(base + kf + kp);
 #pragma unroll
@@ -450,7 +460,7 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
       }
     };
     auto store = [&](int x, const Moved& m) {
-      uint8_t* base = kc.pool + (x / kc.heads) * a.plane_bytes + (x % kc.heads) * head_bytes + to;
+      uint8_t* base = (HOW == kThrough ? space_of(x) : pool_of(x)) + to;
       if (kf >= 0) {
         uint32_t* d = reinterpret_cast<uint32_t*>(base + kt * (D / 2) + (lane & 3) * (D / 8));
 #pragma unroll
@@ -488,8 +498,8 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(KvCache kc, KvCompact a
       }
     };
     Moved now, next;
-    load(part, now);
-    for (int x = part; x < all; x += step) {
+    load(a.x0 + part, now);
+    for (int x = a.x0 + part; x < all; x += step) {
       load(x + step, next);
       if constexpr (HOW == kInPlace) __syncthreads();          // every wave has what it reads of x
       store(x, now);
@@ -531,24 +541,29 @@ struct Read {
     kv_read_kernel<FMT, D><<<dim3(kc.M, row_parts(kc.M, units)), 256, 0, s>>>(kc, K, ldk, V, ldv, f32);
   }
 };
-constexpr int kCompactFew = 64;             // tokens that one wave moves in place
 constexpr int64_t kCompactGroups = 2048;    // workgroups of a compaction, if it has heads and layers for them
 
+template <int FMT, int D, int HOW>
+void compact(const KvCache& kc, KvCompact a, int64_t y, hipStream_t s) {
+  const int64_t all = a.x1 - a.x0, most = HOW == kInPlaceByWave ? (all + 3) / 4 : all;
+  const int64_t fill = kCompactGroups / (kc.batch * y);
+  a.parts = int(fill < 1 ? 1 : fill < most ? fill : most);
+  kv_compact_kernel<FMT, D, HOW><<<dim3(unsigned(kc.batch) * a.parts, unsigned(y)), 256, 0, s>>>(kc, a);
+}
 template <int FMT, int D>
 struct Compact {
   static void run(const KvCache& kc, KvCompact a, bool in_place, hipStream_t s) {
-    const int64_t tiles = a.most / 16 + 2, all = int64_t(a.planes) * kc.heads;
-    const bool by_wave = in_place && a.most <= kCompactFew;
-    const int64_t y = in_place ? 1 : tiles < 4 * 65535 ? (tiles + 3) / 4 : 65535, most = by_wave ? (all + 3) / 4 : all;
-    const int64_t fill = kCompactGroups / (kc.batch * y);
-    a.parts = int(fill < 1 ? 1 : fill < most ? fill : most);
-    const dim3 grid(unsigned(kc.batch) * a.parts, unsigned(y));
-    if (by_wave)
-      kv_compact_kernel<FMT, D, kInPlaceByWave><<<grid, 256, 0, s>>>(kc, a);
-    else if (in_place)
-      kv_compact_kernel<FMT, D, kInPlace><<<grid, 256, 0, s>>>(kc, a);
-    else
-      kv_compact_kernel<FMT, D, kApart><<<grid, 256, 0, s>>>(kc, a);
+    const int64_t tiles = kv_compact_tiles(a.most), y = tiles < 4 * 65535 ? (tiles + 3) / 4 : 65535;
+    if (!in_place) return compact<FMT, D, kApart>(kc, a, y, s);
+    if (a.most <= kKvCompactFew) return compact<FMT, D, kInPlaceByWave>(kc, a, 1, s);
+    const int all = a.x1, slab = kv_compact_slab(FMT, D, kc.batch, all, a.most);
+    if (slab == 0) return compact<FMT, D, kInPlace>(kc, a, 1, s);
+    a.tiles = int(tiles);
+    for (a.x0 = 0; a.x0 < all; a.x0 += slab) {
+      a.x1 = a.x0 + slab < all ? a.x0 + slab : all;
+      compact<FMT, D, kThrough>(kc, a, y, s);
+      compact<FMT, D, kBack>(kc, a, y, s);
+    }
   }
 };
 
@@ -589,8 +604,9 @@ hipError_t launch_kv_copy(uint8_t* pool, int planes, int64_t plane_bytes, int64_
 
 hipError_t launch_kv_compact(int fmt, int D, const KvCache& kc, int planes, int64_t plane_bytes, const int32_t* to,
                              int64_t ldto, int cols_to, const int32_t* start, const int32_t* keep, int64_t ldkeep,
-                             const int32_t* n_keep, int most, bool in_place, hipStream_t s) {
-  const KvCompact a = {to, start, keep, n_keep, ldto, ldkeep, plane_bytes, cols_to, most, planes, 1};
+                             const int32_t* n_keep, int most, bool in_place, void* space, hipStream_t s) {
+  const KvCompact a = {to, start, keep, n_keep, ldto, ldkeep, plane_bytes, cols_to, most, 1, static_cast<uint8_t*>(space),
+                       0, planes * kc.heads, 0};
   by_format<Compact>(fmt, D, kc, a, in_place, s);
   return hipGetLastError();
 }
