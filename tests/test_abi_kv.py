@@ -108,7 +108,7 @@ def test_attention_validation(L, forced_device_error):
     for i in (0, 1, 3, 6, 10, 16, 19):
         assert call(**{f"_{i}": None}) == 1, i
     for bad in [b for b in BAD_CACHE if b != dict(_4=7)] + [dict(_4=79), dict(_11=2040), dict(_17=2040), dict(_12=6, _20=BIG), dict(_12=0), dict(_13=0.0),
-                            dict(_13=-1.0), dict(_13=float("nan")), dict(_13=float("inf")), dict(_14=-1),
+                            dict(_13=-1.0), dict(_13=float("nan")), dict(_13=float("inf")), dict(_13=2.1e38), dict(_14=-1),
                             dict(_8=16000, _4=1 << 25, _5=1 << 25, _20=BIG)] + [dict(_0=D(**b)) for b in BAD_DESC]:
         assert call(**bad) == 2, bad
     assert call(_15=2) == 3 and call(_0=D(fmt=0)) == 3
@@ -135,6 +135,13 @@ def test_copy_validation(L, forced_device_error):
     assert call(_5=ints(*many), _6=ints(*range(199, 399)), **ok) == 2       # page 199 is both
     assert call(_5=ints(*many), _6=ints(*([500] + list(range(500, 699)))), **ok) == 2
     assert call(_5=ints(*many), _6=ints(*many), **ok) == 6
+    for n in (256, 257, 900):                                              # each size of the table they are looked up in
+        ok = dict(_2=2000, _4=2000 * per, _7=n)
+        src, dst = [7 * i % 1000 for i in range(n)], [1999 - i for i in range(n)]
+        assert call(_5=ints(*src), _6=ints(*dst), **ok) == 6
+        for i, j in ((0, n - 1), (n - 1, 0), (n // 2, 3)):
+            assert call(_5=ints(*src), _6=ints(*[dst[j] if k == i else p for k, p in enumerate(dst)]), **ok) == 2
+            assert call(_5=ints(*[dst[j] if k == i else p for k, p in enumerate(src)]), _6=ints(*dst), **ok) == 2
     assert call(_0=D(fmt=7)) == 3
     assert call(_1=P + 16) == 4 and call(_4=100 * per + 32) == 4
 

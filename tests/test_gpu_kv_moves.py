@@ -38,6 +38,7 @@ def test_copy(td, heads, page, planes, n):
     assert sq.kv_copy(kv, pool, src, dst) is pool and torch.equal(pool, want)
     sq.kv_copy(kv, pool, [], [])
     sq.kv_copy(kv, pool, dst, dst)
+    sq.kv_copy(kv, pool, np.array(src), torch.tensor(dst))
     assert torch.equal(pool, want)
     if planes == 1:
         sq.kv_copy(kv, pool[0], dst[:1], src[:1])

@@ -8,6 +8,7 @@ call raises if the library is not built or the device is not gfx950.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 from dataclasses import dataclass
@@ -556,6 +557,8 @@ def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = Non
     D, shape = kv.head_dim, Q.shape
     if len(shape) != 2 or shape[1] % D:
         raise ValueError(f"Q: expected rows of heads x {D}, got {tuple(shape)}")
+    if window >= 1 << 31:
+        raise ValueError(f"window: expected an int32, got {window}")
     M, cols = shape
     q_heads = cols // D
     args = _cache_args(kv, pool, table, lens, cu, M)
@@ -589,13 +592,17 @@ def kv_copy(kv: KvLayout, pool, src, dst, stream=None):
         return _elsewhere(dev, stream, lambda: kv_copy(kv, pool, src, dst))
     p, nbytes = _kept_kv(kv)
     _pool(pool, nbytes, 3)
-    n = len(src)
-    if len(dst) != n:
-        raise ValueError(f"{n} sources for {len(dst)} destinations")
-    array = ctypes.c_int32 * n
+    try:
+        a, b = (array.array("i", v if isinstance(v, (list, tuple)) else list(v)) for v in (src, dst))
+    except (TypeError, OverflowError) as e:
+        raise ValueError(f"src, dst: expected sequences of page numbers ({e})") from None
+    n = len(a)
+    if len(b) != n:
+        raise ValueError(f"{n} sources for {len(b)} destinations")
     pages = pool.shape[-2]
     st = lib().svdq_kv_copy(p, pool.data_ptr(), pages, pool.shape[0] if pool.dim() == 3 else 1, pages * nbytes,
-                            array(*src), array(*dst), n, _torch()._C._cuda_getCurrentRawStream(dev.index))
+                            a.buffer_info()[0], b.buffer_info()[0], n,
+                            _torch()._C._cuda_getCurrentRawStream(dev.index))
     if st:
         check("svdq_kv_copy", st)
     return pool
