@@ -375,8 +375,9 @@ svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages,
  * over the tokens t < lens[b] that are there, up to the row's own (not with SVDQ_KV_FULL), and with
  * window > 0 only the last `window` of those up to the row's own.  A row that sees nothing gives
  * zeros and an lse of -infinity.  Scores and sums are fp32; p_t enters the sum over V rounded to
- * 2^-11 of itself with NVFP4, else to 2^-16 where a sequence has at most 32 query rows a K/V head (tokens
- * x q_heads / heads, on average) and to 2^-8 where it has more; the same call gives the same bits.
+ * 2^-11 of itself with NVFP4, else to 2^-16, and to 2^-8 in long prompts: where M x q_heads is 384 x 128 or
+ * more and a sequence has 128 query rows a K/V head (tokens x q_heads / heads, on average).  The same call gives
+ * the same bits.
  *   Q      device, bf16 bits, M x q_heads head_dim, row stride ldq; q_heads a multiple of heads
  *   scale  > 0
  *   Y      device, bf16 bits, M x q_heads head_dim; its elements are none of Q's

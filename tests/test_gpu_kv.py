@@ -236,6 +236,68 @@ def test_attention_many_sequences_of_rows(td, fmt):
                         "nvfp4" if fmt == "nvfp4" else "few" if few else "many")
 
 
+PROMPTS = {
+    # the same, of 128-row tiles: 128 rows a sequence on average, M x q_heads >= 384 x 128; the last sequence of "groups"
+    # has more rows than tokens
+    "groups": ([200, 1, 129, 0, 333, 140], [200, 700, 500, 9, 400, 100], 64, 8, 16),
+    "own heads": ([900, 100, 600], [1000, 100, 601], 32, 32, 64),
+}
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("name,D,masks", [("groups", 64, ((True, 2 ** 31 - 1), (True, 40))), ("groups", 128, ((True, 0), (False, 200))),
+                                          ("own heads", 64, ((True, 0), (False, 200)))])
+def test_attention_prompts(td, fmt, name, D, masks):
+    torch, dev = td
+    q_lens, lens, Hq, H, page = PROMPTS[name]
+    M = sum(q_lens)
+    assert M * Hq >= 384 * 128 and M * (Hq // H) >= 128 * len(lens)
+    kv = sq.KvLayout(fmt, H, D, page)
+    c = Cache(torch, dev, kv, lens, 5 + D)
+    Qv = c.bf16(c.rng.standard_normal((M, Hq, D)) * 1.5)
+    q, cu, n = c.dev_bf16(Qv.reshape(M, -1)), i32(np.r_[0, np.cumsum(q_lens)], dev, torch), i32(lens, dev, torch)
+    for causal, window in masks:
+        what = f"{fmt} D{D} {name} causal {causal} window {window}"
+        print(what, flush=True)
+        out, lse = sq.kv_attention(kv, c.pool, c.table, n, q, cu=cu, causal=causal, window=window, lse=True)
+        check_attention(c, Qv, out, lse, q_lens, lens, Hq, D ** -0.5, causal, window, what,
+                        "nvfp4" if fmt == "nvfp4" else "many")
+        assert torch.equal(sq.kv_attention(kv, c.pool, c.table, n, q, cu=cu, causal=causal, window=window), out), what
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_drafts_of_a_large_batch(td, fmt):
+    """Few rows of many sequences: 32-row tiles and P to 2^-16, however many there are; whole and split."""
+    torch, dev = td
+    kv = sq.KvLayout(fmt, 8, 64, 16)
+    rng = np.random.default_rng(1)
+    lens = [int(x) for x in rng.integers(5, 60, 200)]
+    q_lens = [4] * 200
+    for cols in (None, 100):
+        c = Cache(torch, dev, kv, lens, 6, cols=cols)
+        Qv = c.bf16(c.rng.standard_normal((800, 64, 64)))
+        out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(800, -1)),
+                                   cu=i32(np.arange(201) * 4, dev, torch), lse=True)
+        check_attention(c, Qv, out, lse, q_lens, lens, 64, 0.125, True, 0, f"{fmt} {cols}", "nvfp4" if fmt == "nvfp4" else "few")
+
+
+@pytest.mark.parametrize("cols", [None, 200])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_widest_windows(td, cols, causal):
+    """A window of every size up to the largest int32, with more rows than tokens: it ends before the first place."""
+    torch, dev = td
+    kv = sq.KvLayout("mxfp4", 1, 64, 16)
+    lens, q_lens = [0, 1, 5, 40, 2], [2, 4, 5, 3, 1]
+    c = Cache(torch, dev, kv, lens, 2, cols=cols)
+    M = sum(q_lens)
+    for Hq in (1, 8):                                                  # 16 rows a tile, 32 rows
+        Qv = c.bf16(c.rng.standard_normal((M, Hq, 64)))
+        for window in (2 ** 30, 2 ** 31 - 8, 2 ** 31 - 2, 2 ** 31 - 1):
+            out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(M, -1)),
+                                       cu=i32(np.r_[0, np.cumsum(q_lens)], dev, torch), causal=causal, window=window, lse=True)
+            check_attention(c, Qv, out, lse, q_lens, lens, Hq, 0.125, causal, window, f"window {window}", "few")
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_attention_scales_and_magnitudes(td, fmt):
     """Peaked and flat softmaxes, tiny and large K, V and Q; a rising running maximum; lengths beyond the table."""
@@ -352,7 +414,7 @@ def test_attention_refusals(td):
     ok()
     for kw in (dict(Q=q[:, :100]), dict(Q=q.float()), dict(Q=q.cpu()), dict(Q=q[:1]), dict(out=q[:, :128]), dict(out=q.float()),
                dict(lse=torch.zeros((2, 3), device=dev)), dict(workspace=q), dict(cu=n32), dict(Q=q.t().contiguous().t()),
-               dict(workspace=torch.zeros(4, dtype=torch.uint8))):
+               dict(workspace=torch.zeros(4, dtype=torch.uint8)), dict(window=1 << 32)):
         with pytest.raises(ValueError):
             ok(**kw)
     for kw in (dict(scale=0.0), dict(window=-1), dict(Q=q[:, :192]), dict(workspace=torch.zeros(256, dtype=torch.uint8, device=dev))):
@@ -380,5 +442,8 @@ def test_attention_refusals(td):
         sq.kv_copy(kv, c.pool, [0, 1], [2, 0])
     with pytest.raises(ValueError):
         sq.kv_copy(kv, c.pool, [0, 1], [2])
+    for bad in ([1 << 32], [0.5], None, torch.zeros(1, device=dev)):
+        with pytest.raises(ValueError):
+            sq.kv_copy(kv, c.pool, bad, [2])
     with pytest.raises(ValueError):
         sq.kv_compact(kv, c.pool, c.table, n32, n32)

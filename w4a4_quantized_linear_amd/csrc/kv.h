@@ -56,12 +56,17 @@ inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most)
 // How a call of svdq_kv_attention is cut: `rows` query rows of a K/V head (a sequence's tokens x the heads that share
 // it) a workgroup, `jobs` such tiles at most; split: `ranges` workgroups a head share the units of all jobs.
 //
-// Rows by what a sequence has on average, and 128 where there are 256 such tiles (then a wave's 32 rows see all
-// tokens, 4 waves side by side; with fewer, a tile's tokens are shared out).  us in a graph, MXFP4, 8 heads x 4
-// queries of 128, 16 sequences of 2000 tokens, new tokens each: 16 rows / 32 / 128
-//   q 2 21.0 / 21.3 / 61    q 12 29.1 / 28.7 / 64    q 32 - / 41.5 / 66    q 64 - / 74 / 68    q 256 - / 242 / 182
-// and one sequence of 8192: q 8 17.5 / 17.4 / 228, q 256 - / 78 / 225, q 512 - / 130 / 225 (128 tiles), and of 16000
-// 4 sequences, 2 x 8 heads: q 512 - / 420 / 428 (256 tiles).
+// Rows by what a sequence has on average, and 128 where that fills them and there are 384 such tiles (then a wave's 32
+// rows see all tokens, 4 waves side by side; with fewer, a tile's tokens are shared out).  us in a graph, MXFP4, 8 heads
+// x 4 queries of 128, 16 sequences of 2000 tokens, new tokens each: 16 rows / 32 / 128
+//   q 2 21.0 / 21.3 / 61    q 12 29.1 / 28.7 / 64    q 32 - / 41.5 / 66
+// and 32 rows / 128 (rows a sequence, 128-row tiles in all):
+//   128 sequences to 2000 tokens, 32 rows, 256 tiles 59.0 / 98.8     128 to 2000, 64 rows, 512 tiles 94.3 / 116
+//   64 to 2000, 128 rows, 512 tiles 91.8 / 72.6                      32 to 4000, 128 rows, 256 tiles 90.1 / 111
+//   48 to 2000, 132 rows, 392 tiles 82.5 / 89.9                      4 to 4000, 1536 rows, 384 tiles 126 / 134
+//   4 of 4000, 1536 rows, 384 tiles 165 / 148
+//   1 of 8192, 4096 rows, 256 tiles 220 / 215                        1 of 8192, 8192 rows, 512 tiles 372 / 265
+// (INT4 alike: 512 tiles 141 / 108, 256 tiles 263 / 277.)
 // Split where tokens are many for the tiles: one query a sequence, ragged, whole against split at 512, 1024, 2048, 4096
 // tokens: 8 tiles 7.2 / 8.7, 9.6 / 9.1, 14.5 / 9.4, 23.5 / 10.4; 128 tiles 7.6 / 10.9, 10.0 / 12.5, 14.8 / 13.4,
 // 23.8 / 18.4; 512 tiles 13.0 / 15.2, 18.4 / 21.2, 27.3 / 25.3, 44.2 / 34.9 (INT4 and NVFP4 alike); with 32 rows at
@@ -79,7 +84,7 @@ inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads, int64
   KvPlan p;
   const int64_t group = q_heads / heads, each = (M * group + batch - 1) / (batch > 0 ? batch : 1);
   auto tiles = [&](int rows) { return (M * group + rows - 1) / rows + batch; };
-  p.rows = each <= 16 ? 16 : (tiles(128) - batch) * heads >= 256 ? 128 : 32;
+  p.rows = each <= 16 ? 16 : each >= 128 && M * q_heads >= 384 * 128 ? 128 : 32;
   const int64_t jobs = tiles(p.rows);
   p.jobs = int(jobs);
   p.split = p.rows < 128 && places > (jobs * heads >= 64 ? kKvWholeMany : kKvWhole) &&

@@ -1223,6 +1223,7 @@ hipError_t launch_kv_attention(int fmt, int D, const KvCache& kc, const uint16_t
                                float scale, int window, bool causal, uint16_t* Y, int64_t ldy, float* lse, float* part,
                                hipStream_t s) {
   const KvPlan p = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
+  if (window > INT32_MAX - int(kKvMaxRows) - 1) window = INT32_MAX - int(kKvMaxRows) - 1;   // a row's place minus it fits
   const KvAttn a = {Q, Y, lse, part, ldq, ldy, q_heads / kc.heads, q_heads, window, causal ? 1 : 0, p.ranges,
                     scale * 1.44269504088896341f};
   if (fmt == kFmtMXFP4)
