@@ -281,6 +281,28 @@ def test_attention_drafts_of_a_large_batch(td, fmt):
         check_attention(c, Qv, out, lse, q_lens, lens, 64, 0.125, True, 0, f"{fmt} {cols}", "nvfp4" if fmt == "nvfp4" else "few")
 
 
+@pytest.mark.parametrize("q_lens,Hq,H", [
+    ([8] * 90, 8, 1), ([8] * 90, 16, 2), ([0, 0, 24, 0, 8, 1, 0, 40, 0] * 11, 4, 1), ([0] * 70 + [33] + [0] * 70, 8, 8), ([1] * 130, 40, 1),
+    ([2] * 5000, 8, 1)])
+def test_attention_tiles_of_many_sequences(td, q_lens, Hq, H):
+    """Every tile of every sequence is done once: whole tiles, a row more, sequences without rows, rows of none."""
+    torch, dev = td
+    rng = np.random.default_rng(3)
+    lens = [int(q + x) for q, x in zip(q_lens, rng.integers(0, 20, len(q_lens)))]
+    kv = sq.KvLayout("mxfp4", H, 64, 16)
+    c = Cache(torch, dev, kv, lens, 8)
+    M, before, behind = sum(q_lens), 3, 70
+    Qv = c.bf16(c.rng.standard_normal((M, Hq, 64)))
+    q = torch.cat([torch.zeros((before, Hq * 64), device=dev).bfloat16(), c.dev_bf16(Qv.reshape(M, -1)),
+                   torch.zeros((behind, Hq * 64), device=dev).bfloat16()])
+    out, lse = torch.full_like(q, 7.0), torch.full((len(q), Hq), 7.0, device=dev)
+    sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), q, cu=i32(before + np.r_[0, np.cumsum(q_lens)], dev, torch),
+                    out=out, lse=lse)
+    check_attention(c, Qv, out[before:before + M], lse[before:before + M], q_lens, lens, Hq, 0.125, True, 0, "tiles", "few")
+    for x in (out, lse):
+        assert (x[:before] == 7.0).all() and (x[before + M:] == 7.0).all()
+
+
 @pytest.mark.parametrize("cols", [None, 200])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_widest_windows(td, cols, causal):

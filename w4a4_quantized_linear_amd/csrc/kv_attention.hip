@@ -499,8 +499,53 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// The work of all sequences in units (SPLIT: of jobs x tokens; else jobs), and the sequence that unit `at`
-// falls into with the units before it (b = -1: none).  A batch of up to 64 is one wave's scan, which each
+// A job of a call that is not split, by its workgroup's number; a number that no tile has does nothing.  One query a
+// sequence: a division.  Up to 64 sequences: counted by a wave's scan, without a gap.  More: the first `batch` numbers
+// are one tile of each; sequence b's others have the numbers from cu[b] group / R (rounded down) on, which are enough
+// for its x = rows group rows: x / R, rounded down, at least.  Where gaps come in turn with tiles, as with x = 2 R,
+// every 8 numbers are put in another order, so that they fall on all XCDs.  Counting all lengths in every workgroup,
+// as ranges do, grew with the square of the batch: 16384 sequences to 300 tokens, 2 heads, 3291 us (561 so), drafts of
+// 4 tokens, 16 query heads, 4740 (570).  Gaps cost little among many tiles, but one prompt's 512 tiles, two for every
+// CU, took 379 us with one gap among them, 265 without.
+struct KvJob {
+  int b, tile;
+};
+template <int R>
+int kv_numbers(const KvCache& kc, const KvAttn& a) {
+  if (kc.cu == nullptr) return kc.batch * ((a.group + R - 1) / R);
+  return kc.batch + (int(unsigned(kc.M) * unsigned(a.group) / R) + 7) / 8 * 8;
+}
+template <int R>
+__device__ __forceinline__ KvJob kv_job(const KvCache& kc, const KvAttn& a, int index, int lane) {
+  if (kc.cu == nullptr) {
+    const int each = (a.group + R - 1) / R, b = int(unsigned(index) / unsigned(each));   // tiles of one token
+    return {b, index - b * each};
+  }
+  auto row = [&](int b) { return min(max(kc.cu[b], 0), kc.M); };
+  if (kc.batch <= 64) {
+    const int n = lane < kc.batch ? (max(row(lane + 1) - row(lane), 0) * a.group + R - 1) / R : 0, end = wave_scan(n);
+    const uint64_t in = __ballot(index < end);
+    if (in == 0) return {0, -1};
+    const int b = __builtin_ctzll(in);
+    return {b, index - __builtin_amdgcn_readlane(end - n, b)};
+  }
+  if (index < kc.batch) return {index, 0};
+  index -= kc.batch;
+  index ^= (index >> 3) & 7;
+  auto from = [&](int b) { return int(unsigned(row(b)) * unsigned(a.group) / R); };
+  int lo = 0, n = kc.batch;                                   // the last b with from(b) <= index is in lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 63) / 64, i = lane * step;
+    const uint64_t le = __ballot(i < n && from(lo + i) <= index);
+    const int k = 63 - __builtin_clzll(le | 1);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return {lo, 1 + index - uni(from(lo))};
+}
+
+// The work of all sequences in units (of jobs x tokens), and the sequence that unit `at` falls into with the units
+// before it (b = -1: none).  A batch of up to 64 is one wave's scan, which each
 // wave does for itself; a larger one goes through the workgroup in chunks of NT.
 struct KvFound {
   int b, before;
@@ -508,7 +553,7 @@ struct KvFound {
 constexpr int kLeastUnits = 2;           // of a range
 constexpr int kShortUnits = 8;           // of a range, up to which a range is part of one job
 
-template <int R, int U, bool SPLIT, int NT>
+template <int R, int U, int NT>
 struct KvScan {
   const KvCache& kc;
   const KvAttn& a;
@@ -520,7 +565,7 @@ struct KvScan {
   __device__ __forceinline__ KvSeq seq(int b) const {
     int len, row, rows;
     kc.sequence(b, len, row, rows);
-    return kv_seq<R, U, SPLIT>(kc, a, len, row, rows);
+    return kv_seq<R, U, true>(kc, a, len, row, rows);
   }
   __device__ __forceinline__ int units_of(int b) const {
     if (b >= kc.batch) return 0;
@@ -625,26 +670,36 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
   const int r = lane & 15, c = lane >> 4, wq = wave / WK, wk = wave % WK;
   const int h = blockIdx.x % kc.heads, range = blockIdx.x / kc.heads;
 
-  KvScan<R, U, SPLIT, NT> scan{kc, a, sh};
-  const int total = scan.count();
-  if constexpr (SPLIT) scan.cut(a.ranges);
-  const int per = SPLIT ? scan.per : 1;
-  const int64_t first64 = scan.short_ranges ? range : int64_t(range) * per;
-  if (!scan.short_ranges && first64 >= total) return;
-  const int first = int(first64);
-  const KvFound f = scan.find(first);
-  int left = min(per, total - first), b = f.b;
-  if (b < 0) return;
-  KvSeq s = kv_seq_of<R, U, SPLIT>(kc, a, b);
-  int job, unit;
-  if (scan.short_ranges) {
-    const int each = (s.units + per - 1) / per;               // ranges of a job
-    job = (first - f.before) / each;
-    unit = ((first - f.before) % each) * per;
-    left = min(per, s.units - unit);
+  int b, job, unit = 0, left = 1;
+  KvSeq s;
+  if constexpr (SPLIT) {
+    KvScan<R, U, NT> scan{kc, a, sh};
+    const int total = scan.count();
+    scan.cut(a.ranges);
+    const int per = scan.per;
+    const int64_t first64 = scan.short_ranges ? range : int64_t(range) * per;
+    if (!scan.short_ranges && first64 >= total) return;
+    const int first = int(first64);
+    const KvFound f = scan.find(first);
+    left = min(per, total - first);
+    b = f.b;
+    if (b < 0) return;
+    s = kv_seq_of<R, U, SPLIT>(kc, a, b);
+    if (scan.short_ranges) {
+      const int each = (s.units + per - 1) / per;             // ranges of a job
+      job = (first - f.before) / each;
+      unit = ((first - f.before) % each) * per;
+      left = min(per, s.units - unit);
+    } else {
+      job = (first - f.before) / s.units;
+      unit = (first - f.before) % s.units;
+    }
   } else {
-    job = (first - f.before) / s.units;
-    unit = (first - f.before) % s.units;
+    const KvJob f = kv_job<R>(kc, a, range, lane);
+    b = f.b;
+    job = f.tile;
+    s = kv_seq_of<R, U, SPLIT>(kc, a, b);
+    if (job < 0 || job >= s.tiles) return;
   }
 
   while (left > 0) {
@@ -915,17 +970,14 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a) {
   constexpr int NQ = 2, R = 128, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1, TB = kv_tile_bytes(FMT, D);
   __shared__ KvShared<FMT, D> shared;
-  __shared__ int words[16];
+  __shared__ int marks[2][4];                                  // of a half's tiles: whether they are there
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int h = blockIdx.x % kc.heads, index = blockIdx.x / kc.heads;
-  KvScan<R, 32, false, 256> scan{kc, a, words};
-  const int total = scan.count();
-  if (index >= total) return;
-  const KvFound f = scan.find(index);
-  if (f.b < 0) return;
+  const KvJob f = kv_job<R>(kc, a, index, lane);
   const KvSeq s = kv_seq_of<R, 32, false>(kc, a, f.b);
-  const int tile_rows = s.tiles - 1 - (index - f.before);      // long causal tiles first
+  if (f.tile < 0 || f.tile >= s.tiles) return;
+  const int tile_rows = s.tiles - 1 - f.tile;                  // long causal tiles first
   const KvRows rows(kc, a, s);
   const int wg0 = tile_rows * R, row0 = wg0 + wave * 32;
 
@@ -962,7 +1014,7 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
     const int t = t0 + i * 64 + wave * 16;
     if (t + 16 > wg.behind || t < wg.first) clear_outside<FMT, D>(wg.first - t, wg.behind - t, c, st);
     share_tile<FMT, D>(st, wave, lane, shared, i & 1);
-    if (lane == 0) words[8 + (i & 1) * 4 + wave] = there;
+    if (lane == 0) marks[i & 1][wave] = there;
   };
 
   bool there = fetch(0);
@@ -978,7 +1030,6 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) off[n][g] = v4f{0.f, 0.f, 0.f, 0.f};
   }
-  __syncthreads();                                             // words were the scan's
   if (chunks > 0) share(0, there);
   if (chunks > 1) there = fetch(1);
   for (int i = 0; i < chunks; ++i) {
@@ -987,7 +1038,7 @@ __global__ void __launch_bounds__(256, 2) kv_prompt_kernel(KvCache kc, KvAttn a)
     if (t + 64 > span.first && t < span.behind) {
       bool ok[4];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) ok[y] = uni(words[8 + half * 4 + y]) != 0;
+      for (int y = 0; y < 4; ++y) ok[y] = uni(marks[half][y]) != 0;
       float z[NQ][4][4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
@@ -1091,7 +1142,10 @@ constexpr int kJoinGroups = 2048;        // workgroups of a join at most, if job
 
 // Joins the parts of split jobs.  A workgroup takes a job and its rows: D / 8 threads take a row's features, and of the
 // 2048 / D such groups as many share a row as the parts keep busy.  How it finds its job: by number, in a batch whose
-// scan is one wave's; by sequence, where each is one job; else as the one inside which a range border is the first.
+// scan is one wave's; by sequence, where each is one job and they are not many; else as the one inside which a range
+// border is the first (by sequence / border, 2 heads to 2000 tokens: 256 sequences 31.4 / 32.1 us with the attention,
+// 1024 73.5 / 72.6, 4096 316 / 279).
+constexpr int kJoinSeqs = 512;
 enum { kByJob = 0, kBySeq = 1, kByBorder = 2 };
 template <int D, int R, int U, int HOW>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
@@ -1099,7 +1153,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   __shared__ int sh[16];
   __shared__ float sm[NP], sl[NP], so[NP][D];
   const int h = blockIdx.x % kc.heads, index = blockIdx.x / kc.heads;
-  KvScan<R, U, true, 256> scan{kc, a, sh};
+  KvScan<R, U, 256> scan{kc, a, sh};
   const int total = scan.count();
   scan.cut(a.ranges);
   const int per = scan.per;
@@ -1186,8 +1240,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
 }
 
 template <int FMT, int D, int NQ, int WQ, int WK, int PL>
-void attend_whole(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
-  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(unsigned(jobs) * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
+void attend_whole(const KvCache& kc, const KvAttn& a, hipStream_t s) {
+  const unsigned n = kv_numbers<KvTiles<NQ, WQ, WK>::R>(kc, a);
+  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(n * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
 }
 template <int FMT, int D, int NQ, int WQ, int WK, int PL>
 void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
@@ -1195,7 +1250,7 @@ void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
   kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
   if (a.ranges < 2) return;
   const int64_t most = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group, rows = most < R ? most : R;
-  const int how = kc.batch <= 64 ? kByJob : kc.cu == nullptr && a.group <= R ? kBySeq : kByBorder;
+  const int how = kc.batch <= 64 ? kByJob : kc.cu == nullptr && a.group <= R && kc.batch <= kJoinSeqs ? kBySeq : kByBorder;
   const int x = (how == kByJob ? jobs : how == kBySeq ? kc.batch : a.ranges - 1) * kc.heads;
   const int fill = kJoinGroups / x;
   const dim3 grid(x, unsigned(fill < 1 ? 1 : fill < rows ? fill : rows));
@@ -1210,11 +1265,11 @@ void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
 template <int FMT, int D>
 void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_t s) {
   if (p.rows == 16)
-    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, p.jobs, s);
+    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, s);
   else if (p.rows == 32)
-    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s);
+    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, s);
   else
-    kv_prompt_kernel<FMT, D><<<dim3(unsigned(p.jobs) * kc.heads), 256, 0, s>>>(kc, a);
+    kv_prompt_kernel<FMT, D><<<dim3(unsigned(kv_numbers<128>(kc, a)) * kc.heads), 256, 0, s>>>(kc, a);
 }
 
 }  // namespace
