@@ -108,9 +108,9 @@ def test_attention_validation(L, forced_device_error):
     for i in (0, 1, 3, 6, 10, 16, 19):
         assert call(**{f"_{i}": None}) == 1, i
     for bad in [b for b in BAD_CACHE if b != dict(_4=7)] + [dict(_4=79), dict(_11=2040), dict(_17=2040), dict(_12=6, _20=BIG), dict(_12=0), dict(_13=0.0),
-                            dict(_13=-1.0), dict(_13=float("nan")), dict(_13=float("inf")), dict(_13=2.1e38), dict(_14=-1),
-                            dict(_8=16000, _4=1 << 25, _5=1 << 25, _20=BIG)] + [dict(_0=D(**b)) for b in BAD_DESC]:
+                            dict(_13=-1.0), dict(_13=float("nan")), dict(_13=float("inf")), dict(_13=2.1e38), dict(_14=-1)] + [dict(_0=D(**b)) for b in BAD_DESC]:
         assert call(**bad) == 2, bad
+    assert call(_8=16000, _4=1 << 25, _5=1 << 25, _20=BIG) == 6            # more units than 32 bits count: not split
     assert call(_15=2) == 3 and call(_0=D(fmt=0)) == 3
     for bad in (dict(_10=P + 8), dict(_16=P + 8), dict(_18=P + 2), dict(_19=P + 64), dict(_11=2052), dict(_1=P + 16)):
         assert call(**bad) == 4, bad

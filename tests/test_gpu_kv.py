@@ -209,7 +209,7 @@ def test_attention_long(td, fmt):
     torch, dev = td
     kv = sq.KvLayout(fmt, 1, 64, 64)
     short = [int(n) for n in np.random.default_rng(3).integers(0, 50, 600)]
-    for lens, Hq, cols in (([70001], 2, None), ([3, 40000, 5], 1, None), (short, 2, None), (short, 2, 100)):
+    for lens, Hq, cols in (([70001], 2, None), ([3, 40000, 5], 1, None), (short, 2, None), (short, 2, 100), (short[:200], 2, 100), (short[:200] + [5000], 2, 100)):
         c = Cache(torch, dev, kv, lens, 9, cols=cols)
         Qv = c.bf16(c.rng.standard_normal((len(lens), Hq, 64)))
         out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(len(lens), -1)), lse=True)
@@ -222,7 +222,7 @@ def test_attention_many_sequences_of_rows(td, fmt):
     """More than 256 sequences of several rows (the scan's chunks), prompts among them, in both kinds of plan."""
     torch, dev = td
     rng = np.random.default_rng(8)
-    for B, most, H, Hq, cols in ((300, 3, 1, 2, None), (300, 3, 1, 2, 80), (270, 90, 2, 4, None), (270, 90, 1, 4, 10)):
+    for B, most, H, Hq, cols in ((300, 3, 1, 2, None), (300, 3, 1, 2, 300), (270, 90, 2, 4, None), (270, 90, 1, 4, 300)):
         q_lens = [int(x) for x in rng.integers(0, most + 1, B)]
         lens = [int(x + y) for x, y in zip(q_lens, rng.integers(0, 40, B))]
         kv = sq.KvLayout(fmt, H, 64, 16)
@@ -273,7 +273,7 @@ def test_attention_drafts_of_a_large_batch(td, fmt):
     rng = np.random.default_rng(1)
     lens = [int(x) for x in rng.integers(5, 60, 200)]
     q_lens = [4] * 200
-    for cols in (None, 100):
+    for cols in (None, 300):
         c = Cache(torch, dev, kv, lens, 6, cols=cols)
         Qv = c.bf16(c.rng.standard_normal((800, 64, 64)))
         out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(800, -1)),

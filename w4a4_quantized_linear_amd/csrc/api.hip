@@ -555,8 +555,7 @@ svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t p
   svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
   if (s == SVDQ_ERR_SHAPE) return s;
   if (q_heads < 1 || q_heads > kKvMaxQHeads || q_heads % d->heads != 0 || window < 0 ||
-      !(scale > 0.0f && scale <= 2.0e38f) || M * q_heads > kKvMaxRowHeads ||
-      !kv_units_fit(d->head_dim, batch, M, q_heads, d->heads, int64_t(cols) * d->page))
+      !(scale > 0.0f && scale <= 2.0e38f) || M * q_heads > kKvMaxRowHeads)
     return SVDQ_ERR_SHAPE;
   const int64_t cols_q = int64_t(q_heads) * d->head_dim;
   const svdq_status rq = check_rows(Q, ldq, cols_q), ry = check_rows(Y, ldy, cols_q);

@@ -67,14 +67,18 @@ inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most)
 //   4 of 4000, 1536 rows, 384 tiles 165 / 148
 //   1 of 8192, 4096 rows, 256 tiles 220 / 215                        1 of 8192, 8192 rows, 512 tiles 372 / 265
 // (INT4 alike: 512 tiles 141 / 108, 256 tiles 263 / 277.)
-// Split where tokens are many for the tiles: one query a sequence, ragged, whole against split at 512, 1024, 2048, 4096
-// tokens: 8 tiles 7.2 / 8.7, 9.6 / 9.1, 14.5 / 9.4, 23.5 / 10.4; 128 tiles 7.6 / 10.9, 10.0 / 12.5, 14.8 / 13.4,
-// 23.8 / 18.4; 512 tiles 13.0 / 15.2, 18.4 / 21.2, 27.3 / 25.3, 44.2 / 34.9 (INT4 and NVFP4 alike); with 32 rows at
-// 256 tiles of 2000 tokens 28.7 / 31.5, 128 tiles 28.1 / 24.8.
+// Split where a table's tokens are many for the tiles there are (more than 16 a tile, at least 1024, at most 4096: a few
+// long sequences among many short ones are not to be a workgroup's each), whole / split, 8 heads, one query of 8 heads,
+// ragged and (all of one length): 8 tiles, 512 tokens 8.0 / 10.0, 1024 10.4 / 10.2, 2048 15.1 / 10.5; 64 tiles, 1024 10.4
+// / 11.1 (10.6 / 11.2), 2048 15.3 / 13.0 (15.5 / 13.3); 128 tiles, 2048 15.5 / 14.8 (15.9 / 17.8), 4096 24.7 / 18.4
+// (25.5 / 24.1); 256 tiles, 4096 25.9 / 25.7 (26.9 / 34.9), 8192 44.2 / 36.2 (46.3 / 55.1); 2048 tiles, 4096 122 / 125
+// (204 / 221); 32 rows: 128 tiles, 2048 25.5 / 22.0 (26.8 / 23.8), 256 tiles, 4096 43.8 / 41.3 (45.1 / 44.0), 8192 76.3 /
+// 56.2 (80.1 / 71.6), 1024 tiles, 4096 95.5 / 94.6 (136 / 145), 8192 174 / 164 (280 / 286); INT4 alike.
 // Ranges: three workgroups a CU (1, 2, 3, 4 a CU: 64 x 8192 MXFP4 76.9 63.7 59.7 63.4, 3 x 131072 38.7 35.0 35.7
 // 38.2, INT4 64 x 8192 89.3 75.7 69.0 72.7), two where a wave has 32 rows and registers for two.
-constexpr int64_t kKvWhole = 1024;           // tokens of a table up to which a job is one workgroup's
-constexpr int64_t kKvWholeMany = 1536;       // the same from 64 jobs on
+constexpr int64_t kKvWhole = 1024;           // tokens of a table up to which a job is one workgroup's, at least
+constexpr int64_t kKvWholeMany = 4096;       // and at most
+constexpr int64_t kKvWholeTile = 16;         // between them, for each tile
 struct KvPlan {
   int rows, jobs, ranges;
   bool split;
@@ -87,17 +91,12 @@ inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads, int64
   p.rows = each <= 16 ? 16 : each >= 128 && M * q_heads >= 384 * 128 ? 128 : 32;
   const int64_t jobs = tiles(p.rows);
   p.jobs = int(jobs);
-  p.split = p.rows < 128 && places > (jobs * heads >= 64 ? kKvWholeMany : kKvWhole) &&
-            (p.rows == 16 || jobs * heads < 384);
+  const int64_t whole = kKvWholeTile * heads * (jobs - batch > batch ? jobs - batch : batch);
+  p.split = p.rows < 128 && places > (whole < kKvWhole ? kKvWhole : whole > kKvWholeMany ? kKvWholeMany : whole) &&
+            jobs * (places / 128 + 1) <= INT32_MAX - 4096;     // units are counted in 32 bits
   p.ranges = p.split ? (256 * (p.rows == 16 ? 3 : 2) + heads - 1) / heads : 0;
   p.bytes = p.split ? align256(size_t(p.ranges) * heads * 2 * p.rows * (D + 2) * 4) : 0;
   return p;
-}
-
-// Whether the units of all jobs, of tables with `places` tokens each, can be counted in 32 bits.
-inline bool kv_units_fit(int D, int batch, int64_t M, int q_heads, int heads, int64_t places) {
-  const KvPlan p = kv_plan(D, batch, M, q_heads, heads, places);
-  return !p.split || p.jobs * (places / 128 + 1) <= INT32_MAX - 4096;
 }
 
 // A cache and its sequences, as the kernels take them.  Places beyond a sequence's table or with a page outside

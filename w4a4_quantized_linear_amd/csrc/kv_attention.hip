@@ -1264,8 +1264,13 @@ void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
 
 template <int FMT, int D>
 void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_t s) {
-  if (p.rows == 16)
-    p.split ? attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, s);
+  // 8 waves are a CU's at a time, 4 three times: 8 heads, to 700 tokens, 8 waves / 4 (us): 32 sequences 9.8 / 10.2, 64
+  // 16.3 / 12.7, 1024 176 / 98.8; to 300 7.5 / 7.7, 11.5 / 8.8, 125 / 59.3; INT4 8.4 / 8.6, 13.0 / 9.9.
+  if (p.rows == 16 && p.split)
+    attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s);
+  else if (p.rows == 16)
+    kv_numbers<16>(kc, a) * kc.heads > 256 ? attend_whole<FMT, D, 1, 1, 4, 2>(kc, a, s)
+                                           : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, s);
   else if (p.rows == 32)
     p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, s);
   else
