@@ -297,3 +297,94 @@ def test_compact_walks(td, fmt):
         for b, kk in enumerate(kept):
             want[c.cu[b] + start[b]:c.cu[b] + start[b] + len(kk)] = held.reshape(M, -1)[c.cu[b] + kk]
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_block_of_packed_layers(td, fmt):
+    """A decoder's attention between packed layers: a prompt, then tokens one by one, a fork and a copy between them,
+    each [Q | K | V] row from linear_w4a16 (the prompt's from linear), appended in place, attended, projected; the step as
+    a captured graph with the page copy in it, replayed, against eager calls; the attention against the oracle on the
+    device's own rows."""
+    torch, dev = td
+    H, Hq, D, page = 2, 4, 128, 16
+    K, N = 512, (Hq + 2 * H) * D
+    kv = sq.KvLayout(fmt, H, D, page)
+    fm = "mxfp4" if fmt == "nvfp4" else fmt
+    g = torch.Generator(device=dev)
+    g.manual_seed(5)
+    draw = lambda *shape: torch.randn(shape, generator=g, device=dev)
+    qkv, proj = sq.Layer(fm, K, N, 0), sq.Layer(fm, Hq * D, K, 0)
+    pack = lambda layer: sq.pack_weight(layer, draw(layer.N, layer.K) / layer.K ** 0.5, None, None,
+                                        torch.ones(layer.K, device=dev), torch.zeros(layer.N, device=dev).bfloat16())
+    w_qkv, w_proj = pack(qkv), pack(proj)
+    tab = np.full((2, 8), -1)
+    tab[0, :6], tab[1, :6] = np.arange(6), np.arange(6, 12)
+    table = i32(tab, dev, torch)
+    prompt = draw(50, K).bfloat16()
+    freq = (10000.0 ** (-torch.arange(64, device=dev) / 64)).float()
+
+    def attend(pool, x, lens, cu, layer=sq.linear_w4a16):
+        rows = layer(qkv, w_qkv, x, sq.EPI_BIAS)
+        q, k, v = rows[:, :Hq * D], rows[:, Hq * D:(Hq + H) * D], rows[:, (Hq + H) * D:]
+        sq.kv_append(kv, pool, table, lens, k, v, cu=cu, Q=q, q_out=q, freq=freq, halves=True)
+        out, lse = sq.kv_attention(kv, pool, table, lens, q, cu=cu, lse=True)
+        return rows, out, lse, sq.linear_w4a16(proj, w_proj, out, sq.EPI_BIAS)
+
+    pool = torch.full((12, sq.kv_page_bytes(kv)), 255, dtype=torch.uint8, device=dev)
+    attend(pool, prompt, i32([50, 0], dev, torch), i32([0, 50, 50], dev, torch), sq.linear)
+    sq.kv_copy(kv, pool, [0, 1, 2, 3], [6, 7, 8, 9])                   # sequence 1 is a copy of 0
+    lens, x = i32([50, 50], dev, torch), draw(2, K).bfloat16()
+
+    def step(p):
+        y = attend(p, x, lens, None)
+        sq.kv_copy(kv, p, [3], [10])                                   # a page behind the sequences'
+        return y
+
+    start_pool = pool.clone()
+    step(pool.clone())
+    graph, held = torch.cuda.CUDAGraph(), pool.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(held)
+    held.copy_(start_pool)
+    for i in range(5):
+        lens += 1
+        x.copy_(draw(2, K).bfloat16())
+        graph.replay()
+        want = step(pool)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+        assert torch.equal(pool, held), i
+    n = int(lens[0])
+    k, v = (t.cpu().numpy().astype(np.float64).reshape(2, n, H, D) for t in sq.kv_read(
+        kv, pool, table, lens, 2 * n, cu=i32([0, n, 2 * n], dev, torch), f32=True))
+    c = type("Pool", (), {})()
+    c.kv, c.values = kv, lambda b: (k[b], v[b])
+    c.magnitudes = lambda t: Cache.magnitudes(c, t)
+    Qv = got[0][:, :Hq * D].float().cpu().numpy().astype(np.float64).reshape(2, Hq, D)
+    check_attention(c, Qv, got[1], got[2], [1, 1], [n, n], Hq, D ** -0.5, True, 0, fmt, "nvfp4" if fmt == "nvfp4" else "few")
+    assert torch.isfinite(got[3].float()).all()
+
+
+def test_nothing_to_do(td):
+    """No sequences, sequences without rows, rows without sequences, no kept tokens: nothing is read or written."""
+    torch, dev = td
+    kv = sq.KvLayout("int4", 2, 64, 16)
+    c = Cache(torch, dev, kv, [40, 3], 1)
+    was = c.pool.clone()
+    none, zero = torch.zeros((0, 256), device=dev).bfloat16(), i32([0, 0, 0], dev, torch)
+    lens, no_lens, no_table = i32([40, 3], dev, torch), i32([], dev, torch), c.table[:0]
+    half = none[:, :128]
+    for table, n, cu in ((no_table, no_lens, None), (no_table, no_lens, zero[:1]), (c.table, lens, zero)):
+        assert sq.kv_append(kv, c.pool, table, n, half, half, cu=cu, Q=none).shape == (0, 256)
+        assert sq.kv_attention(kv, c.pool, table, n, none, cu=cu).shape == (0, 256)
+        assert sq.kv_read(kv, c.pool, table, n, 0, cu=cu)[0].shape == (0, 128)
+    q, out = torch.ones((5, 256), device=dev).bfloat16(), torch.full((5, 256), 9.0, device=dev).bfloat16()
+    sq.kv_attention(kv, c.pool, c.table, lens, q, cu=zero, out=out)
+    sq.kv_append(kv, c.pool, c.table, lens, q[:, :128], q[:, 128:], cu=zero)
+    assert (out == 9.0).all()
+    sq.kv_compact(kv, c.pool, c.table, i32([[0, 1], [0, 1]], dev, torch), i32([0, -5], dev, torch))
+    sq.kv_compact(kv, c.pool, c.table, i32([[], []], dev, torch), i32([7, 7], dev, torch))
+    sq.kv_compact(kv, c.pool, no_table, i32(np.zeros((0, 4)), dev, torch), no_lens)
+    assert torch.equal(c.pool, was)

@@ -435,7 +435,7 @@ def _int_rows(t, name: str, rows: int, device) -> int:
     if len(shape) != 2 or shape[0] != rows or t.dtype is not _torch().int32 or t.device != device:
         raise ValueError(f"{name}: expected {rows} rows of int32 on {device}, got {tuple(shape)} of {t.dtype} on {t.device}")
     ld, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
+    if inner != 1 and shape[1] > 1 and rows:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return ld if rows > 1 else shape[1]
 
