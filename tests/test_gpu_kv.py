@@ -212,9 +212,11 @@ def test_attention_long(td, fmt):
     for lens, Hq, cols in (([70001], 2, None), ([3, 40000, 5], 1, None), (short, 2, None), (short, 2, 100), (short[:200], 2, 100), (short[:200] + [5000], 2, 100)):
         c = Cache(torch, dev, kv, lens, 9, cols=cols)
         Qv = c.bf16(c.rng.standard_normal((len(lens), Hq, 64)))
-        out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(len(lens), -1)), lse=True)
-        check_attention(c, Qv, out, lse, [1] * len(lens), lens, Hq, 0.125, True, 0, f"{fmt} {len(lens)}",
-                        "nvfp4" if fmt == "nvfp4" else "few")
+        for window in (0, 1500, 37777, 500):                           # the last is no longer split
+            out, lse = sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), c.dev_bf16(Qv.reshape(len(lens), -1)),
+                                       window=window, lse=True)
+            check_attention(c, Qv, out, lse, [1] * len(lens), lens, Hq, 0.125, True, window, f"{fmt} {len(lens)} {window}",
+                            "nvfp4" if fmt == "nvfp4" else "few")
 
 
 @pytest.mark.parametrize("fmt", FMTS)

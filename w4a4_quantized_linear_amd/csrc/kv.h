@@ -67,18 +67,24 @@ inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most)
 //   4 of 4000, 1536 rows, 384 tiles 165 / 148
 //   1 of 8192, 4096 rows, 256 tiles 220 / 215                        1 of 8192, 8192 rows, 512 tiles 372 / 265
 // (INT4 alike: 512 tiles 141 / 108, 256 tiles 263 / 277.)
-// Split where a table's tokens are many for the tiles there are (more than 16 a tile, at least 1024, at most 4096: a few
-// long sequences among many short ones are not to be a workgroup's each), whole / split, 8 heads, one query of 8 heads,
-// ragged and (all of one length): 8 tiles, 512 tokens 8.0 / 10.0, 1024 10.4 / 10.2, 2048 15.1 / 10.5; 64 tiles, 1024 10.4
-// / 11.1 (10.6 / 11.2), 2048 15.3 / 13.0 (15.5 / 13.3); 128 tiles, 2048 15.5 / 14.8 (15.9 / 17.8), 4096 24.7 / 18.4
-// (25.5 / 24.1); 256 tiles, 4096 25.9 / 25.7 (26.9 / 34.9), 8192 44.2 / 36.2 (46.3 / 55.1); 2048 tiles, 4096 122 / 125
-// (204 / 221); 32 rows: 128 tiles, 2048 25.5 / 22.0 (26.8 / 23.8), 256 tiles, 4096 43.8 / 41.3 (45.1 / 44.0), 8192 76.3 /
-// 56.2 (80.1 / 71.6), 1024 tiles, 4096 95.5 / 94.6 (136 / 145), 8192 174 / 164 (280 / 286); INT4 alike.
+// Split where a table's tokens are many for the tiles there are: more than 16 a tile, at least 1024 (32 rows: 12 and
+// 512), at most 4096, since a few long sequences among many short ones are not to be a workgroup's each.  Whole / split,
+// 8 heads, ragged lengths (and all of one):
+//   16 rows    8 tiles  512 8.0 / 10.0    1024 10.4 / 10.2    2048 15.1 / 10.5
+//             64        1024 10.4 / 11.1 (10.6 / 11.2)        2048 15.3 / 13.0 (15.5 / 13.3)
+//            128        2048 15.5 / 14.8 (15.9 / 17.8)        4096 24.7 / 18.4 (25.5 / 24.1)
+//            256        4096 25.9 / 25.7 (26.9 / 34.9)        8192 44.2 / 36.2 (46.3 / 55.1)
+//           2048        4096 122 / 125 (204 / 221)
+//   32 rows    8        512 13.1 / 13.0    1024 17.9 / 13.2
+//            128        1024 16.6 / 17.9 (17.1 / 19.4)        1536 21.3 / 20.1 (21.8 / 21.7)    2048 25.5 / 22.0
+//            256        2048 26.5 / 27.7 (27.4 / 30.3)        4096 43.8 / 41.3 (45.1 / 44.0)    8192 76.3 / 56.2
+//           1024        4096 95.5 / 94.6 (136 / 145)          8192 174 / 164 (280 / 286)
+// INT4 alike.
 // Ranges: three workgroups a CU (1, 2, 3, 4 a CU: 64 x 8192 MXFP4 76.9 63.7 59.7 63.4, 3 x 131072 38.7 35.0 35.7
 // 38.2, INT4 64 x 8192 89.3 75.7 69.0 72.7), two where a wave has 32 rows and registers for two.
-constexpr int64_t kKvWhole = 1024;           // tokens of a table up to which a job is one workgroup's, at least
+constexpr int64_t kKvWhole = 1024;           // tokens up to which a job is one workgroup's, at least (32 rows: half)
 constexpr int64_t kKvWholeMany = 4096;       // and at most
-constexpr int64_t kKvWholeTile = 16;         // between them, for each tile
+constexpr int64_t kKvWholeTile = 16;         // between them, for each tile (32 rows: 12)
 struct KvPlan {
   int rows, jobs, ranges;
   bool split;
@@ -91,8 +97,9 @@ inline KvPlan kv_plan(int D, int batch, int64_t M, int q_heads, int heads, int64
   p.rows = each <= 16 ? 16 : each >= 128 && M * q_heads >= 384 * 128 ? 128 : 32;
   const int64_t jobs = tiles(p.rows);
   p.jobs = int(jobs);
-  const int64_t whole = kKvWholeTile * heads * (jobs - batch > batch ? jobs - batch : batch);
-  p.split = p.rows < 128 && places > (whole < kKvWhole ? kKvWhole : whole > kKvWholeMany ? kKvWholeMany : whole) &&
+  const int64_t least = p.rows == 16 ? kKvWhole : kKvWhole / 2, each_tile = p.rows == 16 ? kKvWholeTile : 12;
+  const int64_t whole = each_tile * heads * (jobs - batch > batch ? jobs - batch : batch);
+  p.split = p.rows < 128 && places > (whole < least ? least : whole > kKvWholeMany ? kKvWholeMany : whole) &&
             jobs * (places / 128 + 1) <= INT32_MAX - 4096;     // units are counted in 32 bits
   p.ranges = p.split ? (256 * (p.rows == 16 ? 3 : 2) + heads - 1) / heads : 0;
   p.bytes = p.split ? align256(size_t(p.ranges) * heads * 2 * p.rows * (D + 2) * 4) : 0;

@@ -139,7 +139,8 @@ __device__ __forceinline__ double rsqrt64(double x) {
 // or on a sine's last bit; the angle pos x freq is a 64-bit product, which holds far positions.  Q's are
 // in 32 bits with the same sines.
 // 9165 rows, 32 + 2 x 8 heads of 128, NVFP4, norm and three axes (209 MB): with a feature pair a lane, IEEE divisions
-// and 64-bit quotients it was bound by its instructions, 98 us.
+// and 64-bit quotients it was bound by its instructions, 98 us; so 57.7
+// (3.6 TB/s).
 template <int FMT, int D>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend a, int parts) {
   constexpr int L = D / 8, HPW = 64 / L, G = kv_group(FMT), AHEAD = 2;
@@ -379,7 +380,8 @@ struct KvMoved {
 // A wave fills a tile of the new places of one sequence: it finds where the tile's 16 tokens come from once, then
 // gathers and writes the tile of every head and layer (of a part of them where there are few tiles), the next one's
 // loads on their way before the stores.  With a tile of one head a wave the four dependent loads in front (count,
-// index, page, bytes) cost as much as the bytes: 18000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) took 72 us.  In place a
+// index, page, bytes) cost as much as the bytes: 32 sequences' 20 tokens, 24 layers of 8 heads took 11.0 us, so 6.4.  18000
+// of 60000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) take 72 us: of the lines read, most bytes are other tokens'.  In place a
 // workgroup walks a sequence's tiles in order, four at a time, all loads of a head before its stores: the tokens that
 // are kept come in rising order, so those of later tiles lie behind every place written so far.
 enum { kApart = 0, kInPlace = 1, kInPlaceByWave = 2, kThrough = 3, kBack = 4 };

@@ -607,7 +607,7 @@ struct KvScan {
   // Cuts the units into ranges.  Evenly, so that a range may end one job and begin others; but where ranges are
   // short, what a second job costs (its rows, pages and first tokens one after the other, some 5 us) is more than an
   // uneven cut: then a job is cut into as many ranges as it has `per` units, if all of them are no more than the
-  // workgroups there are (16 sequences of 400 .. 4000 tokens, 8 heads: 17.0 us evenly).
+  // workgroups there are (16 sequences of 400 .. 4000 tokens, 8 heads: 17.0 us evenly, 14.9 so).
   __device__ __forceinline__ void cut(int ranges) {
     per = max((total + ranges - 1) / ranges, kLeastUnits);
     if (kc.batch == 1 || kc.batch > 64 || per > kShortUnits) return;
@@ -916,7 +916,8 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
 // of 64; of a chunk each wave makes one tile's operands 16-bit and puts them in LDS in operand order (K's of a
 // tile, its half of V's of a step of 32 tokens), the next chunk's while this one is worked on, with a barrier a chunk.
 // Then a wave's vector instructions are the softmax's and a quarter of the conversions.  2048 queries x 32 heads on
-// 8192 tokens, 8 heads of 128, MXFP4 (241 GFLOP): a wave converting for itself 312 us.
+// 8192 tokens, 8 heads of 128, MXFP4 (241 GFLOP): a wave converting for itself 312 us, so 243
+// (987 TFLOP/s).
 template <int FMT, int D>
 struct KvShared {
   uint4 k[2][4][D / 32][64];
@@ -1282,7 +1283,13 @@ void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_
 hipError_t launch_kv_attention(int fmt, int D, const KvCache& kc, const uint16_t* Q, int64_t ldq, int q_heads,
                                float scale, int window, bool causal, uint16_t* Y, int64_t ldy, float* lse, float* part,
                                hipStream_t s) {
-  const KvPlan p = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
+  KvPlan p = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads, kc.capacity());
+  // A window is all that a row sees of a long table: where its tokens would not be split, they are not (8 heads to 8192
+  // tokens, split / whole: window 512, 4 sequences 10.9 / 8.5 us, 64 17.5 / 12.5; 1024, 1 10.2 / 10.2, 64 24.2 / 18.2).
+  if (p.split && window > 0 && causal && window < kc.capacity()) {
+    const KvPlan w = kv_plan(D, kc.batch, kc.M, q_heads, kc.heads, window);
+    if (!w.split) p = w;
+  }
   if (window > INT32_MAX - int(kKvMaxRows) - 1) window = INT32_MAX - int(kKvMaxRows) - 1;   // a row's place minus it fits
   const KvAttn a = {Q, Y, lse, part, ldq, ldy, q_heads / kc.heads, q_heads, window, causal ? 1 : 0, p.ranges,
                     scale * 1.44269504088896341f};
