@@ -388,3 +388,43 @@ def test_nothing_to_do(td):
     sq.kv_compact(kv, c.pool, c.table, i32([[], []], dev, torch), i32([7, 7], dev, torch))
     sq.kv_compact(kv, c.pool, no_table, i32(np.zeros((0, 4)), dev, torch), no_lens)
     assert torch.equal(c.pool, was)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pool_of_many_gigabytes(td, fmt):
+    """Two layers of over 4 GiB each: the calls on pages at both ends give the bytes of the same calls on a small pool."""
+    torch, dev = td
+    kv = sq.KvLayout(fmt, 8, 128, 1024)
+    per = sq.kv_page_bytes(kv)
+    pages = (5 << 30) // per + 3
+    if torch.cuda.mem_get_info()[0] < 3 * pages * per:
+        pytest.skip("memory")
+    big = torch.empty((2, pages, per), dtype=torch.uint8, device=dev)
+    small = torch.full((2, 8, per), 255, dtype=torch.uint8, device=dev)
+    where = [0, pages - 1, pages // 2, pages - 2, 1, pages - 3, pages - 4, 2]      # of the small pool's pages
+    big[:, where] = small
+    tab = np.array([[0, 1, 2], [3, 4, 5]])
+    tables = {id(small): i32(tab, dev, torch), id(big): i32(np.array(where)[tab], dev, torch)}
+    lens, cu = [3000, 2100], [0, 3000, 5100]
+    g = torch.Generator(device=dev)
+    g.manual_seed(2)
+    x = torch.randn((5100, 2 * 1024), generator=g, device=dev).bfloat16()
+    q1, q9 = (torch.randn((n, 16 * 128), generator=g, device=dev).bfloat16() for n in (2, 1800))
+    keep = i32([sorted(np.random.default_rng(b).choice(2000, 900, replace=False)) for b in range(2)], dev, torch)
+
+    def run(pool):
+        table, n = tables[id(pool)], i32(lens, dev, torch)
+        at = (lambda p: where[p]) if pool is big else (lambda p: p)
+        for layer in pool:
+            sq.kv_append(kv, layer, table, n, x[:, :1024], x[:, 1024:], cu=i32(cu, dev, torch))
+        got = [sq.kv_attention(kv, layer, table, n, q1) for layer in pool]
+        got.append(sq.kv_attention(kv, pool[1], table, n, q9, cu=i32([0, 900, 1800], dev, torch)))
+        sq.kv_copy(kv, pool, [at(2), at(5)], [at(6), at(7)])
+        sq.kv_compact(kv, pool, table, keep, i32([900, 900], dev, torch))
+        to = i32([[at(2)], [at(5)]], dev, torch)
+        sq.kv_compact(kv, pool, table[:, :2].contiguous(), keep[:, :100].contiguous(), i32([100, 100], dev, torch), to=to)
+        return got + list(sq.kv_read(kv, pool[1], to, i32([100, 100], dev, torch), 200, cu=i32([0, 100, 200], dev, torch)))
+
+    for a, b in zip(run(big), run(small)):
+        assert torch.equal(a, b)
+    assert torch.equal(big[:, where], small)
