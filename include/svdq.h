@@ -341,8 +341,9 @@ size_t svdq_kv_page_bytes(const svdq_kv_desc* d);
  *         features from 2 pairs on stay
  * so several axes (time, height, width) share a head as the caller lays them out.  K is rounded
  * to fp32, to bf16, then quantized; its norm and rotation are computed in float64, so its codes
- * do not hang on an order of summation.  Q is computed in fp32 (the sines in float64) and written as
- * bf16.  V is quantized as it is.  A NaN in K or V is stored as 0, an infinity as the largest bf16 of
+ * do not hang on an order of summation.  Q is computed in fp32 (in float64 the sines, and the norm of a
+ * head whose squares leave fp32) and written as bf16; a head of zeros is NaN with eps 0, as the formula
+ * has it.  V is quantized as it is.  A NaN in K or V is stored as 0, an infinity as the largest bf16 of
  * its sign: whatever a pool is given, no token's values are NaN or infinite.
  *   K, V     device, bf16 bits, M x heads head_dim, row strides ldk, ldv (parts of one projection's
  *            rows, say)

@@ -1,0 +1,63 @@
+"""The 4-bit key-value cache at its edges: Q heads of any magnitude."""
+import numpy as np
+import pytest
+
+import w4a4_quantized_linear_amd as sq
+from oracle import kv as Kv
+
+from _kv_helpers import bits, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def td():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sq.lib()
+    assert sq.device_check(), "current device is not gfx950"
+    return torch, torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1.0])
+@pytest.mark.parametrize("pairs", [0, 16])
+def test_append_norm_of_any_magnitude(td, D, eps, pairs):
+    """Q heads whose squares leave float32 on either side are normalized as the others, and the others keep their bits
+    beside them."""
+    torch, dev = td
+    kv = sq.KvLayout("mxfp4", 1, D, 16)
+    rng = np.random.default_rng(D)
+    mags = [2.0 ** e for e in (-133, -126, -100, -80, -66, -45, -41, -40, -39, -20, 0, 20, 58, 61, 62, 64, 80, 100, 125)]
+    M, Hq = 5, len(mags)
+    x = rng.standard_normal((M, Hq, D)) * np.array(mags)[None, :, None]
+    x[0] = np.array(mags)[:, None]                                    # alike values: the largest sums
+    x[1, :, 1:] = 0                                                   # one value
+    x = np.clip(Kv.F.to_bf16(x), -Kv.BF16_MAX, Kv.BF16_MAX)
+    x[:, :, 0] = np.where(np.abs(x).max(-1) == 0, 2.0 ** -133, x[:, :, 0])        # no head of zeros: 0 / 0 with eps 0
+    w = Kv.F.to_bf16(1 + 0.2 * rng.standard_normal(D))
+    freq = (100.0 ** (-np.arange(pairs) / 16)).astype(np.float32)
+    place = np.arange(M)
+    bf = lambda t: torch.tensor(np.asarray(t), dtype=torch.float32).bfloat16().to(dev)
+    pool = torch.zeros((1, sq.kv_page_bytes(kv)), dtype=torch.uint8, device=dev)
+    row, lens, cu = bf(rng.standard_normal((M, D))), i32([M], dev, torch), i32([0, M], dev, torch)
+    more = dict(freq=torch.tensor(freq, device=dev)) if pairs else {}
+    call = lambda v: sq.kv_append(kv, pool, i32([[0]], dev, torch), lens, row, row, cu=cu, Q=bf(v.reshape(M, -1)), norm_q=bf(w),
+                                  eps=eps, **more)
+    out = call(x)
+    how = dict(freq=freq, pos=place[None]) if pairs else {}
+    z = Kv.head_rows(x, w, eps, **how)
+    plain = np.abs(Kv.head_rows(x, w, eps))
+    # float32: the mean of squares (D / 2 + 8 roundings), root, quotient and products at 2^-24 each, of either feature;
+    # bf16's half step, 2^-134 below its normal numbers, and float32's own subnormals on the way
+    lim = 2.0 ** -8 * np.abs(z) + (D / 2 + 16) * 2.0 ** -24 * 2 * plain.max(-1, keepdims=True) + 2.0 ** -134 + 2.0 ** -148
+    err = np.abs(bits(out).reshape(z.shape) - z)
+    assert np.isfinite(bits(out)).all() and (err <= lim).all(), \
+        [(m, float((err / lim)[:, i].max())) for i, m in enumerate(mags) if not (err[:, i] <= lim[:, i]).all()]
+    ordinary = np.where(np.isin(mags, [2.0 ** -20, 1.0, 2.0 ** 20])[None, :, None], x, 1.0)
+    alone = call(ordinary).view(M, Hq, D)
+    for i, m in enumerate(mags):
+        if m in (2.0 ** -20, 1.0, 2.0 ** 20):
+            assert torch.equal(alone[:, i], out.view(M, Hq, D)[:, i])
+

@@ -132,12 +132,25 @@ __device__ __forceinline__ double rsqrt64(double x) {
   return y;
 }
 
+// A head's 8 features of a lane, normalized in 64 bits.
+template <int D>
+__device__ __forceinline__ void norm64(double (&z)[8], const float (&w)[8], float eps) {
+  double sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = fma(z[j], z[j], sum);
+  const double mean = group_sum<D / 8>(sum) * (1.0 / D) + double(eps);
+  // a row of zeros with eps 0, or of infinities: as the definition has it
+  const double k = mean > 0 && mean < __builtin_huge_val() ? rsqrt64(mean) : 1 / sqrt(mean);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = z[j] * k * w[j];
+}
+
 // A wave takes units of one row: 8 features a lane, so D / 8 lanes a head, and 4 heads (of 64 features: 8) of K, V
 // or Q at once; all units of a row, or every `parts`-th where few rows would leave CUs idle.  The inputs of the next
 // units are on their way while one is worked on.  A row's sines are computed once by its wave, pair p in lane p.
 // K's norm and rotation are in 64 bits, so that its codes, which are choices, do not hang on an order of summation
 // or on a sine's last bit; the angle pos x freq is a 64-bit product, which holds far positions.  Q's are
-// in 32 bits with the same sines.
+// in 32 bits with the same sines, but for the norm of a head whose squares are not in their range.
 // 9165 rows, 32 + 2 x 8 heads of 128, NVFP4, norm and three axes (209 MB): with a feature pair a lane, IEEE divisions
 // and 64-bit quotients it was bound by its instructions, 98 us; so 57.7
 // (3.6 TB/s).
@@ -247,16 +260,9 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] = x[j];
       if (a.norm_k != nullptr) {
-        double sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fma(z[j], z[j], sum);
-        const double mean = group_sum<L>(sum) * (1.0 / D) + double(a.eps);
-        // a row of zeros with eps 0, or of infinities: as the definition has it
-        const double k = mean > 0 && mean < __builtin_huge_val() ? rsqrt64(mean) : 1 / sqrt(mean);
         float w[8];
         unpack_bf8(wk, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = z[j] * k * w[j];
+        norm64<D>(z, w, a.eps);
       }
       if (r.pairs > 0) turn<L, double>(z, r, l, sines);
 #pragma unroll
@@ -282,10 +288,23 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
       float sum = 0.f, w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
-      const float k = __builtin_amdgcn_rsqf(group_sum<L>(sum) * (1.0f / D) + a.eps);
+      sum = group_sum<L>(sum);
+      const float k = __builtin_amdgcn_rsqf(sum * (1.0f / D) + a.eps);
       unpack_bf8(wq, w);
+      // Squares that leave 32 bits, above or (with an eps no larger) below: the head in 64 bits.  From 2^-80 on the
+      // squares that underflow are no part of the sum's 24 bits.
+      const bool in32 = sum >= 0x1p-80f && sum <= 0x1p127f;
+      if (__any(!in32)) {
+        double z[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * k * w[j];
+        for (int j = 0; j < 8; ++j) z[j] = x[j];
+        norm64<D>(z, w, a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = in32 ? x[j] * k * w[j] : float(z[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * k * w[j];
+      }
     }
     if (r.pairs > 0) turn<L, float>(x, r, l, sines32);
     const int h = (u - 2 * kv_units) * HPW + lane / L;
