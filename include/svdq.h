@@ -385,7 +385,8 @@ svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages,
  *   lse    device, float32, M x q_heads, or NULL
  *   workspace  device, svdq_kv_attention_bytes(d, cols, batch, M, q_heads) bytes, 256-byte aligned (NULL
  *              where that is 0); every call writes what it reads of it
- * A row with a NaN or an infinity in Q, or for which scale |Q| or a score leaves fp32's range, has no defined result; no other row changes.
+ * A row with a NaN or an infinity in Q, or for which scale |Q| or a score leaves fp32's range, has no
+ * defined result; it changes no bit of another row.
  * M x q_heads <= 2^27 and q_heads <= 4096, else SVDQ_ERR_SHAPE. */
 size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t cols, int32_t batch, int64_t M, int32_t q_heads);
 svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,

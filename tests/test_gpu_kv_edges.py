@@ -1,13 +1,14 @@
-"""The 4-bit key-value cache at its edges: Q heads of any magnitude."""
+"""The 4-bit key-value cache at its edges: Q heads of any magnitude, rows beside an infinity."""
 import numpy as np
 import pytest
 
 import w4a4_quantized_linear_amd as sq
 from oracle import kv as Kv
 
-from _kv_helpers import bits, i32
+from _kv_helpers import Cache, bits, i32
 
 pytestmark = pytest.mark.gpu
+FMTS = ["mxfp4", "int4", "nvfp4"]
 
 
 @pytest.fixture(scope="module")
@@ -61,3 +62,42 @@ def test_append_norm_of_any_magnitude(td, D, eps, pairs):
         if m in (2.0 ** -20, 1.0, 2.0 ** 20):
             assert torch.equal(alone[:, i], out.view(M, Hq, D)[:, i])
 
+
+FORMS = {
+    # query rows a sequence, lengths, query heads, heads, columns of the table: each form of the call
+    "16 rows": ([1, 1], [700, 900], 4, 1, None),
+    "16 rows, ranges": ([1], [9000], 4, 1, None),
+    "32 rows": ([6, 5], [700, 900], 4, 1, None),
+    "32 rows, ranges": ([6], [9000], 4, 1, None),
+    "128 rows": ([768], [2000], 64, 8, None),
+}
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("name", list(FORMS))
+def test_attention_rows_beside_an_infinity(td, fmt, name):
+    """A row with an infinity, whose scores are lowest at first and highest behind, leaves every bit of the others."""
+    torch, dev = td
+    q_lens, lens, Hq, H, cols = FORMS[name]
+    kv = sq.KvLayout(fmt, H, 64, 32)
+    c = Cache(torch, dev, kv, lens, 17, cols=cols, gain=False)
+    K = c.K.copy()
+    at = np.concatenate([np.arange(n) for n in lens])
+    K[:, :, 5] = np.where(at % 700 < 300, -2.0, 2.0)[:, None]
+    n32, all32 = i32(lens, dev, torch), i32(c.cu, dev, torch)
+    sq.kv_append(kv, c.pool, c.table, n32, c.dev_bf16(K.reshape(len(K), -1)), c.dev_bf16(c.V.reshape(len(K), -1)), cu=all32)
+    M = sum(q_lens)
+    q = c.dev_bf16(c.rng.standard_normal((M, Hq * 64)) * 1.5)
+    cu = None if set(q_lens) == {1} else i32(np.r_[0, np.cumsum(q_lens)], dev, torch)
+    for value in (float("inf"), float("nan")):
+        bad = q.clone()
+        rows = [(m, 0) for m in range(0, M, 7)]
+        for m, h in rows:
+            bad[m, h * 64 + 5] = value
+        a, la = sq.kv_attention(kv, c.pool, c.table, n32, q, cu=cu, lse=True)
+        b, lb = sq.kv_attention(kv, c.pool, c.table, n32, bad, cu=cu, lse=True)
+        other = torch.ones((M, Hq), dtype=torch.bool, device=dev)
+        for m, h in rows:
+            other[m, h] = False
+        assert torch.equal(la[other], lb[other]), f"{value}: lse of {int((la[other] != lb[other]).sum())} other rows"
+        assert torch.equal(a.view(M, Hq, 64)[other], b.view(M, Hq, 64)[other]), f"{value}: other rows"

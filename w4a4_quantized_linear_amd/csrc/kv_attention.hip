@@ -445,7 +445,8 @@ __device__ __forceinline__ float largest(const float (&x)[N]) {
 }
 
 // Probabilities e of the scores z, relative to the running maxima, which move where a score exceeds one by kGrow; l, O
-// and off with them.  The scores are brought to the exponent first and their largest sought there: what a matrix
+// and off with them.  A column's maximum moves by its own scores alone, so no row's bits hang on what stands beside it
+// (a row of infinities, say).  The scores are brought to the exponent first and their largest sought there: what a matrix
 // instruction gives would cost one more operation each on its way into a maximum.
 template <int FMT, int D, int NQ, int T>
 __device__ __forceinline__ void probabilities(const float (&z)[NQ][T][4], const float (&k2)[NQ], float (&m)[NQ],
@@ -466,7 +467,9 @@ __device__ __forceinline__ void probabilities(const float (&z)[NQ][T][4], const 
       float top = z[n][0][0];
 #pragma unroll
       for (int i = 1; i < 4 * T; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
-      const float now = fmaxf(m[n], rowgroup_max(top) * k2[n]), x = __builtin_amdgcn_exp2f(m[n] - now);
+      top = rowgroup_max(top);
+      const bool up = fmaf(top, k2[n], kUp - m[n]) > kGrow + kUp;
+      const float now = up ? top * k2[n] : m[n], x = __builtin_amdgcn_exp2f(m[n] - now);
       m[n] = now;
       l[n] *= x;
 #pragma unroll
