@@ -1,4 +1,4 @@
-"""The 4-bit key-value cache at its edges: Q heads of any magnitude, rows beside an infinity."""
+"""The 4-bit key-value cache at its edges: Q heads of any magnitude, rows beside an infinity, windows beyond int32."""
 import numpy as np
 import pytest
 
@@ -101,3 +101,16 @@ def test_attention_rows_beside_an_infinity(td, fmt, name):
             other[m, h] = False
         assert torch.equal(la[other], lb[other]), f"{value}: lse of {int((la[other] != lb[other]).sum())} other rows"
         assert torch.equal(a.view(M, Hq, 64)[other], b.view(M, Hq, 64)[other]), f"{value}: other rows"
+
+
+def test_attention_window_beyond_int32(td):
+    torch, dev = td
+    kv = sq.KvLayout("mxfp4", 1, 64, 16)
+    c = Cache(torch, dev, kv, [40], 3)
+    q, n32 = torch.zeros((1, 64), device=dev).bfloat16(), i32([40], dev, torch)
+    for window in (1 << 31, (1 << 32) + 5, -(1 << 32) + 5, -(1 << 31) - 1, -(1 << 33)):
+        with pytest.raises(ValueError):
+            sq.kv_attention(kv, c.pool, c.table, n32, q, window=window)
+    for window in (-1, -(1 << 31)):
+        with pytest.raises(sq.SvdqError):
+            sq.kv_attention(kv, c.pool, c.table, n32, q, window=window)

@@ -557,7 +557,7 @@ def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = Non
     D, shape = kv.head_dim, Q.shape
     if len(shape) != 2 or shape[1] % D:
         raise ValueError(f"Q: expected rows of heads x {D}, got {tuple(shape)}")
-    if window >= 1 << 31:
+    if not -(1 << 31) <= window < 1 << 31:
         raise ValueError(f"window: expected an int32, got {window}")
     M, cols = shape
     q_heads = cols // D
