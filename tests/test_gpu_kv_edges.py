@@ -1,11 +1,12 @@
-"""The 4-bit key-value cache at its edges: Q heads of any magnitude, rows beside an infinity, windows beyond int32."""
+"""The 4-bit key-value cache at its edges: Q heads of any magnitude, rows beside an infinity, windows beyond int32, rows in front
+of the sequences."""
 import numpy as np
 import pytest
 
 import w4a4_quantized_linear_amd as sq
 from oracle import kv as Kv
 
-from _kv_helpers import Cache, bits, i32
+from _kv_helpers import Cache, bits, check_attention, i32
 
 pytestmark = pytest.mark.gpu
 FMTS = ["mxfp4", "int4", "nvfp4"]
@@ -114,3 +115,22 @@ def test_attention_window_beyond_int32(td):
     for window in (-1, -(1 << 31)):
         with pytest.raises(sq.SvdqError):
             sq.kv_attention(kv, c.pool, c.table, n32, q, window=window)
+
+
+@pytest.mark.parametrize("q_lens,Hq,H", [([8] * 90, 8, 1), ([0, 3, 24, 0, 8, 1, 40] * 11, 4, 1), ([1] * 130, 40, 1)])
+@pytest.mark.parametrize("before", [4, 32, 100])
+def test_attention_many_rows_in_front(td, q_lens, Hq, H, before):
+    """Rows of no sequence that would be tiles, in front of more than 64 sequences."""
+    torch, dev = td
+    rng = np.random.default_rng(4)
+    lens = [int(q + x) for q, x in zip(q_lens, rng.integers(0, 20, len(q_lens)))]
+    kv = sq.KvLayout("mxfp4", H, 64, 16)
+    c = Cache(torch, dev, kv, lens, 18)
+    M = sum(q_lens)
+    Qv = c.bf16(c.rng.standard_normal((M, Hq, 64)))
+    q = torch.cat([torch.zeros((before, Hq * 64), device=dev).bfloat16(), c.dev_bf16(Qv.reshape(M, -1))])
+    out, lse = torch.full_like(q, 7.0), torch.full((len(q), Hq), 7.0, device=dev)
+    sq.kv_attention(kv, c.pool, c.table, i32(lens, dev, torch), q, cu=i32(before + np.r_[0, np.cumsum(q_lens)], dev, torch),
+                    out=out, lse=lse)
+    check_attention(c, Qv, out[before:], lse[before:], q_lens, lens, Hq, 0.125, True, 0, "rows in front", "few")
+    assert (out[:before] == 7.0).all() and (lse[:before] == 7.0).all()

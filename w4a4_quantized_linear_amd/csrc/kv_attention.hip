@@ -544,7 +544,8 @@ __device__ __forceinline__ KvJob kv_job(const KvCache& kc, const KvAttn& a, int 
     lo += k * step;
     n = min(step, n - k * step);
   }
-  return {lo, 1 + index - uni(from(lo))};
+  const int at = index - uni(from(lo));                        // below 0: rows in front of the first sequence
+  return {lo, at < 0 ? -1 : 1 + at};
 }
 
 // The work of all sequences in units (of jobs x tokens), and the sequence that unit `at` falls into with the units
