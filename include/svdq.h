@@ -409,7 +409,8 @@ svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32
  * accepted, tokens that eviction keeps.)  The sequence then has start[b] + n_keep[b] tokens; pages
  * behind those are free.
  *   table    device, batch x cols, ldt: where the tokens are
- *   to       device, batch x cols_to, ldto: where they go, none of these pages in `table`; NULL: in place.
+ *   to       device, batch x cols_to, ldto: where they go, none of these pages in `table`; NULL, or `table`
+ *            itself (with its columns and stride, else SVDQ_ERR_SHAPE): in place.
  *            Tokens before start[b] do not move in either case
  *   start    device, int32[batch], or NULL: 0
  *   keep     device, int32, batch x most, row stride ldkeep: rising, and so keep[i] >= start + i in place

@@ -185,3 +185,12 @@ def test_host_tensors_and_shapes():
         with pytest.raises(ValueError):
             call()
     assert sq.kv_page_bytes(sq.KvLayout("mxfp4", 2, 96, 16)) == 0
+
+
+def test_compact_onto_its_own_table(L, forced_device_error):
+    """The same table is in place; a part of it, or its bytes with another stride, is neither form."""
+    per = L.svdq_kv_page_bytes(D())
+    call = caller(L.svdq_kv_compact, [D(), P, 100, 2, 100 * per, P, 8, 8, P, 8, 8, P, P, 50, 50, P, 5, None, 0, None])
+    assert call() == 6 and call(_16=1, _9=20) == 6 and call(_16=0) == 6
+    for bad in (dict(_10=6), dict(_9=16), dict(_9=16, _10=16), dict(_10=6, _16=1)):
+        assert call(**bad) == 2, bad

@@ -608,7 +608,8 @@ svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, in
   KvCache kc;
   svdq_status s = check_cache(d, pool, pages, table, ldt, cols, n_keep, nullptr, batch, batch, &kc);
   if (s == SVDQ_ERR_SHAPE || planes < 1 || planes > kKvMaxPlanes || most < 0 || most > kKvMaxTokens || ldkeep < most ||
-      (to && (cols_to < 1 || ldto < cols_to || int64_t(cols_to) * d->page > kKvMaxTokens)))
+      (to && (cols_to < 1 || ldto < cols_to || int64_t(cols_to) * d->page > kKvMaxTokens)) ||
+      (to && in_place && (cols_to != cols || (batch > 1 && ldto != ldt))))
     return SVDQ_ERR_SHAPE;
   if (s == SVDQ_ERR_FORMAT) return s;
   if (planes > 1 && plane_bytes < pages * kv_page_bytes(d)) return SVDQ_ERR_SHAPE;
