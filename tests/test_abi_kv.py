@@ -194,3 +194,19 @@ def test_compact_onto_its_own_table(L, forced_device_error):
     assert call() == 6 and call(_16=1, _9=20) == 6 and call(_16=0) == 6
     for bad in (dict(_10=6), dict(_9=16), dict(_9=16, _10=16), dict(_10=6, _16=1)):
         assert call(**bad) == 2, bad
+
+
+@pytest.mark.parametrize("wrap", [1 << 32, -(1 << 32), 1 << 64])
+def test_numbers_beyond_int32(wrap):
+    """A size whose low 32 bits would be a valid one is invalid."""
+    kv = sq.KvLayout("mxfp4", 4, 128, 32)
+    for i in range(3):
+        a = [4, 128, 32]
+        a[i] += wrap
+        assert sq.kv_page_bytes(sq.KvLayout("mxfp4", *a)) == 0
+    for f, ok in ((sq.kv_attention_bytes, [100, 3, 3, 16]), (sq.kv_compact_bytes, [2, 5, 5000])):
+        assert f(kv, *ok) > 0
+        for i in range(len(ok)):
+            a = list(ok)
+            a[i] += wrap
+            assert f(kv, *a) == 0, (f.__name__, i)

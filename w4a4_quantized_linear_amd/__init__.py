@@ -392,6 +392,11 @@ def moe(gate_up: Layer, wg_packed, down: Layer, wd_packed, X, ids, weights, epi:
 # kv_page_bytes (for kv_copy and kv_compact also layers x pages x kv_page_bytes); table (batch x pages of a
 # sequence), lens (batch) and cu (batch + 1, or None: one row a sequence) are int32 tensors beside it.
 
+def _i32(n) -> int:
+    """n for an int32 argument; what does not fit is -1, which no call takes (ctypes would drop the bits above)."""
+    return n if -(1 << 31) <= n < 1 << 31 else -1
+
+
 @dataclass(frozen=True)
 class KvLayout:
     """A key-value cache: 4-bit format, K/V heads, features of a head (64, 128), tokens of a page
@@ -403,7 +408,7 @@ class KvLayout:
     page: int
 
     def desc(self) -> KvDesc:
-        return KvDesc(FORMATS[self.fmt], self.heads, self.head_dim, self.page)
+        return KvDesc(FORMATS[self.fmt], _i32(self.heads), _i32(self.head_dim), _i32(self.page))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -543,7 +548,8 @@ def kv_read(kv: KvLayout, pool, table, lens, M: int, cu=None, f32: bool = False,
 
 def kv_attention_bytes(kv: KvLayout, cols: int, batch: int, M: int, q_heads: int) -> int:
     """Workspace bytes of kv_attention for tables of `cols` pages (0: none needed, or invalid)."""
-    return int(lib().svdq_kv_attention_bytes(_kept_kv(kv)[0], int(cols), int(batch), int(M), int(q_heads)))
+    return int(lib().svdq_kv_attention_bytes(_kept_kv(kv)[0], _i32(int(cols)), _i32(int(batch)), _i32(int(M)),
+                                             _i32(int(q_heads))))
 
 
 def kv_attention(kv: KvLayout, pool, table, lens, Q, cu=None, scale: float = None, window: int = 0, causal: bool = True,
@@ -610,7 +616,8 @@ def kv_copy(kv: KvLayout, pool, src, dst, stream=None):
 
 def kv_compact_bytes(kv: KvLayout, planes: int, batch: int, most: int, in_place: bool = True) -> int:
     """Workspace bytes of kv_compact for lists of `most` tokens (0: none needed, or invalid)."""
-    return int(lib().svdq_kv_compact_bytes(_kept_kv(kv)[0], int(planes), int(batch), int(most), int(in_place)))
+    return int(lib().svdq_kv_compact_bytes(_kept_kv(kv)[0], _i32(int(planes)), _i32(int(batch)), _i32(int(most)),
+                                           bool(in_place)))
 
 
 def kv_compact(kv: KvLayout, pool, table, keep, n_keep, start=None, to=None, workspace=None, stream=None):
