@@ -17,8 +17,8 @@
 //          against -8, is added at the end
 //   NVFP4  fp16: E2M1 times E4M3 (2^-10 .. 2688); Q's rows scaled by a power of two; P fp16, times 2^11 so that
 //          probabilities down to 2^-25 of the largest keep all bits
-// P is rounded to half a unit in its last place (2^-8 of it in bf16, 2^-11 in fp16); with PLANES = 2 what bf16
-// leaves is a second operand (2^-16).
+// P is rounded to half a unit in its last place (2^-8 of it in bf16, 2^-11 in fp16); what bf16 leaves is a second
+// operand (2^-16), but in kv_prompt_kernel, where that would be half again the matrix work.
 #include "kv.h"
 #include "w4frag.h"
 
@@ -312,9 +312,9 @@ __device__ __forceinline__ void kv_store(const KvAttn& a, int64_t token, int hea
 }
 
 // A job is a tile of R query rows of one sequence on one K/V head; its tokens are cut into units of U.
-template <int NQ, int WQ, int WK>
+template <int NQ, int WK>
 struct KvTiles {
-  static constexpr int R = 16 * NQ * WQ, U = 32 * WK;
+  static constexpr int R = 16 * NQ, U = 32 * WK;
 };
 
 struct KvSeq {
@@ -661,17 +661,18 @@ struct KvScan {
   }
 };
 
-template <int FMT, int D, int NQ, int WQ, int WK, int PLANES, bool SPLIT>
-__global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
-  using TL = KvTiles<NQ, WQ, WK>;
-  constexpr int R = TL::R, U = TL::U, NT = 64 * WQ * WK, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1;
-  constexpr int PL = FMT == kFmtNVFP4 ? 1 : PLANES;            // fp16 needs no second plane
+// WK waves take the steps of the same 16 NQ rows in turn.
+template <int FMT, int D, int NQ, int WK, bool SPLIT>
+__global__ void __launch_bounds__(64 * WK, NQ == 1 ? 3 : 2) kv_attention_kernel(KvCache kc, KvAttn a) {
+  using TL = KvTiles<NQ, WK>;
+  constexpr int R = TL::R, U = TL::U, NT = 64 * WK, DT = D / 16, NG = FMT == kFmtINT4 ? D / 64 : 1;
+  constexpr int PL = FMT == kFmtNVFP4 ? 1 : 2;                 // fp16 needs no second plane
   constexpr int TB = kv_tile_bytes(FMT, D), OS = D + 4;        // floats of a row of O in LDS
   __shared__ int sh[16];
-  __shared__ float merge_o[WK > 1 ? WK * 16 * OS : 4];
-  __shared__ float merge_m[WK > 1 ? WK : 1][16], merge_l[WK > 1 ? WK : 1][16];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, c = lane >> 4, wq = wave / WK, wk = wave % WK;
+  __shared__ float merge_o[WK * 16 * OS];
+  __shared__ float merge_m[WK][16], merge_l[WK][16];
+  const int lane = threadIdx.x & 63, wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
   const int h = blockIdx.x % kc.heads, range = blockIdx.x / kc.heads;
 
   int b, job, unit = 0, left = 1;
@@ -715,9 +716,9 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
     }
     const int n_units = min(left, s.units - unit);
     const int tile_rows = SPLIT ? job : s.tiles - 1 - job;    // long causal tiles first
-    const int row0 = tile_rows * R + wq * 16 * NQ;
+    const int row0 = tile_rows * R;
     const KvRows rows(kc, a, s);
-    const KvSpan span = rows.span(row0, 16 * NQ);
+    const KvSpan span = rows.span(row0, R);
     uint4 q[NQ][D / 32];
     float k2[NQ];
     int lo[NQ], hi[NQ];
@@ -870,42 +871,32 @@ __global__ void __launch_bounds__(64 * WQ * WK, NQ == 1 ? 3 : 2) kv_attention_ke
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[n][d] += off[n][d >> 2];
       const float mm = FMT == kFmtNVFP4 ? m[n] - 11.0f : m[n];
-      if constexpr (WK == 1) {
+      __syncthreads();                                      // the rows before are read
+      float* mine_o = merge_o + (wk * 16 + er) * OS;
 #pragma unroll
-        for (int d = 0; d < DT; d += 4)
+      for (int d = 0; d < DT; d += 4)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v[4] = {o[n][d][i], o[n][d + 1][i], o[n][d + 2][i], o[n][d + 3][i]};
-            emit(wq * 16 * NQ + n * 16 + er, o_feature<FMT, D>(ec, d, i), v, mm, l[n]);
-          }
-      } else {
-        __syncthreads();                                      // the rows before are read
-        float* mine_o = merge_o + (wk * 16 + er) * OS;
-#pragma unroll
-        for (int d = 0; d < DT; d += 4)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(mine_o + o_feature<FMT, D>(ec, d, i)) =
-                make_float4(o[n][d][i], o[n][d + 1][i], o[n][d + 2][i], o[n][d + 3][i]);
-        if (ec == 0) {
-          merge_m[wk][er] = mm;
-          merge_l[wk][er] = l[n];
-        }
-        __syncthreads();
-        constexpr int TPR = NT / 16, FPT = D / TPR;           // threads a row, features a thread
-        const int row = tid / TPR, d = tid % TPR * FPT;
-        float mx = merge_m[0][row], ll = 0.f, v[FPT] = {};
-#pragma unroll
-        for (int w = 1; w < WK; ++w) mx = fmaxf(mx, merge_m[w][row]);
-#pragma unroll
-        for (int w = 0; w < WK; ++w) {
-          const float x = __builtin_amdgcn_exp2f(merge_m[w][row] - mx);
-          ll += merge_l[w][row] * x;
-#pragma unroll
-          for (int e = 0; e < FPT; ++e) v[e] += merge_o[(w * 16 + row) * OS + d + e] * x;
-        }
-        emit(n * 16 + row, d, v, mx, ll);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(mine_o + o_feature<FMT, D>(ec, d, i)) =
+              make_float4(o[n][d][i], o[n][d + 1][i], o[n][d + 2][i], o[n][d + 3][i]);
+      if (ec == 0) {
+        merge_m[wk][er] = mm;
+        merge_l[wk][er] = l[n];
       }
+      __syncthreads();
+      constexpr int TPR = NT / 16, FPT = D / TPR;           // threads a row, features a thread
+      const int row = tid / TPR, d = tid % TPR * FPT;
+      float mx = merge_m[0][row], ll = 0.f, v[FPT] = {};
+#pragma unroll
+      for (int w = 1; w < WK; ++w) mx = fmaxf(mx, merge_m[w][row]);
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        const float x = __builtin_amdgcn_exp2f(merge_m[w][row] - mx);
+        ll += merge_l[w][row] * x;
+#pragma unroll
+        for (int e = 0; e < FPT; ++e) v[e] += merge_o[(w * 16 + row) * OS + d + e] * x;
+      }
+      emit(n * 16 + row, d, v, mx, ll);
     }
     left -= n_units;
     unit += n_units;
@@ -1244,16 +1235,15 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvCache kc, KvAttn a) {
   }
 }
 
-template <int FMT, int D, int NQ, int WQ, int WK, int PL>
+template <int FMT, int D, int NQ, int WK>
 void attend_whole(const KvCache& kc, const KvAttn& a, hipStream_t s) {
-  const unsigned n = kv_numbers<KvTiles<NQ, WQ, WK>::R>(kc, a);
-  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, false><<<dim3(n * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
+  const unsigned n = kv_numbers<KvTiles<NQ, WK>::R>(kc, a);
+  kv_attention_kernel<FMT, D, NQ, WK, false><<<dim3(n * kc.heads), 64 * WK, 0, s>>>(kc, a);
 }
-template <int FMT, int D, int NQ, int WQ, int WK, int PL>
+template <int FMT, int D, int NQ, int WK>
 void attend_split(const KvCache& kc, const KvAttn& a, int jobs, hipStream_t s) {
-  constexpr int R = KvTiles<NQ, WQ, WK>::R, U = KvTiles<NQ, WQ, WK>::U;
-  kv_attention_kernel<FMT, D, NQ, WQ, WK, PL, true><<<dim3(a.ranges * kc.heads), 64 * WQ * WK, 0, s>>>(kc, a);
-  if (a.ranges < 2) return;
+  constexpr int R = KvTiles<NQ, WK>::R, U = KvTiles<NQ, WK>::U;
+  kv_attention_kernel<FMT, D, NQ, WK, true><<<dim3(a.ranges * kc.heads), 64 * WK, 0, s>>>(kc, a);   // two ranges at least
   const int64_t most = kc.cu == nullptr ? a.group : int64_t(kc.M) * a.group, rows = most < R ? most : R;
   const int how = kc.batch <= 64 ? kByJob : kc.cu == nullptr && a.group <= R && kc.batch <= kJoinSeqs ? kBySeq : kByBorder;
   const int x = (how == kByJob ? jobs : how == kBySeq ? kc.batch : a.ranges - 1) * kc.heads;
@@ -1272,12 +1262,12 @@ void attend_plan(const KvPlan& p, const KvCache& kc, const KvAttn& a, hipStream_
   // 8 waves are a CU's at a time, 4 three times: 8 heads, to 700 tokens, 8 waves / 4 (us): 32 sequences 9.8 / 10.2, 64
   // 16.3 / 12.7, 1024 176 / 98.8; to 300 7.5 / 7.7, 11.5 / 8.8, 125 / 59.3; INT4 8.4 / 8.6, 13.0 / 9.9.
   if (p.rows == 16 && p.split)
-    attend_split<FMT, D, 1, 1, 4, 2>(kc, a, p.jobs, s);
+    attend_split<FMT, D, 1, 4>(kc, a, p.jobs, s);
   else if (p.rows == 16)
-    kv_numbers<16>(kc, a) * kc.heads > 256 ? attend_whole<FMT, D, 1, 1, 4, 2>(kc, a, s)
-                                           : attend_whole<FMT, D, 1, 1, 8, 2>(kc, a, s);
+    kv_numbers<16>(kc, a) * kc.heads > 256 ? attend_whole<FMT, D, 1, 4>(kc, a, s)
+                                           : attend_whole<FMT, D, 1, 8>(kc, a, s);
   else if (p.rows == 32)
-    p.split ? attend_split<FMT, D, 2, 1, 4, 2>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 1, 4, 2>(kc, a, s);
+    p.split ? attend_split<FMT, D, 2, 4>(kc, a, p.jobs, s) : attend_whole<FMT, D, 2, 4>(kc, a, s);
   else
     kv_prompt_kernel<FMT, D><<<dim3(unsigned(kv_numbers<128>(kc, a)) * kc.heads), 256, 0, s>>>(kc, a);
 }
