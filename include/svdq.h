@@ -303,8 +303,8 @@ svdq_status svdq_moe(const svdq_layer_desc* dg, const void* wg_packed, const svd
  * the output projection.  A pool holds `pages` pages of `page` tokens, each with K and V of all
  * heads, quantized per token and head by the Q4 rule above (the groups run along head_dim;
  * NVFP4's tensor scale is 1).  The pool is pages x svdq_kv_page_bytes(d) device bytes, 64-byte
- * aligned (a page's bytes are a multiple of 64), one per layer; its layout is opaque, but a page is the same bytes wherever it lies,
- * and the bytes of one token are no other's.  Sequence b's token t is in page
+ * aligned (a page's bytes are a multiple of 64), one per layer; its layout is opaque, but a page is
+ * the same bytes wherever it lies, and the bytes of one token are no other's.  Sequence b's token t is in page
  * table[b ldt + t / page], at t % page.
  *   d       fmt; heads K/V heads (1 .. 256); head_dim 64 or 128; page 16, 32, ... 1024 tokens
  *   pool    may hold anything (NaN bits too) where no token was written
@@ -352,7 +352,7 @@ size_t svdq_kv_page_bytes(const svdq_kv_desc* d);
  *   eps      in [0, 1]
  *   freq     device, float32[pairs] (pairs even, with SVDQ_ROPE_HALVES a multiple of 8, 0 .. head_dim / 2;
  *            0: no rotation)
- *   axis     device, int32[pairs], or NULL: all 0
+ *   axis     device, int32[pairs], or NULL: all 0; a pair whose axis `pos` does not have is at position 0
  *   pos      device, int32, axes x M, or NULL: every axis is the token's place in its sequence
  * A row whose token has no place (lens[b] too small, a page outside the pool) is dropped; its Q is
  * still written.  Two rows of a call with one place (a page in two sequences) are the caller's to avoid:
@@ -379,14 +379,19 @@ svdq_status svdq_kv_read(const svdq_kv_desc* d, const void* pool, int64_t pages,
  * 2^-11 of itself with NVFP4, else to 2^-16, and to 2^-8 in long prompts: where M x q_heads is 384 x 128 or
  * more and a sequence has 128 query rows a K/V head (tokens x q_heads / heads, on average).  The same call gives
  * the same bits.
+ * How a call is cut follows from its sizes alone (batch, M, heads, cols x page, window), the same for all of its
+ * sequences: by the rows that a sequence has on average, and by the table's width, since lengths are on the
+ * device.  So a prompt is better a call of its own beside sequences of single tokens, whose rows would share its
+ * form and its rounding of p_t; and short sequences are faster under a table cut to the longest of them.
  *   Q      device, bf16 bits, M x q_heads head_dim, row stride ldq; q_heads a multiple of heads
  *   scale  > 0
  *   Y      device, bf16 bits, M x q_heads head_dim; its elements are none of Q's
  *   lse    device, float32, M x q_heads, or NULL
  *   workspace  device, svdq_kv_attention_bytes(d, cols, batch, M, q_heads) bytes, 256-byte aligned (NULL
  *              where that is 0); every call writes what it reads of it
- * A row with a NaN or an infinity in Q, or for which scale |Q| or a score leaves fp32's range, has no
- * defined result; it changes no bit of another row.
+ * A row with a NaN or an infinity in Q, or for which scale |Q|, a score or a sum over V leaves fp32's range
+ * (MXFP4 values of 2^94 and more, a stored infinity say, are summed before they are divided), has no defined
+ * result; it changes no bit of another row.
  * M x q_heads <= 2^27 and q_heads <= 4096, else SVDQ_ERR_SHAPE. */
 size_t svdq_kv_attention_bytes(const svdq_kv_desc* d, int32_t cols, int32_t batch, int64_t M, int32_t q_heads);
 svdq_status svdq_kv_attention(const svdq_kv_desc* d, const void* pool, int64_t pages, const int32_t* table,
@@ -413,12 +418,13 @@ svdq_status svdq_kv_copy(const svdq_kv_desc* d, void* pool, int64_t pages, int32
  *            itself (with its columns and stride, else SVDQ_ERR_SHAPE): in place.
  *            Tokens before start[b] do not move in either case
  *   start    device, int32[batch], or NULL: 0
- *   keep     device, int32, batch x most, row stride ldkeep: rising, and so keep[i] >= start + i in place
+ *   keep     device, int32, batch x most, row stride ldkeep: rising, in place from start[b] on, so that
+ *            keep[i] >= start + i
  *   n_keep   device, int32[batch], at most `most` (more counts as `most`, less than 0 as 0)
- *   workspace  device, svdq_kv_compact_bytes(d, planes, batch, most, to == NULL) bytes, 256-byte aligned (NULL
+ *   workspace  device, svdq_kv_compact_bytes(d, planes, batch, most, in place or not) bytes, 256-byte aligned (NULL
  *            where that is 0: apart, for few tokens, or with sequences, heads and layers enough)
- * An index without a place, old or new, moves nothing.  In place, keep that does not rise, and pages that
- * several sequences share, give unspecified tokens in the sequences' own places (nothing else). */
+ * An index without a place, old or new, moves nothing.  In place, keep that does not rise from start[b] on, and
+ * pages that several sequences share, give unspecified tokens in the sequences' own places (nothing else). */
 size_t svdq_kv_compact_bytes(const svdq_kv_desc* d, int32_t planes, int32_t batch, int32_t most, int32_t in_place);
 svdq_status svdq_kv_compact(const svdq_kv_desc* d, void* pool, int64_t pages, int32_t planes, int64_t plane_bytes,
                             const int32_t* table, int64_t ldt, int32_t cols, const int32_t* to, int64_t ldto,

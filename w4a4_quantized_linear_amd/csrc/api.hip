@@ -493,8 +493,9 @@ svdq_status svdq_kv_append(const svdq_kv_desc* d, void* pool, int64_t pages, con
   KvCache kc;
   svdq_status s = check_cache(d, pool, pages, table, ldt, cols, lens, cu, batch, M, &kc);
   if (s == SVDQ_ERR_SHAPE) return s;
-  if (q_heads < 0 || q_heads > kKvMaxQHeads || pairs < 0 || pairs > d->head_dim / 2 || pairs % ((flags & SVDQ_ROPE_HALVES) ? 8 : 2) != 0 || axes < 0 ||
-      axes > kKvMaxAxes || (pos && axes < 1) || !(eps >= 0.0f && eps <= 1.0f))
+  if (q_heads < 0 || q_heads > kKvMaxQHeads || pairs < 0 || pairs > d->head_dim / 2 ||
+      pairs % ((flags & SVDQ_ROPE_HALVES) ? 8 : 2) != 0 || axes < 0 || axes > kKvMaxAxes || (pos && axes < 1) ||
+      !(eps >= 0.0f && eps <= 1.0f))
     return SVDQ_ERR_SHAPE;
   if (s == SVDQ_ERR_FORMAT || (flags & ~uint32_t(SVDQ_ROPE_HALVES)) != 0) return SVDQ_ERR_FORMAT;
   const int64_t cols_kv = int64_t(d->heads) * d->head_dim, cols_q = int64_t(q_heads) * d->head_dim;

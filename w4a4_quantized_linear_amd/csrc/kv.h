@@ -67,6 +67,10 @@ inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most)
 //   4 of 4000, 1536 rows, 384 tiles 165 / 148
 //   1 of 8192, 4096 rows, 256 tiles 220 / 215                        1 of 8192, 8192 rows, 512 tiles 372 / 265
 // (INT4 alike: 512 tiles 141 / 108, 256 tiles 263 / 277.)
+// That is by the average: the sweeps have sequences of alike rows.  A call that holds a prompt and single tokens has
+// one form for both, and one of 128 rows is not split.  2048 rows on 8192 tokens beside n single ones, 8 heads x 4
+// queries, MXFP4, in one call / in two (us): n 16, 63, 127 of 8192 tokens 411 / 284, 465 / 360, 657 / 458; of 65536
+// 1638 / 475, 1832 / 1002, 2278 / 1793.
 // Split where a table's tokens are many for the tiles there are: more than 16 a tile, at least 1024 (32 rows: 12 and
 // 512), at most 4096, since a few long sequences among many short ones are not to be a workgroup's each.  Whole / split,
 // 8 heads, ragged lengths (and all of one):
@@ -79,7 +83,8 @@ inline int kv_compact_slab(int fmt, int D, int batch, int64_t all, int64_t most)
 //            128        1024 16.6 / 17.9 (17.1 / 19.4)        1536 21.3 / 20.1 (21.8 / 21.7)    2048 25.5 / 22.0
 //            256        2048 26.5 / 27.7 (27.4 / 30.3)        4096 43.8 / 41.3 (45.1 / 44.0)    8192 76.3 / 56.2
 //           1024        4096 95.5 / 94.6 (136 / 145)          8192 174 / 164 (280 / 286)
-// INT4 alike.
+// INT4 alike.  The table's width counts, not the lengths, which are on the device: tables of the longest sequence /
+// of 131072 tokens, 1 of 700 9.4 / 11.6, 64 to 300 8.8 / 14.6, 1024 to 300 56.6 / 75.2, 16 to 4000 16.6 / 16.3.
 // Ranges: three workgroups a CU (1, 2, 3, 4 a CU: 64 x 8192 MXFP4 76.9 63.7 59.7 63.4, 3 x 131072 38.7 35.0 35.7
 // 38.2, INT4 64 x 8192 89.3 75.7 69.0 72.7), two where a wave has 32 rows and registers for two.
 constexpr int64_t kKvWhole = 1024;           // tokens up to which a job is one workgroup's, at least (32 rows: half)

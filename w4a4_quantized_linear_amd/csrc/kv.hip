@@ -151,9 +151,10 @@ __device__ __forceinline__ void norm64(double (&z)[8], const float (&w)[8], floa
 // K's norm and rotation are in 64 bits, so that its codes, which are choices, do not hang on an order of summation
 // or on a sine's last bit; the angle pos x freq is a 64-bit product, which holds far positions.  Q's are
 // in 32 bits with the same sines, but for the norm of a head whose squares are not in their range.
-// 9165 rows, 32 + 2 x 8 heads of 128, NVFP4, norm and three axes (209 MB): with a feature pair a lane, IEEE divisions
-// and 64-bit quotients it was bound by its instructions, 98 us; so 57.7
-// (3.6 TB/s).
+// 9165 rows, 32 + 2 x 8 heads of 128, NVFP4, norm and three axes (198 MB): with a feature pair a lane, IEEE divisions
+// and 64-bit quotients it was bound by its instructions, 98 us; so 57.9 (3.4 TB/s), the vector units busy 67% of the
+// time.  Without the norm 53.7, without the rotation 50.9, without both, so without 64-bit arithmetic, 49.5 (4.0 TB/s,
+// busy 48%).  At the four waves a SIMD that the loads want, INT4 heads of 128 spill 11 registers, NVFP4's one.
 template <int FMT, int D>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend a, int parts) {
   constexpr int L = D / 8, HPW = 64 / L, G = kv_group(FMT), AHEAD = 2;
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
   }
 }
 
-// A workgroup takes a row, a wave heads of K or V of it; a row without a place reads as zeros.
+// A workgroup takes a row, a wave heads of K or V of it; a row without a place reads as zeros.  The append's 9165 rows
+// to fp32 (85.6 MB) take 24.4 us (3.5 TB/s): two features a lane, the vector units busy 19% of the time, the rest waits.
 template <int FMT, int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(KvCache kc, void* K, int64_t ldk, void* V, int64_t ldv, int f32) {
   constexpr int LPH = D / 2, HPW = 64 / LPH, G = kv_group(FMT);
@@ -400,7 +402,8 @@ struct KvMoved {
 // gathers and writes the tile of every head and layer (of a part of them where there are few tiles), the next one's
 // loads on their way before the stores.  With a tile of one head a wave the four dependent loads in front (count,
 // index, page, bytes) cost as much as the bytes: 32 sequences' 20 tokens, 24 layers of 8 heads took 11.0 us, so 6.4.  18000
-// of 60000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) take 72 us: of the lines read, most bytes are other tokens'.  In place a
+// of 60000 tokens, 8 heads, 4 layers, NVFP4 (179 MB) take 73 us: a kept token's lines hold others' bytes too, and twice
+// the tokens' own are read.  In place a
 // workgroup walks a sequence's tiles in order, four at a time, all loads of a head before its stores: the tokens that
 // are kept come in rising order, so those of later tiles lie behind every place written so far.
 enum { kApart = 0, kInPlace = 1, kInPlaceByWave = 2, kThrough = 3, kBack = 4 };

@@ -6,8 +6,8 @@
 //     P = exp2(S k - m)
 //     O^T += V^T P^T  A operand: V's codes; B operand: P as it lies in the score registers
 // so nothing passes through LDS or a shuffle but the rare new maximum.  m is the running maximum of a column, moved
-// only when a score exceeds it by kGrow (powers of two that then stand in P, l and O alike cancel), l the running
-// sum in fp32 of the probabilities before they are rounded.
+// only when a score of its own exceeds it by kGrow (powers of two that then stand in P, l and O alike cancel), l the
+// running sum in fp32 of the probabilities before they are rounded.
 //
 // The 16-bit operands, exact but for P:
 //   MXFP4  bf16: E2M1 times its power of two; P bf16
@@ -911,8 +911,8 @@ __global__ void __launch_bounds__(64 * WK, NQ == 1 ? 3 : 2) kv_attention_kernel(
 // of 64; of a chunk each wave makes one tile's operands 16-bit and puts them in LDS in operand order (K's of a
 // tile, its half of V's of a step of 32 tokens), the next chunk's while this one is worked on, with a barrier a chunk.
 // Then a wave's vector instructions are the softmax's and a quarter of the conversions.  2048 queries x 32 heads on
-// 8192 tokens, 8 heads of 128, MXFP4 (241 GFLOP): a wave converting for itself 312 us, so 243
-// (987 TFLOP/s).
+// 8192 tokens, 8 heads of 128, MXFP4 (241 GFLOP): a wave converting for itself 312 us, so 249 (967 TFLOP/s); NVFP4 261,
+// INT4, whose scales multiply scores and probabilities, 343.
 template <int FMT, int D>
 struct KvShared {
   uint4 k[2][4][D / 32][64];
