@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
     sines32.s[j] = float(sines.s[j]);
   }
   for (; u < units; u += parts) {
+    const int h = (u - 2 * kv_units) * HPW + lane / L;
     float x[8];
     unpack_bf8(next(), x);
     if (a.norm_q != nullptr) {
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
       unpack_bf8(wq, w);
       // Squares that leave 32 bits, above or (with an eps no larger) below: the head in 64 bits.  From 2^-80 on the
       // squares that underflow are no part of the sum's 24 bits.
-      const bool in32 = sum >= 0x1p-80f && sum <= 0x1p127f;
+      const bool in32 = h >= a.q_heads || (sum >= 0x1p-80f && sum <= 0x1p127f);
       if (__any(!in32)) {
         double z[8];
 #pragma unroll
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(KvCache kc, KvAppend 
       }
     }
     if (r.pairs > 0) turn<L, float>(x, r, l, sines32);
-    const int h = (u - 2 * kv_units) * HPW + lane / L;
     if (h < a.q_heads)
       *reinterpret_cast<uint4*>(a.Q_out + int64_t(m) * a.ldqo + h * D + 8 * l) =
           make_uint4(cvt_bf2(x[0], x[1]), cvt_bf2(x[2], x[3]), cvt_bf2(x[4], x[5]), cvt_bf2(x[6], x[7]));
